@@ -21,6 +21,7 @@ OK, ERR_ARG, ERR_TREE, ERR_UNSUPPORTED, ERR_CUDA = 0, 1, 2, 3, 4
 F32, BF16 = 0, 1
 SOLVE = {"fwdsub": 0, "neumann": 1, "squaring": 2, "split": 3}
 DEVERR_TREE, DEVERR_GATE, DEVERR_ACCEPTED, DEVERR_TIMEOUT, DEVERR_LENGTH = 0x1, 0x2, 0x4, 0x8, 0x10
+DEVERR_TOKEN = 0x20
 VERIFY_INPUTS_READY = 0x1
 VERIFY_STATE_READY = 0x2
 VERIFY_CLOSED_FORM = 0x4
@@ -28,6 +29,8 @@ VERIFY_PATH_REPLAY = 0x8
 PLAN = {"none": -1, "path_replay": 0, "tc_block": 1, "tc_neumann": 2, "tc_blocked": 3, "fp32": 4, "variant": 5}
 FORCE = {None: 0, "closed_form": VERIFY_CLOSED_FORM, "path_replay": VERIFY_PATH_REPLAY}
 COMMIT_STATE_READY = 0x1
+PREFILL_FORCE = {None: 0, "scan": 0x1, "chunked": 0x2}
+PREFILL_PLAN = {"none": -1, "scan": 0, "chunked": 1}
 ACT = {"none": 0, "silu": 1}
 WS_REGION = {"err": 0, "l": 1, "depth": 2, "mask": 3, "order": 4, "u": 5}
 
@@ -47,6 +50,12 @@ SIGNATURES = {
                                   _P]),
     "canopy_serial_replay_static": (_I, [_P, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P, _I, _P,
                                          _P]),
+    "canopy_prefill_workspace_bytes": (_S, [_I, _I, _I, _I, _I]),
+    "canopy_prefill": (_I, [_P, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P, _I, _P, _P,
+                            ctypes.c_uint, _P]),
+    "canopy_prefill_plan": (_I, [_I, _I, _I, _I, _I, _I, _I, ctypes.c_uint]),
+    "canopy_step": (_I, [_P, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _I, _P, _P]),
+    "canopy_accept": (_I, [_P, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P]),
     "canopy_tree_conv": (_I, [_P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P]),
     "canopy_conv_commit": (_I, [_P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
     "canopy_read_device_error": (_I, [_P, ctypes.POINTER(ctypes.c_int32), _P]),
@@ -274,6 +283,136 @@ def serial_replay_static(q, k, v, g, beta, S0, parent, err=None, o_dtype=torch.f
                                             errp, _stream())
     _check(st, "canopy_serial_replay_static")
     return out
+
+
+def _err(err):
+    if err is None:
+        return None
+    _need(err, "err", torch.int32, (1,))
+    return _ptr(err)
+
+
+def prefill_workspace(N: int, B: int, HV: int, d: int, device="cuda") -> torch.Tensor:
+    """Workspace of prefill calls over up to N packed tokens of B sequences
+    with HV value heads."""
+    n = int(load().canopy_prefill_workspace_bytes(N, B, HV, d, d))
+    if n == 0:
+        raise CanopyError("unsupported sizes for the prefill workspace")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    _check(load().canopy_workspace_init(_ptr(ws), 256, _stream()), "canopy_workspace_init")
+    return ws
+
+
+def prefill(q, k, v, g, beta, S0, starts, ws, o_dtype=torch.float32, out=None, S_out=None, scale: float = 1.0,
+            force=None):
+    """The layer over packed prompts: (o [N, HV, dv], S_new [B, HV, dv, dk]).
+    q, k [N, H, dk] and v [N, HV, dv] hold the tokens of B sequences one
+    after the other; sequence b is tokens starts[b] .. starts[b+1] - 1
+    (starts int32 [B+1], CUDA) and starts from S0[b] (fp32 [B, HV, dv, dk], or
+    None for zero states).  S_out may be S0.  ws: prefill_workspace for at
+    least these sizes.  force: None (the library's dispatch), "scan" or
+    "chunked" (bf16, d = 128)."""
+    _need(q, "q")
+    if q.dim() != 3:
+        raise CanopyError(f"q must have shape (N, H, dk), got {tuple(q.shape)}")
+    N, H, dk = q.shape
+    _need(k, "k", q.dtype, q.shape)
+    _need(v, "v", q.dtype)
+    if v.dim() != 3 or v.shape[0] != N:
+        raise CanopyError(f"v must have shape ({N}, HV, dv), got {tuple(v.shape)}")
+    HV, dv = v.shape[1:]
+    _need(g, "g", torch.float32, (N, HV))
+    _need(beta, "beta", torch.float32, (N, HV))
+    _need(starts, "starts", torch.int32)
+    if starts.dim() != 1 or starts.numel() < 2:
+        raise CanopyError(f"starts must have shape (B + 1,), got {tuple(starts.shape)}")
+    B = starts.numel() - 1
+    if S0 is not None:
+        _need(S0, "S0", torch.float32, (B, HV, dv, dk))
+    _need(ws, "workspace", torch.uint8)
+    lib = load()
+    if ws.numel() < lib.canopy_prefill_workspace_bytes(N, B, HV, dk, dv):
+        raise CanopyError("the workspace is too small for these sizes")
+    if out is None:
+        out = torch.empty((N, HV, dv), dtype=o_dtype, device=q.device)
+    else:
+        _need(out, "o", None, (N, HV, dv))
+    if S_out is None:
+        S_out = torch.empty((B, HV, dv, dk), dtype=torch.float32, device=q.device)
+    else:
+        _need(S_out, "S_new", torch.float32, (B, HV, dv, dk))
+    _check(lib.canopy_prefill(_ptr(q), _ptr(k), _ptr(v), _dt(q), _ptr(g), _ptr(beta),
+                              _ptr(S0) if S0 is not None else None, _ptr(starts), N, B, H, HV, dk, dv, float(scale),
+                              _ptr(out), _dt(out), _ptr(S_out), _ptr(ws), PREFILL_FORCE[force], _stream()),
+           "canopy_prefill")
+    return out, S_out
+
+
+def prefill_plan(N: int, B: int, H: int, HV: int, bf16: bool, d: int, force=None) -> str:
+    """Which path canopy_prefill takes for these sizes (a PREFILL_PLAN name)."""
+    code = load().canopy_prefill_plan(N, B, H, HV, BF16 if bf16 else F32, d, d, PREFILL_FORCE[force])
+    return {v: k for k, v in PREFILL_PLAN.items()}[code]
+
+
+def step(q, k, v, g, beta, S, o_dtype=torch.float32, out=None, S_out=None, scale: float = 1.0, err=None):
+    """One token of every stream: (o [B, HV, dv], S_new [B, HV, dv, dk]).
+    q, k [B, H, dk]; v [B, HV, dv]; g, beta fp32 [B, HV]; S fp32
+    [B, HV, dv, dk].  S_out may be S (in place).  err: an optional int32 CUDA
+    tensor of one element that receives device error bits (OR-ed)."""
+    _need(q, "q")
+    if q.dim() != 3:
+        raise CanopyError(f"q must have shape (B, H, dk), got {tuple(q.shape)}")
+    B, H, dk = q.shape
+    _need(k, "k", q.dtype, q.shape)
+    _need(v, "v", q.dtype)
+    if v.dim() != 3 or v.shape[0] != B:
+        raise CanopyError(f"v must have shape ({B}, HV, dv), got {tuple(v.shape)}")
+    HV, dv = v.shape[1:]
+    _need(g, "g", torch.float32, (B, HV))
+    _need(beta, "beta", torch.float32, (B, HV))
+    _need(S, "S", torch.float32, (B, HV, dv, dk))
+    if out is None:
+        out = torch.empty((B, HV, dv), dtype=o_dtype, device=q.device)
+    else:
+        _need(out, "o", None, (B, HV, dv))
+    if S_out is None:
+        S_out = torch.empty_like(S)
+    else:
+        _need(S_out, "S_new", torch.float32, (B, HV, dv, dk))
+    _check(load().canopy_step(_ptr(q), _ptr(k), _ptr(v), _dt(q), _ptr(g), _ptr(beta), _ptr(S), _ptr(S_out), B, H, HV,
+                              dk, dv, float(scale), _ptr(out), _dt(out), _err(err),
+                              _stream()), "canopy_step")
+    return out, S_out
+
+
+def accept(p, tokens, parent, u, noise, q=None, lengths=None, err=None):
+    """The accepted node of every stream's draft tree, from the target's
+    probabilities and given random numbers: (accepted int32 [B], out_tokens
+    int32 [B, T], counts int32 [B]).  p [B, T, V]: the target's distribution
+    after each node; q: the draft's that each node's children were drawn from
+    (same shape and dtype), or None where the candidates are fixed choices;
+    tokens, parent int32 [B, T] (node 0 is the last emitted token); u fp32
+    [B, T] uniform in [0, 1); noise fp32 [B, V] exponential variates.
+    out_tokens: the accepted tokens in path order, the next token after them,
+    then -1; counts: how many; accepted is what commit and conv_commit take."""
+    _need(p, "p")
+    if p.dim() != 3:
+        raise CanopyError(f"p must have shape (B, T, V), got {tuple(p.shape)}")
+    B, T, V = p.shape
+    if q is not None:
+        _need(q, "q", p.dtype, p.shape)
+    _need(tokens, "tokens", torch.int32, (B, T))
+    _need(parent, "parent", torch.int32, (B, T))
+    _need(u, "u", torch.float32, (B, T))
+    _need(noise, "noise", torch.float32, (B, V))
+    accepted = torch.empty(B, dtype=torch.int32, device=p.device)
+    out_tokens = torch.empty((B, T), dtype=torch.int32, device=p.device)
+    counts = torch.empty(B, dtype=torch.int32, device=p.device)
+    _check(load().canopy_accept(_ptr(p), _ptr(q) if q is not None else None, _dt(p), _ptr(tokens), _ptr(parent),
+                                _lengths(lengths, B), _ptr(u), _ptr(noise), T, B, V, _ptr(accepted),
+                                _ptr(out_tokens), _ptr(counts), _err(err), _stream()),
+           "canopy_accept")
+    return accepted, out_tokens, counts
 
 
 def tree_conv(x, conv_state, weight, parent, bias=None, act: str = "silu", err=None, out=None):

@@ -43,6 +43,16 @@ cudaError_t launch_tree_conv(const void* x, int bf16, const float* state, const 
 cudaError_t launch_conv_commit(const int32_t* accepted, const void* x, int bf16, const int32_t* parent,
                                const float* state, float* state_new, int T, int B, int C, int K, int32_t* err,
                                cudaStream_t st);
+cudaError_t launch_step(const void* q, const void* k, const void* v, int in_bf16, const float* g, const float* beta,
+                        const float* S, float* S_new, int B, int H, int HV, int d, void* o, int o_bf16, float scale,
+                        int32_t* err, cudaStream_t st);
+cudaError_t launch_prefill_scan(const void* q, const void* k, const void* v, int in_bf16, const float* g,
+                                const float* beta, const float* S0, float* S_new, const int32_t* starts, int N, int B,
+                                int H, int HV, int d, void* o, int o_bf16, float scale, int32_t* err,
+                                cudaStream_t st);
+cudaError_t launch_accept(const void* p, const void* q, int bf16, const int32_t* tokens, const int32_t* parent,
+                          const int32_t* lengths, const float* u, const float* noise, int T, int B, int V,
+                          int32_t* accepted, int32_t* out, int32_t* count, int32_t* err, cudaStream_t st);
 }  // namespace canopy
 
 using namespace canopy;
@@ -108,6 +118,24 @@ canopy_plan verify_plan(int T, int B, int HV, canopy_dtype in_dtype, int dk, can
     if (solve == CANOPY_SOLVE_NEUMANN && T <= 64) return CANOPY_PLAN_TC_NEUMANN;
     return CANOPY_PLAN_VARIANT;
 }
+
+constexpr int kMaxGrid = 65535;  // B and HV are launch-grid extents
+
+// The checks of a prefill call that do not look at pointers.
+canopy_status prefill_args(int N, int B, int H, int HV, canopy_dtype in_dtype, canopy_dtype o_dtype, int dk, int dv,
+                           unsigned flags, float scale) {
+    if ((in_dtype != CANOPY_F32 && in_dtype != CANOPY_BF16) || (o_dtype != CANOPY_F32 && o_dtype != CANOPY_BF16) ||
+        !std::isfinite(scale) || (flags & ~(CANOPY_PREFILL_SCAN | CANOPY_PREFILL_CHUNKED)) ||
+        flags == (CANOPY_PREFILL_SCAN | CANOPY_PREFILL_CHUNKED))
+        return CANOPY_ERR_ARG;
+    if (N <= 0 || B <= 0 || H <= 0 || !heads_ok(H, HV)) return CANOPY_ERR_ARG;
+    if (B > kMaxGrid || HV > kMaxGrid || dk != dv || (dk != 128 && dk != 32)) return CANOPY_ERR_UNSUPPORTED;
+    if ((flags & CANOPY_PREFILL_CHUNKED) && (in_dtype != CANOPY_BF16 || dk != 128)) return CANOPY_ERR_UNSUPPORTED;
+    return CANOPY_OK;
+}
+
+// The plan of a prefill call whose arguments passed prefill_args.
+canopy_prefill_plan_t prefill_plan(int, int, int, canopy_dtype, int, unsigned) { return CANOPY_PREFILL_PLAN_SCAN; }
 
 }  // namespace
 
@@ -236,6 +264,62 @@ canopy_status canopy_serial_replay(const void* q, const void* k, const void* v, 
     return cuda_status(launch_serial(q, k, v, in_dtype == CANOPY_BF16, g, beta, S0, parent, T, B, HV, H, dk, o,
                                      o_dtype == CANOPY_BF16, scale, static_cast<float*>(snapshot), ws.err,
                                      static_cast<cudaStream_t>(stream)));
+}
+
+size_t canopy_prefill_workspace_bytes(int N, int B, int HV, int dk, int dv) {
+    if (N < 1 || B < 1 || B > kMaxGrid || HV < 1 || HV > kMaxGrid || dk != dv || (dk != 128 && dk != 32)) return 0;
+    return 256;
+}
+
+canopy_prefill_plan_t canopy_prefill_plan(int N, int B, int H, int HV, canopy_dtype in_dtype, int dk, int dv,
+                                          unsigned flags) {
+    if (prefill_args(N, B, H, HV, in_dtype, CANOPY_F32, dk, dv, flags, 1.f) != CANOPY_OK)
+        return CANOPY_PREFILL_PLAN_NONE;
+    return prefill_plan(N, B, HV, in_dtype, dk, flags);
+}
+
+canopy_status canopy_prefill(const void* q, const void* k, const void* v, canopy_dtype in_dtype, const float* g,
+                             const float* beta, const float* S0, const int32_t* starts, int N, int B, int H, int HV,
+                             int dk, int dv, float scale, void* o, canopy_dtype o_dtype, float* S_new,
+                             void* workspace, unsigned flags, void* stream) {
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(g) || !aligned16(beta) ||
+        (S0 && !aligned16(S0)) || !aligned16(starts) || !aligned16(o) || !aligned16(S_new) || !aligned16(workspace))
+        return CANOPY_ERR_ARG;
+    const canopy_status as = prefill_args(N, B, H, HV, in_dtype, o_dtype, dk, dv, flags, scale);
+    if (as != CANOPY_OK) return as;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(launch_prefill_scan(q, k, v, in_dtype == CANOPY_BF16, g, beta, S0, S_new, starts, N, B, H, HV,
+                                           dk, o, o_dtype == CANOPY_BF16, scale, static_cast<int32_t*>(workspace),
+                                           st));
+}
+
+canopy_status canopy_step(const void* q, const void* k, const void* v, canopy_dtype in_dtype, const float* g,
+                          const float* beta, const float* S, float* S_new, int B, int H, int HV, int dk, int dv,
+                          float scale, void* o, canopy_dtype o_dtype, int32_t* err, void* stream) {
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(g) || !aligned16(beta) || !aligned16(S) ||
+        !aligned16(S_new) || !aligned16(o) || (err && (reinterpret_cast<uintptr_t>(err) & 3u)))
+        return CANOPY_ERR_ARG;
+    if ((in_dtype != CANOPY_F32 && in_dtype != CANOPY_BF16) || (o_dtype != CANOPY_F32 && o_dtype != CANOPY_BF16) ||
+        !std::isfinite(scale))
+        return CANOPY_ERR_ARG;
+    if (B <= 0 || H <= 0 || !heads_ok(H, HV)) return CANOPY_ERR_ARG;
+    if (B > kMaxGrid || HV > kMaxGrid || dk != dv || (dk != 128 && dk != 32)) return CANOPY_ERR_UNSUPPORTED;
+    return cuda_status(launch_step(q, k, v, in_dtype == CANOPY_BF16, g, beta, S, S_new, B, H, HV, dk, o,
+                                   o_dtype == CANOPY_BF16, scale, err, static_cast<cudaStream_t>(stream)));
+}
+
+canopy_status canopy_accept(const void* p, const void* q, canopy_dtype dtype, const int32_t* tokens,
+                            const int32_t* parent, const int32_t* lengths, const float* u, const float* noise, int T,
+                            int B, int V, int32_t* accepted, int32_t* out_tokens, int32_t* counts, int32_t* err,
+                            void* stream) {
+    if (!aligned16(p) || (q && !aligned16(q)) || !aligned16(tokens) || !aligned16(parent) ||
+        (lengths && !aligned16(lengths)) || !aligned16(u) || !aligned16(noise) || !aligned16(accepted) ||
+        !aligned16(out_tokens) || !aligned16(counts) || (err && (reinterpret_cast<uintptr_t>(err) & 3u)))
+        return CANOPY_ERR_ARG;
+    if ((dtype != CANOPY_F32 && dtype != CANOPY_BF16) || B <= 0 || T <= 0 || V <= 0) return CANOPY_ERR_ARG;
+    if (T > kMaxT || V > (1 << 24) || B > kMaxGrid) return CANOPY_ERR_UNSUPPORTED;
+    return cuda_status(launch_accept(p, q, dtype == CANOPY_BF16, tokens, parent, lengths, u, noise, T, B, V, accepted,
+                                     out_tokens, counts, err, static_cast<cudaStream_t>(stream)));
 }
 
 canopy_status canopy_tree_conv(const void* x, canopy_dtype dtype, const float* conv_state, const float* weight,

@@ -1,0 +1,175 @@
+// The layer over packed prompts, token by token in fp32: every input type
+// and head size.
+//
+// canopy page (projects.dotslasha.me/p/canopy.md), "The gated delta rule":
+// per sequence and value head, for its tokens in order,
+//     u = beta (v - g S k),  o = scale (g S q + (k.q) u),  S <- g S + u k^T.
+// Value rows are independent: a CTA of 128 threads keeps 16 rows of one
+// state in registers (eight lanes per row, dk / 8 entries each) and walks
+// the sequence.  Blocks of 16 tokens are read into registers while the block
+// before them is computed from shared memory, so that a token costs the
+// latency of its products, two three-step reductions and the update.
+#include "common.cuh"
+
+namespace canopy {
+
+namespace scan {
+
+constexpr int ROWS = 16;  // state rows per CTA
+constexpr int TB = 16;    // tokens per block
+constexpr int NT = 128;
+
+// Tokens [lo, hi) of sequence b; bounds outside [0, N] or out of order are
+// read as the nearest admissible ones and reported.
+__device__ inline void sequence(const int32_t* starts, int b, int N, int& lo, int& hi, int* bad) {
+    const int s0 = starts[b], s1 = starts[b + 1];
+    lo = min(max(s0, 0), N);
+    hi = min(max(s1, lo), N);
+    if (s0 != lo || s1 != hi) *bad |= CANOPY_DEVERR_LENGTH;
+}
+
+template <typename InT, typename OutT, int D>
+__global__ void __launch_bounds__(NT) scan_kernel(const InT* __restrict__ q, const InT* __restrict__ k,
+                                                  const InT* __restrict__ v, const float* __restrict__ g,
+                                                  const float* __restrict__ beta, const float* S0, float* S_new,
+                                                  const int32_t* __restrict__ starts, OutT* __restrict__ o, int N,
+                                                  int HV, int ratio, float scale, int32_t* __restrict__ err) {
+    constexpr int C4 = D / 32;             // float4 chunks per lane
+    constexpr int PER = TB * D / 4 / NT;   // float4 chunks of a block's q (and k) per thread
+    static_assert(PER >= 1 && TB * ROWS / NT == 2, "staging");
+    __shared__ float4 sQ[TB][D / 4], sK[TB][D / 4];
+    __shared__ float sV[TB][ROWS], sG[TB], sB[TB];
+    const int h = blockIdx.y, b = blockIdx.z, t = threadIdx.x;
+    const int gl = t & 7, row = t >> 3, r0 = blockIdx.x * ROWS;
+    const int H = HV / ratio, hk = h / ratio;
+    pdl_wait();
+    pdl_trigger();  // after the wait: the next kernel may rely on everything before this one
+    int lo, hi, bad = 0;
+    sequence(starts, b, N, lo, hi, &bad);
+
+    const size_t at = ((size_t(b) * HV + h) * D + r0 + row) * D;
+    float4 s[C4];
+#pragma unroll
+    for (int c = 0; c < C4; ++c)
+        s[c] = S0 ? *reinterpret_cast<const float4*>(S0 + at + (c * 8 + gl) * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+
+    float4 nq[PER], nk[PER];
+    float nv[2], ng = 1.f, nb = 0.f;
+    auto fetch = [&](int n0) {  // the block from token n0 into registers; tokens past the end are not read
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            const int i = t + e * NT, n = n0 + i / (D / 4), c = i % (D / 4);
+            nq[e] = nk[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (n < hi) {
+                const size_t p = (size_t(n) * H + hk) * D + c * 4;
+                nq[e] = load4(q + p);
+                nk[e] = load4(k + p);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = t + e * NT, n = n0 + i / ROWS;
+            nv[e] = n < hi ? to_f(v[(size_t(n) * HV + h) * D + r0 + i % ROWS]) : 0.f;
+        }
+        ng = 1.f;
+        nb = 0.f;
+        if (t < TB && n0 + t < hi) {
+            ng = g[size_t(n0 + t) * HV + h];
+            nb = beta[size_t(n0 + t) * HV + h];
+            if (!gate_ok(ng, nb)) {
+                bad |= CANOPY_DEVERR_GATE;
+                ng = 1.f;
+                nb = 0.f;
+            }
+        }
+    };
+    if (lo < hi) fetch(lo);
+    for (int n0 = lo; n0 < hi; n0 += TB) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            const int i = t + e * NT;
+            sQ[i / (D / 4)][i % (D / 4)] = nq[e];
+            sK[i / (D / 4)][i % (D / 4)] = nk[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) sV[(t + e * NT) / ROWS][(t + e * NT) % ROWS] = nv[e];
+        if (t < TB) {
+            sG[t] = ng;
+            sB[t] = nb;
+        }
+        __syncthreads();
+        if (n0 + TB < hi) fetch(n0 + TB);
+        const int m = min(TB, hi - n0);
+#pragma unroll 4
+        for (int n = 0; n < m; ++n) {
+            const float a = sG[n], be = sB[n], vv = sV[n][row];
+            float4 kk[C4];
+            float sk = 0.f, sq = 0.f, kq = 0.f;
+#pragma unroll
+            for (int c = 0; c < C4; ++c) {
+                const float4 x = sK[n][c * 8 + gl], y = sQ[n][c * 8 + gl];
+                kk[c] = x;
+                sk += s[c].x * x.x + s[c].y * x.y + s[c].z * x.z + s[c].w * x.w;
+                sq += s[c].x * y.x + s[c].y * y.y + s[c].z * y.z + s[c].w * y.w;
+                kq += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
+            }
+#pragma unroll
+            for (int x = 4; x; x >>= 1) {
+                sk += __shfl_xor_sync(0xffffffffu, sk, x);
+                sq += __shfl_xor_sync(0xffffffffu, sq, x);
+                kq += __shfl_xor_sync(0xffffffffu, kq, x);
+            }
+            const float u = be * (vv - a * sk);
+#pragma unroll
+            for (int c = 0; c < C4; ++c) {
+                s[c].x = a * s[c].x + u * kk[c].x;
+                s[c].y = a * s[c].y + u * kk[c].y;
+                s[c].z = a * s[c].z + u * kk[c].z;
+                s[c].w = a * s[c].w + u * kk[c].w;
+            }
+            if (gl == 0)
+                store_out(o + (size_t(n0 + n) * HV + h) * D + r0 + row, scale * (a * sq + u * kq));
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < C4; ++c) *reinterpret_cast<float4*>(S_new + at + (c * 8 + gl) * 4) = s[c];
+    if (bad && blockIdx.x == 0) raise_err(err, bad);
+}
+
+template <typename InT, typename OutT, int D>
+cudaError_t launch(const void* q, const void* k, const void* v, const float* g, const float* beta, const float* S0,
+                   float* S_new, const int32_t* starts, void* o, int N, int B, int H, int HV, float scale,
+                   int32_t* err, cudaStream_t st) {
+    return launch_pdl(scan_kernel<InT, OutT, D>, dim3(D / ROWS, HV, B), dim3(NT), 0, st, static_cast<const InT*>(q),
+                      static_cast<const InT*>(k), static_cast<const InT*>(v), g, beta, S0, S_new, starts,
+                      static_cast<OutT*>(o), N, HV, HV / H, scale, err);
+}
+
+}  // namespace scan
+
+cudaError_t launch_prefill_scan(const void* q, const void* k, const void* v, int in_bf16, const float* g,
+                                const float* beta, const float* S0, float* S_new, const int32_t* starts, int N, int B,
+                                int H, int HV, int d, void* o, int o_bf16, float scale, int32_t* err,
+                                cudaStream_t st) {
+    using bf = __nv_bfloat16;
+#define CANOPY_SCAN(IT, OT, D) \
+    return scan::launch<IT, OT, D>(q, k, v, g, beta, S0, S_new, starts, o, N, B, H, HV, scale, err, st)
+    if (d == 128) {
+        if (in_bf16) {
+            if (o_bf16) CANOPY_SCAN(bf, bf, 128);
+            CANOPY_SCAN(bf, float, 128);
+        }
+        if (o_bf16) CANOPY_SCAN(float, bf, 128);
+        CANOPY_SCAN(float, float, 128);
+    }
+    if (in_bf16) {
+        if (o_bf16) CANOPY_SCAN(bf, bf, 32);
+        CANOPY_SCAN(bf, float, 32);
+    }
+    if (o_bf16) CANOPY_SCAN(float, bf, 32);
+    CANOPY_SCAN(float, float, 32);
+#undef CANOPY_SCAN
+}
+
+}  // namespace canopy

@@ -112,7 +112,8 @@ typedef enum {
 #define CANOPY_DEVERR_GATE     0x2  /* g <= 0, g or beta not finite                     */
 #define CANOPY_DEVERR_ACCEPTED 0x4  /* commit: accepted node not in [-1, T)             */
 #define CANOPY_DEVERR_TIMEOUT  0x8  /* an internal bounded wait gave up                 */
-#define CANOPY_DEVERR_LENGTH   0x10 /* verify/commit: lengths[b] not in [0, T]           */
+#define CANOPY_DEVERR_LENGTH   0x10 /* lengths[b] not in [0, T], or starts out of order  */
+#define CANOPY_DEVERR_TOKEN    0x20 /* accept: a drafted token not in [0, V)            */
 
 /* Size in bytes of the workspace one verify/commit pair needs, for HV value
  * heads.  It holds the pseudo-values U fp32 [B][T][HV][dv], the cumulative
@@ -231,6 +232,105 @@ canopy_status canopy_commit(const int32_t* accepted, const float* S0, float* S_n
                             const void* k, const int32_t* parent, const int32_t* lengths,
                             canopy_dtype in_dtype, int T, int B, int H, int HV, int dk, int dv,
                             const void* workspace, unsigned flags, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The steps of a serving loop around the verify and the commit: the layer
+ * over whole prompts, the layer for one token, and the choice of the accepted
+ * node.  Rule, shapes of heads and dtypes are the verify's ("The gated delta
+ * rule"): per sequence and value head,
+ *     S_t = g_t S_{t-1} (I - beta_t k_t k_t^T) + beta_t v_t k_t^T,
+ *     o_t = S_t (scale * q_t). */
+
+/* Flags of canopy_prefill. */
+#define CANOPY_PREFILL_SCAN 0x1u     /* always token by token in fp32                     */
+#define CANOPY_PREFILL_CHUNKED 0x2u  /* always in chunks on the tensor cores (bf16 q/k/v
+                                        and dk = dv = 128, else CANOPY_ERR_UNSUPPORTED)  */
+
+/* How a prefill call is carried out (canopy_prefill_plan). */
+typedef enum {
+    CANOPY_PREFILL_PLAN_NONE = -1,   /* the call would be refused (an argument error)        */
+    CANOPY_PREFILL_PLAN_SCAN = 0,    /* token by token in fp32, one launch                    */
+    CANOPY_PREFILL_PLAN_CHUNKED = 1  /* 64-token chunks on the tensor cores, two launches     */
+} canopy_prefill_plan_t;
+
+/* Size in bytes of the workspace of a prefill over N packed tokens of B
+ * sequences with HV value heads: the device error word (offset 0), and per
+ * 64-token chunk and value head 32 KiB of chunk operands and 768 bytes of
+ * decays.  At most floor(N / 64) + B chunks.  Zero it once with
+ * canopy_workspace_init (the error word; the rest is scratch), read the
+ * word with canopy_read_device_error.  Returns 0 for unsupported sizes. */
+size_t canopy_prefill_workspace_bytes(int N, int B, int HV, int dk, int dv);
+
+/* The layer over B packed prompts of different lengths: sequence b is tokens
+ * starts[b] .. starts[b+1] - 1 of the N packed ones (it may be empty), from
+ * state S0[b] (S0 NULL: zero states) to S_new[b].
+ *   q, k device [N][H][dk], v device [N][HV][dv] in in_dtype; g, beta device
+ *   fp32 [N][HV]; S0 (or NULL), S_new device fp32 [B][HV][dv][dk]; starts
+ *   device int32 [B+1], non-decreasing within [0, N]; o device [N][HV][dv]
+ *   in o_dtype.
+ * S_new may alias S0.  Rows of o outside every sequence are not written.  A
+ * start outside [0, N] or below the one before it sets CANOPY_DEVERR_LENGTH
+ * and is read as the nearest admissible one; gates are checked as the verify
+ * checks them.  A sequence's tokens influence no other sequence, whatever
+ * they hold.  bf16 q/k/v with dk = dv = 128 run in 64-token chunks on the
+ * tensor cores (bf16 operands split so that 24 bits of the state, of U and of
+ * R enter their products; fp32 accumulation, fp32 states), other inputs and
+ * calls of few tokens per sequence token by token in fp32
+ * (canopy_prefill_plan says which).  flags: 0 or one CANOPY_PREFILL_ bit. */
+canopy_status canopy_prefill(const void* q, const void* k, const void* v, canopy_dtype in_dtype, const float* g,
+                             const float* beta, const float* S0, const int32_t* starts, int N, int B, int H, int HV,
+                             int dk, int dv, float scale, void* o, canopy_dtype o_dtype, float* S_new,
+                             void* workspace, unsigned flags, void* stream);
+
+/* The plan canopy_prefill follows for these sizes, dtype and flags.
+ * Host-only, no CUDA call. */
+canopy_prefill_plan_t canopy_prefill_plan(int N, int B, int H, int HV, canopy_dtype in_dtype, int dk, int dv,
+                                          unsigned flags);
+
+/* One token of every stream (the recurrent form): S_new and o from S.
+ *   q, k device [B][H][dk], v device [B][HV][dv] in in_dtype; g, beta device
+ *   fp32 [B][HV]; S, S_new device fp32 [B][HV][dv][dk] (S_new may be S); o
+ *   device [B][HV][dv] in o_dtype; err: optional device int32 that receives
+ *   device error bits (OR-ed), or NULL. */
+canopy_status canopy_step(const void* q, const void* k, const void* v, canopy_dtype in_dtype, const float* g,
+                          const float* beta, const float* S, float* S_new, int B, int H, int HV, int dk, int dv,
+                          float scale, void* o, canopy_dtype o_dtype, int32_t* err, void* stream);
+
+/* Which node of every stream's draft tree the target's probabilities accept,
+ * from given random numbers; the emitted tokens come out distributed as the
+ * target's.  Node 0 is the last emitted token (its own acceptance is not in
+ * question); row i of p is the target's distribution after node i's path,
+ * row i of q the distribution that node i's children were drawn from.  The
+ * walk starts at node 0.  At node i, with r = p_i and Z = 1, the children c
+ * are tried in index order:
+ *   with q:  c is accepted if (u_c Z) q_i(x_c) < r(x_c), x_c its token; a
+ *            refused one leaves r <- max(r - Z q_i, 0), Z <- sum_x r(x)
+ *            (children drawn independently of one another);
+ *   q NULL:  c is accepted if u_c Z < r(x_c); a refused one leaves
+ *            r(x_c) <- 0, Z <- max(Z - r(x_c), 0) (children that are fixed
+ *            choices, all different).
+ * The walk goes on from an accepted child; where none is accepted it ends,
+ * and the next token is the lowest index x with the largest r(x) / noise(x)
+ * (of p_i where r is zero throughout): a draw from r / Z for exponential
+ * noise.  Every product and difference is rounded to fp32 by itself and Z is
+ * summed in units of 2^-46, each r rounded down, so that results do not
+ * depend on any order of summation.
+ *   p, q (or NULL) device [B][T][V] in dtype, non-negative, rows of sum 1;
+ *   tokens, parent device int32 [B][T]; lengths as the verify's (device int32
+ *   [B] or NULL); u device fp32 [B][T], uniform in [0, 1); noise device fp32
+ *   [B][V], exponential variates > 0;
+ *   accepted device int32 [B]: the last accepted node, as canopy_commit and
+ *   canopy_conv_commit take it; out_tokens device int32 [B][T]: the accepted
+ *   children's tokens in path order, then the next token, then -1; counts
+ *   device int32 [B]: how many tokens that is.  A stream of length 0 gets
+ *   accepted -1 and count 0.  A token outside [0, V) is never accepted and
+ *   sets CANOPY_DEVERR_TOKEN in *err (optional device int32, or NULL);
+ *   parents are sanitised as the verify sanitises them.
+ * 1 <= T <= 256, 1 <= V <= 2^24. */
+canopy_status canopy_accept(const void* p, const void* q, canopy_dtype dtype, const int32_t* tokens,
+                            const int32_t* parent, const int32_t* lengths, const float* u, const float* noise, int T,
+                            int B, int V, int32_t* accepted, int32_t* out_tokens, int32_t* counts, int32_t* err,
+                            void* stream);
 
 /* Activation after the short convolution. */
 typedef enum { CANOPY_ACT_NONE = 0, CANOPY_ACT_SILU = 1 } canopy_activation;

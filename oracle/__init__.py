@@ -30,6 +30,8 @@ Modules
                every head of one stream at once (the round trip's check)
   commit       the accepted node's state from the pseudo-values
   conv         the tree-aware short causal convolution and its state commit
+  serving      the layer over packed prompts token by token; the accepted node
+               of a draft tree from probabilities and random numbers
 
 Pins (tests/test_oracle_*.py, run with -m "not gpu"): chain = sequential
 recurrence; brute force on every tree of at most 8 nodes; closed form = replay
@@ -58,3 +60,4 @@ from .closed_form import (  # noqa: F401
 )
 from .commit import commit, commit_batch  # noqa: F401
 from .conv import tree_conv, tree_conv_batch, conv_commit, conv_commit_batch  # noqa: F401
+from . import serving  # noqa: F401

@@ -50,6 +50,10 @@ cudaError_t launch_prefill_scan(const void* q, const void* k, const void* v, int
                                 const float* beta, const float* S0, float* S_new, const int32_t* starts, int N, int B,
                                 int H, int HV, int d, void* o, int o_bf16, float scale, int32_t* err,
                                 cudaStream_t st);
+size_t prefill_chunk_ws_bytes(int N, int B, int HV);
+cudaError_t launch_prefill_chunk(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                                 const float* S0, float* S_new, const int32_t* starts, int N, int B, int H, int HV,
+                                 void* o, int o_bf16, float scale, void* workspace, cudaStream_t st);
 cudaError_t launch_accept(const void* p, const void* q, int bf16, const int32_t* tokens, const int32_t* parent,
                           const int32_t* lengths, const float* u, const float* noise, int T, int B, int V,
                           int32_t* accepted, int32_t* out, int32_t* count, int32_t* err, cudaStream_t st);
@@ -121,6 +125,9 @@ canopy_plan verify_plan(int T, int B, int HV, canopy_dtype in_dtype, int dk, can
 
 constexpr int kMaxGrid = 65535;  // B and HV are launch-grid extents
 
+// (chunk, value head) pairs of a prefill are one launch-grid extent
+bool chunks_ok(int N, int B, int HV) { return (size_t(N) / 64 + B) * HV <= 0x7FFFFFFF; }
+
 // The checks of a prefill call that do not look at pointers.
 canopy_status prefill_args(int N, int B, int H, int HV, canopy_dtype in_dtype, canopy_dtype o_dtype, int dk, int dv,
                            unsigned flags, float scale) {
@@ -130,12 +137,18 @@ canopy_status prefill_args(int N, int B, int H, int HV, canopy_dtype in_dtype, c
         return CANOPY_ERR_ARG;
     if (N <= 0 || B <= 0 || H <= 0 || !heads_ok(H, HV)) return CANOPY_ERR_ARG;
     if (B > kMaxGrid || HV > kMaxGrid || dk != dv || (dk != 128 && dk != 32)) return CANOPY_ERR_UNSUPPORTED;
+    if (!chunks_ok(N, B, HV)) return CANOPY_ERR_UNSUPPORTED;
     if ((flags & CANOPY_PREFILL_CHUNKED) && (in_dtype != CANOPY_BF16 || dk != 128)) return CANOPY_ERR_UNSUPPORTED;
     return CANOPY_OK;
 }
 
 // The plan of a prefill call whose arguments passed prefill_args.
-canopy_prefill_plan_t prefill_plan(int, int, int, canopy_dtype, int, unsigned) { return CANOPY_PREFILL_PLAN_SCAN; }
+canopy_prefill_plan_t prefill_plan(int N, int B, canopy_dtype in_dtype, int dk, unsigned flags) {
+    if (flags & CANOPY_PREFILL_SCAN) return CANOPY_PREFILL_PLAN_SCAN;
+    if (flags & CANOPY_PREFILL_CHUNKED) return CANOPY_PREFILL_PLAN_CHUNKED;
+    const bool bf16_128 = in_dtype == CANOPY_BF16 && dk == 128;
+    return bf16_128 && N >= size_t(32) * B ? CANOPY_PREFILL_PLAN_CHUNKED : CANOPY_PREFILL_PLAN_SCAN;
+}
 
 }  // namespace
 
@@ -267,15 +280,16 @@ canopy_status canopy_serial_replay(const void* q, const void* k, const void* v, 
 }
 
 size_t canopy_prefill_workspace_bytes(int N, int B, int HV, int dk, int dv) {
-    if (N < 1 || B < 1 || B > kMaxGrid || HV < 1 || HV > kMaxGrid || dk != dv || (dk != 128 && dk != 32)) return 0;
-    return 256;
+    if (N < 1 || B < 1 || B > kMaxGrid || HV < 1 || HV > kMaxGrid || dk != dv || (dk != 128 && dk != 32) || !chunks_ok(N, B, HV))
+        return 0;
+    return dk == 128 ? prefill_chunk_ws_bytes(N, B, HV) : 256;
 }
 
 canopy_prefill_plan_t canopy_prefill_plan(int N, int B, int H, int HV, canopy_dtype in_dtype, int dk, int dv,
                                           unsigned flags) {
     if (prefill_args(N, B, H, HV, in_dtype, CANOPY_F32, dk, dv, flags, 1.f) != CANOPY_OK)
         return CANOPY_PREFILL_PLAN_NONE;
-    return prefill_plan(N, B, HV, in_dtype, dk, flags);
+    return prefill_plan(N, B, in_dtype, dk, flags);
 }
 
 canopy_status canopy_prefill(const void* q, const void* k, const void* v, canopy_dtype in_dtype, const float* g,
@@ -288,6 +302,9 @@ canopy_status canopy_prefill(const void* q, const void* k, const void* v, canopy
     const canopy_status as = prefill_args(N, B, H, HV, in_dtype, o_dtype, dk, dv, flags, scale);
     if (as != CANOPY_OK) return as;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (prefill_plan(N, B, in_dtype, dk, flags) == CANOPY_PREFILL_PLAN_CHUNKED)
+        return cuda_status(launch_prefill_chunk(q, k, v, g, beta, S0, S_new, starts, N, B, H, HV, o,
+                                                o_dtype == CANOPY_BF16, scale, workspace, st));
     return cuda_status(launch_prefill_scan(q, k, v, in_dtype == CANOPY_BF16, g, beta, S0, S_new, starts, N, B, H, HV,
                                            dk, o, o_dtype == CANOPY_BF16, scale, static_cast<int32_t*>(workspace),
                                            st));

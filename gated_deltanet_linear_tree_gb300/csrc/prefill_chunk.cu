@@ -1,0 +1,803 @@
+// The layer over packed prompts in 64-token chunks on tcgen05 tensor cores
+// (bf16 q/k/v, dk = dv = 128; fp32 states and accumulation).
+//
+// canopy page (projects.dotslasha.me/p/canopy.md), "The gated delta rule"
+// and "The tree closed form" on a chain: within a chunk, with l_i the sum of
+// log2 g up to token i and S the state before it,
+//     G_ij = beta_i 2^(l_i - l_j) k_i.k_j (j < i),  C_ij = 2^(l_i - l_j) q_i.k_j (j <= i),
+//     M = C (I + G)^-1,  W_i = 2^(l_last - l_i) (I + G)^-1_i,
+//     R = beta (V - 2^l K S^T),  o = scale (2^l Q S^T + M R),  U = W R,
+//     S <- 2^l_last S + sum_j u_j k_j^T.
+// M and W do not depend on the state.  A first launch forms them for every
+// (chunk, value head) at once; a second walks each sequence's chunks in
+// order, and there a chunk is three dependent products:
+//     [X_Q; X_K] = [Q; K] S^T,   [o; U] = [M; W] R,   S += K^T U.
+// Value columns never meet, so the second launch splits a state's 128 value
+// columns into chains of 32.
+//
+// Precision.  q, k and v are exact bf16; S, R, U, M and W enter their
+// products as three bf16 parts (8 + 8 + 8 bits by truncation: the 24 bits of
+// an fp32 value).  The right operand's parts stand side by side along N, so
+// that the left operand is read once for all of them, and products of parts
+// below 2^-24 of the result are left out.  All accumulation is fp32 and S
+// itself stays in fp32 registers across chunks.
+//
+// Chunk slots: sequence b's chunk c is slot starts[b] / 64 + b + c; these
+// never collide, and there are at most N / 64 + B of them.
+#include "common.cuh"
+
+namespace canopy {
+
+bool make_bf16_row_map(CUtensorMap* m, const void* base, int B, int T, int H);
+
+namespace pfc {
+
+constexpr int D = 128;            // dk = dv
+constexpr int C = 64;             // tokens per chunk
+constexpr int QK_BYTES = 32768;   // [Q; K]: 2 atoms of 64 keys x 128 rows x 128 B
+constexpr int MW_PART = 16384;    // [M; W]: 128 rows x 128 B
+constexpr int MW_BYTES = 3 * MW_PART;
+constexpr int GATE_FLOATS = 128;  // 2^l and beta, 64 each
+
+__host__ __device__ inline size_t slot_count(int N, int B) { return size_t(N / C) + B; }
+
+struct WsView {
+    int32_t* err;
+    uint8_t* mw;   // [slot][HV] images of MW_BYTES
+    float* gates;  // [slot][HV][GATE_FLOATS]
+};
+
+__host__ __device__ inline size_t ws_bytes(int N, int B, int HV) {
+    return 256 + slot_count(N, B) * HV * (MW_BYTES + GATE_FLOATS * 4);
+}
+inline WsView ws_view(void* base, int N, int B, int HV) {
+    uint8_t* p = static_cast<uint8_t*>(base);
+    WsView w;
+    w.err = reinterpret_cast<int32_t*>(p);
+    w.mw = p + 256;
+    w.gates = reinterpret_cast<float*>(p + 256 + slot_count(N, B) * HV * MW_BYTES);
+    return w;
+}
+
+// Tokens [lo, hi) of sequence b (see prefill_scan.cu).
+__device__ inline void sequence(const int32_t* starts, int b, int N, int& lo, int& hi, int* bad) {
+    const int s0 = starts[b], s1 = starts[b + 1];
+    lo = min(max(s0, 0), N);
+    hi = min(max(s1, lo), N);
+    if (s0 != lo || s1 != hi) *bad |= CANOPY_DEVERR_LENGTH;
+}
+
+__device__ inline uint32_t bits(float x) { return __float_as_uint(x); }
+__device__ inline float top(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); }
+__device__ inline uint32_t pack_top(float lo, float hi) { return __byte_perm(bits(lo), bits(hi), 0x7632); }
+
+// fp32 pairs in one 64-bit register.
+__device__ inline uint64_t pack2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ inline uint64_t pack2(uint32_t x, uint32_t y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(x), "r"(y));
+    return r;
+}
+__device__ inline float2 unpack2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ inline uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ inline uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ inline uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Two fp32 values as three packed bf16 pairs that sum to them exactly (for
+// normal parts; each part is the top 16 bits of what is left).
+__device__ inline void split3(uint64_t v, uint32_t& h, uint32_t& m, uint32_t& l) {
+    const uint64_t minus1 = 0xBF800000BF800000ull;
+    const float2 x = unpack2(v);
+    const uint64_t v1 = fma2(pack2(top(x.x), top(x.y)), minus1, v);
+    const float2 y = unpack2(v1);
+    const float2 z = unpack2(fma2(pack2(top(y.x), top(y.y)), minus1, v1));
+    h = pack_top(x.x, x.y);
+    m = pack_top(y.x, y.y);
+    l = pack_top(z.x, z.y);
+}
+
+// Shared-memory matrix descriptor.  K-major 128-byte swizzle: sbo = 1024.
+// MN-major: rows of one K index, w bytes of the MN dimension each, in the
+// w-byte swizzle; sbo between groups of 8 K indices, lbo between w-byte
+// groups of the MN dimension.
+__device__ inline uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t swizzle_code) {
+    return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(lbo >> 4) << 16) | (uint64_t(sbo >> 4) << 32) |
+           (uint64_t(1) << 46) | (uint64_t(swizzle_code) << 61);
+}
+constexpr uint32_t kMajorA = 1u << 15, kMajorB = 1u << 16;  // instruction descriptor: operand is MN-major
+
+__device__ inline void bulk_store(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(reinterpret_cast<uint64_t>(dst)),
+                 "r"(smem_u32(src)), "r"(bytes)
+                 : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// M, W and the gates of one (chunk, value head): 128 threads, a row of
+// [C; G] each; the thread of C's row i then solves for row i of M and of W.
+
+struct PrepSmem {
+    static constexpr int QK = 0;                     // later the [M; W] image, over G's space too
+    static constexpr int G = QK + QK_BYTES;          // float [64][GP]
+    static constexpr int GP = 68;                    // row pitch of G
+    static constexpr int L = G + C * GP * 4;         // float2 [64]: l as high and low part
+    static constexpr int BE = L + C * 8;             // float [64]: beta
+    static constexpr int E = BE + C * 4;             // float [64]: 2^(l at the end of j's 16 tokens - l_j)
+    static constexpr int TOT = E + C * 4;            // double: l of the first 32 tokens
+    static constexpr int BAR = TOT + 8;              // u64 [2]
+    static constexpr int SLOT = BAR + 16;
+    static constexpr int TOTAL = SLOT + 8;
+    static_assert(BAR % 8 == 0 && L >= MW_BYTES, "layout");
+};
+
+// Right-looking substitution x (I + G) = x0 for two rows at once, from
+// column HI - 1 down to LO: x[j] -= x[i] G[i][j] for j < i, two columns per
+// instruction.  Every thread reads the same row of G, and a 128-bit broadcast
+// takes the shared-memory pipe four cycles: two rows per thread halve that.
+template <int HI, int LO>
+__device__ inline void substitute(uint64_t (&x)[C / 2], uint64_t (&y)[C / 2], const float* G) {
+#pragma unroll
+    for (int i = HI - 1; i >= LO; --i) {
+        const float2 x2 = unpack2(x[i / 2]), y2 = unpack2(y[i / 2]);
+        const float xi = -((i & 1) ? x2.y : x2.x), yi = -((i & 1) ? y2.y : y2.x);
+        const uint64_t xx = pack2(xi, xi), yy = pack2(yi, yi);
+        const ulonglong2* row = reinterpret_cast<const ulonglong2*>(G + i * PrepSmem::GP);
+#pragma unroll
+        for (int j4 = 0; j4 < (i + 3) / 4; ++j4) {
+            const ulonglong2 g = row[j4];
+            x[2 * j4] = fma2(xx, g.x, x[2 * j4]);
+            y[2 * j4] = fma2(yy, g.x, y[2 * j4]);
+            if (4 * j4 + 2 < i) {
+                x[2 * j4 + 1] = fma2(xx, g.y, x[2 * j4 + 1]);
+                y[2 * j4 + 1] = fma2(yy, g.y, y[2 * j4 + 1]);
+            }
+        }
+    }
+}
+
+// Row `row` of the image's three parts.
+__device__ inline void put_row(uint8_t* image, int row, const uint64_t (&x)[C / 2]) {
+    uint8_t* dst = image + row * 128;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        uint32_t h[4], m[4], l[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split3(x[4 * c + e], h[e], m[e], l[e]);
+        const int off = (c ^ (row & 7)) << 4;
+        *reinterpret_cast<uint4*>(dst + off) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(dst + off + MW_PART) = make_uint4(m[0], m[1], m[2], m[3]);
+        *reinterpret_cast<uint4*>(dst + off + 2 * MW_PART) = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+}
+
+__global__ void __launch_bounds__(128, 3)
+    prep_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                const float* __restrict__ g, const float* __restrict__ beta, const int32_t* __restrict__ starts,
+                int N, int B, int HV, int ratio, WsView ws) {
+    using P = PrepSmem;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float* sG = reinterpret_cast<float*>(sm + P::G);
+    float2* sL = reinterpret_cast<float2*>(sm + P::L);
+    float* sBe = reinterpret_cast<float*>(sm + P::BE);
+    float* sE = reinterpret_cast<float*>(sm + P::E);
+    double* sTot = reinterpret_cast<double*>(sm + P::TOT);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + P::BAR);
+    uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + P::SLOT);
+    int* sFlag = reinterpret_cast<int*>(sm + P::SLOT + 4);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int slot = blockIdx.x / HV, h = blockIdx.x - slot * HV;
+    // Every other CTA has K's rows first: the warp with the longest rows to
+    // solve (tokens 32..63 of C) then sits on another of the SM's four schedulers.
+    const int kfirst = blockIdx.x & 1;
+
+    pdl_wait();
+    // the sequence whose chunk this slot is: the last b with starts[b] / 64 + b <= slot
+    int b = -1;
+    for (int b0 = 0; b0 < B; b0 += 128) {
+        const int j = b0 + tid;
+        const int here = __syncthreads_count(j < B && min(max(starts[min(j, B)], 0), N) / C + j <= slot);
+        b += here;
+        if (here < 128) break;
+    }
+    b = max(b, 0);
+    int s0, s1, bad = 0;
+    sequence(starts, b, N, s0, s1, &bad);
+    const int n0 = s0 + C * (slot - (s0 / C + b));
+    const int valid = min(C, s1 - n0);  // tokens of this chunk
+    if (valid <= 0 || n0 < s0) return;
+
+    uint8_t* tileQ = sm + P::QK + (kfirst ? 8192 : 0);
+    uint8_t* tileK = sm + P::QK + (kfirst ? 0 : 8192);
+    if (tid == 0) {
+        mbar_init(&bars[0], 1);
+        mbar_init(&bars[1], 1);
+        fence_mbar_init();
+        *sFlag = 0;
+        const int hk = h / ratio;
+        mbar_expect_tx(&bars[0], QK_BYTES);
+        tma_load_4d(tileQ, &tmQ, &bars[0], 0, hk, n0, 0);
+        tma_load_4d(tileK, &tmK, &bars[0], 0, hk, n0, 0);
+        tma_load_4d(tileQ + 16384, &tmQ, &bars[0], 64, hk, n0, 0);
+        tma_load_4d(tileK + 16384, &tmK, &bars[0], 64, hk, n0, 0);
+    }
+    if (warp == 3) {
+        tmem_alloc(sTmem, 64);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    pdl_trigger();  // after the wait: the next kernel may rely on everything before this one
+    // gates: l by a scan over the chunk in fp64 (differences of l stay
+    // accurate however far l has fallen); tokens past the end decay nothing
+    double l = 0.0;
+    float be = 0.f;
+    if (tid < C) {
+        float a = 1.f;
+        if (tid < valid) {
+            a = g[size_t(n0 + tid) * HV + h];
+            be = beta[size_t(n0 + tid) * HV + h];
+            if (!gate_ok(a, be)) {
+                bad |= CANOPY_DEVERR_GATE;
+                a = 1.f;
+                be = 0.f;
+            }
+        }
+        l = log2f(a);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const double up = __shfl_up_sync(0xffffffffu, l, d);
+            if (lane >= d) l += up;
+        }
+        if (tid == 31) *sTot = l;
+    }
+    if (bad) raise_err(ws.err, bad);
+    __syncthreads();
+    if (tid < C) {
+        if (warp == 1) l += *sTot;
+        const float lh = float(l);
+        sL[tid] = make_float2(lh, float(l - lh));
+        sBe[tid] = be;
+    }
+    if (tid == 0) {
+        if (mbar_wait(&bars[0], 0)) {
+            const uint32_t aQK = smem_u32(sm + P::QK), aK = smem_u32(tileK), tmem = *sTmem;
+            tc_fence_after();
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+                mma_bf16_ss(tmem, sdesc_sw128(aQK + (ks >> 2) * 16384 + (ks & 3) * 32),
+                            sdesc_sw128(aK + (ks >> 2) * 16384 + (ks & 3) * 32), idesc_bf16(128, 64), ks != 0);
+            mma_commit(&bars[1]);
+        } else {
+            *sFlag = 1;
+        }
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *sTmem;
+    const size_t at = size_t(slot) * HV + h;
+    if (tid < C) {
+        const float2 x = sL[tid], e = sL[tid | 15];
+        sE[tid] = exp2f((e.x - x.x) + (e.y - x.y));
+        float* out = ws.gates + at * GATE_FLOATS;
+        out[tid] = exp2f(x.x + x.y);
+        out[C + tid] = be;
+    }
+    bool ok = !*sFlag && mbar_wait(&bars[1], 0);
+    ok = __syncthreads_and(ok);
+    tc_fence_after();
+
+    if (ok) {
+        // Row i of C or G: the product times 2^(l_i - l_j) (and beta).
+        // Columns before i's own 16 take the decay in two factors <= 1,
+        // split at the end of the column's 16.
+        const int i = tid & 63;
+        const bool krow = (tid >= 64) != bool(kfirst);
+        const float2 li = sL[i];
+        const float f0 = krow ? sBe[i] : 1.f;
+        const bool live = i < valid;
+        uint64_t x[C / 2];
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb) {
+            uint32_t a[16];
+            tmem_ld16(tmem + (uint32_t(warp * 32) << 16) + 16 * kb, a);
+            tmem_wait_ld();
+            const float2 le = sL[16 * kb + 15];
+            const float f = f0 * exp2f((li.x - le.x) + (li.y - le.y));
+            float y[16];
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+                const int j = 16 * kb + u;
+                y[u] = 0.f;
+                if (kb < (i >> 4)) {
+                    y[u] = f * sE[j] * __uint_as_float(a[u]);
+                } else if (kb == (i >> 4)) {
+                    const float2 lj = sL[j];
+                    if (krow ? j < i : j <= i)
+                        y[u] = f0 * exp2f((li.x - lj.x) + (li.y - lj.y)) * __uint_as_float(a[u]);
+                }
+                if (!live) y[u] = 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) x[8 * kb + u] = pack2(y[2 * u], y[2 * u + 1]);
+        }
+        if (krow) {
+#pragma unroll
+            for (int j4 = 0; j4 < 16; ++j4)
+                *reinterpret_cast<ulonglong2*>(sG + i * P::GP + 4 * j4) = make_ulonglong2(x[2 * j4], x[2 * j4 + 1]);
+        }
+        __syncthreads();
+        // rows i of M (x (I + G) = c_i) and of W (the unit row e_i, then
+        // its decay to the chunk's end); the first 32 tokens have nothing
+        // past column 31
+        uint64_t w[C / 2];
+        if (!krow) {
+#pragma unroll
+            for (int j = 0; j < C / 2; ++j) w[j] = pack2(2 * j == i ? 1.f : 0.f, 2 * j + 1 == i ? 1.f : 0.f);
+            if (warp & 1) substitute<64, 32>(x, w, sG);
+            substitute<32, 1>(x, w, sG);
+            const float2 z = sL[C - 1];
+            const float dec = exp2f((z.x - li.x) + (z.y - li.y));
+            const uint64_t dd = pack2(dec, dec);
+#pragma unroll
+            for (int j = 0; j < C / 2; ++j) w[j] = mul2(w[j], dd);
+        }
+        __syncthreads();  // G is free
+        if (!krow) {
+            put_row(sm + P::QK, i, x);
+            put_row(sm + P::QK, C + i, w);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        if (tid == 0) {
+            bulk_store(ws.mw + at * MW_BYTES, sm + P::QK, MW_BYTES);
+            bulk_commit();
+            bulk_wait<0>();
+        }
+    } else if (tid == 0) {
+        raise_err(ws.err, CANOPY_DEVERR_TIMEOUT);
+        mbar_wait(&bars[0], 0);
+    }
+    if (warp == 3) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 64);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The walk over a sequence's chunks for NCH chains of NV value columns each
+// of one head.  A chain has eight compute warps (TMEM quadrant w & 3, columns
+// half w >> 2) and a warp that issues its products; the chains read the same
+// [Q; K] and [M; W] tiles, which one more warp copies in.
+
+constexpr int NV = 32;                   // value columns per chain
+constexpr int HN = NV / 2;               // of a compute thread
+constexpr int ROW = NV * 2;              // bytes of one K index of a B operand part
+constexpr int SPART = D * ROW;           // one part of S
+constexpr int RPART = C * ROW;           // one part of R (and U)
+constexpr uint32_t TX = 0, TO = 3 * NV;  // TMEM columns: [X_Q; X_K] and later K^T U; [o; U]
+constexpr uint32_t CHAIN_COLS = 6 * NV;
+constexpr int kMaxRanked = 128;          // sequences that are started by length
+
+enum { CB_X, CB_OU, CB_DS, CB_S, CB_R, CB_U, CB_N };          // a chain's barriers
+enum { PB_QK = 0, PB_QKE = 2, PB_MW = 4, PB_MWE = 6, PB_LO = 8, PB_LOE, PB_N };  // tiles: full and empty
+
+template <int NCH>
+struct WalkSmem {
+    static constexpr int QK = 0;                  // two buffers
+    static constexpr int MW = QK + 2 * QK_BYTES;  // parts 0 and 1: two buffers
+    static constexpr int LO = MW + 4 * MW_PART;   // part 2: one buffer
+    static constexpr int S = LO + MW_PART;
+    static constexpr int R = S + NCH * 3 * SPART;
+    static constexpr int BAR = R + NCH * 3 * RPART;
+    static constexpr int SLOT = BAR + (PB_N + NCH * CB_N) * 8;
+    static constexpr int TOTAL = SLOT + 8;
+    static_assert(TOTAL + 1024 <= 227 * 1024, "shared memory");
+};
+
+// Columns 16 half .. + 15 of K index k as three parts of a B operand: rows
+// of 64 bytes in the 64-byte swizzle.
+__device__ inline void put_parts(uint8_t* base, int part, int k, int half, const uint64_t (&x)[HN / 2]) {
+#pragma unroll
+    for (int c = 0; c < HN / 8; ++c) {
+        uint32_t h[4], m[4], l[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split3(x[4 * c + e], h[e], m[e], l[e]);
+        uint8_t* p = base + k * ROW + (((half * (HN / 8) + c) ^ ((k >> 1) & 3)) << 4);
+        *reinterpret_cast<uint4*>(p) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(p + part) = make_uint4(m[0], m[1], m[2], m[3]);
+        *reinterpret_cast<uint4*>(p + 2 * part) = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+}
+
+// The three column groups of an accumulator, NV apart, summed: 16 columns
+// at a time where registers allow, else 8.
+__device__ inline void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+template <int NCH>
+__device__ inline void sum_parts(uint32_t taddr, uint64_t (&x)[HN / 2]) {
+    if constexpr (NCH == 1) {
+        uint32_t a[16], b[16], d[16];
+        tmem_ld16(taddr, a);
+        tmem_ld16(taddr + NV, b);
+        tmem_ld16(taddr + 2 * NV, d);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            x[e] = add2(pack2(a[2 * e], a[2 * e + 1]),
+                        add2(pack2(b[2 * e], b[2 * e + 1]), pack2(d[2 * e], d[2 * e + 1])));
+    } else {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            uint32_t a[8], b[8], d[8];
+            tmem_ld8(taddr + 8 * q, a);
+            tmem_ld8(taddr + NV + 8 * q, b);
+            tmem_ld8(taddr + 2 * NV + 8 * q, d);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                x[4 * q + e] = add2(pack2(a[2 * e], a[2 * e + 1]),
+                                    add2(pack2(b[2 * e], b[2 * e + 1]), pack2(d[2 * e], d[2 * e + 1])));
+        }
+    }
+}
+
+template <int NCH, typename OutT>
+__global__ void __launch_bounds__(32 * (9 * NCH + 1), 1)
+    walk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                const __nv_bfloat16* __restrict__ v, const float* S0, float* S_new,
+                const int32_t* __restrict__ starts, OutT* __restrict__ o, int N, int HV, int ratio, float scale,
+                WsView ws) {
+    using L = WalkSmem<NCH>;
+    constexpr uint32_t kCols = NCH == 1 ? 256 : 512;
+    static_assert(NCH * CHAIN_COLS <= kCols, "TMEM columns");
+    constexpr int kComputeWarps = 8 * NCH;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* pb = reinterpret_cast<uint64_t*>(sm + L::BAR);
+    uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + L::SLOT);
+    int* sSeq = reinterpret_cast<int*>(sm + L::SLOT + 4);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int SPLITS = D / (NV * NCH);
+    const int h = blockIdx.x / SPLITS, v0 = (blockIdx.x - h * SPLITS) * NV * NCH;
+
+    if (tid == 0) {
+        *sSeq = blockIdx.y;
+        for (int i = 0; i < PB_N; ++i)
+            mbar_init(&pb[i], (i >= PB_QKE && i < PB_MW) || (i >= PB_MWE && i < PB_LO) || i == PB_LOE ? NCH : 1);
+        for (int c = 0; c < NCH; ++c)
+            for (int i = 0; i < CB_N; ++i)
+                mbar_init(&pb[PB_N + c * CB_N + i], i < CB_S ? 1 : i == CB_U ? 4 : 8);
+        fence_mbar_init();
+    }
+    if (warp == kComputeWarps) {
+        tmem_alloc(sTmem, kCols);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    pdl_wait();
+    pdl_trigger();
+    // The longest sequences start first (they end last): this block takes
+    // the one of its rank.  Every block ranks all sequences, so not for many.
+    const int nseq = gridDim.y;
+    if (nseq > 1 && nseq <= kMaxRanked) {
+        for (int j = tid; j < nseq; j += blockDim.x) {
+            const int len = starts[j + 1] - starts[j];
+            int rank = 0;
+            for (int k = 0; k < nseq; ++k) {
+                const int other = starts[k + 1] - starts[k];
+                rank += other > len || (other == len && k < j);
+            }
+            if (rank == blockIdx.y) *sSeq = j;
+        }
+        __syncthreads();
+    }
+    const int b = *sSeq;
+    int lo, hi, bad = 0;
+    sequence(starts, b, N, lo, hi, &bad);
+    const int nc = (hi - lo + C - 1) / C;
+    const size_t slot0 = size_t(lo / C) + b;
+    bool ok = true;
+
+    if (warp == kComputeWarps + NCH) {
+        // ---- copies -----------------------------------------------------------
+        if (lane == 0) {
+            const int hk = h / ratio;
+            int qk_n = 0, mw_n = 0, lo_n = 0;  // copies issued
+            for (int t = 0; t < nc; ++t) {
+                const int s = t & 1, n = lo + C * t;
+                const uint32_t freed = ((t >> 1) & 1) ^ 1;  // a fresh barrier passes for parity 1
+                const uint8_t* image = ws.mw + ((slot0 + t) * HV + h) * MW_BYTES;
+                uint8_t* qk = sm + L::QK + s * QK_BYTES;
+                if (!(ok = mbar_wait(&pb[PB_QKE + s], freed))) break;
+                mbar_expect_tx(&pb[PB_QK + s], QK_BYTES);
+                tma_load_4d(qk, &tmQ, &pb[PB_QK + s], 0, hk, n, 0);
+                tma_load_4d(qk + 8192, &tmK, &pb[PB_QK + s], 0, hk, n, 0);
+                tma_load_4d(qk + 16384, &tmQ, &pb[PB_QK + s], 64, hk, n, 0);
+                tma_load_4d(qk + 24576, &tmK, &pb[PB_QK + s], 64, hk, n, 0);
+                ++qk_n;
+                if (!(ok = mbar_wait(&pb[PB_MWE + s], freed))) break;
+                mbar_expect_tx(&pb[PB_MW + s], 2 * MW_PART);
+                bulk_load(sm + L::MW + s * 2 * MW_PART, image, 2 * MW_PART, &pb[PB_MW + s]);
+                ++mw_n;
+                if (!(ok = mbar_wait(&pb[PB_LOE], (t & 1) ^ 1))) break;
+                mbar_expect_tx(&pb[PB_LO], MW_PART);
+                bulk_load(sm + L::LO, image + 2 * MW_PART, MW_PART, &pb[PB_LO]);
+                ++lo_n;
+            }
+            if (!ok) {  // the copies in flight land before the block ends
+                raise_err(ws.err, CANOPY_DEVERR_TIMEOUT);
+                for (int e = max(0, qk_n - 2); e < qk_n; ++e) mbar_wait(&pb[PB_QK + (e & 1)], (e >> 1) & 1);
+                for (int e = max(0, mw_n - 2); e < mw_n; ++e) mbar_wait(&pb[PB_MW + (e & 1)], (e >> 1) & 1);
+                if (lo_n) mbar_wait(&pb[PB_LO], (lo_n - 1) & 1);
+            }
+        }
+    } else if (warp >= kComputeWarps) {
+        // ---- the chain's products -----------------------------------------------
+        if (lane == 0) {
+            const int ch = warp - kComputeWarps;
+            uint64_t* cb = pb + PB_N + ch * CB_N;
+            const uint32_t tmem = *sTmem + ch * CHAIN_COLS;
+            const uint32_t aS = smem_u32(sm + L::S + ch * 3 * SPART), aR = smem_u32(sm + L::R + ch * 3 * RPART);
+            const uint32_t aLo = smem_u32(sm + L::LO);
+            constexpr uint32_t i3 = idesc_bf16(128, 3 * NV) | kMajorB, i2 = idesc_bf16(128, 2 * NV) | kMajorB,
+                               i1 = idesc_bf16(128, NV) | kMajorB;
+            for (int t = 0; t < nc; ++t) {
+                const int s = t & 1;
+                const uint32_t par = t & 1, fpar = (t >> 1) & 1;
+                const uint32_t aQK = smem_u32(sm + L::QK + s * QK_BYTES);
+                const uint32_t aMW = smem_u32(sm + L::MW + s * 2 * MW_PART);
+                if (!(ok = mbar_wait(&pb[PB_QK + s], fpar))) break;
+                if (!(ok = mbar_wait(&cb[CB_S], par))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    mma_bf16_ss(tmem + TX, sdesc(aQK + (ks >> 2) * 16384 + (ks & 3) * 32, 0, 1024, 2),
+                                sdesc(aS + ks * 16 * ROW, SPART, 8 * ROW, 4), i3, ks != 0);
+                mma_commit(&cb[CB_X]);
+                if (!(ok = mbar_wait(&pb[PB_MW + s], fpar))) break;
+                if (!(ok = mbar_wait(&pb[PB_LO], par))) break;
+                if (!(ok = mbar_wait(&cb[CB_R], par))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_bf16_ss(tmem + TO, sdesc(aMW + ks * 32, 0, 1024, 2),
+                                sdesc(aR + ks * 16 * ROW, RPART, 8 * ROW, 4), i3, ks != 0);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_bf16_ss(tmem + TO, sdesc(aMW + MW_PART + ks * 32, 0, 1024, 2),
+                                sdesc(aR + ks * 16 * ROW, RPART, 8 * ROW, 4), i2, 1);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_bf16_ss(tmem + TO, sdesc(aLo + ks * 32, 0, 1024, 2),
+                                sdesc(aR + ks * 16 * ROW, RPART, 8 * ROW, 4), i1, 1);
+                mma_commit(&cb[CB_OU]);
+                mma_commit(&pb[PB_MWE + s]);
+                mma_commit(&pb[PB_LOE]);
+                if (!(ok = mbar_wait(&cb[CB_U], par))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_bf16_ss(tmem + TX, sdesc(aQK + 8192 + ks * 2048, 16384, 1024, 2),
+                                sdesc(aR + ks * 16 * ROW, RPART, 8 * ROW, 4), i3 | kMajorA, ks != 0);
+                mma_commit(&cb[CB_DS]);
+                mma_commit(&pb[PB_QKE + s]);
+            }
+            if (!ok) raise_err(ws.err, CANOPY_DEVERR_TIMEOUT);
+        }
+    } else {
+        // ---- the chain's state, R, U and o ----------------------------------------
+        const int ch = warp >> 3, quad = warp & 3, half = (warp >> 2) & 1;
+        uint64_t* cb = pb + PB_N + ch * CB_N;
+        uint8_t* sS = sm + L::S + ch * 3 * SPART;
+        uint8_t* sR = sm + L::R + ch * 3 * RPART;
+        const uint32_t taddr = *sTmem + ch * CHAIN_COLS + (uint32_t(quad * 32) << 16) + half * HN;
+        const int krow = quad * 32 + lane;             // key row of S^T
+        const bool kside = quad >= 2;                  // lanes of K (and U) rather than Q (and o)
+        const int i = (quad & 1) * 32 + lane;          // token row
+        const int col = v0 + ch * NV + half * HN;      // first value column of this thread
+        const size_t sbase = ((size_t(b) * HV + h) * D + col) * D + krow;
+        uint64_t S[HN / 2];
+#pragma unroll
+        for (int c = 0; c < HN / 2; ++c)
+            S[c] = S0 ? pack2(S0[sbase + size_t(2 * c) * D], S0[sbase + size_t(2 * c + 1) * D]) : 0ull;
+        if (bad && tid == 0 && blockIdx.x == 0) raise_err(ws.err, bad);
+
+        // chunk t's values and gates for this thread's token, one chunk ahead
+        uint4 nv[HN / 8];
+        float ng = 0.f, nb = 0.f, nlast = 1.f;
+        const float* gates = ws.gates + (slot0 * HV + h) * GATE_FLOATS;
+        const __nv_bfloat16* vp = v + (size_t(lo + i) * HV + h) * D + col;
+        auto fetch = [&](int t) {
+            ng = gates[i];
+            nlast = gates[C - 1];
+            if (kside) {
+                nb = gates[C + i];
+#pragma unroll
+                for (int c = 0; c < HN / 8; ++c)
+                    nv[c] = lo + C * t + i < hi ? __ldg(reinterpret_cast<const uint4*>(vp) + c) : make_uint4(0, 0, 0, 0);
+            }
+            gates += size_t(HV) * GATE_FLOATS;
+            vp += size_t(C) * HV * D;
+        };
+        if (nc > 0) fetch(0);
+        for (int t = 0; t < nc; ++t) {
+            const uint32_t par = t & 1;
+            const bool live = lo + C * t + i < hi;
+            // S as the B operand of the chunk's first product
+            put_parts(sS, SPART, krow, half, S);
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&cb[CB_S]);
+            const float ga = ng, last = nlast;
+            uint64_t x[HN / 2];
+            if (kside) {  // beta v
+                const uint64_t bb = pack2(nb, nb);
+#pragma unroll
+                for (int c = 0; c < HN / 8; ++c) {
+                    const uint32_t w[4] = {nv[c].x, nv[c].y, nv[c].z, nv[c].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[4 * c + e] = mul2(bb, pack2(w[e] << 16, w[e] & 0xFFFF0000u));
+                }
+            }
+            const float coef = kside ? -nb * ga : ga;
+            if (t + 1 < nc) fetch(t + 1);
+
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&cb[CB_X], par)))) break;
+            tc_fence_after();
+            uint64_t y[HN / 2];
+            sum_parts<NCH>(taddr + TX, y);
+            const uint64_t cc = pack2(coef, coef);
+            if (kside) {
+                // R = beta (v - 2^l X_K); rows past the sequence are zero,
+                // and so are their keys in the last product's operand
+#pragma unroll
+                for (int c = 0; c < HN / 2; ++c) x[c] = fma2(cc, y[c], x[c]);
+                if (!live) {
+#pragma unroll
+                    for (int c = 0; c < HN / 2; ++c) x[c] = 0ull;
+                    uint4* z =
+                        reinterpret_cast<uint4*>(sm + L::QK + (t & 1) * QK_BYTES + half * 16384 + 8192 + i * 128);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) z[c] = make_uint4(0, 0, 0, 0);
+                }
+                put_parts(sR, RPART, i, half, x);
+                fence_proxy_async_smem();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&cb[CB_R]);
+            if (!kside) {
+#pragma unroll
+                for (int c = 0; c < HN / 2; ++c) y[c] = mul2(cc, y[c]);
+            }
+
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&cb[CB_OU], par)))) break;
+            tc_fence_after();
+            sum_parts<NCH>(taddr + TO, x);
+            if (kside) {
+                put_parts(sR, RPART, i, half, x);
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&cb[CB_U]);
+            } else if (live) {
+                OutT* dst = o + (size_t(lo + C * t + i) * HV + h) * D + col;
+                const uint64_t sc = pack2(scale, scale);
+                float f[HN];
+#pragma unroll
+                for (int c = 0; c < HN / 2; ++c) {
+                    const float2 z = unpack2(mul2(sc, add2(x[c], y[c])));
+                    f[2 * c] = z.x;
+                    f[2 * c + 1] = z.y;
+                }
+                if constexpr (sizeof(OutT) == 4) {
+#pragma unroll
+                    for (int c = 0; c < HN / 4; ++c)
+                        reinterpret_cast<float4*>(dst)[c] =
+                            make_float4(f[4 * c], f[4 * c + 1], f[4 * c + 2], f[4 * c + 3]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < HN / 8; ++c) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const __nv_bfloat162 p2 = __floats2bfloat162_rn(f[8 * c + 2 * e], f[8 * c + 2 * e + 1]);
+                            w[e] = *reinterpret_cast<const uint32_t*>(&p2);
+                        }
+                        reinterpret_cast<uint4*>(dst)[c] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&cb[CB_DS], par)))) break;
+            tc_fence_after();
+            sum_parts<NCH>(taddr + TX, y);
+            const uint64_t ll = pack2(last, last);
+#pragma unroll
+            for (int c = 0; c < HN / 2; ++c) S[c] = fma2(ll, S[c], y[c]);
+        }
+#pragma unroll
+        for (int c = 0; c < HN / 2; ++c) {
+            const float2 z = unpack2(S[c]);
+            S_new[sbase + size_t(2 * c) * D] = z.x;
+            S_new[sbase + size_t(2 * c + 1) * D] = z.y;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kComputeWarps) {
+        tc_fence_after();
+        tmem_dealloc(*sTmem, kCols);
+    }
+}
+
+template <int NCH, typename OutT>
+cudaError_t launch_walk(const CUtensorMap& mq, const CUtensorMap& mk, const void* v, const float* S0, float* S_new,
+                        const int32_t* starts, void* o, int N, int B, int H, int HV, float scale, const WsView& ws,
+                        cudaStream_t st) {
+    const int smem = WalkSmem<NCH>::TOTAL + 1024;
+    static const cudaError_t attr = cudaFuncSetAttribute(walk_kernel<NCH, OutT>,
+                                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (attr != cudaSuccess) return attr;
+    return launch_pdl(walk_kernel<NCH, OutT>, dim3(HV * (D / (NV * NCH)), B), dim3(32 * (9 * NCH + 1)), smem, st, mq,
+                      mk, static_cast<const __nv_bfloat16*>(v), S0, S_new, starts, static_cast<OutT*>(o), N, HV,
+                      HV / H, scale, ws);
+}
+
+}  // namespace pfc
+
+size_t prefill_chunk_ws_bytes(int N, int B, int HV) { return pfc::ws_bytes(N, B, HV); }
+
+cudaError_t launch_prefill_chunk(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                                 const float* S0, float* S_new, const int32_t* starts, int N, int B, int H, int HV,
+                                 void* o, int o_bf16, float scale, void* workspace, cudaStream_t st) {
+    CUtensorMap mq, mk;
+    if (!make_bf16_row_map(&mq, q, 1, N, H) || !make_bf16_row_map(&mk, k, 1, N, H)) return cudaErrorInvalidValue;
+    const pfc::WsView ws = pfc::ws_view(workspace, N, B, HV);
+    const int smem = pfc::PrepSmem::TOTAL + 1024;
+    static const cudaError_t attr =
+        cudaFuncSetAttribute(pfc::prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (attr != cudaSuccess) return attr;
+    const cudaError_t e = launch_pdl(pfc::prep_kernel, dim3(unsigned(pfc::slot_count(N, B) * HV)), dim3(128), smem, st,
+                                     mq, mk, g, beta, starts, N, B, HV, HV / H, ws);
+    if (e != cudaSuccess) return e;
+    const bool narrow = size_t(B) * HV <= 76;
+#define CANOPY_WALK(NCH, OT) \
+    return pfc::launch_walk<NCH, OT>(mq, mk, v, S0, S_new, starts, o, N, B, H, HV, scale, ws, st)
+    if (narrow) {
+        if (o_bf16) CANOPY_WALK(1, __nv_bfloat16);
+        CANOPY_WALK(1, float);
+    }
+    if (o_bf16) CANOPY_WALK(2, __nv_bfloat16);
+    CANOPY_WALK(2, float);
+#undef CANOPY_WALK
+}
+
+}  // namespace canopy

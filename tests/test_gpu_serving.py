@@ -69,7 +69,7 @@ def test_step_bad_gate_is_reported_and_contained(lib):
 
 # ---- prefill ----------------------------------------------------------------
 
-PATHS = [("scan", True, 128), ("scan", False, 128), ("scan", False, 32), ("scan", True, 32)]
+PATHS = [("chunked", True, 128), ("scan", True, 128), ("scan", False, 128), ("scan", False, 32), ("scan", True, 32)]
 LENS = [[1], [37], [64], [65], [0, 5, 128, 0], [200, 1, 0, 63, 129], [16, 16, 17]]
 
 
@@ -95,6 +95,18 @@ def test_prefill(lib, force, bf16, d, lens):
     o16, S16, _ = prefill(lib, t, force, d, scale=0.3, o_dtype=torch.bfloat16, S_out=t["S0"])  # in place
     assert torch.equal(o16, o.bfloat16())
     assert torch.equal(S16, S) and S16.data_ptr() == t["S0"].data_ptr()
+
+
+@pytest.mark.parametrize("lens,H,HV", [([130, 1, 0, 64, 77, 191], 7, 14), ([320], 26, 78), ([3] * 140, 1, 1)])
+def test_prefill_many_states(lib, lens, H, HV):
+    """Enough (sequence, value head) pairs for two chains of value columns per block, and more sequences than
+    are started by length."""
+    x = sc.layer_inputs(lens, H, HV, 128, True, seed=HV, kind="rates")
+    o_ref, S_ref = oracle.serving.recurrence(**x)
+    o, S, err = prefill(lib, sc.to_cuda(x, True), "chunked", 128)
+    assert err == 0
+    close(o, o_ref)
+    close(S, S_ref)
 
 
 @pytest.mark.parametrize("force,bf16,d", PATHS)

@@ -28,7 +28,7 @@
 
 namespace canopy {
 
-bool make_bf16_row_map(CUtensorMap* m, const void* base, int B, int T, int H);
+bool make_bf16_row_map(CUtensorMap* m, const void* base, int B, int T, int H, int rows);
 
 namespace pfc {
 
@@ -126,6 +126,10 @@ __device__ inline uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo, uin
 }
 constexpr uint32_t kMajorA = 1u << 15, kMajorB = 1u << 16;  // instruction descriptor: operand is MN-major
 
+__device__ inline void prefetch_map(const CUtensorMap* m) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+
 __device__ inline void bulk_store(void* dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(reinterpret_cast<uint64_t>(dst)),
                  "r"(smem_u32(src)), "r"(bytes)
@@ -134,83 +138,94 @@ __device__ inline void bulk_store(void* dst, const void* src, uint32_t bytes) {
 
 // ---------------------------------------------------------------------------
 // M, W and the gates of one (chunk, value head): 128 threads, a row of
-// [C; G] each; the thread of C's row i then solves for row i of M and of W.
+// [C; I] each.
+//
+// Decays are running products of the gates, from the row's own token back:
+// each is one multiplication from the last (an error of 2^-24 a step, as
+// near as logs and their differences come) and underflows to zero quietly.
+//
+// The substitution x (I + G) = x0 goes by halves of 32 columns, with
+// G = [G00 0; G10 G11]:  x1 (I + G11) = x0_1,  x0 (I + G00) = x0_0 - x1 G10.
+// All threads read the same row of G at a time.  The kernel's shared memory
+// is one array at a fixed, aligned place, so that these addresses are
+// constants: a 128-bit read at a constant address is one pass of the
+// shared-memory pipe, at an address in a register it is four, even where all
+// threads give the same one (measured: 7,100 cycles per block with four
+// blocks on the SM, bound by that pipe).
 
 struct PrepSmem {
-    static constexpr int QK = 0;                     // later the [M; W] image, over G's space too
-    static constexpr int G = QK + QK_BYTES;          // float [64][GP]
-    static constexpr int GP = 68;                    // row pitch of G
-    static constexpr int L = G + C * GP * 4;         // float2 [64]: l as high and low part
-    static constexpr int BE = L + C * 8;             // float [64]: beta
-    static constexpr int E = BE + C * 4;             // float [64]: 2^(l at the end of j's 16 tokens - l_j)
-    static constexpr int TOT = E + C * 4;            // double: l of the first 32 tokens
-    static constexpr int BAR = TOT + 8;              // u64 [2]
+    static constexpr int QK = 0;                     // later the [M; W] image, over all that follows up to GATE
+    static constexpr int P = 68, PW = 36;            // row pitches in floats (no two rows of a store on one bank)
+    static constexpr int ROWC = QK;                  // float [64][P]: rows of C, then x1 of M (over Q and K)
+    static constexpr int ROWW = ROWC + C * P * 4;    // float [64][PW]: x1 of W
+    static constexpr int G = QK + QK_BYTES;          // float [64][P]
+    static constexpr int GATE = G + C * P * 4;       // float [64]: g
+    static constexpr int BE = GATE + C * 4;          // float [64]: beta
+    static constexpr int BAR = BE + C * 4;           // u64 [2]
     static constexpr int SLOT = BAR + 16;
     static constexpr int TOTAL = SLOT + 8;
-    static_assert(BAR % 8 == 0 && L >= MW_BYTES, "layout");
+    static_assert(BAR % 8 == 0 && GATE >= MW_BYTES && ROWW + C * PW * 4 <= G, "layout");
+    static_assert(TOTAL + 1024 <= 56 * 1024, "four blocks per SM");
 };
 
-// Right-looking substitution x (I + G) = x0 for two rows at once, from
-// column HI - 1 down to LO: x[j] -= x[i] G[i][j] for j < i, two columns per
-// instruction.  Every thread reads the same row of G, and a 128-bit broadcast
-// takes the shared-memory pipe four cycles: two rows per thread halve that.
-template <int HI, int LO>
-__device__ inline void substitute(uint64_t (&x)[C / 2], uint64_t (&y)[C / 2], const float* G) {
+// x (I + G) = x0 for 32 columns, from the last one down: x[j] -= x[i] G[i][j]
+// for j < i, two columns per instruction; G's rows are P floats apart.
+__device__ inline void solve32(uint64_t (&x)[16], const float* G) {
 #pragma unroll
-    for (int i = HI - 1; i >= LO; --i) {
-        const float2 x2 = unpack2(x[i / 2]), y2 = unpack2(y[i / 2]);
-        const float xi = -((i & 1) ? x2.y : x2.x), yi = -((i & 1) ? y2.y : y2.x);
-        const uint64_t xx = pack2(xi, xi), yy = pack2(yi, yi);
-        const ulonglong2* row = reinterpret_cast<const ulonglong2*>(G + i * PrepSmem::GP);
+    for (int i = 31; i >= 1; --i) {
+        const float2 x2 = unpack2(x[i / 2]);
+        const float xi = -((i & 1) ? x2.y : x2.x);
+        const uint64_t xx = pack2(xi, xi);
+        const ulonglong2* row = reinterpret_cast<const ulonglong2*>(G + i * PrepSmem::P);
 #pragma unroll
         for (int j4 = 0; j4 < (i + 3) / 4; ++j4) {
             const ulonglong2 g = row[j4];
             x[2 * j4] = fma2(xx, g.x, x[2 * j4]);
-            y[2 * j4] = fma2(yy, g.x, y[2 * j4]);
-            if (4 * j4 + 2 < i) {
-                x[2 * j4 + 1] = fma2(xx, g.y, x[2 * j4 + 1]);
-                y[2 * j4 + 1] = fma2(yy, g.y, y[2 * j4 + 1]);
-            }
+            if (4 * j4 + 2 < i) x[2 * j4 + 1] = fma2(xx, g.y, x[2 * j4 + 1]);
         }
     }
 }
 
-// Row `row` of the image's three parts.
-__device__ inline void put_row(uint8_t* image, int row, const uint64_t (&x)[C / 2]) {
+// Columns 32 half .. + 31 of row `row` of the image's three parts.
+__device__ inline void put_half_row(uint8_t* image, int row, int half, const uint64_t (&x)[16]) {
     uint8_t* dst = image + row * 128;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
+    for (int c = 0; c < 4; ++c) {
         uint32_t h[4], m[4], l[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) split3(x[4 * c + e], h[e], m[e], l[e]);
-        const int off = (c ^ (row & 7)) << 4;
+        const int off = ((4 * half + c) ^ (row & 7)) << 4;
         *reinterpret_cast<uint4*>(dst + off) = make_uint4(h[0], h[1], h[2], h[3]);
         *reinterpret_cast<uint4*>(dst + off + MW_PART) = make_uint4(m[0], m[1], m[2], m[3]);
         *reinterpret_cast<uint4*>(dst + off + 2 * MW_PART) = make_uint4(l[0], l[1], l[2], l[3]);
     }
 }
 
-__global__ void __launch_bounds__(128, 3)
+__global__ void __launch_bounds__(128, 4)
     prep_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const float* __restrict__ g, const float* __restrict__ beta, const int32_t* __restrict__ starts,
                 int N, int B, int HV, int ratio, WsView ws) {
     using P = PrepSmem;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t sm[];
     float* sG = reinterpret_cast<float*>(sm + P::G);
-    float2* sL = reinterpret_cast<float2*>(sm + P::L);
+    float* sGate = reinterpret_cast<float*>(sm + P::GATE);
     float* sBe = reinterpret_cast<float*>(sm + P::BE);
-    float* sE = reinterpret_cast<float*>(sm + P::E);
-    double* sTot = reinterpret_cast<double*>(sm + P::TOT);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + P::BAR);
     uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + P::SLOT);
-    int* sFlag = reinterpret_cast<int*>(sm + P::SLOT + 4);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5;
     const int slot = blockIdx.x / HV, h = blockIdx.x - slot * HV;
-    // Every other CTA has K's rows first: the warp with the longest rows to
-    // solve (tokens 32..63 of C) then sits on another of the SM's four schedulers.
-    const int kfirst = blockIdx.x & 1;
+    // Tile row r is token (r & 63) ^ flip, of Q for r < 64 and of K beyond:
+    // the two warps with the long rows sit on the SM's schedulers 1 and 3 in
+    // even blocks, 0 and 2 in odd ones.
+    const int flip = (blockIdx.x & 1) * 32;
 
+    if (tid == 0) {
+        mbar_init(&bars[0], 1);
+        mbar_init(&bars[1], 1);
+        fence_mbar_init();
+        prefetch_map(&tmQ);
+        prefetch_map(&tmK);
+    }
     pdl_wait();
     // the sequence whose chunk this slot is: the last b with starts[b] / 64 + b <= slot
     int b = -1;
@@ -227,19 +242,15 @@ __global__ void __launch_bounds__(128, 3)
     const int valid = min(C, s1 - n0);  // tokens of this chunk
     if (valid <= 0 || n0 < s0) return;
 
-    uint8_t* tileQ = sm + P::QK + (kfirst ? 8192 : 0);
-    uint8_t* tileK = sm + P::QK + (kfirst ? 0 : 8192);
     if (tid == 0) {
-        mbar_init(&bars[0], 1);
-        mbar_init(&bars[1], 1);
-        fence_mbar_init();
-        *sFlag = 0;
         const int hk = h / ratio;
         mbar_expect_tx(&bars[0], QK_BYTES);
-        tma_load_4d(tileQ, &tmQ, &bars[0], 0, hk, n0, 0);
-        tma_load_4d(tileK, &tmK, &bars[0], 0, hk, n0, 0);
-        tma_load_4d(tileQ + 16384, &tmQ, &bars[0], 64, hk, n0, 0);
-        tma_load_4d(tileK + 16384, &tmK, &bars[0], 64, hk, n0, 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // 32 tokens of 64 keys: (half, atom)
+            const int off = ((32 * (e & 1)) ^ flip) * 128 + (e >> 1) * 16384;
+            tma_load_4d(sm + P::QK + off, &tmQ, &bars[0], 64 * (e >> 1), hk, n0 + 32 * (e & 1), 0);
+            tma_load_4d(sm + P::QK + off + 8192, &tmK, &bars[0], 64 * (e >> 1), hk, n0 + 32 * (e & 1), 0);
+        }
     }
     if (warp == 3) {
         tmem_alloc(sTmem, 64);
@@ -247,12 +258,8 @@ __global__ void __launch_bounds__(128, 3)
         tc_fence_before();
     }
     pdl_trigger();  // after the wait: the next kernel may rely on everything before this one
-    // gates: l by a scan over the chunk in fp64 (differences of l stay
-    // accurate however far l has fallen); tokens past the end decay nothing
-    double l = 0.0;
-    float be = 0.f;
-    if (tid < C) {
-        float a = 1.f;
+    if (tid < C) {  // tokens past the end decay and write nothing
+        float a = 1.f, be = 0.f;
         if (tid < valid) {
             a = g[size_t(n0 + tid) * HV + h];
             be = beta[size_t(n0 + tid) * HV + h];
@@ -262,109 +269,123 @@ __global__ void __launch_bounds__(128, 3)
                 be = 0.f;
             }
         }
-        l = log2f(a);
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const double up = __shfl_up_sync(0xffffffffu, l, d);
-            if (lane >= d) l += up;
-        }
-        if (tid == 31) *sTot = l;
+        sGate[tid] = a;
+        sBe[tid] = be;
     }
     if (bad) raise_err(ws.err, bad);
     __syncthreads();
-    if (tid < C) {
-        if (warp == 1) l += *sTot;
-        const float lh = float(l);
-        sL[tid] = make_float2(lh, float(l - lh));
-        sBe[tid] = be;
-    }
-    if (tid == 0) {
-        if (mbar_wait(&bars[0], 0)) {
-            const uint32_t aQK = smem_u32(sm + P::QK), aK = smem_u32(tileK), tmem = *sTmem;
-            tc_fence_after();
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-                mma_bf16_ss(tmem, sdesc_sw128(aQK + (ks >> 2) * 16384 + (ks & 3) * 32),
-                            sdesc_sw128(aK + (ks >> 2) * 16384 + (ks & 3) * 32), idesc_bf16(128, 64), ks != 0);
-            mma_commit(&bars[1]);
-        } else {
-            *sFlag = 1;
-        }
-    }
-    __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *sTmem;
-    const size_t at = size_t(slot) * HV + h;
-    if (tid < C) {
-        const float2 x = sL[tid], e = sL[tid | 15];
-        sE[tid] = exp2f((e.x - x.x) + (e.y - x.y));
-        float* out = ws.gates + at * GATE_FLOATS;
-        out[tid] = exp2f(x.x + x.y);
-        out[C + tid] = be;
+    if (tid == 0 && mbar_wait(&bars[0], 0)) {
+        const uint32_t aQK = smem_u32(sm + P::QK);
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+            mma_bf16_ss(tmem, sdesc_sw128(aQK + (ks >> 2) * 16384 + (ks & 3) * 32),
+                        sdesc_sw128(aQK + (ks >> 2) * 16384 + 8192 + (ks & 3) * 32), idesc_bf16(128, 64), ks != 0);
+        mma_commit(&bars[1]);
     }
-    bool ok = !*sFlag && mbar_wait(&bars[1], 0);
-    ok = __syncthreads_and(ok);
+    __syncwarp();
+    const bool ok = __syncthreads_and(mbar_wait(&bars[1], 0));
     tc_fence_after();
 
     if (ok) {
-        // Row i of C or G: the product times 2^(l_i - l_j) (and beta).
-        // Columns before i's own 16 take the decay in two factors <= 1,
-        // split at the end of the column's 16.
-        const int i = tid & 63;
-        const bool krow = (tid >= 64) != bool(kfirst);
-        const float2 li = sL[i];
-        const float f0 = krow ? sBe[i] : 1.f;
+        // Row i of C (2^(l_i - l_j) q_i.k_j, j <= i) or G (times beta, j < i).
+        const int i = (tid & 63) ^ flip;
+        const bool krow = tid >= C;
         const bool live = i < valid;
-        uint64_t x[C / 2];
-#pragma unroll
-        for (int kb = 0; kb < 4; ++kb) {
+        const size_t at = size_t(slot) * HV + h;
+        float* rowp = (krow ? sG : reinterpret_cast<float*>(sm + P::ROWC)) + i * P::P;
+        float d = krow ? sBe[i] : 1.f;  // beta g_{j+1} .. g_i
+        float end = 1.f;                // g_{i+1} .. g_63
+#pragma unroll 1
+        for (int kb = 3; kb >= 0; --kb) {
             uint32_t a[16];
-            tmem_ld16(tmem + (uint32_t(warp * 32) << 16) + 16 * kb, a);
+            tmem_ld16(tmem + (uint32_t(warp * 32) << 16) + ((16 * kb) ^ flip), a);
             tmem_wait_ld();
-            const float2 le = sL[16 * kb + 15];
-            const float f = f0 * exp2f((li.x - le.x) + (li.y - le.y));
-            float y[16];
+            const int last = i - 16 * kb;  // the row's own column in this 16
+            const int lim = !live ? -1 : krow ? last - 1 : last;
 #pragma unroll
-            for (int u = 0; u < 16; ++u) {
-                const int j = 16 * kb + u;
-                y[u] = 0.f;
-                if (kb < (i >> 4)) {
-                    y[u] = f * sE[j] * __uint_as_float(a[u]);
-                } else if (kb == (i >> 4)) {
-                    const float2 lj = sL[j];
-                    if (krow ? j < i : j <= i)
-                        y[u] = f0 * exp2f((li.x - lj.x) + (li.y - lj.y)) * __uint_as_float(a[u]);
+            for (int u4 = 3; u4 >= 0; --u4) {
+                const float4 g4 = *reinterpret_cast<const float4*>(sGate + 16 * kb + 4 * u4);
+                const float gg[4] = {g4.x, g4.y, g4.z, g4.w};
+                float y[4];
+#pragma unroll
+                for (int u = 3; u >= 0; --u) {
+                    y[u] = 4 * u4 + u <= lim ? d * __uint_as_float(a[4 * u4 + u]) : 0.f;
+                    if (4 * u4 + u <= last) d *= gg[u];
+                    else end *= gg[u];
                 }
-                if (!live) y[u] = 0.f;
+                *reinterpret_cast<float4*>(rowp + 16 * kb + 4 * u4) = make_float4(y[0], y[1], y[2], y[3]);
             }
-#pragma unroll
-            for (int u = 0; u < 8; ++u) x[8 * kb + u] = pack2(y[2 * u], y[2 * u + 1]);
         }
-        if (krow) {
-#pragma unroll
-            for (int j4 = 0; j4 < 16; ++j4)
-                *reinterpret_cast<ulonglong2*>(sG + i * P::GP + 4 * j4) = make_ulonglong2(x[2 * j4], x[2 * j4 + 1]);
-        }
+        float* gates = ws.gates + at * GATE_FLOATS;
+        gates[krow ? C + i : i] = krow ? sBe[i] : d;
         __syncthreads();
-        // rows i of M (x (I + G) = c_i) and of W (the unit row e_i, then
-        // its decay to the chunk's end); the first 32 tokens have nothing
-        // past column 31
-        uint64_t w[C / 2];
-        if (!krow) {
+        // Row i of M (from c_i), or of W (from the unit row e_i, with its
+        // decay to the chunk's end at last).  x1 is kept in shared memory;
+        // the first 32 tokens have none.
+        float* keep = krow ? reinterpret_cast<float*>(sm + P::ROWW) + i * P::PW : rowp + 32;
+        const bool upper = i >= 32;
+        uint64_t x[16];
+        auto start = [&](int half) {
+            if (krow) {
 #pragma unroll
-            for (int j = 0; j < C / 2; ++j) w[j] = pack2(2 * j == i ? 1.f : 0.f, 2 * j + 1 == i ? 1.f : 0.f);
-            if (warp & 1) substitute<64, 32>(x, w, sG);
-            substitute<32, 1>(x, w, sG);
-            const float2 z = sL[C - 1];
-            const float dec = exp2f((z.x - li.x) + (z.y - li.y));
-            const uint64_t dd = pack2(dec, dec);
+                for (int j = 0; j < 16; ++j)
+                    x[j] = pack2(32 * half + 2 * j == i ? 1.f : 0.f, 32 * half + 2 * j + 1 == i ? 1.f : 0.f);
+            } else {
 #pragma unroll
-            for (int j = 0; j < C / 2; ++j) w[j] = mul2(w[j], dd);
+                for (int j = 0; j < 8; ++j) {
+                    const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(rowp + 32 * half + 4 * j);
+                    x[2 * j] = y.x;
+                    x[2 * j + 1] = y.y;
+                }
+            }
+        };
+        if (upper) {
+            start(1);
+            solve32(x, sG + 32 * P::P + 32);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<ulonglong2*>(keep + 4 * j) = make_ulonglong2(x[2 * j], x[2 * j + 1]);
+            start(0);
+#pragma unroll
+            for (int k4 = 0; k4 < 8; ++k4) {
+                const float4 xk4 = *reinterpret_cast<const float4*>(keep + 4 * k4);
+                const float xk[4] = {xk4.x, xk4.y, xk4.z, xk4.w};
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint64_t xx = pack2(-xk[u], -xk[u]);
+                    const ulonglong2* row = reinterpret_cast<const ulonglong2*>(sG + (32 + 4 * k4 + u) * P::P);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const ulonglong2 y = row[j];
+                        x[2 * j] = fma2(xx, y.x, x[2 * j]);
+                        x[2 * j + 1] = fma2(xx, y.y, x[2 * j + 1]);
+                    }
+                }
+            }
+        } else {
+            start(0);
         }
-        __syncthreads();  // G is free
-        if (!krow) {
-            put_row(sm + P::QK, i, x);
-            put_row(sm + P::QK, C + i, w);
+        solve32(x, sG);
+        uint64_t x1[16];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const ulonglong2 y = upper ? *reinterpret_cast<const ulonglong2*>(keep + 4 * j) : make_ulonglong2(0, 0);
+            x1[2 * j] = y.x;
+            x1[2 * j + 1] = y.y;
+        }
+        __syncthreads();  // everything before the image is done with
+        const int row = (i >> 4) * 32 + (i & 15) + (krow ? 16 : 0);
+        const uint64_t dd = krow ? pack2(end, end) : pack2(1.f, 1.f);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] = mul2(x[j], dd);
+            put_half_row(sm + P::QK, row, half, x);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] = x1[j];
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -389,6 +410,12 @@ __global__ void __launch_bounds__(128, 3)
 // of one head.  A chain has eight compute warps (TMEM quadrant w & 3, columns
 // half w >> 2) and a warp that issues its products; the chains read the same
 // [Q; K] and [M; W] tiles, which one more warp copies in.
+//
+// The tiles' rows alternate by 16 tokens: Q (M), K (W), Q, K, ..., so that
+// each TMEM quadrant holds 16 token rows of X_Q (o) and 16 of X_K (U), and
+// the rows of K, on the critical path, are shared by the SM's four
+// schedulers.  A warp reads 16 of its lanes at a time with all its threads:
+// thread t has rows t / 4 and t / 4 + 8, columns 2 (t % 4), + 1, + 8, + 9.
 
 constexpr int NV = 32;                   // value columns per chain
 constexpr int HN = NV / 2;               // of a compute thread
@@ -414,6 +441,46 @@ struct WalkSmem {
     static constexpr int TOTAL = SLOT + 8;
     static_assert(TOTAL + 1024 <= 227 * 1024, "shared memory");
 };
+
+// 16 TMEM lanes x 16 columns: for e = 0, 1 (rows) and c = 0, 1 (groups of 8
+// columns) x[2 e + c] is the pair at row t / 4 + 8 e, columns 8 c + 2 (t % 4);
+// the three column groups of an accumulator, NV apart, summed.
+__device__ inline void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ inline void sum_rows16(uint32_t taddr, uint64_t (&x)[4]) {
+    uint32_t a[8], b[8], d[8];
+    tmem_ld_16x256b_x2(taddr, a);
+    tmem_ld_16x256b_x2(taddr + NV, b);
+    tmem_ld_16x256b_x2(taddr + 2 * NV, d);
+    tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = 4 * c + 2 * e;
+            x[2 * e + c] = add2(pack2(a[r], a[r + 1]), add2(pack2(b[r], b[r + 1]), pack2(d[r], d[r + 1])));
+        }
+}
+
+// The same values as three parts of a B operand whose K index is the token:
+// k0 is the first of the 16 tokens.
+__device__ inline void put_rows16(uint8_t* base, int k0, int half, int lane, const uint64_t (&x)[4]) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int k = k0 + (lane >> 2) + 8 * e;
+            uint32_t h, m, l;
+            split3(x[2 * e + c], h, m, l);
+            uint8_t* p = base + k * ROW + (((half * 2 + c) ^ ((k >> 1) & 3)) << 4) + (lane & 3) * 4;
+            *reinterpret_cast<uint32_t*>(p) = h;
+            *reinterpret_cast<uint32_t*>(p + RPART) = m;
+            *reinterpret_cast<uint32_t*>(p + 2 * RPART) = l;
+        }
+}
 
 // Columns 16 half .. + 15 of K index k as three parts of a B operand: rows
 // of 64 bytes in the 64-byte swizzle.
@@ -475,8 +542,7 @@ __global__ void __launch_bounds__(32 * (9 * NCH + 1), 1)
     constexpr uint32_t kCols = NCH == 1 ? 256 : 512;
     static_assert(NCH * CHAIN_COLS <= kCols, "TMEM columns");
     constexpr int kComputeWarps = 8 * NCH;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t* pb = reinterpret_cast<uint64_t*>(sm + L::BAR);
     uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + L::SLOT);
     int* sSeq = reinterpret_cast<int*>(sm + L::SLOT + 4);
@@ -485,12 +551,14 @@ __global__ void __launch_bounds__(32 * (9 * NCH + 1), 1)
     const int h = blockIdx.x / SPLITS, v0 = (blockIdx.x - h * SPLITS) * NV * NCH;
 
     if (tid == 0) {
+        prefetch_map(&tmQ);
+        prefetch_map(&tmK);
         *sSeq = blockIdx.y;
         for (int i = 0; i < PB_N; ++i)
             mbar_init(&pb[i], (i >= PB_QKE && i < PB_MW) || (i >= PB_MWE && i < PB_LO) || i == PB_LOE ? NCH : 1);
         for (int c = 0; c < NCH; ++c)
             for (int i = 0; i < CB_N; ++i)
-                mbar_init(&pb[PB_N + c * CB_N + i], i < CB_S ? 1 : i == CB_U ? 4 : 8);
+                mbar_init(&pb[PB_N + c * CB_N + i], i < CB_S ? 1 : 8);
         fence_mbar_init();
     }
     if (warp == kComputeWarps) {
@@ -536,10 +604,12 @@ __global__ void __launch_bounds__(32 * (9 * NCH + 1), 1)
                 uint8_t* qk = sm + L::QK + s * QK_BYTES;
                 if (!(ok = mbar_wait(&pb[PB_QKE + s], freed))) break;
                 mbar_expect_tx(&pb[PB_QK + s], QK_BYTES);
-                tma_load_4d(qk, &tmQ, &pb[PB_QK + s], 0, hk, n, 0);
-                tma_load_4d(qk + 8192, &tmK, &pb[PB_QK + s], 0, hk, n, 0);
-                tma_load_4d(qk + 16384, &tmQ, &pb[PB_QK + s], 64, hk, n, 0);
-                tma_load_4d(qk + 24576, &tmK, &pb[PB_QK + s], 64, hk, n, 0);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {  // 16 tokens of 64 keys: (tokens, atom)
+                    uint8_t* dst = qk + (e & 3) * 4096 + (e >> 2) * 16384;
+                    tma_load_4d(dst, &tmQ, &pb[PB_QK + s], 64 * (e >> 2), hk, n + 16 * (e & 3), 0);
+                    tma_load_4d(dst + 2048, &tmK, &pb[PB_QK + s], 64 * (e >> 2), hk, n + 16 * (e & 3), 0);
+                }
                 ++qk_n;
                 if (!(ok = mbar_wait(&pb[PB_MWE + s], freed))) break;
                 mbar_expect_tx(&pb[PB_MW + s], 2 * MW_PART);
@@ -567,7 +637,10 @@ __global__ void __launch_bounds__(32 * (9 * NCH + 1), 1)
             const uint32_t aLo = smem_u32(sm + L::LO);
             constexpr uint32_t i3 = idesc_bf16(128, 3 * NV) | kMajorB, i2 = idesc_bf16(128, 2 * NV) | kMajorB,
                                i1 = idesc_bf16(128, NV) | kMajorB;
-            for (int t = 0; t < nc; ++t) {
+            // The second chain starts half a chunk after the first, so that
+            // one's products run beside the other's register work.
+            if (ch && nc > 0) ok = mbar_wait(&pb[PB_N + CB_R], 0);
+            for (int t = 0; t < nc && ok; ++t) {
                 const int s = t & 1;
                 const uint32_t par = t & 1, fpar = (t >> 1) & 1;
                 const uint32_t aQK = smem_u32(sm + L::QK + s * QK_BYTES);
@@ -603,7 +676,7 @@ __global__ void __launch_bounds__(32 * (9 * NCH + 1), 1)
                 tc_fence_after();
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    mma_bf16_ss(tmem + TX, sdesc(aQK + 8192 + ks * 2048, 16384, 1024, 2),
+                    mma_bf16_ss(tmem + TX, sdesc(aQK + 2048 + ks * 4096, 16384, 1024, 2),
                                 sdesc(aR + ks * 16 * ROW, RPART, 8 * ROW, 4), i3 | kMajorA, ks != 0);
                 mma_commit(&cb[CB_DS]);
                 mma_commit(&pb[PB_QKE + s]);
@@ -617,10 +690,10 @@ __global__ void __launch_bounds__(32 * (9 * NCH + 1), 1)
         uint8_t* sS = sm + L::S + ch * 3 * SPART;
         uint8_t* sR = sm + L::R + ch * 3 * RPART;
         const uint32_t taddr = *sTmem + ch * CHAIN_COLS + (uint32_t(quad * 32) << 16) + half * HN;
-        const int krow = quad * 32 + lane;             // key row of S^T
-        const bool kside = quad >= 2;                  // lanes of K (and U) rather than Q (and o)
-        const int i = (quad & 1) * 32 + lane;          // token row
-        const int col = v0 + ch * NV + half * HN;      // first value column of this thread
+        const int krow = quad * 32 + lane;          // key row of S^T
+        const int col = v0 + ch * NV + half * HN;   // first value column of this warp
+        const int i0 = quad * 16 + (lane >> 2);     // this thread's token rows: i0, i0 + 8
+        const int cp = 2 * (lane & 3);              // and column pairs: cp, cp + 8
         const size_t sbase = ((size_t(b) * HV + h) * D + col) * D + krow;
         uint64_t S[HN / 2];
 #pragma unroll
@@ -628,19 +701,22 @@ __global__ void __launch_bounds__(32 * (9 * NCH + 1), 1)
             S[c] = S0 ? pack2(S0[sbase + size_t(2 * c) * D], S0[sbase + size_t(2 * c + 1) * D]) : 0ull;
         if (bad && tid == 0 && blockIdx.x == 0) raise_err(ws.err, bad);
 
-        // chunk t's values and gates for this thread's token, one chunk ahead
-        uint4 nv[HN / 8];
-        float ng = 0.f, nb = 0.f, nlast = 1.f;
+        // chunk t's values and gates for this thread's tokens, one chunk ahead
+        uint32_t nv[4];
+        float ng[2], nb[2], nlast = 1.f;
         const float* gates = ws.gates + (slot0 * HV + h) * GATE_FLOATS;
-        const __nv_bfloat16* vp = v + (size_t(lo + i) * HV + h) * D + col;
+        const __nv_bfloat16* vp = v + (size_t(lo + i0) * HV + h) * D + col + cp;
         auto fetch = [&](int t) {
-            ng = gates[i];
             nlast = gates[C - 1];
-            if (kside) {
-                nb = gates[C + i];
 #pragma unroll
-                for (int c = 0; c < HN / 8; ++c)
-                    nv[c] = lo + C * t + i < hi ? __ldg(reinterpret_cast<const uint4*>(vp) + c) : make_uint4(0, 0, 0, 0);
+            for (int e = 0; e < 2; ++e) {
+                ng[e] = gates[i0 + 8 * e];
+                nb[e] = gates[C + i0 + 8 * e];
+                const bool live = lo + C * t + i0 + 8 * e < hi;
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    nv[2 * e + c] =
+                        live ? __ldg(reinterpret_cast<const uint32_t*>(vp + size_t(8 * e) * HV * D + 8 * c)) : 0u;
             }
             gates += size_t(HV) * GATE_FLOATS;
             vp += size_t(C) * HV * D;
@@ -648,100 +724,86 @@ __global__ void __launch_bounds__(32 * (9 * NCH + 1), 1)
         if (nc > 0) fetch(0);
         for (int t = 0; t < nc; ++t) {
             const uint32_t par = t & 1;
-            const bool live = lo + C * t + i < hi;
+            const int left = hi - (lo + C * t);  // tokens from this chunk's first on
             // S as the B operand of the chunk's first product
             put_parts(sS, SPART, krow, half, S);
             fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&cb[CB_S]);
-            const float ga = ng, last = nlast;
-            uint64_t x[HN / 2];
-            if (kside) {  // beta v
-                const uint64_t bb = pack2(nb, nb);
+            const float last = nlast;
+            uint64_t x[4], ga[2], be[2];
 #pragma unroll
-                for (int c = 0; c < HN / 8; ++c) {
-                    const uint32_t w[4] = {nv[c].x, nv[c].y, nv[c].z, nv[c].w};
+            for (int e = 0; e < 2; ++e) {
+                ga[e] = pack2(ng[e], ng[e]);
+                be[e] = pack2(-nb[e] * ng[e], -nb[e] * ng[e]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[4 * c + e] = mul2(bb, pack2(w[e] << 16, w[e] & 0xFFFF0000u));
-                }
+                for (int c = 0; c < 2; ++c)  // beta v
+                    x[2 * e + c] =
+                        mul2(pack2(nb[e], nb[e]), pack2(nv[2 * e + c] << 16, nv[2 * e + c] & 0xFFFF0000u));
             }
-            const float coef = kside ? -nb * ga : ga;
             if (t + 1 < nc) fetch(t + 1);
 
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&cb[CB_X], par)))) break;
             tc_fence_after();
-            uint64_t y[HN / 2];
-            sum_parts<NCH>(taddr + TX, y);
-            const uint64_t cc = pack2(coef, coef);
-            if (kside) {
-                // R = beta (v - 2^l X_K); rows past the sequence are zero,
-                // and so are their keys in the last product's operand
+            uint64_t y[4];
+            sum_rows16(taddr + (16u << 16) + TX, y);
+            // R = beta (v - 2^l X_K)
 #pragma unroll
-                for (int c = 0; c < HN / 2; ++c) x[c] = fma2(cc, y[c], x[c]);
-                if (!live) {
+            for (int r = 0; r < 4; ++r) x[r] = fma2(be[r >> 1], y[r], x[r]);
+            if (left < C) {
+                // rows past the sequence are zero, and so are their keys in
+                // the last product's operand
 #pragma unroll
-                    for (int c = 0; c < HN / 2; ++c) x[c] = 0ull;
-                    uint4* z =
-                        reinterpret_cast<uint4*>(sm + L::QK + (t & 1) * QK_BYTES + half * 16384 + 8192 + i * 128);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) z[c] = make_uint4(0, 0, 0, 0);
-                }
-                put_parts(sR, RPART, i, half, x);
-                fence_proxy_async_smem();
+                for (int r = 0; r < 4; ++r)
+                    if (i0 + 8 * (r >> 1) >= left) x[r] = 0ull;
+                uint8_t* z = sm + L::QK + (t & 1) * QK_BYTES + half * 16384 + quad * 4096 + 2048;
+                for (int r = lane >> 3; r < 16; r += 4)
+                    if (quad * 16 + r >= left)
+                        *reinterpret_cast<uint4*>(z + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
             }
+            put_rows16(sR, quad * 16, half, lane, x);
+            fence_proxy_async_smem();
+            sum_rows16(taddr + TX, y);  // X_Q
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&cb[CB_R]);
-            if (!kside) {
 #pragma unroll
-                for (int c = 0; c < HN / 2; ++c) y[c] = mul2(cc, y[c]);
-            }
+            for (int r = 0; r < 4; ++r) y[r] = mul2(ga[r >> 1], y[r]);
 
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&cb[CB_OU], par)))) break;
             tc_fence_after();
-            sum_parts<NCH>(taddr + TO, x);
-            if (kside) {
-                put_parts(sR, RPART, i, half, x);
-                fence_proxy_async_smem();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&cb[CB_U]);
-            } else if (live) {
-                OutT* dst = o + (size_t(lo + C * t + i) * HV + h) * D + col;
-                const uint64_t sc = pack2(scale, scale);
-                float f[HN];
+            sum_rows16(taddr + (16u << 16) + TO, x);
+            put_rows16(sR, quad * 16, half, lane, x);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&cb[CB_U]);
+            sum_rows16(taddr + TO, x);
+            OutT* dst = o + (size_t(lo + C * t + i0) * HV + h) * D + col + cp;
+            const uint64_t sc = pack2(scale, scale);
 #pragma unroll
-                for (int c = 0; c < HN / 2; ++c) {
-                    const float2 z = unpack2(mul2(sc, add2(x[c], y[c])));
-                    f[2 * c] = z.x;
-                    f[2 * c + 1] = z.y;
-                }
-                if constexpr (sizeof(OutT) == 4) {
+            for (int e = 0; e < 2; ++e)
 #pragma unroll
-                    for (int c = 0; c < HN / 4; ++c)
-                        reinterpret_cast<float4*>(dst)[c] =
-                            make_float4(f[4 * c], f[4 * c + 1], f[4 * c + 2], f[4 * c + 3]);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < HN / 8; ++c) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const __nv_bfloat162 p2 = __floats2bfloat162_rn(f[8 * c + 2 * e], f[8 * c + 2 * e + 1]);
-                            w[e] = *reinterpret_cast<const uint32_t*>(&p2);
+                for (int c = 0; c < 2; ++c) {
+                    const float2 f = unpack2(mul2(sc, add2(x[2 * e + c], y[2 * e + c])));
+                    OutT* p = dst + size_t(8 * e) * HV * D + 8 * c;
+                    if (i0 + 8 * e < left) {
+                        if constexpr (sizeof(OutT) == 4) {
+                            *reinterpret_cast<float2*>(p) = f;
+                        } else {
+                            const __nv_bfloat162 f2 = __floats2bfloat162_rn(f.x, f.y);
+                            *reinterpret_cast<__nv_bfloat162*>(p) = f2;
                         }
-                        reinterpret_cast<uint4*>(dst)[c] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
-            }
 
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&cb[CB_DS], par)))) break;
             tc_fence_after();
-            sum_parts<NCH>(taddr + TX, y);
+            uint64_t ds[HN / 2];
+            sum_parts<NCH>(taddr + TX, ds);
             const uint64_t ll = pack2(last, last);
 #pragma unroll
-            for (int c = 0; c < HN / 2; ++c) S[c] = fma2(ll, S[c], y[c]);
+            for (int c = 0; c < HN / 2; ++c) S[c] = fma2(ll, S[c], ds[c]);
         }
 #pragma unroll
         for (int c = 0; c < HN / 2; ++c) {
@@ -762,7 +824,7 @@ template <int NCH, typename OutT>
 cudaError_t launch_walk(const CUtensorMap& mq, const CUtensorMap& mk, const void* v, const float* S0, float* S_new,
                         const int32_t* starts, void* o, int N, int B, int H, int HV, float scale, const WsView& ws,
                         cudaStream_t st) {
-    const int smem = WalkSmem<NCH>::TOTAL + 1024;
+    const int smem = WalkSmem<NCH>::TOTAL;
     static const cudaError_t attr = cudaFuncSetAttribute(walk_kernel<NCH, OutT>,
                                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (attr != cudaSuccess) return attr;
@@ -778,15 +840,16 @@ size_t prefill_chunk_ws_bytes(int N, int B, int HV) { return pfc::ws_bytes(N, B,
 cudaError_t launch_prefill_chunk(const void* q, const void* k, const void* v, const float* g, const float* beta,
                                  const float* S0, float* S_new, const int32_t* starts, int N, int B, int H, int HV,
                                  void* o, int o_bf16, float scale, void* workspace, cudaStream_t st) {
-    CUtensorMap mq, mk;
-    if (!make_bf16_row_map(&mq, q, 1, N, H) || !make_bf16_row_map(&mk, k, 1, N, H)) return cudaErrorInvalidValue;
+    CUtensorMap pq, pk, mq, mk;
+    if (!make_bf16_row_map(&pq, q, 1, N, H, 32) || !make_bf16_row_map(&pk, k, 1, N, H, 32) ||
+        !make_bf16_row_map(&mq, q, 1, N, H, 16) || !make_bf16_row_map(&mk, k, 1, N, H, 16)) return cudaErrorInvalidValue;
     const pfc::WsView ws = pfc::ws_view(workspace, N, B, HV);
-    const int smem = pfc::PrepSmem::TOTAL + 1024;
+    const int smem = pfc::PrepSmem::TOTAL;
     static const cudaError_t attr =
         cudaFuncSetAttribute(pfc::prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (attr != cudaSuccess) return attr;
     const cudaError_t e = launch_pdl(pfc::prep_kernel, dim3(unsigned(pfc::slot_count(N, B) * HV)), dim3(128), smem, st,
-                                     mq, mk, g, beta, starts, N, B, HV, HV / H, ws);
+                                     pq, pk, g, beta, starts, N, B, HV, HV / H, ws);
     if (e != cudaSuccess) return e;
     const bool narrow = size_t(B) * HV <= 76;
 #define CANOPY_WALK(NCH, OT) \

@@ -650,16 +650,19 @@ static EncodeTiledFn encode_fn() {
 
 // [B][T][H][128] bf16 (q, k or v) -> boxes of 64 (last dim) x 64 (nodes) with
 // the 128-byte swizzle; nodes past T read as zero.
-bool make_bf16_row_map(CUtensorMap* m, const void* base, int B, int T, int H) {
+bool make_bf16_row_map(CUtensorMap* m, const void* base, int B, int T, int H, int rows) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
     const cuuint64_t dims[4] = {128, cuuint64_t(H), cuuint64_t(T), cuuint64_t(B)};
     const cuuint64_t strides[3] = {128 * 2, cuuint64_t(H) * 128 * 2, cuuint64_t(T) * H * 128 * 2};
-    const cuuint32_t box[4] = {64, 1, 64, 1};
+    const cuuint32_t box[4] = {64, 1, cuuint32_t(rows), 1};
     const cuuint32_t es[4] = {1, 1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool make_bf16_row_map(CUtensorMap* m, const void* base, int B, int T, int H) {
+    return make_bf16_row_map(m, base, B, T, H, 64);
 }
 
 // Node rows of o or U ([B][T][H][128], fp32 or bf16) for tiled bulk stores:

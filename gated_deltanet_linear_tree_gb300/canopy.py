@@ -285,11 +285,38 @@ def serial_replay_static(q, k, v, g, beta, S0, parent, err=None, o_dtype=torch.f
     return out
 
 
-def _err(err):
-    if err is None:
-        return None
-    _need(err, "err", torch.int32, (1,))
-    return _ptr(err)
+def _need_all(dev: int, *specs):
+    """_need for (tensor, name, dtype, shape) specs, all on device `dev`; the
+    calls of a few microseconds below check a tensor in one expression and
+    come to _need for its message only where that fails."""
+    for t, name, dtype, shape in specs:
+        try:
+            good = (t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous())
+        except AttributeError:
+            good = False
+        if dev < 0 or not good:
+            _need(t, name, dtype, shape)
+            raise CanopyError(f"{name} must be on the same device as the other tensors")
+
+
+def _raw_stream(dev: int) -> int:
+    """The current stream's handle on CUDA device `dev`."""
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
+
+
+def _heads3(q, v):
+    """Sizes of q [n, H, dk] and v [n, HV, dv], their dtype's code, and v's shape."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise CanopyError("q must have shape (n, H, dk)")
+    n, H, dk = q.shape
+    if not isinstance(v, torch.Tensor) or v.dim() != 3 or v.shape[0] != n:
+        raise CanopyError(f"v must have shape ({n}, HV, dv)")
+    _, HV, dv = v.shape
+    return n, H, HV, dk, dv
 
 
 def prefill_workspace(N: int, B: int, HV: int, d: int, device="cuda") -> torch.Tensor:
@@ -312,39 +339,32 @@ def prefill(q, k, v, g, beta, S0, starts, ws, o_dtype=torch.float32, out=None, S
     None for zero states).  S_out may be S0.  ws: prefill_workspace for at
     least these sizes.  force: None (the library's dispatch), "scan" or
     "chunked" (bf16, d = 128)."""
-    _need(q, "q")
-    if q.dim() != 3:
-        raise CanopyError(f"q must have shape (N, H, dk), got {tuple(q.shape)}")
-    N, H, dk = q.shape
-    _need(k, "k", q.dtype, q.shape)
-    _need(v, "v", q.dtype)
-    if v.dim() != 3 or v.shape[0] != N:
-        raise CanopyError(f"v must have shape ({N}, HV, dv), got {tuple(v.shape)}")
-    HV, dv = v.shape[1:]
-    _need(g, "g", torch.float32, (N, HV))
-    _need(beta, "beta", torch.float32, (N, HV))
-    _need(starts, "starts", torch.int32)
-    if starts.dim() != 1 or starts.numel() < 2:
-        raise CanopyError(f"starts must have shape (B + 1,), got {tuple(starts.shape)}")
-    B = starts.numel() - 1
+    N, H, HV, dk, dv = _heads3(q, v)
+    if not isinstance(starts, torch.Tensor) or starts.dim() != 1 or starts.shape[0] < 2:
+        raise CanopyError("starts must have shape (B + 1,)")
+    B = starts.shape[0] - 1
+    state = (B, HV, dv, dk)
+    dt, f32, dev = q.dtype, torch.float32, q.get_device()
+    _need_all(dev, (q, "q", dt, q.shape), (k, "k", dt, q.shape), (v, "v", dt, v.shape), (g, "g", f32, (N, HV)),
+              (beta, "beta", f32, (N, HV)), (starts, "starts", torch.int32, starts.shape),
+              (ws, "workspace", torch.uint8, ws.shape))
     if S0 is not None:
-        _need(S0, "S0", torch.float32, (B, HV, dv, dk))
-    _need(ws, "workspace", torch.uint8)
+        _need_all(dev, (S0, "S0", f32, state))
     lib = load()
     if ws.numel() < lib.canopy_prefill_workspace_bytes(N, B, HV, dk, dv):
         raise CanopyError("the workspace is too small for these sizes")
     if out is None:
-        out = torch.empty((N, HV, dv), dtype=o_dtype, device=q.device)
+        out = torch.empty(v.shape, dtype=o_dtype, device=q.device)
     else:
-        _need(out, "o", None, (N, HV, dv))
+        _need(out, "o", None, v.shape)
     if S_out is None:
-        S_out = torch.empty((B, HV, dv, dk), dtype=torch.float32, device=q.device)
+        S_out = torch.empty(state, dtype=f32, device=q.device)
     else:
-        _need(S_out, "S_new", torch.float32, (B, HV, dv, dk))
-    _check(lib.canopy_prefill(_ptr(q), _ptr(k), _ptr(v), _dt(q), _ptr(g), _ptr(beta),
-                              _ptr(S0) if S0 is not None else None, _ptr(starts), N, B, H, HV, dk, dv, float(scale),
-                              _ptr(out), _dt(out), _ptr(S_out), _ptr(ws), PREFILL_FORCE[force], _stream()),
-           "canopy_prefill")
+        _need(S_out, "S_new", f32, state)
+    st = lib.canopy_prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dt(q), g.data_ptr(), beta.data_ptr(), _opt(S0),
+                            starts.data_ptr(), N, B, H, HV, dk, dv, scale, out.data_ptr(), _dt(out), S_out.data_ptr(),
+                            ws.data_ptr(), PREFILL_FORCE[force], _raw_stream(dev))
+    _check(st, "canopy_prefill")
     return out, S_out
 
 
@@ -359,29 +379,25 @@ def step(q, k, v, g, beta, S, o_dtype=torch.float32, out=None, S_out=None, scale
     q, k [B, H, dk]; v [B, HV, dv]; g, beta fp32 [B, HV]; S fp32
     [B, HV, dv, dk].  S_out may be S (in place).  err: an optional int32 CUDA
     tensor of one element that receives device error bits (OR-ed)."""
-    _need(q, "q")
-    if q.dim() != 3:
-        raise CanopyError(f"q must have shape (B, H, dk), got {tuple(q.shape)}")
-    B, H, dk = q.shape
-    _need(k, "k", q.dtype, q.shape)
-    _need(v, "v", q.dtype)
-    if v.dim() != 3 or v.shape[0] != B:
-        raise CanopyError(f"v must have shape ({B}, HV, dv), got {tuple(v.shape)}")
-    HV, dv = v.shape[1:]
-    _need(g, "g", torch.float32, (B, HV))
-    _need(beta, "beta", torch.float32, (B, HV))
-    _need(S, "S", torch.float32, (B, HV, dv, dk))
+    B, H, HV, dk, dv = _heads3(q, v)
+    state = (B, HV, dv, dk)
+    dt, f32, dev = q.dtype, torch.float32, q.get_device()
+    _need_all(dev, (q, "q", dt, q.shape), (k, "k", dt, q.shape), (v, "v", dt, v.shape), (g, "g", f32, (B, HV)),
+              (beta, "beta", f32, (B, HV)), (S, "S", f32, state))
+    if err is not None:
+        _need(err, "err", torch.int32, (1,))
     if out is None:
-        out = torch.empty((B, HV, dv), dtype=o_dtype, device=q.device)
+        out = torch.empty(v.shape, dtype=o_dtype, device=q.device)
     else:
-        _need(out, "o", None, (B, HV, dv))
+        _need(out, "o", None, v.shape)
     if S_out is None:
         S_out = torch.empty_like(S)
     else:
-        _need(S_out, "S_new", torch.float32, (B, HV, dv, dk))
-    _check(load().canopy_step(_ptr(q), _ptr(k), _ptr(v), _dt(q), _ptr(g), _ptr(beta), _ptr(S), _ptr(S_out), B, H, HV,
-                              dk, dv, float(scale), _ptr(out), _dt(out), _err(err),
-                              _stream()), "canopy_step")
+        _need_all(dev, (S_out, "S_new", f32, state))
+    st = load().canopy_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dt(q), g.data_ptr(), beta.data_ptr(),
+                            S.data_ptr(), S_out.data_ptr(), B, H, HV, dk, dv, scale, out.data_ptr(), _dt(out),
+                            _opt(err), _raw_stream(dev))
+    _check(st, "canopy_step")
     return out, S_out
 
 
@@ -395,23 +411,25 @@ def accept(p, tokens, parent, u, noise, q=None, lengths=None, err=None):
     [B, T] uniform in [0, 1); noise fp32 [B, V] exponential variates.
     out_tokens: the accepted tokens in path order, the next token after them,
     then -1; counts: how many; accepted is what commit and conv_commit take."""
-    _need(p, "p")
-    if p.dim() != 3:
-        raise CanopyError(f"p must have shape (B, T, V), got {tuple(p.shape)}")
+    if not isinstance(p, torch.Tensor) or p.dim() != 3:
+        raise CanopyError("p must have shape (B, T, V)")
     B, T, V = p.shape
+    i32, f32, dev = torch.int32, torch.float32, p.get_device()
+    _need_all(dev, (p, "p", p.dtype, p.shape), (tokens, "tokens", i32, (B, T)), (parent, "parent", i32, (B, T)),
+              (u, "u", f32, (B, T)), (noise, "noise", f32, (B, V)))
     if q is not None:
-        _need(q, "q", p.dtype, p.shape)
-    _need(tokens, "tokens", torch.int32, (B, T))
-    _need(parent, "parent", torch.int32, (B, T))
-    _need(u, "u", torch.float32, (B, T))
-    _need(noise, "noise", torch.float32, (B, V))
-    accepted = torch.empty(B, dtype=torch.int32, device=p.device)
-    out_tokens = torch.empty((B, T), dtype=torch.int32, device=p.device)
-    counts = torch.empty(B, dtype=torch.int32, device=p.device)
-    _check(load().canopy_accept(_ptr(p), _ptr(q) if q is not None else None, _dt(p), _ptr(tokens), _ptr(parent),
-                                _lengths(lengths, B), _ptr(u), _ptr(noise), T, B, V, _ptr(accepted),
-                                _ptr(out_tokens), _ptr(counts), _err(err), _stream()),
-           "canopy_accept")
+        _need_all(dev, (q, "q", p.dtype, p.shape))
+    if lengths is not None:
+        _need(lengths, "lengths", i32, (B,))
+    if err is not None:
+        _need(err, "err", i32, (1,))
+    accepted = torch.empty((B,), dtype=i32, device=p.device)
+    out_tokens = torch.empty_like(tokens)
+    counts = torch.empty_like(accepted)
+    st = load().canopy_accept(p.data_ptr(), _opt(q), _dt(p), tokens.data_ptr(), parent.data_ptr(), _opt(lengths),
+                              u.data_ptr(), noise.data_ptr(), T, B, V, accepted.data_ptr(), out_tokens.data_ptr(),
+                              counts.data_ptr(), _opt(err), _raw_stream(dev))
+    _check(st, "canopy_accept")
     return accepted, out_tokens, counts
 
 

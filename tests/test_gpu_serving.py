@@ -204,7 +204,7 @@ def same(got, ref):
 @pytest.mark.parametrize("B,T,V,kind,ragged", [
     (1, 1, 1, "chain", False), (2, 2, 3, "chain", False), (3, 8, 1000, "chain", False), (5, 33, 777, "random", True),
     (4, 64, 4096, "wide", True), (2, 40, 5003, "star", False), (1, 256, 2048, "random", False),
-    (2, 12, 50021, "random", False), (70, 9, 130, "random", True)])
+    (2, 12, 50021, "random", False), (70, 9, 130, "random", True), (2, 7, 140001, "star", False)])
 def test_accept(lib, B, T, V, kind, ragged, bf16, draft):
     for spread in (0.5, 4.0):
         x = sc.accept_inputs(B, T, V, seed=V + T, kind=kind, draft=draft, bf16=bf16, spread=spread, ragged=ragged)

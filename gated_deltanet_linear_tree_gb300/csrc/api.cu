@@ -142,12 +142,20 @@ canopy_status prefill_args(int N, int B, int H, int HV, canopy_dtype in_dtype, c
     return CANOPY_OK;
 }
 
-// The plan of a prefill call whose arguments passed prefill_args.
-canopy_prefill_plan_t prefill_plan(int N, int B, canopy_dtype in_dtype, int dk, unsigned flags) {
+// The plan of a prefill call whose arguments passed prefill_args.  Chunks
+// cost two launches and a chain of products however short the prompts are,
+// the scan a fixed time per token.  Measured scan / chunked time (equal
+// lengths, 16 or 32 value heads): with 8 to 64 (sequence, value head) pairs
+// 0.75-0.89 at 32 tokens and 1.07-1.29 at 48; with 128 and more 0.75-0.87 at
+// 16 tokens and 1.01-1.23 at 24.  The host knows the mean length only, and an
+// uneven batch takes as long as its longest prompt, which costs the scan
+// more: the rule leans to the lower end.
+canopy_prefill_plan_t prefill_plan(int N, int B, int HV, canopy_dtype in_dtype, int dk, unsigned flags) {
     if (flags & CANOPY_PREFILL_SCAN) return CANOPY_PREFILL_PLAN_SCAN;
     if (flags & CANOPY_PREFILL_CHUNKED) return CANOPY_PREFILL_PLAN_CHUNKED;
-    const bool bf16_128 = in_dtype == CANOPY_BF16 && dk == 128;
-    return bf16_128 && N >= size_t(32) * B ? CANOPY_PREFILL_PLAN_CHUNKED : CANOPY_PREFILL_PLAN_SCAN;
+    const size_t least = size_t(B) * HV < 128 ? (B == 1 ? 40 : 32) : (B == 1 ? 24 : 16);
+    return in_dtype == CANOPY_BF16 && dk == 128 && size_t(N) >= least * B ? CANOPY_PREFILL_PLAN_CHUNKED
+                                                                           : CANOPY_PREFILL_PLAN_SCAN;
 }
 
 }  // namespace
@@ -289,7 +297,7 @@ canopy_prefill_plan_t canopy_prefill_plan(int N, int B, int H, int HV, canopy_dt
                                           unsigned flags) {
     if (prefill_args(N, B, H, HV, in_dtype, CANOPY_F32, dk, dv, flags, 1.f) != CANOPY_OK)
         return CANOPY_PREFILL_PLAN_NONE;
-    return prefill_plan(N, B, in_dtype, dk, flags);
+    return prefill_plan(N, B, HV, in_dtype, dk, flags);
 }
 
 canopy_status canopy_prefill(const void* q, const void* k, const void* v, canopy_dtype in_dtype, const float* g,
@@ -302,7 +310,7 @@ canopy_status canopy_prefill(const void* q, const void* k, const void* v, canopy
     const canopy_status as = prefill_args(N, B, H, HV, in_dtype, o_dtype, dk, dv, flags, scale);
     if (as != CANOPY_OK) return as;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (prefill_plan(N, B, in_dtype, dk, flags) == CANOPY_PREFILL_PLAN_CHUNKED)
+    if (prefill_plan(N, B, HV, in_dtype, dk, flags) == CANOPY_PREFILL_PLAN_CHUNKED)
         return cuda_status(launch_prefill_chunk(q, k, v, g, beta, S0, S_new, starts, N, B, H, HV, o,
                                                 o_dtype == CANOPY_BF16, scale, workspace, st));
     return cuda_status(launch_prefill_scan(q, k, v, in_dtype == CANOPY_BF16, g, beta, S0, S_new, starts, N, B, H, HV,

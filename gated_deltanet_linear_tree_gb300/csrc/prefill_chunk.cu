@@ -5,21 +5,24 @@
 // and "The tree closed form" on a chain: within a chunk, with l_i the sum of
 // log2 g up to token i and S the state before it,
 //     G_ij = beta_i 2^(l_i - l_j) k_i.k_j (j < i),  C_ij = 2^(l_i - l_j) q_i.k_j (j <= i),
-//     M = C (I + G)^-1,  W_i = 2^(l_last - l_i) (I + G)^-1_i,
-//     R = beta (V - 2^l K S^T),  o = scale (2^l Q S^T + M R),  U = W R,
-//     S <- 2^l_last S + sum_j u_j k_j^T.
+//     W = (I + G)^-1,  M = C W,  R = beta (V - 2^l K S^T),
+//     U = W R,  o = scale (2^l Q S^T + M R),
+//     S <- 2^l_last S + sum_j 2^(l_last - l_j) u_j k_j^T.
 // M and W do not depend on the state.  A first launch forms them for every
 // (chunk, value head) at once; a second walks each sequence's chunks in
 // order, and there a chunk is three dependent products:
-//     [X_Q; X_K] = [Q; K] S^T,   [o; U] = [M; W] R,   S += K^T U.
+//     [X_Q; X_K] = [Q; K] S^T,   [o; U] = [M; W] R,   S += K^T (2^(l_last - l) U).
 // Value columns never meet, so the second launch splits a state's 128 value
 // columns into chains of 32.
 //
 // Precision.  q, k and v are exact bf16; S, R, U, M and W enter their
-// products as three bf16 parts (8 + 8 + 8 bits by truncation: the 24 bits of
-// an fp32 value).  The right operand's parts stand side by side along N, so
-// that the left operand is read once for all of them, and products of parts
-// below 2^-24 of the result are left out.  All accumulation is fp32 and S
+// products as three bf16 parts that hold the 24 bits of an fp32 value.  The
+// right operand's parts stand side by side along N, so that the left operand
+// is read once for all of them (a product's time hardly depends on N: about
+// 60 cycles for N = 32 to 192, what reading the left operand takes), and
+// products of parts below 2^-24 of the result are left out.  W's third part
+// is left out of U where that shortens the way to it (one chain, below):
+// 2^-18 of W's entries off its unit diagonal.  All accumulation is fp32 and S
 // itself stays in fp32 registers across chunks.
 //
 // Chunk slots: sequence b's chunk c is slot starts[b] / 64 + b + c; these
@@ -37,7 +40,7 @@ constexpr int C = 64;             // tokens per chunk
 constexpr int QK_BYTES = 32768;   // [Q; K]: 2 atoms of 64 keys x 128 rows x 128 B
 constexpr int MW_PART = 16384;    // [M; W]: 128 rows x 128 B
 constexpr int MW_BYTES = 3 * MW_PART;
-constexpr int GATE_FLOATS = 128;  // 2^l and beta, 64 each
+constexpr int GATE_FLOATS = 192;  // 2^l, beta and the decay to the chunk's end, 64 each
 
 __host__ __device__ inline size_t slot_count(int N, int B) { return size_t(N / C) + B; }
 
@@ -68,7 +71,6 @@ __device__ inline void sequence(const int32_t* starts, int b, int N, int& lo, in
 }
 
 __device__ inline uint32_t bits(float x) { return __float_as_uint(x); }
-__device__ inline float top(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); }
 __device__ inline uint32_t pack_top(float lo, float hi) { return __byte_perm(bits(lo), bits(hi), 0x7632); }
 
 // fp32 pairs in one 64-bit register.
@@ -105,14 +107,17 @@ __device__ inline uint64_t mul2(uint64_t a, uint64_t b) {
 
 // Two fp32 values as three packed bf16 pairs that sum to them exactly (for
 // normal parts; each part is the top 16 bits of what is left).
-__device__ inline void split3(uint64_t v, uint32_t& h, uint32_t& m, uint32_t& l) {
+__device__ inline uint64_t rest(uint64_t v, uint32_t packed) {  // v less the pair's bf16 values
     const uint64_t minus1 = 0xBF800000BF800000ull;
+    return fma2(pack2(packed << 16, packed & 0xFFFF0000u), minus1, v);
+}
+__device__ inline void split3(uint64_t v, uint32_t& h, uint32_t& m, uint32_t& l) {
     const float2 x = unpack2(v);
-    const uint64_t v1 = fma2(pack2(top(x.x), top(x.y)), minus1, v);
-    const float2 y = unpack2(v1);
-    const float2 z = unpack2(fma2(pack2(top(y.x), top(y.y)), minus1, v1));
     h = pack_top(x.x, x.y);
+    const uint64_t v1 = rest(v, h);
+    const float2 y = unpack2(v1);
     m = pack_top(y.x, y.y);
+    const float2 z = unpack2(rest(v1, m));
     l = pack_top(z.x, z.y);
 }
 
@@ -186,6 +191,16 @@ __device__ inline void solve32(uint64_t (&x)[16], const float* G) {
     }
 }
 
+// The same with the first two parts rounded (ties away), so that they alone
+// are within 2^-18.
+__device__ inline float near16(float x) { return __uint_as_float((__float_as_uint(x) + 0x8000u) & 0xFFFF0000u); }
+__device__ inline void split3_near(float x, float y, uint32_t& h, uint32_t& m, uint32_t& l) {
+    const float hx = near16(x), hy = near16(y), x1 = x - hx, y1 = y - hy, mx = near16(x1), my = near16(y1);
+    h = pack_top(hx, hy);
+    m = pack_top(mx, my);
+    l = pack_top(x1 - mx, y1 - my);
+}
+
 // Columns 32 half .. + 31 of row `row` of the image's three parts.
 __device__ inline void put_half_row(uint8_t* image, int row, int half, const uint64_t (&x)[16]) {
     uint8_t* dst = image + row * 128;
@@ -193,7 +208,10 @@ __device__ inline void put_half_row(uint8_t* image, int row, int half, const uin
     for (int c = 0; c < 4; ++c) {
         uint32_t h[4], m[4], l[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) split3(x[4 * c + e], h[e], m[e], l[e]);
+        for (int e = 0; e < 4; ++e) {
+            const float2 y = unpack2(x[4 * c + e]);
+            split3_near(y.x, y.y, h[e], m[e], l[e]);
+        }
         const int off = ((4 * half + c) ^ (row & 7)) << 4;
         *reinterpret_cast<uint4*>(dst + off) = make_uint4(h[0], h[1], h[2], h[3]);
         *reinterpret_cast<uint4*>(dst + off + MW_PART) = make_uint4(m[0], m[1], m[2], m[3]);
@@ -257,7 +275,6 @@ __global__ void __launch_bounds__(128, 4)
         tmem_relinquish();
         tc_fence_before();
     }
-    pdl_trigger();  // after the wait: the next kernel may rely on everything before this one
     if (tid < C) {  // tokens past the end decay and write nothing
         float a = 1.f, be = 0.f;
         if (tid < valid) {
@@ -274,6 +291,10 @@ __global__ void __launch_bounds__(128, 4)
     }
     if (bad) raise_err(ws.err, bad);
     __syncthreads();
+    // After the wait (the next kernel may rely on everything before this one)
+    // and after the allocation: a block of the second launch may take the
+    // whole tensor memory and then waits for this kernel.
+    pdl_trigger();
     tc_fence_after();
     const uint32_t tmem = *sTmem;
     if (tid == 0 && mbar_wait(&bars[0], 0)) {
@@ -321,9 +342,9 @@ __global__ void __launch_bounds__(128, 4)
         }
         float* gates = ws.gates + at * GATE_FLOATS;
         gates[krow ? C + i : i] = krow ? sBe[i] : d;
+        if (krow) gates[2 * C + i] = end;
         __syncthreads();
-        // Row i of M (from c_i), or of W (from the unit row e_i, with its
-        // decay to the chunk's end at last).  x1 is kept in shared memory;
+        // Row i of M (from c_i), or of W (from the unit row e_i).  x1 is kept in shared memory;
         // the first 32 tokens have none.
         float* keep = krow ? reinterpret_cast<float*>(sm + P::ROWW) + i * P::PW : rowp + 32;
         const bool upper = i >= 32;
@@ -378,11 +399,8 @@ __global__ void __launch_bounds__(128, 4)
         }
         __syncthreads();  // everything before the image is done with
         const int row = (i >> 4) * 32 + (i & 15) + (krow ? 16 : 0);
-        const uint64_t dd = krow ? pack2(end, end) : pack2(1.f, 1.f);
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] = mul2(x[j], dd);
             put_half_row(sm + P::QK, row, half, x);
 #pragma unroll
             for (int j = 0; j < 16; ++j) x[j] = x1[j];
@@ -415,19 +433,27 @@ __global__ void __launch_bounds__(128, 4)
 // each TMEM quadrant holds 16 token rows of X_Q (o) and 16 of X_K (U), and
 // the rows of K, on the critical path, are shared by the SM's four
 // schedulers.  A warp reads 16 of its lanes at a time with all its threads:
-// thread t has rows t / 4 and t / 4 + 8, columns 2 (t % 4), + 1, + 8, + 9.
+// thread t has rows t / 4 and t / 4 + 8, columns 2 (t % 4), + 1 of every 8.
 
-constexpr int NV = 32;                   // value columns per chain
-constexpr int HN = NV / 2;               // of a compute thread
-constexpr int ROW = NV * 2;              // bytes of one K index of a B operand part
-constexpr int SPART = D * ROW;           // one part of S
-constexpr int RPART = C * ROW;           // one part of R (and U)
-constexpr uint32_t TX = 0, TO = 3 * NV;  // TMEM columns: [X_Q; X_K] and later K^T U; [o; U]
-constexpr uint32_t CHAIN_COLS = 6 * NV;
-constexpr int kMaxRanked = 128;          // sequences that are started by length
+constexpr int NV = 32;           // value columns per chain
+constexpr int ROW = NV * 2;      // bytes of one K index of a B operand part
+constexpr int SPART = D * ROW;   // one part of S
+constexpr int RPART = C * ROW;   // one part of R (and U)
+// TMEM columns of a chain: [X_Q; X_K] and later K^T U in three groups, [o; U]
+// in three, the third part's share of o.
+constexpr uint32_t TX = 0, TO = 3 * NV, TL = 6 * NV, CHAIN_COLS = 7 * NV;
+constexpr int kMaxRanked = 128;  // sequences that are started by length
 
-enum { CB_X, CB_OU, CB_DS, CB_S, CB_R, CB_U, CB_N };          // a chain's barriers
+enum { CB_X, CB_OU, CB_O2, CB_DS, CB_S, CB_R, CB_U, CB_N };  // a chain's barriers (from CB_S on: its warps arrive)
 enum { PB_QK = 0, PB_QKE = 2, PB_MW = 4, PB_MWE = 6, PB_LO = 8, PB_LOE, PB_N };  // tiles: full and empty
+
+// One chain per block (few states: latency counts) has U apart from R, so
+// that the third part's products need not be over before U is taken on.
+// (16 warps of 8 columns for it were no faster than 8 warps of 16.)
+constexpr int WARPS = 8;  // compute warps per chain
+constexpr int HN = 16;    // value columns of a compute thread
+template <int NCH>
+constexpr bool kLate = NCH == 1;
 
 template <int NCH>
 struct WalkSmem {
@@ -436,104 +462,95 @@ struct WalkSmem {
     static constexpr int LO = MW + 4 * MW_PART;   // part 2: one buffer
     static constexpr int S = LO + MW_PART;
     static constexpr int R = S + NCH * 3 * SPART;
-    static constexpr int BAR = R + NCH * 3 * RPART;
+    static constexpr int U = R + (kLate<NCH> ? NCH * 3 * RPART : 0);
+    static constexpr int BAR = U + NCH * 3 * RPART;
     static constexpr int SLOT = BAR + (PB_N + NCH * CB_N) * 8;
     static constexpr int TOTAL = SLOT + 8;
     static_assert(TOTAL + 1024 <= 227 * 1024, "shared memory");
 };
 
-// 16 TMEM lanes x 16 columns: for e = 0, 1 (rows) and c = 0, 1 (groups of 8
-// columns) x[2 e + c] is the pair at row t / 4 + 8 e, columns 8 c + 2 (t % 4);
-// the three column groups of an accumulator, NV apart, summed.
+// 16 TMEM lanes x HN columns: for e = 0, 1 (rows) and c < HN / 8 (groups of 8
+// columns) x[(HN / 8) e + c] is the pair at row t / 4 + 8 e, columns
+// 8 c + 2 (t % 4); GROUPS column groups, NV apart, summed.
 __device__ inline void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t (&r)[8]) {
     asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr));
 }
+template <int GROUPS>
 __device__ inline void sum_rows16(uint32_t taddr, uint64_t (&x)[4]) {
-    uint32_t a[8], b[8], d[8];
-    tmem_ld_16x256b_x2(taddr, a);
-    tmem_ld_16x256b_x2(taddr + NV, b);
-    tmem_ld_16x256b_x2(taddr + 2 * NV, d);
+    uint32_t a[GROUPS][8];
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) tmem_ld_16x256b_x2(taddr + g * NV, a[g]);
     tmem_wait_ld();
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+    for (int c = 0; c < HN / 8; ++c)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int r = 4 * c + 2 * e;
-            x[2 * e + c] = add2(pack2(a[r], a[r + 1]), add2(pack2(b[r], b[r + 1]), pack2(d[r], d[r + 1])));
+            uint64_t y = pack2(a[GROUPS - 1][r], a[GROUPS - 1][r + 1]);
+#pragma unroll
+            for (int g = GROUPS - 2; g >= 0; --g) y = add2(pack2(a[g][r], a[g][r + 1]), y);
+            x[HN / 8 * e + c] = y;
         }
 }
 
 // The same values as three parts of a B operand whose K index is the token:
-// k0 is the first of the 16 tokens.
-__device__ inline void put_rows16(uint8_t* base, int k0, int half, int lane, const uint64_t (&x)[4]) {
+// k0 is the first of the 16 tokens, c0 the first group of 8 columns.
+__device__ inline void put_rows16(uint8_t* base, int k0, int c0, int lane, const uint64_t (&x)[HN / 4]) {
 #pragma unroll
     for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < HN / 8; ++c) {
             const int k = k0 + (lane >> 2) + 8 * e;
             uint32_t h, m, l;
-            split3(x[2 * e + c], h, m, l);
-            uint8_t* p = base + k * ROW + (((half * 2 + c) ^ ((k >> 1) & 3)) << 4) + (lane & 3) * 4;
+            split3(x[HN / 8 * e + c], h, m, l);
+            uint8_t* p = base + k * ROW + (((c0 + c) ^ ((k >> 1) & 3)) << 4) + (lane & 3) * 4;
             *reinterpret_cast<uint32_t*>(p) = h;
             *reinterpret_cast<uint32_t*>(p + RPART) = m;
             *reinterpret_cast<uint32_t*>(p + 2 * RPART) = l;
         }
 }
 
-// Columns 16 half .. + 15 of K index k as three parts of a B operand: rows
+// HN columns from group c0 of K index k as three parts of a B operand: rows
 // of 64 bytes in the 64-byte swizzle.
-__device__ inline void put_parts(uint8_t* base, int part, int k, int half, const uint64_t (&x)[HN / 2]) {
+__device__ inline void put_parts(uint8_t* base, int k, int c0, const uint64_t (&x)[HN / 2]) {
 #pragma unroll
     for (int c = 0; c < HN / 8; ++c) {
         uint32_t h[4], m[4], l[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) split3(x[4 * c + e], h[e], m[e], l[e]);
-        uint8_t* p = base + k * ROW + (((half * (HN / 8) + c) ^ ((k >> 1) & 3)) << 4);
+        uint8_t* p = base + k * ROW + (((c0 + c) ^ ((k >> 1) & 3)) << 4);
         *reinterpret_cast<uint4*>(p) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(p + part) = make_uint4(m[0], m[1], m[2], m[3]);
-        *reinterpret_cast<uint4*>(p + 2 * part) = make_uint4(l[0], l[1], l[2], l[3]);
+        *reinterpret_cast<uint4*>(p + SPART) = make_uint4(m[0], m[1], m[2], m[3]);
+        *reinterpret_cast<uint4*>(p + 2 * SPART) = make_uint4(l[0], l[1], l[2], l[3]);
     }
 }
 
-// The three column groups of an accumulator, NV apart, summed: 16 columns
-// at a time where registers allow, else 8.
+// The three column groups of an accumulator, NV apart, summed: this lane's
+// HN columns, 8 at a time.
 __device__ inline void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr));
 }
-template <int NCH>
 __device__ inline void sum_parts(uint32_t taddr, uint64_t (&x)[HN / 2]) {
-    if constexpr (NCH == 1) {
-        uint32_t a[16], b[16], d[16];
-        tmem_ld16(taddr, a);
-        tmem_ld16(taddr + NV, b);
-        tmem_ld16(taddr + 2 * NV, d);
+#pragma unroll
+    for (int q = 0; q < HN / 8; ++q) {
+        uint32_t a[8], b[8], d[8];
+        tmem_ld8(taddr + 8 * q, a);
+        tmem_ld8(taddr + NV + 8 * q, b);
+        tmem_ld8(taddr + 2 * NV + 8 * q, d);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            x[e] = add2(pack2(a[2 * e], a[2 * e + 1]),
-                        add2(pack2(b[2 * e], b[2 * e + 1]), pack2(d[2 * e], d[2 * e + 1])));
-    } else {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            uint32_t a[8], b[8], d[8];
-            tmem_ld8(taddr + 8 * q, a);
-            tmem_ld8(taddr + NV + 8 * q, b);
-            tmem_ld8(taddr + 2 * NV + 8 * q, d);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                x[4 * q + e] = add2(pack2(a[2 * e], a[2 * e + 1]),
-                                    add2(pack2(b[2 * e], b[2 * e + 1]), pack2(d[2 * e], d[2 * e + 1])));
-        }
+        for (int e = 0; e < 4; ++e)
+            x[4 * q + e] = add2(pack2(a[2 * e], a[2 * e + 1]),
+                                add2(pack2(b[2 * e], b[2 * e + 1]), pack2(d[2 * e], d[2 * e + 1])));
     }
 }
 
 template <int NCH, typename OutT>
-__global__ void __launch_bounds__(32 * (9 * NCH + 1), 1)
+__global__ void __launch_bounds__(32 * ((WARPS + 1) * NCH + 1), 1)
     walk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __nv_bfloat16* __restrict__ v, const float* S0, float* S_new,
                 const int32_t* __restrict__ starts, OutT* __restrict__ o, int N, int HV, int ratio, float scale,
@@ -541,7 +558,8 @@ __global__ void __launch_bounds__(32 * (9 * NCH + 1), 1)
     using L = WalkSmem<NCH>;
     constexpr uint32_t kCols = NCH == 1 ? 256 : 512;
     static_assert(NCH * CHAIN_COLS <= kCols, "TMEM columns");
-    constexpr int kComputeWarps = 8 * NCH;
+    constexpr int kComputeWarps = WARPS * NCH;
+    constexpr bool LATE = kLate<NCH>;
     extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t* pb = reinterpret_cast<uint64_t*>(sm + L::BAR);
     uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + L::SLOT);
@@ -558,7 +576,7 @@ __global__ void __launch_bounds__(32 * (9 * NCH + 1), 1)
             mbar_init(&pb[i], (i >= PB_QKE && i < PB_MW) || (i >= PB_MWE && i < PB_LO) || i == PB_LOE ? NCH : 1);
         for (int c = 0; c < NCH; ++c)
             for (int i = 0; i < CB_N; ++i)
-                mbar_init(&pb[PB_N + c * CB_N + i], i < CB_S ? 1 : 8);
+                mbar_init(&pb[PB_N + c * CB_N + i], i < CB_S ? 1 : WARPS);
         fence_mbar_init();
     }
     if (warp == kComputeWarps) {
@@ -568,8 +586,8 @@ __global__ void __launch_bounds__(32 * (9 * NCH + 1), 1)
     }
     __syncthreads();
     tc_fence_after();
-    pdl_wait();
-    pdl_trigger();
+    // This kernel starts after the first launch has waited for everything
+    // before it, so that only the workspace has to be waited for.
     // The longest sequences start first (they end last): this block takes
     // the one of its rank.  Every block ranks all sequences, so not for many.
     const int nseq = gridDim.y;
@@ -591,6 +609,10 @@ __global__ void __launch_bounds__(32 * (9 * NCH + 1), 1)
     const int nc = (hi - lo + C - 1) / C;
     const size_t slot0 = size_t(lo / C) + b;
     bool ok = true;
+    if (warp >= kComputeWarps) {
+        pdl_wait();
+        pdl_trigger();
+    }
 
     if (warp == kComputeWarps + NCH) {
         // ---- copies -----------------------------------------------------------
@@ -634,18 +656,24 @@ __global__ void __launch_bounds__(32 * (9 * NCH + 1), 1)
             uint64_t* cb = pb + PB_N + ch * CB_N;
             const uint32_t tmem = *sTmem + ch * CHAIN_COLS;
             const uint32_t aS = smem_u32(sm + L::S + ch * 3 * SPART), aR = smem_u32(sm + L::R + ch * 3 * RPART);
+            const uint32_t aU = smem_u32(sm + L::U + ch * 3 * RPART);
             const uint32_t aLo = smem_u32(sm + L::LO);
             constexpr uint32_t i3 = idesc_bf16(128, 3 * NV) | kMajorB, i2 = idesc_bf16(128, 2 * NV) | kMajorB,
                                i1 = idesc_bf16(128, NV) | kMajorB;
-            // The second chain starts half a chunk after the first, so that
-            // one's products run beside the other's register work.
-            if (ch && nc > 0) ok = mbar_wait(&pb[PB_N + CB_R], 0);
-            for (int t = 0; t < nc && ok; ++t) {
+            for (int t = 0; t < nc; ++t) {
                 const int s = t & 1;
                 const uint32_t par = t & 1, fpar = (t >> 1) & 1;
                 const uint32_t aQK = smem_u32(sm + L::QK + s * QK_BYTES);
                 const uint32_t aMW = smem_u32(sm + L::MW + s * 2 * MW_PART);
                 if (!(ok = mbar_wait(&pb[PB_QK + s], fpar))) break;
+                if (NCH > 1) {
+                    // Half a chunk between the chains, so that one's products
+                    // run beside the other's register work: the second starts
+                    // a chunk once the first has its X, the first the next
+                    // one once the second has its X.
+                    const uint64_t* other = pb + PB_N + (1 - ch) * CB_N;
+                    if ((ch || t) && !(ok = mbar_wait(const_cast<uint64_t*>(&other[CB_X]), ch ? par : par ^ 1))) break;
+                }
                 if (!(ok = mbar_wait(&cb[CB_S], par))) break;
                 tc_fence_after();
 #pragma unroll
@@ -665,11 +693,12 @@ __global__ void __launch_bounds__(32 * (9 * NCH + 1), 1)
                 for (int ks = 0; ks < 4; ++ks)
                     mma_bf16_ss(tmem + TO, sdesc(aMW + MW_PART + ks * 32, 0, 1024, 2),
                                 sdesc(aR + ks * 16 * ROW, RPART, 8 * ROW, 4), i2, 1);
+                if (LATE) mma_commit(&cb[CB_OU]);
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    mma_bf16_ss(tmem + TO, sdesc(aLo + ks * 32, 0, 1024, 2),
-                                sdesc(aR + ks * 16 * ROW, RPART, 8 * ROW, 4), i1, 1);
-                mma_commit(&cb[CB_OU]);
+                    mma_bf16_ss(tmem + (LATE ? TL : TO), sdesc(aLo + ks * 32, 0, 1024, 2),
+                                sdesc(aR + ks * 16 * ROW, RPART, 8 * ROW, 4), i1, !LATE || ks != 0);
+                mma_commit(&cb[LATE ? CB_O2 : CB_OU]);
                 mma_commit(&pb[PB_MWE + s]);
                 mma_commit(&pb[PB_LOE]);
                 if (!(ok = mbar_wait(&cb[CB_U], par))) break;
@@ -677,7 +706,7 @@ __global__ void __launch_bounds__(32 * (9 * NCH + 1), 1)
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
                     mma_bf16_ss(tmem + TX, sdesc(aQK + 2048 + ks * 4096, 16384, 1024, 2),
-                                sdesc(aR + ks * 16 * ROW, RPART, 8 * ROW, 4), i3 | kMajorA, ks != 0);
+                                sdesc(aU + ks * 16 * ROW, RPART, 8 * ROW, 4), i3 | kMajorA, ks != 0);
                 mma_commit(&cb[CB_DS]);
                 mma_commit(&pb[PB_QKE + s]);
             }
@@ -685,25 +714,29 @@ __global__ void __launch_bounds__(32 * (9 * NCH + 1), 1)
         }
     } else {
         // ---- the chain's state, R, U and o ----------------------------------------
-        const int ch = warp >> 3, quad = warp & 3, half = (warp >> 2) & 1;
+        const int ch = warp / WARPS, quad = warp & 3, part = (warp % WARPS) >> 2, c0 = part * (HN / 8);
         uint64_t* cb = pb + PB_N + ch * CB_N;
         uint8_t* sS = sm + L::S + ch * 3 * SPART;
         uint8_t* sR = sm + L::R + ch * 3 * RPART;
-        const uint32_t taddr = *sTmem + ch * CHAIN_COLS + (uint32_t(quad * 32) << 16) + half * HN;
+        uint8_t* sU = sm + L::U + ch * 3 * RPART;
+        const uint32_t taddr = *sTmem + ch * CHAIN_COLS + (uint32_t(quad * 32) << 16) + part * HN;
         const int krow = quad * 32 + lane;          // key row of S^T
-        const int col = v0 + ch * NV + half * HN;   // first value column of this warp
+        const int col = v0 + ch * NV + part * HN;   // first value column of this warp
         const int i0 = quad * 16 + (lane >> 2);     // this thread's token rows: i0, i0 + 8
-        const int cp = 2 * (lane & 3);              // and column pairs: cp, cp + 8
+        const int cp = 2 * (lane & 3);              // and column pairs: cp, cp + 8, ...
         const size_t sbase = ((size_t(b) * HV + h) * D + col) * D + krow;
         uint64_t S[HN / 2];
 #pragma unroll
         for (int c = 0; c < HN / 2; ++c)
             S[c] = S0 ? pack2(S0[sbase + size_t(2 * c) * D], S0[sbase + size_t(2 * c + 1) * D]) : 0ull;
+        pdl_wait();
+        pdl_trigger();
         if (bad && tid == 0 && blockIdx.x == 0) raise_err(ws.err, bad);
 
         // chunk t's values and gates for this thread's tokens, one chunk ahead
-        uint32_t nv[4];
-        float ng[2], nb[2], nlast = 1.f;
+        constexpr int G8 = HN / 8, NP = 2 * G8;  // column pairs per row, and in all
+        uint32_t nv[NP];
+        float ng[2], nb[2], nd[2], nlast = 1.f;
         const float* gates = ws.gates + (slot0 * HV + h) * GATE_FLOATS;
         const __nv_bfloat16* vp = v + (size_t(lo + i0) * HV + h) * D + col + cp;
         auto fetch = [&](int t) {
@@ -712,82 +745,26 @@ __global__ void __launch_bounds__(32 * (9 * NCH + 1), 1)
             for (int e = 0; e < 2; ++e) {
                 ng[e] = gates[i0 + 8 * e];
                 nb[e] = gates[C + i0 + 8 * e];
+                nd[e] = gates[2 * C + i0 + 8 * e];
                 const bool live = lo + C * t + i0 + 8 * e < hi;
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    nv[2 * e + c] =
+                for (int c = 0; c < G8; ++c)
+                    nv[G8 * e + c] =
                         live ? __ldg(reinterpret_cast<const uint32_t*>(vp + size_t(8 * e) * HV * D + 8 * c)) : 0u;
             }
             gates += size_t(HV) * GATE_FLOATS;
             vp += size_t(C) * HV * D;
         };
-        if (nc > 0) fetch(0);
-        for (int t = 0; t < nc; ++t) {
-            const uint32_t par = t & 1;
-            const int left = hi - (lo + C * t);  // tokens from this chunk's first on
-            // S as the B operand of the chunk's first product
-            put_parts(sS, SPART, krow, half, S);
-            fence_proxy_async_smem();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&cb[CB_S]);
-            const float last = nlast;
-            uint64_t x[4], ga[2], be[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                ga[e] = pack2(ng[e], ng[e]);
-                be[e] = pack2(-nb[e] * ng[e], -nb[e] * ng[e]);
-#pragma unroll
-                for (int c = 0; c < 2; ++c)  // beta v
-                    x[2 * e + c] =
-                        mul2(pack2(nb[e], nb[e]), pack2(nv[2 * e + c] << 16, nv[2 * e + c] & 0xFFFF0000u));
-            }
-            if (t + 1 < nc) fetch(t + 1);
-
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&cb[CB_X], par)))) break;
-            tc_fence_after();
-            uint64_t y[4];
-            sum_rows16(taddr + (16u << 16) + TX, y);
-            // R = beta (v - 2^l X_K)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) x[r] = fma2(be[r >> 1], y[r], x[r]);
-            if (left < C) {
-                // rows past the sequence are zero, and so are their keys in
-                // the last product's operand
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (i0 + 8 * (r >> 1) >= left) x[r] = 0ull;
-                uint8_t* z = sm + L::QK + (t & 1) * QK_BYTES + half * 16384 + quad * 4096 + 2048;
-                for (int r = lane >> 3; r < 16; r += 4)
-                    if (quad * 16 + r >= left)
-                        *reinterpret_cast<uint4*>(z + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
-            put_rows16(sR, quad * 16, half, lane, x);
-            fence_proxy_async_smem();
-            sum_rows16(taddr + TX, y);  // X_Q
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&cb[CB_R]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) y[r] = mul2(ga[r >> 1], y[r]);
-
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&cb[CB_OU], par)))) break;
-            tc_fence_after();
-            sum_rows16(taddr + (16u << 16) + TO, x);
-            put_rows16(sR, quad * 16, half, lane, x);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&cb[CB_U]);
-            sum_rows16(taddr + TO, x);
+        uint64_t oq[NP];  // 2^l X_Q, then o
+        auto store_o = [&](int t) {
             OutT* dst = o + (size_t(lo + C * t + i0) * HV + h) * D + col + cp;
-            const uint64_t sc = pack2(scale, scale);
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const float2 f = unpack2(mul2(sc, add2(x[2 * e + c], y[2 * e + c])));
+                for (int c = 0; c < G8; ++c) {
+                    const float2 f = unpack2(oq[G8 * e + c]);
                     OutT* p = dst + size_t(8 * e) * HV * D + 8 * c;
-                    if (i0 + 8 * e < left) {
+                    if (lo + C * t + i0 + 8 * e < hi) {
                         if constexpr (sizeof(OutT) == 4) {
                             *reinterpret_cast<float2*>(p) = f;
                         } else {
@@ -796,11 +773,89 @@ __global__ void __launch_bounds__(32 * (9 * NCH + 1), 1)
                         }
                     }
                 }
+        };
+        if (nc > 0) fetch(0);
+        for (int t = 0; t < nc; ++t) {
+            const uint32_t par = t & 1;
+            const int left = hi - (lo + C * t);  // tokens from this chunk's first on
+            // S as the B operand of the chunk's first product
+            put_parts(sS, krow, c0, S);
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&cb[CB_S]);
+            const float last = nlast;
+            uint64_t x[NP], ga[2], be[2], de[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                ga[e] = pack2(ng[e], ng[e]);
+                be[e] = pack2(-nb[e] * ng[e], -nb[e] * ng[e]);
+                de[e] = pack2(nd[e], nd[e]);
+#pragma unroll
+                for (int c = 0; c < G8; ++c)  // beta v
+                    x[G8 * e + c] =
+                        mul2(pack2(nb[e], nb[e]), pack2(nv[G8 * e + c] << 16, nv[G8 * e + c] & 0xFFFF0000u));
+            }
+            if (t + 1 < nc) fetch(t + 1);
+
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&cb[CB_X], par)))) break;
+            tc_fence_after();
+            uint64_t y[NP];
+            sum_rows16<3>(taddr + (16u << 16) + TX, y);
+            // R = beta (v - 2^l X_K)
+#pragma unroll
+            for (int r = 0; r < NP; ++r) x[r] = fma2(be[r / G8], y[r], x[r]);
+            if (left < C) {
+                // rows past the sequence are zero, and so are their keys in
+                // the last product's operand
+#pragma unroll
+                for (int r = 0; r < NP; ++r)
+                    if (i0 + 8 * (r / G8) >= left) x[r] = 0ull;
+                if (part < 2) {
+                    uint8_t* z = sm + L::QK + (t & 1) * QK_BYTES + part * 16384 + quad * 4096 + 2048;
+                    for (int r = lane >> 3; r < 16; r += 4)
+                        if (quad * 16 + r >= left)
+                            *reinterpret_cast<uint4*>(z + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                }
+            }
+            put_rows16(sR, quad * 16, c0, lane, x);
+            fence_proxy_async_smem();
+            sum_rows16<3>(taddr + TX, oq);  // (the last product goes where X is)
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&cb[CB_R]);
+#pragma unroll
+            for (int r = 0; r < NP; ++r) oq[r] = mul2(ga[r / G8], oq[r]);
+
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&cb[CB_OU], par)))) break;
+            tc_fence_after();
+            sum_rows16<3>(taddr + (16u << 16) + TO, x);
+#pragma unroll
+            for (int r = 0; r < NP; ++r) x[r] = mul2(de[r / G8], x[r]);
+            put_rows16(sU, quad * 16, c0, lane, x);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&cb[CB_U]);
+            sum_rows16<3>(taddr + TO, x);
+            if (LATE) {
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&cb[CB_O2], par)))) break;
+                tc_fence_after();
+                uint64_t z[NP];
+                sum_rows16<1>(taddr + TL, z);
+#pragma unroll
+                for (int r = 0; r < NP; ++r) x[r] = add2(x[r], z[r]);
+            }
+            {
+                const uint64_t sc = pack2(scale, scale);
+#pragma unroll
+                for (int r = 0; r < NP; ++r) oq[r] = mul2(sc, add2(x[r], oq[r]));
+            }
+            store_o(t);
 
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&cb[CB_DS], par)))) break;
             tc_fence_after();
             uint64_t ds[HN / 2];
-            sum_parts<NCH>(taddr + TX, ds);
+            sum_parts(taddr + TX, ds);
             const uint64_t ll = pack2(last, last);
 #pragma unroll
             for (int c = 0; c < HN / 2; ++c) S[c] = fma2(ll, S[c], ds[c]);
@@ -828,7 +883,7 @@ cudaError_t launch_walk(const CUtensorMap& mq, const CUtensorMap& mk, const void
     static const cudaError_t attr = cudaFuncSetAttribute(walk_kernel<NCH, OutT>,
                                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (attr != cudaSuccess) return attr;
-    return launch_pdl(walk_kernel<NCH, OutT>, dim3(HV * (D / (NV * NCH)), B), dim3(32 * (9 * NCH + 1)), smem, st, mq,
+    return launch_pdl(walk_kernel<NCH, OutT>, dim3(HV * (D / (NV * NCH)), B), dim3(32 * ((WARPS + 1) * NCH + 1)), smem, st, mq,
                       mk, static_cast<const __nv_bfloat16*>(v), S0, S_new, starts, static_cast<OutT*>(o), N, HV,
                       HV / H, scale, ws);
 }

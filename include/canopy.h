@@ -255,7 +255,7 @@ typedef enum {
 
 /* Size in bytes of the workspace of a prefill over N packed tokens of B
  * sequences with HV value heads: the device error word (offset 0), and per
- * 64-token chunk and value head 48 KiB of chunk operands and 512 bytes of
+ * 64-token chunk and value head 48 KiB of chunk operands and 768 bytes of
  * gates.  At most floor(N / 64) + B chunks.  Zero it once with
  * canopy_workspace_init (the error word; the rest is scratch), read the
  * word with canopy_read_device_error.  Returns 0 for unsupported sizes. */

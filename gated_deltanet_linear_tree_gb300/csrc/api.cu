@@ -288,7 +288,8 @@ canopy_status canopy_serial_replay(const void* q, const void* k, const void* v, 
 }
 
 size_t canopy_prefill_workspace_bytes(int N, int B, int HV, int dk, int dv) {
-    if (N < 1 || B < 1 || B > kMaxGrid || HV < 1 || HV > kMaxGrid || dk != dv || (dk != 128 && dk != 32) || !chunks_ok(N, B, HV))
+    if (N < 1 || B < 1 || B > kMaxGrid || HV < 1 || HV > kMaxGrid || dk != dv || (dk != 128 && dk != 32) ||
+        !chunks_ok(N, B, HV))
         return 0;
     return dk == 128 ? prefill_chunk_ws_bytes(N, B, HV) : 256;
 }

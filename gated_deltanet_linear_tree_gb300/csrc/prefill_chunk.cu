@@ -164,9 +164,9 @@ struct PrepSmem {
     static constexpr int ROWC = QK;                  // float [64][P]: rows of C, then x1 of M (over Q and K)
     static constexpr int ROWW = ROWC + C * P * 4;    // float [64][PW]: x1 of W
     static constexpr int G = QK + QK_BYTES;          // float [64][P]
-    static constexpr int GATE = G + C * P * 4;       // float [64]: g
-    static constexpr int BE = GATE + C * 4;          // float [64]: beta
-    static constexpr int BAR = BE + C * 4;           // u64 [2]
+    static constexpr int GATE = G + C * P * 4;       // float [2][64]: g of each head
+    static constexpr int BE = GATE + 2 * C * 4;      // float [2][64]: beta
+    static constexpr int BAR = BE + 2 * C * 4;       // u64 [2]
     static constexpr int SLOT = BAR + 16;
     static constexpr int TOTAL = SLOT + 8;
     static_assert(BAR % 8 == 0 && GATE >= MW_BYTES && ROWW + C * PW * 4 <= G, "layout");
@@ -222,7 +222,7 @@ __device__ inline void put_half_row(uint8_t* image, int row, int half, const uin
 __global__ void __launch_bounds__(128, 4)
     prep_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const float* __restrict__ g, const float* __restrict__ beta, const int32_t* __restrict__ starts,
-                int N, int B, int HV, int ratio, WsView ws) {
+                int N, int B, int HV, int ratio, int heads, WsView ws) {
     using P = PrepSmem;
     extern __shared__ __align__(1024) uint8_t sm[];
     float* sG = reinterpret_cast<float*>(sm + P::G);
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(128, 4)
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + P::BAR);
     uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + P::SLOT);
     const int tid = threadIdx.x, warp = tid >> 5;
-    const int slot = blockIdx.x / HV, h = blockIdx.x - slot * HV;
+    const int per_slot = HV / heads, slot = blockIdx.x / per_slot, h = (blockIdx.x - slot * per_slot) * heads;
     // Tile row r is token (r & 63) ^ flip, of Q for r < 64 and of K beyond:
     // the two warps with the long rows sit on the SM's schedulers 1 and 3 in
     // even blocks, 0 and 2 in odd ones.
@@ -275,11 +275,12 @@ __global__ void __launch_bounds__(128, 4)
         tmem_relinquish();
         tc_fence_before();
     }
-    if (tid < C) {  // tokens past the end decay and write nothing
+    if (tid < C * heads) {  // token tid & 63 of head h + tid / 64; tokens past the end decay and write nothing
+        const int n = tid & (C - 1);
         float a = 1.f, be = 0.f;
-        if (tid < valid) {
-            a = g[size_t(n0 + tid) * HV + h];
-            be = beta[size_t(n0 + tid) * HV + h];
+        if (n < valid) {
+            a = g[size_t(n0 + n) * HV + h + tid / C];
+            be = beta[size_t(n0 + n) * HV + h + tid / C];
             if (!gate_ok(a, be)) {
                 bad |= CANOPY_DEVERR_GATE;
                 a = 1.f;
@@ -315,103 +316,110 @@ __global__ void __launch_bounds__(128, 4)
         const int i = (tid & 63) ^ flip;
         const bool krow = tid >= C;
         const bool live = i < valid;
-        const size_t at = size_t(slot) * HV + h;
-        float* rowp = (krow ? sG : reinterpret_cast<float*>(sm + P::ROWC)) + i * P::P;
-        float d = krow ? sBe[i] : 1.f;  // beta g_{j+1} .. g_i
-        float end = 1.f;                // g_{i+1} .. g_63
 #pragma unroll 1
-        for (int kb = 3; kb >= 0; --kb) {
-            uint32_t a[16];
-            tmem_ld16(tmem + (uint32_t(warp * 32) << 16) + ((16 * kb) ^ flip), a);
-            tmem_wait_ld();
-            const int last = i - 16 * kb;  // the row's own column in this 16
-            const int lim = !live ? -1 : krow ? last - 1 : last;
+        for (int hh = 0; hh < heads; ++hh) {
+            const size_t at = size_t(slot) * HV + h + hh;
+            const float* gate = sGate + hh * C;
+            float* rowp = (krow ? sG : reinterpret_cast<float*>(sm + P::ROWC)) + i * P::P;
+            float d = krow ? sBe[hh * C + i] : 1.f;  // beta g_{j+1} .. g_i
+            float end = 1.f;                         // g_{i+1} .. g_63
+#pragma unroll 1
+            for (int kb = 3; kb >= 0; --kb) {
+                uint32_t a[16];
+                tmem_ld16(tmem + (uint32_t(warp * 32) << 16) + ((16 * kb) ^ flip), a);
+                tmem_wait_ld();
+                const int last = i - 16 * kb;  // the row's own column in this 16
+                const int lim = !live ? -1 : krow ? last - 1 : last;
 #pragma unroll
-            for (int u4 = 3; u4 >= 0; --u4) {
-                const float4 g4 = *reinterpret_cast<const float4*>(sGate + 16 * kb + 4 * u4);
-                const float gg[4] = {g4.x, g4.y, g4.z, g4.w};
-                float y[4];
+                for (int u4 = 3; u4 >= 0; --u4) {
+                    const float4 g4 = *reinterpret_cast<const float4*>(gate + 16 * kb + 4 * u4);
+                    const float gg[4] = {g4.x, g4.y, g4.z, g4.w};
+                    float y[4];
 #pragma unroll
-                for (int u = 3; u >= 0; --u) {
-                    y[u] = 4 * u4 + u <= lim ? d * __uint_as_float(a[4 * u4 + u]) : 0.f;
-                    if (4 * u4 + u <= last) d *= gg[u];
-                    else end *= gg[u];
-                }
-                *reinterpret_cast<float4*>(rowp + 16 * kb + 4 * u4) = make_float4(y[0], y[1], y[2], y[3]);
-            }
-        }
-        float* gates = ws.gates + at * GATE_FLOATS;
-        gates[krow ? C + i : i] = krow ? sBe[i] : d;
-        if (krow) gates[2 * C + i] = end;
-        __syncthreads();
-        // Row i of M (from c_i), or of W (from the unit row e_i).  x1 is kept in shared memory;
-        // the first 32 tokens have none.
-        float* keep = krow ? reinterpret_cast<float*>(sm + P::ROWW) + i * P::PW : rowp + 32;
-        const bool upper = i >= 32;
-        uint64_t x[16];
-        auto start = [&](int half) {
-            if (krow) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    x[j] = pack2(32 * half + 2 * j == i ? 1.f : 0.f, 32 * half + 2 * j + 1 == i ? 1.f : 0.f);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(rowp + 32 * half + 4 * j);
-                    x[2 * j] = y.x;
-                    x[2 * j + 1] = y.y;
+                    for (int u = 3; u >= 0; --u) {
+                        y[u] = 4 * u4 + u <= lim ? d * __uint_as_float(a[4 * u4 + u]) : 0.f;
+                        if (4 * u4 + u <= last) d *= gg[u];
+                        else end *= gg[u];
+                    }
+                    *reinterpret_cast<float4*>(rowp + 16 * kb + 4 * u4) = make_float4(y[0], y[1], y[2], y[3]);
                 }
             }
-        };
-        if (upper) {
-            start(1);
-            solve32(x, sG + 32 * P::P + 32);
+            float* gates = ws.gates + at * GATE_FLOATS;
+            gates[krow ? C + i : i] = krow ? sBe[hh * C + i] : d;
+            if (krow) gates[2 * C + i] = end;
+            __syncthreads();
+            // Row i of M (from c_i), or of W (from the unit row e_i).  x1 is
+            // kept in shared memory; the first 32 tokens have none.
+            float* keep = krow ? reinterpret_cast<float*>(sm + P::ROWW) + i * P::PW : rowp + 32;
+            const bool upper = i >= 32;
+            uint64_t x[16];
+            auto start = [&](int half) {
+                if (krow) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                *reinterpret_cast<ulonglong2*>(keep + 4 * j) = make_ulonglong2(x[2 * j], x[2 * j + 1]);
-            start(0);
-#pragma unroll
-            for (int k4 = 0; k4 < 8; ++k4) {
-                const float4 xk4 = *reinterpret_cast<const float4*>(keep + 4 * k4);
-                const float xk[4] = {xk4.x, xk4.y, xk4.z, xk4.w};
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const uint64_t xx = pack2(-xk[u], -xk[u]);
-                    const ulonglong2* row = reinterpret_cast<const ulonglong2*>(sG + (32 + 4 * k4 + u) * P::P);
+                    for (int j = 0; j < 16; ++j)
+                        x[j] = pack2(32 * half + 2 * j == i ? 1.f : 0.f, 32 * half + 2 * j + 1 == i ? 1.f : 0.f);
+                } else {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const ulonglong2 y = row[j];
-                        x[2 * j] = fma2(xx, y.x, x[2 * j]);
-                        x[2 * j + 1] = fma2(xx, y.y, x[2 * j + 1]);
+                        const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(rowp + 32 * half + 4 * j);
+                        x[2 * j] = y.x;
+                        x[2 * j + 1] = y.y;
                     }
                 }
+            };
+            if (upper) {
+                start(1);
+                solve32(x, sG + 32 * P::P + 32);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    *reinterpret_cast<ulonglong2*>(keep + 4 * j) = make_ulonglong2(x[2 * j], x[2 * j + 1]);
+                start(0);
+#pragma unroll
+                for (int k4 = 0; k4 < 8; ++k4) {
+                    const float4 xk4 = *reinterpret_cast<const float4*>(keep + 4 * k4);
+                    const float xk[4] = {xk4.x, xk4.y, xk4.z, xk4.w};
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const uint64_t xx = pack2(-xk[u], -xk[u]);
+                        const ulonglong2* row = reinterpret_cast<const ulonglong2*>(sG + (32 + 4 * k4 + u) * P::P);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const ulonglong2 y = row[j];
+                            x[2 * j] = fma2(xx, y.x, x[2 * j]);
+                            x[2 * j + 1] = fma2(xx, y.y, x[2 * j + 1]);
+                        }
+                    }
+                }
+            } else {
+                start(0);
             }
-        } else {
-            start(0);
-        }
-        solve32(x, sG);
-        uint64_t x1[16];
+            solve32(x, sG);
+            uint64_t x1[16];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const ulonglong2 y = upper ? *reinterpret_cast<const ulonglong2*>(keep + 4 * j) : make_ulonglong2(0, 0);
-            x1[2 * j] = y.x;
-            x1[2 * j + 1] = y.y;
-        }
-        __syncthreads();  // everything before the image is done with
-        const int row = (i >> 4) * 32 + (i & 15) + (krow ? 16 : 0);
+            for (int j = 0; j < 8; ++j) {
+                const ulonglong2 y =
+                    upper ? *reinterpret_cast<const ulonglong2*>(keep + 4 * j) : make_ulonglong2(0, 0);
+                x1[2 * j] = y.x;
+                x1[2 * j + 1] = y.y;
+            }
+            __syncthreads();  // everything before the image is done with
+            const int row = (i >> 4) * 32 + (i & 15) + (krow ? 16 : 0);
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-            put_half_row(sm + P::QK, row, half, x);
+            for (int half = 0; half < 2; ++half) {
+                put_half_row(sm + P::QK, row, half, x);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] = x1[j];
-        }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncthreads();
-        if (tid == 0) {
-            bulk_store(ws.mw + at * MW_BYTES, sm + P::QK, MW_BYTES);
-            bulk_commit();
-            bulk_wait<0>();
+                for (int j = 0; j < 16; ++j) x[j] = x1[j];
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncthreads();
+            if (tid == 0) {
+                bulk_store(ws.mw + at * MW_BYTES, sm + P::QK, MW_BYTES);
+                bulk_commit();
+                if (hh + 1 < heads) bulk_wait_read<0>();
+                else bulk_wait<0>();
+            }
+            if (hh + 1 < heads) __syncthreads();  // the image is read: its place is free
         }
     } else if (tid == 0) {
         raise_err(ws.err, CANOPY_DEVERR_TIMEOUT);
@@ -435,38 +443,48 @@ __global__ void __launch_bounds__(128, 4)
 // schedulers.  A warp reads 16 of its lanes at a time with all its threads:
 // thread t has rows t / 4 and t / 4 + 8, columns 2 (t % 4), + 1 of every 8.
 
-constexpr int NV = 32;           // value columns per chain
-constexpr int ROW = NV * 2;      // bytes of one K index of a B operand part
-constexpr int SPART = D * ROW;   // one part of S
-constexpr int RPART = C * ROW;   // one part of R (and U)
-// TMEM columns of a chain: [X_Q; X_K] and later K^T U in three groups, [o; U]
-// in three, the third part's share of o.
-constexpr uint32_t TX = 0, TO = 3 * NV, TL = 6 * NV, CHAIN_COLS = 7 * NV;
 constexpr int kMaxRanked = 128;  // sequences that are started by length
+constexpr int WARPS = 8;         // compute warps per chain
 
 enum { CB_X, CB_OU, CB_O2, CB_DS, CB_S, CB_R, CB_U, CB_N };  // a chain's barriers (from CB_S on: its warps arrive)
 enum { PB_QK = 0, PB_QKE = 2, PB_MW = 4, PB_MWE = 6, PB_LO = 8, PB_LOE, PB_N };  // tiles: full and empty
 
-// One chain per block (few states: latency counts) has U apart from R, so
-// that the third part's products need not be over before U is taken on.
-// (16 warps of 8 columns for it were no faster than 8 warps of 16.)
-constexpr int WARPS = 8;  // compute warps per chain
-constexpr int HN = 16;    // value columns of a compute thread
-template <int NCH>
-constexpr bool kLate = NCH == 1;
-
-template <int NCH>
-struct WalkSmem {
-    static constexpr int QK = 0;                  // two buffers
-    static constexpr int MW = QK + 2 * QK_BYTES;  // parts 0 and 1: two buffers
-    static constexpr int LO = MW + 4 * MW_PART;   // part 2: one buffer
+// Three shapes of a block:
+//   <32, 1>  one chain: few states, a chunk's latency counts.  U is apart from
+//            R, so that the third part's products need not be over before U
+//            is taken on (16 warps of 8 columns were no faster);
+//   <32, 2>  two chains half a chunk apart, one's products beside the other's
+//            register work;
+//   <64, 2>  all 128 value columns: [Q; K] and [M; W] are read once for all of
+//            a state, and a product is hardly longer for 192 columns than for
+//            96.  What does not fit twice shares its place: R and U the shared
+//            memory of S, o and U the tensor memory of X, [M; W] has one
+//            buffer, and S itself is in tensor memory.
+template <int NV_, int NCH_>
+struct Shape {
+    static constexpr int NV = NV_, NCH = NCH_;
+    static constexpr int HN = NV * 4 / WARPS;     // value columns of a compute thread
+    static constexpr int ROW = NV * 2;            // bytes of one K index of a B operand part
+    static constexpr int SPART = D * ROW;         // one part of S
+    static constexpr int RPART = C * ROW;         // one part of R (and U)
+    static constexpr uint32_t SWIZZLE = NV == 64 ? 2 : 4;  // rows of 128 or 64 bytes, the swizzle of that width
+    static constexpr bool LATE = NCH == 1, TIGHT = NV == 64;
+    // TMEM columns of a chain: [X_Q; X_K] and later K^T U in three groups,
+    // [o; U] in three, the third part's share of o, S
+    static constexpr uint32_t TX = 0, TO = TIGHT ? 0 : 3 * NV, TL = 6 * NV, TS = 3 * NV;
+    static constexpr uint32_t COLS = TIGHT ? 4 * NV : LATE ? 7 * NV : 6 * NV;
+    static_assert(NCH * COLS <= 512, "tensor memory");
+    // shared memory: [Q; K] twice; parts 0 and 1 of [M; W] (twice, or once), part 2
+    static constexpr int MW_BUFS = TIGHT ? 1 : 2;
+    static constexpr int QK = 0, MW = QK + 2 * QK_BYTES, LO = MW + MW_BUFS * 2 * MW_PART;
     static constexpr int S = LO + MW_PART;
-    static constexpr int R = S + NCH * 3 * SPART;
-    static constexpr int U = R + (kLate<NCH> ? NCH * 3 * RPART : 0);
-    static constexpr int BAR = U + NCH * 3 * RPART;
+    static constexpr int R = TIGHT ? S : S + NCH * 3 * SPART;
+    static constexpr int U = LATE ? R + NCH * 3 * RPART : R;
+    static constexpr int CHAIN_R = TIGHT ? 3 * SPART : 3 * RPART;  // from one chain's R to the next's
+    static constexpr int BAR = TIGHT ? S + NCH * 3 * SPART : U + NCH * 3 * RPART;
     static constexpr int SLOT = BAR + (PB_N + NCH * CB_N) * 8;
     static constexpr int TOTAL = SLOT + 8;
-    static_assert(TOTAL + 1024 <= 227 * 1024, "shared memory");
+    static_assert(TOTAL <= 227 * 1024, "shared memory");
 };
 
 // 16 TMEM lanes x HN columns: for e = 0, 1 (rows) and c < HN / 8 (groups of 8
@@ -477,93 +495,105 @@ __device__ inline void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t (&r)[8]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr));
 }
-template <int GROUPS>
-__device__ inline void sum_rows16(uint32_t taddr, uint64_t (&x)[4]) {
-    uint32_t a[GROUPS][8];
+template <typename P, int GROUPS>
+__device__ inline void sum_rows16(uint32_t taddr, uint64_t (&x)[P::HN / 4]) {
 #pragma unroll
-    for (int g = 0; g < GROUPS; ++g) tmem_ld_16x256b_x2(taddr + g * NV, a[g]);
-    tmem_wait_ld();
+    for (int c2 = 0; c2 < P::HN / 16; ++c2) {
+        uint32_t a[GROUPS][8];
 #pragma unroll
-    for (int c = 0; c < HN / 8; ++c)
+        for (int g = 0; g < GROUPS; ++g) tmem_ld_16x256b_x2(taddr + g * P::NV + 16 * c2, a[g]);
+        tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int r = 4 * c + 2 * e;
-            uint64_t y = pack2(a[GROUPS - 1][r], a[GROUPS - 1][r + 1]);
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int g = GROUPS - 2; g >= 0; --g) y = add2(pack2(a[g][r], a[g][r + 1]), y);
-            x[HN / 8 * e + c] = y;
-        }
+            for (int e = 0; e < 2; ++e) {
+                const int r = 4 * c + 2 * e;
+                uint64_t y = pack2(a[GROUPS - 1][r], a[GROUPS - 1][r + 1]);
+#pragma unroll
+                for (int g = GROUPS - 2; g >= 0; --g) y = add2(pack2(a[g][r], a[g][r + 1]), y);
+                x[P::HN / 8 * e + 2 * c2 + c] = y;
+            }
+    }
+}
+
+// Byte offset of group c of 8 columns of K index k in a part of a B operand.
+template <typename P>
+__device__ inline int part_offset(int k, int c) {
+    return k * P::ROW + ((c ^ (P::NV == 64 ? k & 7 : (k >> 1) & 3)) << 4);
 }
 
 // The same values as three parts of a B operand whose K index is the token:
 // k0 is the first of the 16 tokens, c0 the first group of 8 columns.
-__device__ inline void put_rows16(uint8_t* base, int k0, int c0, int lane, const uint64_t (&x)[HN / 4]) {
+template <typename P>
+__device__ inline void put_rows16(uint8_t* base, int k0, int c0, int lane, const uint64_t (&x)[P::HN / 4]) {
 #pragma unroll
     for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int c = 0; c < HN / 8; ++c) {
+        for (int c = 0; c < P::HN / 8; ++c) {
             const int k = k0 + (lane >> 2) + 8 * e;
             uint32_t h, m, l;
-            split3(x[HN / 8 * e + c], h, m, l);
-            uint8_t* p = base + k * ROW + (((c0 + c) ^ ((k >> 1) & 3)) << 4) + (lane & 3) * 4;
+            split3(x[P::HN / 8 * e + c], h, m, l);
+            uint8_t* p = base + part_offset<P>(k, c0 + c) + (lane & 3) * 4;
             *reinterpret_cast<uint32_t*>(p) = h;
-            *reinterpret_cast<uint32_t*>(p + RPART) = m;
-            *reinterpret_cast<uint32_t*>(p + 2 * RPART) = l;
+            *reinterpret_cast<uint32_t*>(p + P::RPART) = m;
+            *reinterpret_cast<uint32_t*>(p + 2 * P::RPART) = l;
         }
 }
 
-// HN columns from group c0 of K index k as three parts of a B operand: rows
-// of 64 bytes in the 64-byte swizzle.
-__device__ inline void put_parts(uint8_t* base, int k, int c0, const uint64_t (&x)[HN / 2]) {
+// Group c of 8 columns of K index k as three parts of a B operand.
+template <typename P>
+__device__ inline void put_part8(uint8_t* base, int k, int c, const uint64_t* x) {
+    uint32_t h[4], m[4], l[4];
 #pragma unroll
-    for (int c = 0; c < HN / 8; ++c) {
-        uint32_t h[4], m[4], l[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) split3(x[4 * c + e], h[e], m[e], l[e]);
-        uint8_t* p = base + k * ROW + (((c0 + c) ^ ((k >> 1) & 3)) << 4);
-        *reinterpret_cast<uint4*>(p) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(p + SPART) = make_uint4(m[0], m[1], m[2], m[3]);
-        *reinterpret_cast<uint4*>(p + 2 * SPART) = make_uint4(l[0], l[1], l[2], l[3]);
-    }
+    for (int e = 0; e < 4; ++e) split3(x[e], h[e], m[e], l[e]);
+    uint8_t* p = base + part_offset<P>(k, c);
+    *reinterpret_cast<uint4*>(p) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(p + P::SPART) = make_uint4(m[0], m[1], m[2], m[3]);
+    *reinterpret_cast<uint4*>(p + 2 * P::SPART) = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-// The three column groups of an accumulator, NV apart, summed: this lane's
-// HN columns, 8 at a time.
 __device__ inline void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr));
 }
-__device__ inline void sum_parts(uint32_t taddr, uint64_t (&x)[HN / 2]) {
+__device__ inline void tmem_put8(uint32_t taddr, const uint64_t* x) {
+    uint32_t r[8];
 #pragma unroll
-    for (int q = 0; q < HN / 8; ++q) {
-        uint32_t a[8], b[8], d[8];
-        tmem_ld8(taddr + 8 * q, a);
-        tmem_ld8(taddr + NV + 8 * q, b);
-        tmem_ld8(taddr + 2 * NV + 8 * q, d);
-        tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            x[4 * q + e] = add2(pack2(a[2 * e], a[2 * e + 1]),
-                                add2(pack2(b[2 * e], b[2 * e + 1]), pack2(d[2 * e], d[2 * e + 1])));
+    for (int e = 0; e < 4; ++e) {
+        const float2 y = unpack2(x[e]);
+        r[2 * e] = bits(y.x);
+        r[2 * e + 1] = bits(y.y);
     }
+    tmem_st8(taddr, r);
+}
+// 8 columns of this lane, summed over the accumulator's three groups.
+template <typename P>
+__device__ inline void sum8(uint32_t taddr, uint64_t (&x)[4]) {
+    uint32_t a[8], b[8], d[8];
+    tmem_ld8(taddr, a);
+    tmem_ld8(taddr + P::NV, b);
+    tmem_ld8(taddr + 2 * P::NV, d);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        x[e] = add2(pack2(a[2 * e], a[2 * e + 1]),
+                    add2(pack2(b[2 * e], b[2 * e + 1]), pack2(d[2 * e], d[2 * e + 1])));
 }
 
-template <int NCH, typename OutT>
-__global__ void __launch_bounds__(32 * ((WARPS + 1) * NCH + 1), 1)
+template <typename P, typename OutT>
+__global__ void __launch_bounds__(32 * ((WARPS + 1) * P::NCH + 1), 1)
     walk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __nv_bfloat16* __restrict__ v, const float* S0, float* S_new,
                 const int32_t* __restrict__ starts, OutT* __restrict__ o, int N, int HV, int ratio, float scale,
                 WsView ws) {
-    using L = WalkSmem<NCH>;
-    constexpr uint32_t kCols = NCH == 1 ? 256 : 512;
-    static_assert(NCH * CHAIN_COLS <= kCols, "TMEM columns");
+    constexpr int NV = P::NV, NCH = P::NCH, HN = P::HN;
+    constexpr uint32_t kCols = 512;
     constexpr int kComputeWarps = WARPS * NCH;
-    constexpr bool LATE = kLate<NCH>;
     extern __shared__ __align__(1024) uint8_t sm[];
-    uint64_t* pb = reinterpret_cast<uint64_t*>(sm + L::BAR);
-    uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + L::SLOT);
-    int* sSeq = reinterpret_cast<int*>(sm + L::SLOT + 4);
+    uint64_t* pb = reinterpret_cast<uint64_t*>(sm + P::BAR);
+    uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + P::SLOT);
+    int* sSeq = reinterpret_cast<int*>(sm + P::SLOT + 4);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int SPLITS = D / (NV * NCH);
     const int h = blockIdx.x / SPLITS, v0 = (blockIdx.x - h * SPLITS) * NV * NCH;
@@ -623,7 +653,7 @@ __global__ void __launch_bounds__(32 * ((WARPS + 1) * NCH + 1), 1)
                 const int s = t & 1, n = lo + C * t;
                 const uint32_t freed = ((t >> 1) & 1) ^ 1;  // a fresh barrier passes for parity 1
                 const uint8_t* image = ws.mw + ((slot0 + t) * HV + h) * MW_BYTES;
-                uint8_t* qk = sm + L::QK + s * QK_BYTES;
+                uint8_t* qk = sm + P::QK + s * QK_BYTES;
                 if (!(ok = mbar_wait(&pb[PB_QKE + s], freed))) break;
                 mbar_expect_tx(&pb[PB_QK + s], QK_BYTES);
 #pragma unroll
@@ -633,19 +663,23 @@ __global__ void __launch_bounds__(32 * ((WARPS + 1) * NCH + 1), 1)
                     tma_load_4d(dst + 2048, &tmK, &pb[PB_QK + s], 64 * (e >> 2), hk, n + 16 * (e & 3), 0);
                 }
                 ++qk_n;
-                if (!(ok = mbar_wait(&pb[PB_MWE + s], freed))) break;
-                mbar_expect_tx(&pb[PB_MW + s], 2 * MW_PART);
-                bulk_load(sm + L::MW + s * 2 * MW_PART, image, 2 * MW_PART, &pb[PB_MW + s]);
+                const int ms = P::MW_BUFS == 2 ? s : 0;
+                if (!(ok = mbar_wait(&pb[PB_MWE + ms], P::MW_BUFS == 2 ? freed : (t & 1) ^ 1))) break;
+                mbar_expect_tx(&pb[PB_MW + ms], 2 * MW_PART);
+                bulk_load(sm + P::MW + ms * 2 * MW_PART, image, 2 * MW_PART, &pb[PB_MW + ms]);
                 ++mw_n;
                 if (!(ok = mbar_wait(&pb[PB_LOE], (t & 1) ^ 1))) break;
                 mbar_expect_tx(&pb[PB_LO], MW_PART);
-                bulk_load(sm + L::LO, image + 2 * MW_PART, MW_PART, &pb[PB_LO]);
+                bulk_load(sm + P::LO, image + 2 * MW_PART, MW_PART, &pb[PB_LO]);
                 ++lo_n;
             }
             if (!ok) {  // the copies in flight land before the block ends
                 raise_err(ws.err, CANOPY_DEVERR_TIMEOUT);
                 for (int e = max(0, qk_n - 2); e < qk_n; ++e) mbar_wait(&pb[PB_QK + (e & 1)], (e >> 1) & 1);
-                for (int e = max(0, mw_n - 2); e < mw_n; ++e) mbar_wait(&pb[PB_MW + (e & 1)], (e >> 1) & 1);
+                for (int e = max(0, mw_n - P::MW_BUFS); e < mw_n; ++e) {
+                    if (P::MW_BUFS == 2) mbar_wait(&pb[PB_MW + (e & 1)], (e >> 1) & 1);
+                    else mbar_wait(&pb[PB_MW], e & 1);
+                }
                 if (lo_n) mbar_wait(&pb[PB_LO], (lo_n - 1) & 1);
             }
         }
@@ -654,59 +688,62 @@ __global__ void __launch_bounds__(32 * ((WARPS + 1) * NCH + 1), 1)
         if (lane == 0) {
             const int ch = warp - kComputeWarps;
             uint64_t* cb = pb + PB_N + ch * CB_N;
-            const uint32_t tmem = *sTmem + ch * CHAIN_COLS;
-            const uint32_t aS = smem_u32(sm + L::S + ch * 3 * SPART), aR = smem_u32(sm + L::R + ch * 3 * RPART);
-            const uint32_t aU = smem_u32(sm + L::U + ch * 3 * RPART);
-            const uint32_t aLo = smem_u32(sm + L::LO);
+            const uint32_t tmem = *sTmem + ch * P::COLS;
+            const uint32_t aS = smem_u32(sm + P::S + ch * 3 * P::SPART), aR = smem_u32(sm + P::R + ch * P::CHAIN_R);
+            const uint32_t aU = smem_u32(sm + P::U + ch * P::CHAIN_R);
+            const uint32_t aLo = smem_u32(sm + P::LO);
             constexpr uint32_t i3 = idesc_bf16(128, 3 * NV) | kMajorB, i2 = idesc_bf16(128, 2 * NV) | kMajorB,
                                i1 = idesc_bf16(128, NV) | kMajorB;
             for (int t = 0; t < nc; ++t) {
                 const int s = t & 1;
                 const uint32_t par = t & 1, fpar = (t >> 1) & 1;
-                const uint32_t aQK = smem_u32(sm + L::QK + s * QK_BYTES);
-                const uint32_t aMW = smem_u32(sm + L::MW + s * 2 * MW_PART);
+                const uint32_t aQK = smem_u32(sm + P::QK + s * QK_BYTES);
+                const int ms = P::MW_BUFS == 2 ? s : 0;
+                const uint32_t aMW = smem_u32(sm + P::MW + ms * 2 * MW_PART);
                 if (!(ok = mbar_wait(&pb[PB_QK + s], fpar))) break;
                 if (NCH > 1) {
                     // Half a chunk between the chains, so that one's products
                     // run beside the other's register work: the second starts
                     // a chunk once the first has its X, the first the next
                     // one once the second has its X.
-                    const uint64_t* other = pb + PB_N + (1 - ch) * CB_N;
-                    if ((ch || t) && !(ok = mbar_wait(const_cast<uint64_t*>(&other[CB_X]), ch ? par : par ^ 1))) break;
+                    uint64_t* other = pb + PB_N + (1 - ch) * CB_N;
+                    if ((ch || t) && !(ok = mbar_wait(&other[CB_X], ch ? par : par ^ 1))) break;
                 }
                 if (!(ok = mbar_wait(&cb[CB_S], par))) break;
                 tc_fence_after();
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)
-                    mma_bf16_ss(tmem + TX, sdesc(aQK + (ks >> 2) * 16384 + (ks & 3) * 32, 0, 1024, 2),
-                                sdesc(aS + ks * 16 * ROW, SPART, 8 * ROW, 4), i3, ks != 0);
+                    mma_bf16_ss(tmem + P::TX, sdesc(aQK + (ks >> 2) * 16384 + (ks & 3) * 32, 0, 1024, 2),
+                                sdesc(aS + ks * 16 * P::ROW, P::SPART, 8 * P::ROW, P::SWIZZLE), i3, ks != 0);
                 mma_commit(&cb[CB_X]);
-                if (!(ok = mbar_wait(&pb[PB_MW + s], fpar))) break;
+                if (!(ok = mbar_wait(&pb[PB_MW + ms], P::MW_BUFS == 2 ? fpar : par))) break;
                 if (!(ok = mbar_wait(&pb[PB_LO], par))) break;
                 if (!(ok = mbar_wait(&cb[CB_R], par))) break;
                 tc_fence_after();
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    mma_bf16_ss(tmem + TO, sdesc(aMW + ks * 32, 0, 1024, 2),
-                                sdesc(aR + ks * 16 * ROW, RPART, 8 * ROW, 4), i3, ks != 0);
+                    mma_bf16_ss(tmem + P::TO, sdesc(aMW + ks * 32, 0, 1024, 2),
+                                sdesc(aR + ks * 16 * P::ROW, P::RPART, 8 * P::ROW, P::SWIZZLE), i3, ks != 0);
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    mma_bf16_ss(tmem + TO, sdesc(aMW + MW_PART + ks * 32, 0, 1024, 2),
-                                sdesc(aR + ks * 16 * ROW, RPART, 8 * ROW, 4), i2, 1);
-                if (LATE) mma_commit(&cb[CB_OU]);
+                    mma_bf16_ss(tmem + P::TO, sdesc(aMW + MW_PART + ks * 32, 0, 1024, 2),
+                                sdesc(aR + ks * 16 * P::ROW, P::RPART, 8 * P::ROW, P::SWIZZLE), i2, 1);
+                if (P::LATE) mma_commit(&cb[CB_OU]);
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    mma_bf16_ss(tmem + (LATE ? TL : TO), sdesc(aLo + ks * 32, 0, 1024, 2),
-                                sdesc(aR + ks * 16 * ROW, RPART, 8 * ROW, 4), i1, !LATE || ks != 0);
-                mma_commit(&cb[LATE ? CB_O2 : CB_OU]);
-                mma_commit(&pb[PB_MWE + s]);
+                    mma_bf16_ss(tmem + (P::LATE ? P::TL : P::TO), sdesc(aLo + ks * 32, 0, 1024, 2),
+                                sdesc(aR + ks * 16 * P::ROW, P::RPART, 8 * P::ROW, P::SWIZZLE), i1,
+                                !P::LATE || ks != 0);
+                mma_commit(&cb[P::LATE ? CB_O2 : CB_OU]);
+                mma_commit(&pb[PB_MWE + ms]);
                 mma_commit(&pb[PB_LOE]);
                 if (!(ok = mbar_wait(&cb[CB_U], par))) break;
                 tc_fence_after();
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    mma_bf16_ss(tmem + TX, sdesc(aQK + 2048 + ks * 4096, 16384, 1024, 2),
-                                sdesc(aU + ks * 16 * ROW, RPART, 8 * ROW, 4), i3 | kMajorA, ks != 0);
+                    mma_bf16_ss(tmem + P::TX, sdesc(aQK + 2048 + ks * 4096, 16384, 1024, 2),
+                                sdesc(aU + ks * 16 * P::ROW, P::RPART, 8 * P::ROW, P::SWIZZLE),
+                                i3 | kMajorA, ks != 0);
                 mma_commit(&cb[CB_DS]);
                 mma_commit(&pb[PB_QKE + s]);
             }
@@ -716,19 +753,30 @@ __global__ void __launch_bounds__(32 * ((WARPS + 1) * NCH + 1), 1)
         // ---- the chain's state, R, U and o ----------------------------------------
         const int ch = warp / WARPS, quad = warp & 3, part = (warp % WARPS) >> 2, c0 = part * (HN / 8);
         uint64_t* cb = pb + PB_N + ch * CB_N;
-        uint8_t* sS = sm + L::S + ch * 3 * SPART;
-        uint8_t* sR = sm + L::R + ch * 3 * RPART;
-        uint8_t* sU = sm + L::U + ch * 3 * RPART;
-        const uint32_t taddr = *sTmem + ch * CHAIN_COLS + (uint32_t(quad * 32) << 16) + part * HN;
+        uint8_t* sS = sm + P::S + ch * 3 * P::SPART;
+        uint8_t* sR = sm + P::R + ch * P::CHAIN_R;
+        uint8_t* sU = sm + P::U + ch * P::CHAIN_R;
+        const uint32_t taddr = *sTmem + ch * P::COLS + (uint32_t(quad * 32) << 16) + part * HN;
         const int krow = quad * 32 + lane;          // key row of S^T
         const int col = v0 + ch * NV + part * HN;   // first value column of this warp
         const int i0 = quad * 16 + (lane >> 2);     // this thread's token rows: i0, i0 + 8
         const int cp = 2 * (lane & 3);              // and column pairs: cp, cp + 8, ...
         const size_t sbase = ((size_t(b) * HV + h) * D + col) * D + krow;
-        uint64_t S[HN / 2];
+        // S: this lane's key row, HN columns, in registers or (tight) in
+        // tensor memory, and always as the next chunk's operand
+        uint64_t S[P::TIGHT ? 4 : HN / 2];
+        auto held = [&](int g) -> uint64_t* { return S + (P::TIGHT ? 0 : 4 * g); };  // columns 8 g .. 8 g + 7
 #pragma unroll
-        for (int c = 0; c < HN / 2; ++c)
-            S[c] = S0 ? pack2(S0[sbase + size_t(2 * c) * D], S0[sbase + size_t(2 * c + 1) * D]) : 0ull;
+        for (int g = 0; g < HN / 8; ++g) {
+            uint64_t* x = held(g);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                x[c] = S0 ? pack2(S0[sbase + size_t(8 * g + 2 * c) * D], S0[sbase + size_t(8 * g + 2 * c + 1) * D])
+                          : 0ull;
+            put_part8<P>(sS, krow, c0 + g, x);
+            if (P::TIGHT) tmem_put8(taddr + P::TS + 8 * g, x);
+        }
+        if (P::TIGHT) tmem_wait_st();
         pdl_wait();
         pdl_trigger();
         if (bad && tid == 0 && blockIdx.x == 0) raise_err(ws.err, bad);
@@ -778,8 +826,7 @@ __global__ void __launch_bounds__(32 * ((WARPS + 1) * NCH + 1), 1)
         for (int t = 0; t < nc; ++t) {
             const uint32_t par = t & 1;
             const int left = hi - (lo + C * t);  // tokens from this chunk's first on
-            // S as the B operand of the chunk's first product
-            put_parts(sS, krow, c0, S);
+            // S is in place as the B operand of the chunk's first product
             fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
@@ -801,7 +848,7 @@ __global__ void __launch_bounds__(32 * ((WARPS + 1) * NCH + 1), 1)
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&cb[CB_X], par)))) break;
             tc_fence_after();
             uint64_t y[NP];
-            sum_rows16<3>(taddr + (16u << 16) + TX, y);
+            sum_rows16<P, 3>(taddr + (16u << 16) + P::TX, y);
             // R = beta (v - 2^l X_K)
 #pragma unroll
             for (int r = 0; r < NP; ++r) x[r] = fma2(be[r / G8], y[r], x[r]);
@@ -812,15 +859,15 @@ __global__ void __launch_bounds__(32 * ((WARPS + 1) * NCH + 1), 1)
                 for (int r = 0; r < NP; ++r)
                     if (i0 + 8 * (r / G8) >= left) x[r] = 0ull;
                 if (part < 2) {
-                    uint8_t* z = sm + L::QK + (t & 1) * QK_BYTES + part * 16384 + quad * 4096 + 2048;
+                    uint8_t* z = sm + P::QK + (t & 1) * QK_BYTES + part * 16384 + quad * 4096 + 2048;
                     for (int r = lane >> 3; r < 16; r += 4)
                         if (quad * 16 + r >= left)
                             *reinterpret_cast<uint4*>(z + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
                 }
             }
-            put_rows16(sR, quad * 16, c0, lane, x);
+            put_rows16<P>(sR, quad * 16, c0, lane, x);
             fence_proxy_async_smem();
-            sum_rows16<3>(taddr + TX, oq);  // (the last product goes where X is)
+            sum_rows16<P, 3>(taddr + P::TX, oq);  // (the last product goes where X is)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&cb[CB_R]);
@@ -829,19 +876,24 @@ __global__ void __launch_bounds__(32 * ((WARPS + 1) * NCH + 1), 1)
 
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&cb[CB_OU], par)))) break;
             tc_fence_after();
-            sum_rows16<3>(taddr + (16u << 16) + TO, x);
+            sum_rows16<P, 3>(taddr + (16u << 16) + P::TO, x);
 #pragma unroll
             for (int r = 0; r < NP; ++r) x[r] = mul2(de[r / G8], x[r]);
-            put_rows16(sU, quad * 16, c0, lane, x);
+            put_rows16<P>(sU, quad * 16, c0, lane, x);
             fence_proxy_async_smem();
             __syncwarp();
+            if (P::TIGHT) {  // (the last product goes where o is)
+                sum_rows16<P, 3>(taddr + P::TO, x);
+                tc_fence_before();
+                __syncwarp();
+            }
             if (lane == 0) mbar_arrive(&cb[CB_U]);
-            sum_rows16<3>(taddr + TO, x);
-            if (LATE) {
+            if (!P::TIGHT) sum_rows16<P, 3>(taddr + P::TO, x);
+            if (P::LATE) {
                 if (!(ok = __all_sync(0xffffffffu, mbar_wait(&cb[CB_O2], par)))) break;
                 tc_fence_after();
                 uint64_t z[NP];
-                sum_rows16<1>(taddr + TL, z);
+                sum_rows16<P, 1>(taddr + P::TL, z);
 #pragma unroll
                 for (int r = 0; r < NP; ++r) x[r] = add2(x[r], z[r]);
             }
@@ -854,17 +906,43 @@ __global__ void __launch_bounds__(32 * ((WARPS + 1) * NCH + 1), 1)
 
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&cb[CB_DS], par)))) break;
             tc_fence_after();
-            uint64_t ds[HN / 2];
-            sum_parts(taddr + TX, ds);
             const uint64_t ll = pack2(last, last);
 #pragma unroll
-            for (int c = 0; c < HN / 2; ++c) S[c] = fma2(ll, S[c], ds[c]);
+            for (int g = 0; g < HN / 8; ++g) {
+                uint64_t* y8 = held(g);
+                uint64_t ds[4];
+                if (P::TIGHT) {
+                    uint32_t r[8];
+                    tmem_ld8(taddr + P::TS + 8 * g, r);
+                    sum8<P>(taddr + P::TX + 8 * g, ds);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) y8[c] = pack2(r[2 * c], r[2 * c + 1]);
+                } else {
+                    sum8<P>(taddr + P::TX + 8 * g, ds);
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) y8[c] = fma2(ll, y8[c], ds[c]);
+                put_part8<P>(sS, krow, c0 + g, y8);
+                if (P::TIGHT) tmem_put8(taddr + P::TS + 8 * g, y8);
+            }
+            if (P::TIGHT) tmem_wait_st();
         }
 #pragma unroll
-        for (int c = 0; c < HN / 2; ++c) {
-            const float2 z = unpack2(S[c]);
-            S_new[sbase + size_t(2 * c) * D] = z.x;
-            S_new[sbase + size_t(2 * c + 1) * D] = z.y;
+        for (int g = 0; g < HN / 8; ++g) {
+            uint64_t* x = held(g);
+            if (P::TIGHT) {
+                uint32_t r[8];
+                tmem_ld8(taddr + P::TS + 8 * g, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) x[c] = pack2(r[2 * c], r[2 * c + 1]);
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float2 z = unpack2(x[c]);
+                S_new[sbase + size_t(8 * g + 2 * c) * D] = z.x;
+                S_new[sbase + size_t(8 * g + 2 * c + 1) * D] = z.y;
+            }
         }
     }
     tc_fence_before();
@@ -875,20 +953,38 @@ __global__ void __launch_bounds__(32 * ((WARPS + 1) * NCH + 1), 1)
     }
 }
 
-template <int NCH, typename OutT>
+template <typename P, typename OutT>
 cudaError_t launch_walk(const CUtensorMap& mq, const CUtensorMap& mk, const void* v, const float* S0, float* S_new,
                         const int32_t* starts, void* o, int N, int B, int H, int HV, float scale, const WsView& ws,
                         cudaStream_t st) {
-    const int smem = WalkSmem<NCH>::TOTAL;
-    static const cudaError_t attr = cudaFuncSetAttribute(walk_kernel<NCH, OutT>,
-                                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static const cudaError_t attr =
+        cudaFuncSetAttribute(walk_kernel<P, OutT>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::TOTAL);
     if (attr != cudaSuccess) return attr;
-    return launch_pdl(walk_kernel<NCH, OutT>, dim3(HV * (D / (NV * NCH)), B), dim3(32 * ((WARPS + 1) * NCH + 1)), smem, st, mq,
-                      mk, static_cast<const __nv_bfloat16*>(v), S0, S_new, starts, static_cast<OutT*>(o), N, HV,
-                      HV / H, scale, ws);
+    return launch_pdl(walk_kernel<P, OutT>, dim3(HV * (D / (P::NV * P::NCH)), B),
+                      dim3(32 * ((WARPS + 1) * P::NCH + 1)), P::TOTAL, st, mq, mk,
+                      static_cast<const __nv_bfloat16*>(v), S0, S_new, starts, static_cast<OutT*>(o), N, HV, HV / H,
+                      scale, ws);
 }
 
 }  // namespace pfc
+
+// (chunk, value head) pairs from which two value heads of a key head share a
+// block of the first launch: four rounds of four blocks per SM.  With 4,576
+// pairs of 16 key heads 92 us alone and 85 us in twos, with 16,640 327 and 296.
+constexpr size_t kPairFrom = 2432;
+
+// The walk's shape by the number of states (sequences times value heads): by
+// the blocks that it makes of them for 152 SMs and a chunk's time in each,
+// 3,900, 5,400 and 8,200 cycles.  Several sequences are uneven as a rule and
+// take as long as the longest, so that the shorter chunk counts for more.
+// Measured with 1 to 32 sequences of 2,048 tokens, even and uneven, in us:
+// 48 states of 3 sequences 167/183/146/159 in one chain, 131/243/192/210 in
+// two (of one sequence 164 and 128), 128 states 329 and 300 on average, 256
+// states 517 in two chains and 486 in two wide ones, 512 states 948 and 858.
+int walk_shape(int B, int HV) {
+    const size_t states = size_t(B) * HV;
+    return states <= (B == 1 ? 38 : 100) ? 0 : states <= (B == 1 ? 110 : 220) ? 1 : 2;
+}
 
 size_t prefill_chunk_ws_bytes(int N, int B, int HV) { return pfc::ws_bytes(N, B, HV); }
 
@@ -897,25 +993,30 @@ cudaError_t launch_prefill_chunk(const void* q, const void* k, const void* v, co
                                  void* o, int o_bf16, float scale, void* workspace, cudaStream_t st) {
     CUtensorMap pq, pk, mq, mk;
     if (!make_bf16_row_map(&pq, q, 1, N, H, 32) || !make_bf16_row_map(&pk, k, 1, N, H, 32) ||
-        !make_bf16_row_map(&mq, q, 1, N, H, 16) || !make_bf16_row_map(&mk, k, 1, N, H, 16)) return cudaErrorInvalidValue;
+        !make_bf16_row_map(&mq, q, 1, N, H, 16) || !make_bf16_row_map(&mk, k, 1, N, H, 16))
+        return cudaErrorInvalidValue;
     const pfc::WsView ws = pfc::ws_view(workspace, N, B, HV);
     const int smem = pfc::PrepSmem::TOTAL;
     static const cudaError_t attr =
         cudaFuncSetAttribute(pfc::prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (attr != cudaSuccess) return attr;
-    const cudaError_t e = launch_pdl(pfc::prep_kernel, dim3(unsigned(pfc::slot_count(N, B) * HV)), dim3(128), smem, st,
-                                     pq, pk, g, beta, starts, N, B, HV, HV / H, ws);
+    // Two value heads of one key head share a block, its [Q; K] and their
+    // product, where there are many blocks all the same.
+    const size_t pairs = pfc::slot_count(N, B) * HV;
+    const int heads = (HV / H) % 2 == 0 && pairs >= kPairFrom ? 2 : 1;
+    const cudaError_t e = launch_pdl(pfc::prep_kernel, dim3(unsigned(pairs / heads)), dim3(128), smem, st, pq, pk, g,
+                                     beta, starts, N, B, HV, HV / H, heads, ws);
     if (e != cudaSuccess) return e;
-    const bool narrow = size_t(B) * HV <= 76;
-#define CANOPY_WALK(NCH, OT) \
-    return pfc::launch_walk<NCH, OT>(mq, mk, v, S0, S_new, starts, o, N, B, H, HV, scale, ws, st)
-    if (narrow) {
-        if (o_bf16) CANOPY_WALK(1, __nv_bfloat16);
-        CANOPY_WALK(1, float);
+    auto walk = [&](auto shape) {
+        using P = decltype(shape);
+        return o_bf16 ? pfc::launch_walk<P, __nv_bfloat16>(mq, mk, v, S0, S_new, starts, o, N, B, H, HV, scale, ws, st)
+                      : pfc::launch_walk<P, float>(mq, mk, v, S0, S_new, starts, o, N, B, H, HV, scale, ws, st);
+    };
+    switch (walk_shape(B, HV)) {
+        case 0: return walk(pfc::Shape<32, 1>());
+        case 1: return walk(pfc::Shape<32, 2>());
+        default: return walk(pfc::Shape<64, 2>());
     }
-    if (o_bf16) CANOPY_WALK(2, __nv_bfloat16);
-    CANOPY_WALK(2, float);
-#undef CANOPY_WALK
 }
 
 }  // namespace canopy

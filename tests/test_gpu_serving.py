@@ -97,7 +97,8 @@ def test_prefill(lib, force, bf16, d, lens):
     assert torch.equal(S16, S) and S16.data_ptr() == t["S0"].data_ptr()
 
 
-@pytest.mark.parametrize("lens,H,HV", [([130, 1, 0, 64, 77, 191], 7, 14), ([320], 26, 78), ([3] * 140, 1, 1)])
+@pytest.mark.parametrize("lens,H,HV", [([130, 1, 0, 64, 77, 191], 7, 14), ([320], 26, 78), ([3] * 140, 1, 1),
+                                       ([200, 65, 0, 130], 8, 24), ([1, 127], 24, 72)])
 def test_prefill_many_states(lib, lens, H, HV):
     """Enough (sequence, value head) pairs for two chains of value columns per block, and more sequences than
     are started by length."""

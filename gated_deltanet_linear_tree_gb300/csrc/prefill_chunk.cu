@@ -44,21 +44,32 @@ constexpr int GATE_FLOATS = 192;  // 2^l, beta and the decay to the chunk's end,
 
 __host__ __device__ inline size_t slot_count(int N, int B) { return size_t(N / C) + B; }
 
+constexpr int kMaxRanked = 127;  // sequences that the walk is planned for
+constexpr int kMaxHalved = 4;    // of them, at most so many in halves (a block that has no walk costs its start)
+
+// The walk's rows, longest first: the sequence, whether it is walked in
+// halves of a state, and its first block; one more for where they end.
+struct Row {
+    int32_t seq, halved, first, unused;
+};
+
 struct WsView {
     int32_t* err;
+    Row* rows;
     uint8_t* mw;   // [slot][HV] images of MW_BYTES
     float* gates;  // [slot][HV][GATE_FLOATS]
 };
 
 __host__ __device__ inline size_t ws_bytes(int N, int B, int HV) {
-    return 256 + slot_count(N, B) * HV * (MW_BYTES + GATE_FLOATS * 4);
+    return 256 + (kMaxRanked + 1) * sizeof(Row) + slot_count(N, B) * HV * (MW_BYTES + GATE_FLOATS * 4);
 }
 inline WsView ws_view(void* base, int N, int B, int HV) {
     uint8_t* p = static_cast<uint8_t*>(base);
     WsView w;
     w.err = reinterpret_cast<int32_t*>(p);
-    w.mw = p + 256;
-    w.gates = reinterpret_cast<float*>(p + 256 + slot_count(N, B) * HV * MW_BYTES);
+    w.rows = reinterpret_cast<Row*>(p + 256);
+    w.mw = p + 256 + (kMaxRanked + 1) * sizeof(Row);
+    w.gates = reinterpret_cast<float*>(w.mw + slot_count(N, B) * HV * MW_BYTES);
     return w;
 }
 
@@ -219,10 +230,66 @@ __device__ inline void put_half_row(uint8_t* image, int row, int half, const uin
     }
 }
 
+// The walk's plan, by one block of 128 threads.  Sequences are walked by four
+// blocks per state (quarters), or by one, the longest of them by two: so many
+// as give the least estimate for the launch, the largest of the longest walk,
+// the work spread over the SMs, and (m + 1) times the walk at place
+// 152 m + 1 by length (of 152 m + 1 walks some SM has m + 1).  The longest
+// walks start first (they end last).
+constexpr int kSMs = 152, kHalfCycles = 5700, kWholeCycles = 8300, kWalkCycles = 5000;  // per chunk; per walk
+
+__device__ inline void plan_walk(const int32_t* starts, int nseq, int HV, int quarters, Row* rows) {
+    __shared__ int sLen[128], sSorted[128], sCount[128];
+    __shared__ unsigned long long sBest;
+    const int tid = threadIdx.x;
+    if (tid == 0) sBest = quarters ? 0ull : ~0ull;
+    const int len = tid < nseq ? max(starts[tid + 1] - starts[tid], 0) : 0, chunks = (len + C - 1) / C;
+    sLen[tid] = len;
+    __syncthreads();
+    int rank = 0;
+    for (int k = 0; k < nseq; ++k) rank += sLen[k] > len || (sLen[k] == len && k < tid);
+    if (tid < nseq) sSorted[rank] = chunks;
+    __syncthreads();
+    if (!quarters && tid <= min(nseq, kMaxHalved)) {  // the estimate with the first tid sequences halved
+        int i = 0, j = tid, walks = 0, m = 0;
+        float most = 0.f, work = 0.f;
+        while (i < tid || j < nseq) {  // both kinds in descending order
+            const float half = i < tid ? float(sSorted[i]) * kHalfCycles + kWalkCycles : -1.f;
+            const float whole = j < nseq ? float(sSorted[j]) * kWholeCycles + kWalkCycles : -1.f;
+            const float cycles = fmaxf(half, whole);
+            const int count = half >= whole ? 2 * HV : HV;
+            if (half >= whole) ++i;
+            else ++j;
+            work += cycles * count;
+            walks += count;
+            for (; walks > kSMs * m; ++m) most = fmaxf(most, float(m + 1) * cycles);
+        }
+        most = fmaxf(most, work * (1.05f / kSMs));
+        if (tid > 0) most *= 1.08f;  // (and it has to be worth it)
+        atomicMin(&sBest, static_cast<unsigned long long>(most) << 8 | tid);
+    }
+    __syncthreads();
+    const int halved = int(sBest & 255);
+    int place = 0;
+    if (tid < nseq) {
+        const float cycles = float(chunks) * (rank < halved ? kHalfCycles : kWholeCycles);
+        for (int k = 0; k < nseq; ++k) {
+            const float other = float(sSorted[k]) * (k < halved ? kHalfCycles : kWholeCycles);
+            place += other > cycles || (other == cycles && k < rank);
+        }
+        sCount[place] = quarters ? 4 * HV : rank < halved ? 2 * HV : HV;
+    }
+    __syncthreads();
+    int first = 0;
+    for (int k = 0; k < (tid < nseq ? place : nseq); ++k) first += sCount[k];
+    if (tid < nseq) rows[place] = {tid, rank < halved, first, 0};
+    else if (tid == nseq) rows[nseq] = {-1, 0, first, 0};
+}
+
 __global__ void __launch_bounds__(128, 4)
     prep_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const float* __restrict__ g, const float* __restrict__ beta, const int32_t* __restrict__ starts,
-                int N, int B, int HV, int ratio, int heads, WsView ws) {
+                int N, int B, int HV, int ratio, int heads, int quarters, WsView ws) {
     using P = PrepSmem;
     extern __shared__ __align__(1024) uint8_t sm[];
     float* sG = reinterpret_cast<float*>(sm + P::G);
@@ -245,6 +312,7 @@ __global__ void __launch_bounds__(128, 4)
         prefetch_map(&tmK);
     }
     pdl_wait();
+    if (blockIdx.x == 0 && B <= kMaxRanked) plan_walk(starts, B, HV, quarters, ws.rows);
     // the sequence whose chunk this slot is: the last b with starts[b] / 64 + b <= slot
     int b = -1;
     for (int b0 = 0; b0 < B; b0 += 128) {
@@ -443,7 +511,6 @@ __global__ void __launch_bounds__(128, 4)
 // schedulers.  A warp reads 16 of its lanes at a time with all its threads:
 // thread t has rows t / 4 and t / 4 + 8, columns 2 (t % 4), + 1 of every 8.
 
-constexpr int kMaxRanked = 128;  // sequences that are started by length
 constexpr int WARPS = 8;         // compute warps per chain
 
 enum { CB_X, CB_OU, CB_O2, CB_DS, CB_S, CB_R, CB_U, CB_N };  // a chain's barriers (from CB_S on: its warps arrive)
@@ -453,13 +520,14 @@ enum { PB_QK = 0, PB_QKE = 2, PB_MW = 4, PB_MWE = 6, PB_LO = 8, PB_LOE, PB_N }; 
 //   <32, 1>  one chain: few states, a chunk's latency counts.  U is apart from
 //            R, so that the third part's products need not be over before U
 //            is taken on (16 warps of 8 columns were no faster);
-//   <32, 2>  two chains half a chunk apart, one's products beside the other's
-//            register work;
-//   <64, 2>  all 128 value columns: [Q; K] and [M; W] are read once for all of
-//            a state, and a product is hardly longer for 192 columns than for
-//            96.  What does not fit twice shares its place: R and U the shared
-//            memory of S, o and U the tensor memory of X, [M; W] has one
-//            buffer, and S itself is in tensor memory.
+//   <32, 2>  half a state: two chains half a chunk apart, one's products
+//            beside the other's register work;
+//   <64, 2>  a whole state: [Q; K] and [M; W] are read once for all of it, and
+//            a product is hardly longer for 192 columns than for 96.  What
+//            does not fit twice shares its place: R and U the shared memory
+//            of S, o and U the tensor memory of X, [M; W] has one buffer, and
+//            S itself is in tensor memory.
+// A chunk takes about 3,900, 5,400 to 5,900 and 8,200 cycles in them.
 template <int NV_, int NCH_>
 struct Shape {
     static constexpr int NV = NV_, NCH = NCH_;
@@ -581,27 +649,54 @@ __device__ inline void sum8(uint32_t taddr, uint64_t (&x)[4]) {
                     add2(pack2(b[2 * e], b[2 * e + 1]), pack2(d[2 * e], d[2 * e + 1])));
 }
 
+// This block's place in the plan.
+struct Turn {
+    int seq, halved, index;  // index among the sequence's blocks
+};
+__device__ inline Turn take_turn(const Row* rows, int nseq, int per_seq) {
+    __shared__ Turn sTurn;
+    const int tid = threadIdx.x, item = blockIdx.x;
+    if (nseq > kMaxRanked) return {item / per_seq, 0, item % per_seq};
+    if (tid == 0) sTurn.seq = -1;
+    __syncthreads();
+    if (tid < nseq) {
+        const Row r = rows[tid];
+        if (item >= r.first && item < rows[tid + 1].first) sTurn = {r.seq, r.halved, item - r.first};
+    }
+    __syncthreads();
+    return sTurn;
+}
+
+struct WalkArgs {
+    const __nv_bfloat16* v;
+    const float* S0;
+    float* S_new;
+    const int32_t* starts;
+    int N, B, HV, ratio;
+    float scale;
+    WsView ws;
+};
+
+// Value columns v0 .. v0 + NV NCH - 1 of head h of sequence b.
 template <typename P, typename OutT>
-__global__ void __launch_bounds__(32 * ((WARPS + 1) * P::NCH + 1), 1)
-    walk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                const __nv_bfloat16* __restrict__ v, const float* S0, float* S_new,
-                const int32_t* __restrict__ starts, OutT* __restrict__ o, int N, int HV, int ratio, float scale,
-                WsView ws) {
+__device__ __forceinline__ void walk(const CUtensorMap& tmQ, const CUtensorMap& tmK, const WalkArgs& args, OutT* o,
+                                     int b, int h, int v0, uint8_t* sm) {
+    const __nv_bfloat16* const v = args.v;
+    const float* const S0 = args.S0;
+    float* const S_new = args.S_new;
+    const int N = args.N, HV = args.HV, ratio = args.ratio;
+    const float scale = args.scale;
+    const WsView& ws = args.ws;
     constexpr int NV = P::NV, NCH = P::NCH, HN = P::HN;
     constexpr uint32_t kCols = 512;
     constexpr int kComputeWarps = WARPS * NCH;
-    extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t* pb = reinterpret_cast<uint64_t*>(sm + P::BAR);
     uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + P::SLOT);
-    int* sSeq = reinterpret_cast<int*>(sm + P::SLOT + 4);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int SPLITS = D / (NV * NCH);
-    const int h = blockIdx.x / SPLITS, v0 = (blockIdx.x - h * SPLITS) * NV * NCH;
 
     if (tid == 0) {
         prefetch_map(&tmQ);
         prefetch_map(&tmK);
-        *sSeq = blockIdx.y;
         for (int i = 0; i < PB_N; ++i)
             mbar_init(&pb[i], (i >= PB_QKE && i < PB_MW) || (i >= PB_MWE && i < PB_LO) || i == PB_LOE ? NCH : 1);
         for (int c = 0; c < NCH; ++c)
@@ -616,33 +711,12 @@ __global__ void __launch_bounds__(32 * ((WARPS + 1) * P::NCH + 1), 1)
     }
     __syncthreads();
     tc_fence_after();
-    // This kernel starts after the first launch has waited for everything
-    // before it, so that only the workspace has to be waited for.
-    // The longest sequences start first (they end last): this block takes
-    // the one of its rank.  Every block ranks all sequences, so not for many.
-    const int nseq = gridDim.y;
-    if (nseq > 1 && nseq <= kMaxRanked) {
-        for (int j = tid; j < nseq; j += blockDim.x) {
-            const int len = starts[j + 1] - starts[j];
-            int rank = 0;
-            for (int k = 0; k < nseq; ++k) {
-                const int other = starts[k + 1] - starts[k];
-                rank += other > len || (other == len && k < j);
-            }
-            if (rank == blockIdx.y) *sSeq = j;
-        }
-        __syncthreads();
-    }
-    const int b = *sSeq;
     int lo, hi, bad = 0;
-    sequence(starts, b, N, lo, hi, &bad);
+    sequence(args.starts, b, N, lo, hi, &bad);
     const int nc = (hi - lo + C - 1) / C;
     const size_t slot0 = size_t(lo / C) + b;
     bool ok = true;
-    if (warp >= kComputeWarps) {
-        pdl_wait();
-        pdl_trigger();
-    }
+    pdl_trigger();  // after the wait and the allocation
 
     if (warp == kComputeWarps + NCH) {
         // ---- copies -----------------------------------------------------------
@@ -777,9 +851,7 @@ __global__ void __launch_bounds__(32 * ((WARPS + 1) * P::NCH + 1), 1)
             if (P::TIGHT) tmem_put8(taddr + P::TS + 8 * g, x);
         }
         if (P::TIGHT) tmem_wait_st();
-        pdl_wait();
-        pdl_trigger();
-        if (bad && tid == 0 && blockIdx.x == 0) raise_err(ws.err, bad);
+        if (bad && tid == 0) raise_err(ws.err, bad);
 
         // chunk t's values and gates for this thread's tokens, one chunk ahead
         constexpr int G8 = HN / 8, NP = 2 * G8;  // column pairs per row, and in all
@@ -953,17 +1025,46 @@ __global__ void __launch_bounds__(32 * ((WARPS + 1) * P::NCH + 1), 1)
     }
 }
 
-template <typename P, typename OutT>
-cudaError_t launch_walk(const CUtensorMap& mq, const CUtensorMap& mk, const void* v, const float* S0, float* S_new,
-                        const int32_t* starts, void* o, int N, int B, int H, int HV, float scale, const WsView& ws,
+template <typename OutT>
+__global__ void __launch_bounds__(32 * (WARPS + 2), 1)
+    walk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, const WalkArgs args,
+                OutT* __restrict__ o) {
+    extern __shared__ __align__(1024) uint8_t sm[];
+    pdl_wait();
+    const Turn turn = take_turn(args.ws.rows, args.B, 4 * args.HV);
+    walk<Shape<32, 1>>(tmQ, tmK, args, o, turn.seq, turn.index >> 2, (turn.index & 3) * 32, sm);
+}
+
+template <typename OutT>
+__global__ void __launch_bounds__(32 * (2 * WARPS + 3), 1)
+    walk_many_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                     const WalkArgs args, OutT* __restrict__ o) {
+    extern __shared__ __align__(1024) uint8_t sm[];
+    pdl_wait();
+    const Turn turn = take_turn(args.ws.rows, args.B, args.HV);
+    if (turn.seq < 0) return;  // fewer walks than there might be
+    if (turn.halved) walk<Shape<32, 2>>(tmQ, tmK, args, o, turn.seq, turn.index >> 1, (turn.index & 1) * 64, sm);
+    else walk<Shape<64, 2>>(tmQ, tmK, args, o, turn.seq, turn.index, 0, sm);
+}
+
+template <typename OutT>
+cudaError_t launch_walk(bool many, const CUtensorMap& mq, const CUtensorMap& mk, const WalkArgs& args, OutT* o,
                         cudaStream_t st) {
-    static const cudaError_t attr =
-        cudaFuncSetAttribute(walk_kernel<P, OutT>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::TOTAL);
+    constexpr int one = Shape<32, 1>::TOTAL,
+                  two = Shape<32, 2>::TOTAL > Shape<64, 2>::TOTAL ? Shape<32, 2>::TOTAL : Shape<64, 2>::TOTAL;
+    static const cudaError_t attr = [] {
+        const cudaError_t e =
+            cudaFuncSetAttribute(walk_kernel<OutT>, cudaFuncAttributeMaxDynamicSharedMemorySize, one);
+        return e != cudaSuccess ? e
+                                : cudaFuncSetAttribute(walk_many_kernel<OutT>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, two);
+    }();
     if (attr != cudaSuccess) return attr;
-    return launch_pdl(walk_kernel<P, OutT>, dim3(HV * (D / (P::NV * P::NCH)), B),
-                      dim3(32 * ((WARPS + 1) * P::NCH + 1)), P::TOTAL, st, mq, mk,
-                      static_cast<const __nv_bfloat16*>(v), S0, S_new, starts, static_cast<OutT*>(o), N, HV, HV / H,
-                      scale, ws);
+    const unsigned states = unsigned(args.B) * args.HV;
+    if (many)
+        return launch_pdl(walk_many_kernel<OutT>, dim3(states + (args.B <= kMaxRanked ? min(args.B, kMaxHalved) * args.HV : 0)),
+                          dim3(32 * (2 * WARPS + 3)), two, st, mq, mk, args, o);
+    return launch_pdl(walk_kernel<OutT>, dim3(states * 4), dim3(32 * (WARPS + 2)), one, st, mq, mk, args, o);
 }
 
 }  // namespace pfc
@@ -973,18 +1074,17 @@ cudaError_t launch_walk(const CUtensorMap& mq, const CUtensorMap& mk, const void
 // pairs of 16 key heads 92 us alone and 85 us in twos, with 16,640 327 and 296.
 constexpr size_t kPairFrom = 2432;
 
-// The walk's shape by the number of states (sequences times value heads): by
-// the blocks that it makes of them for 152 SMs and a chunk's time in each,
-// 3,900, 5,400 and 8,200 cycles.  Several sequences are uneven as a rule and
-// take as long as the longest, so that the shorter chunk counts for more.
-// Measured with 1 to 32 sequences of 2,048 tokens, even and uneven, in us:
-// 48 states of 3 sequences 167/183/146/159 in one chain, 131/243/192/210 in
-// two (of one sequence 164 and 128), 128 states 329 and 300 on average, 256
-// states 517 in two chains and 486 in two wide ones, 512 states 948 and 858.
-int walk_shape(int B, int HV) {
-    const size_t states = size_t(B) * HV;
-    return states <= (B == 1 ? 38 : 100) ? 0 : states <= (B == 1 ? 110 : 220) ? 1 : 2;
-}
+// States (sequences times value heads) from which the walk takes them in
+// halves and whole rather than in quarters: one sequence fills the SMs in
+// quarters with 38; several are uneven as a rule and wait for the longest,
+// which quarters walk fastest.  Measured with sequences of 2,048 tokens on
+// average, one even and three uneven batches, in us, quarters against the
+// rest: 48 states of three 169/185/147/160 and 136/254/200/218, 96 states
+// 260/236/249/243 and 217/281/226/249, 128 states 342/308/324/339 and
+// 236/386/294/277, 256 states 609/594/611/609 and 453/503/456/475.  (Before
+// halves and wholes were mixed, 256 states took 527 whole and 560 in halves,
+// uneven.)
+bool many_states(int B, int HV) { return size_t(B) * HV > (B == 1 ? 38 : 100); }
 
 size_t prefill_chunk_ws_bytes(int N, int B, int HV) { return pfc::ws_bytes(N, B, HV); }
 
@@ -1002,21 +1102,15 @@ cudaError_t launch_prefill_chunk(const void* q, const void* k, const void* v, co
     if (attr != cudaSuccess) return attr;
     // Two value heads of one key head share a block, its [Q; K] and their
     // product, where there are many blocks all the same.
+    const bool many = many_states(B, HV);
     const size_t pairs = pfc::slot_count(N, B) * HV;
     const int heads = (HV / H) % 2 == 0 && pairs >= kPairFrom ? 2 : 1;
     const cudaError_t e = launch_pdl(pfc::prep_kernel, dim3(unsigned(pairs / heads)), dim3(128), smem, st, pq, pk, g,
-                                     beta, starts, N, B, HV, HV / H, heads, ws);
+                                     beta, starts, N, B, HV, HV / H, heads, !many, ws);
     if (e != cudaSuccess) return e;
-    auto walk = [&](auto shape) {
-        using P = decltype(shape);
-        return o_bf16 ? pfc::launch_walk<P, __nv_bfloat16>(mq, mk, v, S0, S_new, starts, o, N, B, H, HV, scale, ws, st)
-                      : pfc::launch_walk<P, float>(mq, mk, v, S0, S_new, starts, o, N, B, H, HV, scale, ws, st);
-    };
-    switch (walk_shape(B, HV)) {
-        case 0: return walk(pfc::Shape<32, 1>());
-        case 1: return walk(pfc::Shape<32, 2>());
-        default: return walk(pfc::Shape<64, 2>());
-    }
+    const pfc::WalkArgs args = {static_cast<const __nv_bfloat16*>(v), S0, S_new, starts, N, B, HV, HV / H, scale, ws};
+    return o_bf16 ? pfc::launch_walk(many, mq, mk, args, static_cast<__nv_bfloat16*>(o), st)
+                  : pfc::launch_walk(many, mq, mk, args, static_cast<float*>(o), st);
 }
 
 }  // namespace canopy

@@ -254,7 +254,8 @@ typedef enum {
 } canopy_prefill_plan_t;
 
 /* Size in bytes of the workspace of a prefill over N packed tokens of B
- * sequences with HV value heads: the device error word (offset 0), and per
+ * sequences with HV value heads: the device error word (offset 0), the order
+ * of the sequences (2 KiB), and per
  * 64-token chunk and value head 48 KiB of chunk operands and 768 bytes of
  * gates.  At most floor(N / 64) + B chunks.  Zero it once with
  * canopy_workspace_init (the error word; the rest is scratch), read the

@@ -2,7 +2,9 @@
 
 Each .cu under csrc/ compiles to an object in parallel; the objects link into
 ``libcanopy.so`` next to this file (CUDA runtime linked statically, no torch).
-Rebuilds only when a source or header is newer than the library.
+Beside it ``_marshal.so``, the native side of the Python binding's short calls
+(marshal.cpp: host code, against torch, without the library).  Rebuilds only
+when a source or header is newer than either.
 """
 
 from __future__ import annotations
@@ -12,6 +14,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
@@ -19,6 +22,7 @@ ROOT = os.path.dirname(PKG)
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcanopy.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
@@ -37,11 +41,32 @@ def sources():
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
         return True
-    t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
+    deps = sources() + [d for pattern in (os.path.join(CSRC, "*.cpp"), os.path.join(CSRC, "*.cuh"),
+                                          os.path.join(INCLUDE, "*.h")) for d in glob.glob(pattern)]
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _build_marshal(nvcc: str) -> None:
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        raise RuntimeError("g++ not found: it builds the Python binding's native side")
+    inc = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")]
+    tmp = MARSHAL + ".tmp"
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={abi}", *[f"-I{d}" for d in inc],
+           os.path.join(CSRC, "marshal.cpp"), "-o", tmp, "-L" + os.path.join(root, "lib"),
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on marshal.cpp:\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
@@ -61,8 +86,10 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
             print(r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 2)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(12, os.cpu_count() or 2)) as ex:
+        marshal = ex.submit(_build_marshal, nvcc)
         objs = list(ex.map(compile_one, sources()))
+        marshal.result()
     tmp = LIB + ".tmp"
     r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:

@@ -1,7 +1,10 @@
 """Thin ctypes binding of libcanopy.so (include/canopy.h).
 
 Argument marshalling only: every step of the path runs in the library's
-CUDA kernels.  Tensors are torch CUDA tensors (torch provides device memory
+CUDA kernels.  (The calls of a few microseconds, step, prefill and accept, go
+through the native _marshal.so, which checks their arguments, allocates their
+outputs and makes the call; the Python code here is for what it turns down.)
+Tensors are torch CUDA tensors (torch provides device memory
 and the current stream); the calls are enqueued on
 ``torch.cuda.current_stream()`` and return without synchronising.  If the
 library has not been built, loading fails loudly: there is no fallback.
@@ -64,6 +67,7 @@ SIGNATURES = {
 }
 
 _lib = None
+_marshal = None
 
 
 class CanopyError(RuntimeError):
@@ -72,17 +76,32 @@ class CanopyError(RuntimeError):
 
 def load(path: str = LIB_PATH):
     """Load the shared library (no CUDA call is made by loading)."""
-    global _lib
+    global _lib, _marshal
     if _lib is None:
         if not os.path.exists(path):
             raise CanopyError(f"{path} is missing: build it with gated_deltanet_linear_tree_gb300.build.build()")
+        try:
+            from . import _marshal as marshal
+        except ImportError as e:
+            raise CanopyError(f"_marshal.so does not load ({e}): build it with "
+                              "gated_deltanet_linear_tree_gb300.build.build()") from e
         lib = ctypes.CDLL(path)
         for name, (res, args) in SIGNATURES.items():
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args
-        _lib = lib
+        marshal.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.canopy_step, lib.canopy_prefill, lib.canopy_prefill_workspace_bytes, lib.canopy_accept)),
+            torch.bfloat16, torch.float32)
+        _lib, _marshal = lib, marshal
     return _lib
+
+
+def _short_call(name: str, r):
+    """A native call's outputs, or its status raised."""
+    if r.__class__ is int:
+        _check(r, name)
+    return r
 
 
 def _check(status: int, what: str):
@@ -286,16 +305,10 @@ def serial_replay_static(q, k, v, g, beta, S0, parent, err=None, o_dtype=torch.f
 
 
 def _need_all(dev: int, *specs):
-    """_need for (tensor, name, dtype, shape) specs, all on device `dev`; the
-    calls of a few microseconds below check a tensor in one expression and
-    come to _need for its message only where that fails."""
+    """_need for (tensor, name, dtype, shape) specs, all on device `dev`."""
     for t, name, dtype, shape in specs:
-        try:
-            good = (t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous())
-        except AttributeError:
-            good = False
-        if dev < 0 or not good:
-            _need(t, name, dtype, shape)
+        _need(t, name, dtype, shape)
+        if t.get_device() != dev:
             raise CanopyError(f"{name} must be on the same device as the other tensors")
 
 
@@ -339,6 +352,11 @@ def prefill(q, k, v, g, beta, S0, starts, ws, o_dtype=torch.float32, out=None, S
     None for zero states).  S_out may be S0.  ws: prefill_workspace for at
     least these sizes.  force: None (the library's dispatch), "scan" or
     "chunked" (bf16, d = 128)."""
+    if _marshal is None:
+        load()
+    r = _marshal.prefill(q, k, v, g, beta, S0, starts, ws, o_dtype, out, S_out, scale, PREFILL_FORCE[force])
+    if r is not None:
+        return _short_call("canopy_prefill", r)
     N, H, HV, dk, dv = _heads3(q, v)
     if not isinstance(starts, torch.Tensor) or starts.dim() != 1 or starts.shape[0] < 2:
         raise CanopyError("starts must have shape (B + 1,)")
@@ -379,6 +397,11 @@ def step(q, k, v, g, beta, S, o_dtype=torch.float32, out=None, S_out=None, scale
     q, k [B, H, dk]; v [B, HV, dv]; g, beta fp32 [B, HV]; S fp32
     [B, HV, dv, dk].  S_out may be S (in place).  err: an optional int32 CUDA
     tensor of one element that receives device error bits (OR-ed)."""
+    if _marshal is None:
+        load()
+    r = _marshal.step(q, k, v, g, beta, S, o_dtype, out, S_out, scale, err)
+    if r is not None:
+        return _short_call("canopy_step", r)
     B, H, HV, dk, dv = _heads3(q, v)
     state = (B, HV, dv, dk)
     dt, f32, dev = q.dtype, torch.float32, q.get_device()
@@ -411,6 +434,11 @@ def accept(p, tokens, parent, u, noise, q=None, lengths=None, err=None):
     [B, T] uniform in [0, 1); noise fp32 [B, V] exponential variates.
     out_tokens: the accepted tokens in path order, the next token after them,
     then -1; counts: how many; accepted is what commit and conv_commit take."""
+    if _marshal is None:
+        load()
+    r = _marshal.accept(p, tokens, parent, u, noise, q, lengths, err)
+    if r is not None:
+        return _short_call("canopy_accept", r)
     if not isinstance(p, torch.Tensor) or p.dim() != 3:
         raise CanopyError("p must have shape (B, T, V)")
     B, T, V = p.shape

@@ -370,6 +370,43 @@ def test_refusals(lib):
                    torch.zeros(1, 257, device="cuda"), torch.ones(1, 4, device="cuda"))
 
 
+def test_native_and_python_marshalling_agree(lib, monkeypatch):
+    """The native side's calls and the Python side's give the same results,
+    with given outputs and without; what the native side turns down (a whole
+    number for scale) the Python side takes; a size that the library refuses
+    raises from either."""
+    x = sc.to_cuda(sc.layer_inputs([40, 30], 2, 4, 128, True, seed=3), True)
+    a = {n: v if v is None else torch.from_numpy(v).cuda() for n, v in sc.accept_inputs(2, 9, 200, seed=3).items()}
+    ws = lib.prefill_workspace(70, 2, 4, 128)
+    one = [x[n][:2].contiguous() for n in ("q", "k", "v", "g", "beta")]
+    layer = [x[n] for n in ("q", "k", "v", "g", "beta")]
+    odd = torch.zeros(2, 4, 64, device="cuda")
+
+    def calls(scale):
+        out = []
+        given = torch.empty(2, 4, 128, device="cuda", dtype=torch.bfloat16)
+        for kw in (dict(), dict(out=given, S_out=torch.empty_like(x["S0"])), dict(o_dtype=torch.bfloat16)):
+            out += lib.step(*one, x["S0"], scale=scale, **kw)
+        assert out[2].data_ptr() == given.data_ptr()
+        out += lib.prefill(*layer, x["S0"], x["starts"], ws, scale=scale)
+        out += lib.prefill(*layer, None, x["starts"], ws, scale=scale, o_dtype=torch.bfloat16,
+                           S_out=torch.empty_like(x["S0"]), force="scan")
+        out += lib.accept(a["p"], a["tokens"], a["parent"], a["u"], a["noise"], q=a["q"])
+        with pytest.raises(lib.CanopyError, match="unsupported"):
+            lib.step(odd, odd, odd, torch.ones(2, 4, device="cuda"), torch.ones(2, 4, device="cuda"),
+                     torch.zeros(2, 4, 64, 64, device="cuda"))
+        return out
+
+    lib.load()
+    assert lib._marshal.step(*one, x["S0"], torch.float32, None, None, 2, None) is None
+    native, mixed = calls(2.0), calls(2)
+    stub = type("Stub", (), {n: staticmethod(lambda *args: None) for n in ("step", "prefill", "accept")})
+    monkeypatch.setattr(lib, "_marshal", stub)
+    python = calls(2.0)
+    for y in (mixed, python):
+        assert len(y) == len(native) and all(torch.equal(s, t) and s.dtype == t.dtype for s, t in zip(native, y))
+
+
 def test_abi_argument_errors(lib):
     """Refused on the host before any CUDA call: the pointers are never followed."""
     L = lib.load()

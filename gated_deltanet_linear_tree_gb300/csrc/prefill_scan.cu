@@ -13,9 +13,9 @@
 //
 // Bound by instruction issue and, with several CTAs on an SM, by the reads of
 // k and q from shared memory, which every group of eight lanes repeats:
-// 0.18 us a token for one fp32 sequence of 16 heads (256 tokens: 45 us), 96 us
-// for four of 600 tokens together, the longest of 414.  Sixteen lanes per row
-// were 20 % slower throughout.
+// 0.16 us a token for one sequence of 16 heads (256 tokens: 42.5 us), 96 us
+// for four fp32 ones of 600 tokens together, the longest of 414.  Sixteen
+// lanes per row were 20 % slower throughout.
 #include "common.cuh"
 
 namespace canopy {
@@ -35,12 +35,30 @@ __device__ inline void sequence(const int32_t* starts, int b, int N, int& lo, in
     if (s0 != lo || s1 != hi) *bad |= CANOPY_DEVERR_LENGTH;
 }
 
+// Four elements as they are in memory, and as fp32.
+template <typename InT>
+struct Four {
+    using type = float4;
+};
+template <>
+struct Four<__nv_bfloat16> {
+    using type = uint2;
+};
+__device__ inline float4 to_f4(float4 x) { return x; }
+__device__ inline float4 to_f4(uint2 x) {
+    return make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xFFFF0000u), __uint_as_float(x.y << 16),
+                       __uint_as_float(x.y & 0xFFFF0000u));
+}
+
+// (the bound of four blocks is for the register count, 128: with fewer the
+// loop's reads are not moved ahead, 56 us instead of 43 for 256 bf16 tokens)
 template <typename InT, typename OutT, int D>
-__global__ void __launch_bounds__(NT) scan_kernel(const InT* __restrict__ q, const InT* __restrict__ k,
+__global__ void __launch_bounds__(NT, 4) scan_kernel(const InT* __restrict__ q, const InT* __restrict__ k,
                                                   const InT* __restrict__ v, const float* __restrict__ g,
                                                   const float* __restrict__ beta, const float* S0, float* S_new,
                                                   const int32_t* __restrict__ starts, OutT* __restrict__ o, int N,
                                                   int HV, int ratio, float scale, int32_t* __restrict__ err) {
+    using Raw4 = typename Four<InT>::type;
     constexpr int C4 = D / 32;             // float4 chunks per lane
     constexpr int PER = TB * D / 4 / NT;   // float4 chunks of a block's q (and k) per thread
     static_assert(PER >= 1 && TB * ROWS / NT == 2, "staging");
@@ -61,34 +79,33 @@ __global__ void __launch_bounds__(NT) scan_kernel(const InT* __restrict__ q, con
     for (int c = 0; c < C4; ++c)
         s[c] = S0 ? *reinterpret_cast<const float4*>(S0 + at + (c * 8 + gl) * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
 
-    float4 nq[PER], nk[PER];
-    float nv[2], ng = 1.f, nb = 0.f;
-    auto fetch = [&](int n0) {  // the block from token n0 into registers; tokens past the end are not read
+    // The block from token n0 into registers, as it is: whatever looks at a
+    // value (the conversion to fp32, the check of a gate) waits for its load,
+    // so that comes a block later.  Tokens past the end are not read.
+    Raw4 nq[PER], nk[PER];
+    InT nv[2];
+    float ng, nb;
+    auto fetch = [&](int n0) {
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
             const int i = t + e * NT, n = n0 + i / (D / 4), c = i % (D / 4);
-            nq[e] = nk[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            nq[e] = nk[e] = Raw4{};
             if (n < hi) {
                 const size_t p = (size_t(n) * H + hk) * D + c * 4;
-                nq[e] = load4(q + p);
-                nk[e] = load4(k + p);
+                nq[e] = __ldg(reinterpret_cast<const Raw4*>(q + p));
+                nk[e] = __ldg(reinterpret_cast<const Raw4*>(k + p));
             }
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int i = t + e * NT, n = n0 + i / ROWS;
-            nv[e] = n < hi ? to_f(v[(size_t(n) * HV + h) * D + r0 + i % ROWS]) : 0.f;
+            nv[e] = n < hi ? v[(size_t(n) * HV + h) * D + r0 + i % ROWS] : InT(0.f);
         }
         ng = 1.f;
         nb = 0.f;
         if (t < TB && n0 + t < hi) {
             ng = g[size_t(n0 + t) * HV + h];
             nb = beta[size_t(n0 + t) * HV + h];
-            if (!gate_ok(ng, nb)) {
-                bad |= CANOPY_DEVERR_GATE;
-                ng = 1.f;
-                nb = 0.f;
-            }
         }
     };
     if (lo < hi) fetch(lo);
@@ -97,12 +114,19 @@ __global__ void __launch_bounds__(NT) scan_kernel(const InT* __restrict__ q, con
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
             const int i = t + e * NT;
-            sQ[buf][i / (D / 4)][i % (D / 4)] = nq[e];
-            sK[buf][i / (D / 4)][i % (D / 4)] = nk[e];
+            sQ[buf][i / (D / 4)][i % (D / 4)] = to_f4(nq[e]);
+            sK[buf][i / (D / 4)][i % (D / 4)] = to_f4(nk[e]);
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) sV[buf][(t + e * NT) / ROWS][(t + e * NT) % ROWS] = nv[e];
-        if (t < TB) sGB[buf][t] = make_float2(ng, nb);
+        for (int e = 0; e < 2; ++e) sV[buf][(t + e * NT) / ROWS][(t + e * NT) % ROWS] = to_f(nv[e]);
+        if (t < TB) {
+            if (!gate_ok(ng, nb)) {
+                bad |= CANOPY_DEVERR_GATE;
+                ng = 1.f;
+                nb = 0.f;
+            }
+            sGB[buf][t] = make_float2(ng, nb);
+        }
         // (the other buffer's readers are past it: they have met here since)
         __syncthreads();
         if (n0 + TB < hi) fetch(n0 + TB);

@@ -23,9 +23,11 @@ def test_prefill_plan(canopy):
     plan = canopy.prefill_plan
     assert plan(16384, 1, 16, 32, True, 128) == "chunked"
     assert plan(37, 1, 16, 16, True, 128) == "scan"
-    assert plan(40, 1, 16, 16, True, 128) == "chunked"
-    assert plan(16 * 64, 64, 16, 32, True, 128) == "chunked"
-    assert plan(15 * 64, 64, 16, 32, True, 128) == "scan"
+    assert plan(64, 1, 16, 16, True, 128) == "chunked"
+    assert plan(39, 1, 16, 32, True, 128) == "scan"
+    assert plan(40, 1, 16, 32, True, 128) == "chunked"
+    assert plan(18 * 64, 64, 16, 32, True, 128) == "chunked"
+    assert plan(17 * 64, 64, 16, 32, True, 128) == "scan"
     assert plan(16384, 1, 16, 32, False, 128) == "scan"
     assert plan(16384, 1, 16, 32, True, 32) == "scan"
     assert plan(3, 1, 16, 32, True, 128, force="chunked") == "chunked"

@@ -26,8 +26,8 @@
 // itself stays in fp32 registers across chunks.
 //
 // Measured (32 value heads of 16 key heads, both launches in a loop): one
-// sequence of 16,384 tokens 660 us, of which the walk 510; sixteen of 8,191
-// together 236 (85 and 150); eight of 32,768 together 860 to 1,110, by how
+// sequence of 16,384 tokens 652 us, of which the walk 510; sixteen of 8,191
+// together 229 (81 and 150); eight of 32,768 together 845 to 1,090, by how
 // uneven they are.  The first launch is held by the shared-memory and fp32
 // pipes, the walk by the latency of its three products a chunk.
 //
@@ -162,39 +162,46 @@ __device__ inline void bulk_store(void* dst, const void* src, uint32_t bytes) {
 // M, W and the gates of one (chunk, value head): 128 threads, a row of
 // [C; I] each.
 //
-// Decays are running products of the gates, from the row's own token back:
-// each is one multiplication from the last (an error of 2^-24 a step, as
-// near as logs and their differences come) and underflows to zero quietly.
+// Decays are products of the gates, no logs (an error of 2^-24 a step, as near
+// as logs and their differences come), and underflow to zero quietly: running
+// products from the row's own token back in the 32 columns of its own half;
+// before those, the product up to there times that from the column to the end
+// of its 16 (formed once per head).
 //
 // The substitution x (I + G) = x0 goes by halves of 32 columns, with
 // G = [G00 0; G10 G11]:  x1 (I + G11) = x0_1,  x0 (I + G00) = x0_0 - x1 G10.
+// Rows of the first 32 tokens have no x1: their threads take half the columns
+// of x1 G10 for the row 32 tokens on.
 // All threads read the same row of G at a time.  The kernel's shared memory
 // is one array at a fixed, aligned place, so that these addresses are
-// constants: a 128-bit read at a constant address is one pass of the
+// constants, or uniform: a 128-bit read at such an address is one pass of the
 // shared-memory pipe, at an address in a register it is four, even where all
-// threads give the same one (measured: 7,100 cycles per block with four
-// blocks on the SM, bound by that pipe).
+// threads give the same one (measured: 18,000 cycles of substitution per block
+// with four blocks on the SM, now 7,500).
 
 struct PrepSmem {
     static constexpr int QK = 0;                     // later the [M; W] image, over all that follows up to GATE
-    static constexpr int P = 68, PW = 36;            // row pitches in floats (no two rows of a store on one bank)
+    static constexpr int P = 68, PW = 52;            // row pitches in floats (no two rows of a store on one bank)
     static constexpr int ROWC = QK;                  // float [64][P]: rows of C, then x1 of M (over Q and K)
-    static constexpr int ROWW = ROWC + C * P * 4;    // float [64][PW]: x1 of W
+    static constexpr int ROWW = ROWC + C * P * 4;    // float [64][PW]: x1 of W, and 16 sums
     static constexpr int G = QK + QK_BYTES;          // float [64][P]
     static constexpr int GATE = G + C * P * 4;       // float [2][64]: g of each head
     static constexpr int BE = GATE + 2 * C * 4;      // float [2][64]: beta
-    static constexpr int BAR = BE + 2 * C * 4;       // u64 [2]
+    static constexpr int TAIL = BE + 2 * C * 4;      // float [2][64]: the decay from each token to the end of its 16
+    static constexpr int ALL = TAIL + 2 * C * 4;     // float [2][4]: the decay over each 16 tokens
+    static constexpr int BAR = ALL + 2 * 4 * 4;      // u64 [2]
     static constexpr int SLOT = BAR + 16;
     static constexpr int TOTAL = SLOT + 8;
     static_assert(BAR % 8 == 0 && GATE >= MW_BYTES && ROWW + C * PW * 4 <= G, "layout");
     static_assert(TOTAL + 1024 <= 56 * 1024, "four blocks per SM");
 };
 
-// x (I + G) = x0 for 32 columns, from the last one down: x[j] -= x[i] G[i][j]
+// x (I + G) = x0 for W columns, from the last one down: x[j] -= x[i] G[i][j]
 // for j < i, two columns per instruction; G's rows are P floats apart.
-__device__ inline void solve32(uint64_t (&x)[16], const float* G) {
+template <int W>
+__device__ inline void solve(uint64_t (&x)[W / 2], const float* G) {
 #pragma unroll
-    for (int i = 31; i >= 1; --i) {
+    for (int i = W - 1; i >= 1; --i) {
         const float2 x2 = unpack2(x[i / 2]);
         const float xi = -((i & 1) ? x2.y : x2.x);
         const uint64_t xx = pack2(xi, xi);
@@ -206,6 +213,48 @@ __device__ inline void solve32(uint64_t (&x)[16], const float* G) {
             if (4 * j4 + 2 < i) x[2 * j4 + 1] = fma2(xx, g.y, x[2 * j4 + 1]);
         }
     }
+}
+
+// z -= y G for 16 columns and the rows of G that y[0 .. 3] belong to.
+__device__ inline void take4(uint64_t (&z)[8], const float (&y)[4], const float* G) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const uint64_t yy = pack2(-y[u], -y[u]);
+        const ulonglong2* row = reinterpret_cast<const ulonglong2*>(G + u * PrepSmem::P);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const ulonglong2 g = row[j];
+            z[2 * j] = fma2(yy, g.x, z[2 * j]);
+            z[2 * j + 1] = fma2(yy, g.y, z[2 * j + 1]);
+        }
+    }
+}
+// The same for 32 rows, y in shared memory.  Not unrolled: G's addresses stay
+// uniform, and with the loop's 800 instructions in line four blocks at
+// different places took 9 % of their instructions from beyond the SM's cache,
+// 4 % without (the launch for 32,768 tokens 296 against 283 us).
+__device__ inline void take32(uint64_t (&z)[8], const float* y, const float* G) {
+#pragma unroll 1
+    for (int k = 0; k < 32; k += 4) {
+        const float4 y4 = *reinterpret_cast<const float4*>(y + k);
+        const float yy[4] = {y4.x, y4.y, y4.z, y4.w};
+        take4(z, yy, G + k * PrepSmem::P);
+    }
+}
+
+template <int V>
+__device__ inline void read_row(uint64_t (&x)[V], const float* p) {
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) {
+        const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(p + 4 * j);
+        x[2 * j] = y.x;
+        x[2 * j + 1] = y.y;
+    }
+}
+template <int V>
+__device__ inline void write_row(float* p, const uint64_t (&x)[V]) {
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) *reinterpret_cast<ulonglong2*>(p + 4 * j) = make_ulonglong2(x[2 * j], x[2 * j + 1]);
 }
 
 // The same with the first two parts rounded (ties away), so that they alone
@@ -301,6 +350,8 @@ __global__ void __launch_bounds__(128, 4)
     float* sG = reinterpret_cast<float*>(sm + P::G);
     float* sGate = reinterpret_cast<float*>(sm + P::GATE);
     float* sBe = reinterpret_cast<float*>(sm + P::BE);
+    float* sTail = reinterpret_cast<float*>(sm + P::TAIL);
+    float* sAll = reinterpret_cast<float*>(sm + P::ALL);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + P::BAR);
     uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + P::SLOT);
     const int tid = threadIdx.x, warp = tid >> 5;
@@ -363,6 +414,15 @@ __global__ void __launch_bounds__(128, 4)
         }
         sGate[tid] = a;
         sBe[tid] = be;
+        const int n16 = n & 15;
+#pragma unroll
+        for (int step = 1; step < 16; step *= 2) {  // a: g of this token and those after it in its 16
+            const float y = __shfl_down_sync(0xffffffffu, a, step, 16);
+            if (n16 + step < 16) a *= y;
+        }
+        const float y = __shfl_down_sync(0xffffffffu, a, 1, 16);
+        sTail[tid] = n16 < 15 ? y : 1.f;
+        if (n16 == 0) sAll[tid >> 4] = a;
     }
     if (bad) raise_err(ws.err, bad);
     __syncthreads();
@@ -393,12 +453,12 @@ __global__ void __launch_bounds__(128, 4)
 #pragma unroll 1
         for (int hh = 0; hh < heads; ++hh) {
             const size_t at = size_t(slot) * HV + h + hh;
-            const float* gate = sGate + hh * C;
+            const float *gate = sGate + hh * C, *tail = sTail + hh * C, *all = sAll + hh * 4;
             float* rowp = (krow ? sG : reinterpret_cast<float*>(sm + P::ROWC)) + i * P::P;
             float d = krow ? sBe[hh * C + i] : 1.f;  // beta g_{j+1} .. g_i
-            float end = 1.f;                         // g_{i+1} .. g_63
+            const int own = i >= 32 ? 2 : 0;         // the row's half begins at 16 tokens times this
 #pragma unroll 1
-            for (int kb = 3; kb >= 0; --kb) {
+            for (int kb = own + 1; kb >= own; --kb) {
                 uint32_t a[16];
                 tmem_ld16(tmem + (uint32_t(warp * 32) << 16) + ((16 * kb) ^ flip), a);
                 tmem_wait_ld();
@@ -413,69 +473,85 @@ __global__ void __launch_bounds__(128, 4)
                     for (int u = 3; u >= 0; --u) {
                         y[u] = 4 * u4 + u <= lim ? d * __uint_as_float(a[4 * u4 + u]) : 0.f;
                         if (4 * u4 + u <= last) d *= gg[u];
-                        else end *= gg[u];
                     }
                     *reinterpret_cast<float4*>(rowp + 16 * kb + 4 * u4) = make_float4(y[0], y[1], y[2], y[3]);
                 }
             }
+            // In the half before the row's own, every column is before the row.
+            // (The half after it is not read.)
+#pragma unroll 1
+            for (int kb = own - 1; kb >= 0; --kb) {
+                uint32_t a[16];
+                tmem_ld16(tmem + (uint32_t(warp * 32) << 16) + ((16 * kb) ^ flip), a);
+                tmem_wait_ld();
+#pragma unroll
+                for (int u4 = 0; u4 < 4; ++u4) {
+                    const float4 t4 = *reinterpret_cast<const float4*>(tail + 16 * kb + 4 * u4);
+                    const float tt[4] = {t4.x, t4.y, t4.z, t4.w};
+                    float y[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) y[u] = live ? d * tt[u] * __uint_as_float(a[4 * u4 + u]) : 0.f;
+                    *reinterpret_cast<float4*>(rowp + 16 * kb + 4 * u4) = make_float4(y[0], y[1], y[2], y[3]);
+                }
+                d *= all[kb];
+            }
+            float end = tail[i];  // g_{i+1} .. g_63
+#pragma unroll
+            for (int m = 1; m < 4; ++m)
+                if (16 * m > i) end *= all[m];
             float* gates = ws.gates + at * GATE_FLOATS;
             gates[krow ? C + i : i] = krow ? sBe[hh * C + i] : d;
             if (krow) gates[2 * C + i] = end;
             __syncthreads();
-            // Row i of M (from c_i), or of W (from the unit row e_i).  x1 is
-            // kept in shared memory; the first 32 tokens have none.
-            float* keep = krow ? reinterpret_cast<float*>(sm + P::ROWW) + i * P::PW : rowp + 32;
+            // Row i of M (from c_i), or of W (from the unit row e_i).
             const bool upper = i >= 32;
+            float* up = (krow ? reinterpret_cast<float*>(sm + P::ROWW) : reinterpret_cast<float*>(sm + P::ROWC)) +
+                        (i | 32) * (krow ? P::PW : P::P);  // the row itself, or 32 tokens on
+            float *sX1 = up + (krow ? 0 : 32), *sSum = up + (krow ? 32 : 0);
             uint64_t x[16];
-            auto start = [&](int half) {
-                if (krow) {
+            if (krow) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        x[j] = pack2(32 * half + 2 * j == i ? 1.f : 0.f, 32 * half + 2 * j + 1 == i ? 1.f : 0.f);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(rowp + 32 * half + 4 * j);
-                        x[2 * j] = y.x;
-                        x[2 * j + 1] = y.y;
-                    }
-                }
-            };
+                for (int j = 0; j < 16; ++j)
+                    x[j] = pack2(2 * j == (i & 31) ? 1.f : 0.f, 2 * j + 1 == (i & 31) ? 1.f : 0.f);
+            } else {
+                read_row(x, rowp + (i & 32));
+            }
             if (upper) {
-                start(1);
-                solve32(x, sG + 32 * P::P + 32);
+                solve<32>(x, sG + 32 * P::P + 32);
+                write_row(sX1, x);
+            } else {
+                solve<32>(x, sG);
+            }
+            __syncthreads();
+            uint64_t z[8] = {};
+            if (!krow) read_row(z, upper ? rowp + 16 : sSum);
+            if (upper) {
+                uint64_t y[8] = {}, part[8];
+                take32(z, sX1, sG + 32 * P::P + 16);
+                solve<16>(z, sG + 16 * P::P + 16);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<ulonglong2*>(keep + 4 * j) = make_ulonglong2(x[2 * j], x[2 * j + 1]);
-                start(0);
+                for (int k = 0; k < 4; ++k) {
+                    const float2 z0 = unpack2(z[2 * k]), z1 = unpack2(z[2 * k + 1]);
+                    const float zz[4] = {z0.x, z0.y, z1.x, z1.y};
+                    take4(y, zz, sG + (16 + 4 * k) * P::P);
+                }
+                __syncthreads();
+                read_row(part, sSum);
 #pragma unroll
-                for (int k4 = 0; k4 < 8; ++k4) {
-                    const float4 xk4 = *reinterpret_cast<const float4*>(keep + 4 * k4);
-                    const float xk[4] = {xk4.x, xk4.y, xk4.z, xk4.w};
+                for (int j = 0; j < 8; ++j) y[j] = add2(y[j], part[j]);
+                solve<16>(y, sG);
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const uint64_t xx = pack2(-xk[u], -xk[u]);
-                        const ulonglong2* row = reinterpret_cast<const ulonglong2*>(sG + (32 + 4 * k4 + u) * P::P);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const ulonglong2 y = row[j];
-                            x[2 * j] = fma2(xx, y.x, x[2 * j]);
-                            x[2 * j + 1] = fma2(xx, y.y, x[2 * j + 1]);
-                        }
-                    }
+                for (int j = 0; j < 8; ++j) {
+                    x[j] = y[j];
+                    x[8 + j] = z[j];
                 }
             } else {
-                start(0);
+                take32(z, sX1, sG + 32 * P::P);
+                write_row(sSum, z);
+                __syncthreads();
             }
-            solve32(x, sG);
-            uint64_t x1[16];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const ulonglong2 y =
-                    upper ? *reinterpret_cast<const ulonglong2*>(keep + 4 * j) : make_ulonglong2(0, 0);
-                x1[2 * j] = y.x;
-                x1[2 * j + 1] = y.y;
-            }
+            uint64_t x1[16] = {};
+            if (upper) read_row(x1, sX1);
             __syncthreads();  // everything before the image is done with
             const int row = (i >> 4) * 32 + (i & 15) + (krow ? 16 : 0);
 #pragma unroll 1

@@ -145,15 +145,15 @@ canopy_status prefill_args(int N, int B, int H, int HV, canopy_dtype in_dtype, c
 // The plan of a prefill call whose arguments passed prefill_args.  Chunks
 // cost two launches and a chain of products however short the prompts are,
 // the scan a fixed time per token.  Measured scan / chunked time (equal
-// lengths, 16 or 32 value heads) by (sequence, value head) pairs: 8 or 16
-// pairs 0.86 at 56 tokens and 0.96 at 64; 32 or 64 pairs 0.85-0.97 at 40 and
-// 0.99-1.12 at 48; 128 and more 0.80-0.94 at 16 and 0.94-1.16 at 20.  The host
+// lengths, 8 to 32 value heads) by (sequence, value head) pairs: 8 or 16 pairs
+// 0.87 at 56 tokens and 0.96 at 64; 32 or 64 pairs 0.75-0.87 at 40 to 48 and
+// 0.98-1.06 at 56; 128 and more 0.79-0.96 at 24 and 1.00-1.21 at 32.  The host
 // knows the mean length only, and an uneven batch takes as long as its longest
 // prompt, which costs the scan more: the rule leans to the lower end.
 canopy_prefill_plan_t prefill_plan(int N, int B, int HV, canopy_dtype in_dtype, int dk, unsigned flags) {
     if (flags & CANOPY_PREFILL_SCAN) return CANOPY_PREFILL_PLAN_SCAN;
     if (flags & CANOPY_PREFILL_CHUNKED) return CANOPY_PREFILL_PLAN_CHUNKED;
-    const size_t pairs = size_t(B) * HV, least = pairs < 24 ? 64 : pairs < 128 ? 40 : 18;
+    const size_t pairs = size_t(B) * HV, least = pairs < 24 ? 64 : pairs < 128 ? 48 : 26;
     return in_dtype == CANOPY_BF16 && dk == 128 && size_t(N) >= least * B ? CANOPY_PREFILL_PLAN_CHUNKED
                                                                            : CANOPY_PREFILL_PLAN_SCAN;
 }

@@ -4,26 +4,31 @@
 // canopy page (projects.dotslasha.me/p/canopy.md), "The gated delta rule":
 // per sequence and value head, for its tokens in order,
 //     u = beta (v - g S k),  S <- g S + u k^T,  o = scale S q.
-// Value rows are independent: a CTA of 128 threads keeps 16 rows of one
-// state in registers (eight lanes per row, dk / 8 entries each) and walks
-// the sequence.  What a token waits for is S k on the token before: four
-// short sums, a three-step reduction and the update; o hangs off it.  Blocks
-// of 16 tokens are read into registers while the block before them is
-// computed from shared memory.
+// Value rows are independent: a CTA of 128 threads keeps 16 or 32 rows of one
+// state in registers (eight lanes per row, dk / 8 entries of one or two rows
+// each) and walks the sequence.  What a token waits for is S k on the token
+// before: four short sums, a three-step reduction and the update; o hangs off
+// it.  Blocks of 16 tokens are read into registers while the block before
+// them is computed from shared memory.
 //
-// Bound by instruction issue and, with several CTAs on an SM, by the reads of
-// k and q from shared memory, which every group of eight lanes repeats:
-// 0.16 us a token for one sequence of 16 heads (256 tokens: 42.5 us), 96 us
-// for four fp32 ones of 600 tokens together, the longest of 414.  Sixteen
-// lanes per row were 20 % slower throughout.
+// Bound by the reads of k and q from shared memory, which every eight lanes
+// repeat (130 of the 300 cycles of a token of 16 rows on an SM), and by the
+// chain.  With two rows a lane those reads serve both: slower alone (0.21 us a
+// token for 0.17), but two such blocks on an SM take 0.31 and three 0.41, where
+// two of 16 rows take 0.25 and four 0.40.  So 16 rows where every block has an
+// SM for itself.  100 bf16 tokens, d = 128, us at 16 or 32 rows a block:
+// 16 states 18 / 21, 32 states 25 / 21, 64 states 40 / 31, 128 states 70 / 59,
+// 512 states 260 / 187.  Four rows a lane: 30, 31 (32, 64 states), 191 (512).
+// Sixteen or 32 lanes per row, and blocks of 2 or 4 tokens in closed form,
+// were slower or no faster.
 #include "common.cuh"
 
 namespace canopy {
 
 namespace scan {
 
-constexpr int ROWS = 16;  // state rows per CTA
-constexpr int TB = 16;    // tokens per block
+constexpr size_t kSMs = 152;
+constexpr int TB = 16;  // tokens per block
 constexpr int NT = 128;
 
 // Tokens [lo, hi) of sequence b; bounds outside [0, N] or out of order are
@@ -50,23 +55,25 @@ __device__ inline float4 to_f4(uint2 x) {
                        __uint_as_float(x.y & 0xFFFF0000u));
 }
 
-// (the bound of four blocks is for the register count, 128: with fewer the
-// loop's reads are not moved ahead, 56 us instead of 43 for 256 bf16 tokens)
-template <typename InT, typename OutT, int D>
-__global__ void __launch_bounds__(NT, 4) scan_kernel(const InT* __restrict__ q, const InT* __restrict__ k,
+// (the bounds are for the register counts, 128 and 168; R = 1 with 168 takes
+// 77 us for 256 tokens of 32 states instead of 60, R = 2 with 128 as long as
+// with 168 where blocks are many and 5 % longer where they are few)
+template <typename InT, typename OutT, int D, int R>
+__global__ void __launch_bounds__(NT, R == 1 ? 4 : 3) scan_kernel(const InT* __restrict__ q, const InT* __restrict__ k,
                                                   const InT* __restrict__ v, const float* __restrict__ g,
                                                   const float* __restrict__ beta, const float* S0, float* S_new,
                                                   const int32_t* __restrict__ starts, OutT* __restrict__ o, int N,
                                                   int HV, int ratio, float scale, int32_t* __restrict__ err) {
     using Raw4 = typename Four<InT>::type;
-    constexpr int C4 = D / 32;             // float4 chunks per lane
+    constexpr int C4 = D / 32;             // float4 chunks per lane and row
+    constexpr int ROWS = 16 * R;           // state rows per CTA
     constexpr int PER = TB * D / 4 / NT;   // float4 chunks of a block's q (and k) per thread
-    static_assert(PER >= 1 && TB * ROWS / NT == 2, "staging");
+    static_assert(PER >= 1 && D % ROWS == 0, "staging");
     __shared__ float4 sQ[2][TB][D / 4], sK[2][TB][D / 4];
     __shared__ float sV[2][TB][ROWS];
     __shared__ float2 sGB[2][TB];  // g, beta
     const int h = blockIdx.y, b = blockIdx.z, t = threadIdx.x;
-    const int gl = t & 7, row = t >> 3, r0 = blockIdx.x * ROWS;
+    const int gl = t & 7, row = (t >> 3) * R, r0 = blockIdx.x * ROWS;
     const int H = HV / ratio, hk = h / ratio;
     pdl_wait();
     pdl_trigger();  // after the wait: the next kernel may rely on everything before this one
@@ -74,16 +81,20 @@ __global__ void __launch_bounds__(NT, 4) scan_kernel(const InT* __restrict__ q, 
     sequence(starts, b, N, lo, hi, &bad);
 
     const size_t at = ((size_t(b) * HV + h) * D + r0 + row) * D;
-    float4 s[C4];
+    float4 s[R][C4];
 #pragma unroll
-    for (int c = 0; c < C4; ++c)
-        s[c] = S0 ? *reinterpret_cast<const float4*>(S0 + at + (c * 8 + gl) * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int c = 0; c < C4; ++c)
+            s[r][c] = S0 ? *reinterpret_cast<const float4*>(S0 + at + r * D + (c * 8 + gl) * 4)
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
 
     // The block from token n0 into registers, as it is: whatever looks at a
     // value (the conversion to fp32, the check of a gate) waits for its load,
     // so that comes a block later.  Tokens past the end are not read.
     Raw4 nq[PER], nk[PER];
-    InT nv[2];
+    constexpr int VP = TB * ROWS / NT;
+    InT nv[VP];
     float ng, nb;
     auto fetch = [&](int n0) {
 #pragma unroll
@@ -97,7 +108,7 @@ __global__ void __launch_bounds__(NT, 4) scan_kernel(const InT* __restrict__ q, 
             }
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < VP; ++e) {
             const int i = t + e * NT, n = n0 + i / ROWS;
             nv[e] = n < hi ? v[(size_t(n) * HV + h) * D + r0 + i % ROWS] : InT(0.f);
         }
@@ -118,7 +129,7 @@ __global__ void __launch_bounds__(NT, 4) scan_kernel(const InT* __restrict__ q, 
             sK[buf][i / (D / 4)][i % (D / 4)] = to_f4(nk[e]);
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) sV[buf][(t + e * NT) / ROWS][(t + e * NT) % ROWS] = to_f(nv[e]);
+        for (int e = 0; e < VP; ++e) sV[buf][(t + e * NT) / ROWS][(t + e * NT) % ROWS] = to_f(nv[e]);
         if (t < TB) {
             if (!gate_ok(ng, nb)) {
                 bad |= CANOPY_DEVERR_GATE;
@@ -139,53 +150,88 @@ __global__ void __launch_bounds__(NT, 4) scan_kernel(const InT* __restrict__ q, 
             for (int nn = 0; nn < 4; ++nn) {
                 const int n = n4 + nn;
                 const float2 gb = sGB[buf][n];
-                const float vv = sV[buf][n][row];
                 float4 kk[C4];
-                float part[4] = {0.f, 0.f, 0.f, 0.f};
+                float u[R], so[R];
 #pragma unroll
-                for (int c = 0; c < C4; ++c) {
-                    kk[c] = sK[buf][n][c * 8 + gl];
-                    part[0] += s[c].x * kk[c].x;
-                    part[1] += s[c].y * kk[c].y;
-                    part[2] += s[c].z * kk[c].z;
-                    part[3] += s[c].w * kk[c].w;
+                for (int c = 0; c < C4; ++c) kk[c] = sK[buf][n][c * 8 + gl];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < C4; ++c) {
+                        part[0] += s[r][c].x * kk[c].x;
+                        part[1] += s[r][c].y * kk[c].y;
+                        part[2] += s[r][c].z * kk[c].z;
+                        part[3] += s[r][c].w * kk[c].w;
+                    }
+                    u[r] = (part[0] + part[1]) + (part[2] + part[3]);
                 }
-                float sk = (part[0] + part[1]) + (part[2] + part[3]);
 #pragma unroll
-                for (int x = 4; x; x >>= 1) sk += __shfl_xor_sync(0xffffffffu, sk, x);
-                const float a = gb.x, u = gb.y * (vv - a * sk);
-                part[0] = part[1] = part[2] = part[3] = 0.f;
+                for (int x = 4; x; x >>= 1)
+#pragma unroll
+                    for (int r = 0; r < R; ++r) u[r] += __shfl_xor_sync(0xffffffffu, u[r], x);
+                const float a = gb.x;
+#pragma unroll
+                for (int r = 0; r < R; ++r) u[r] = gb.y * (sV[buf][n][row + r] - a * u[r]);
+                float part[R][4] = {};
 #pragma unroll
                 for (int c = 0; c < C4; ++c) {
-                    s[c].x = a * s[c].x + u * kk[c].x;
-                    s[c].y = a * s[c].y + u * kk[c].y;
-                    s[c].z = a * s[c].z + u * kk[c].z;
-                    s[c].w = a * s[c].w + u * kk[c].w;
                     const float4 qq = sQ[buf][n][c * 8 + gl];
-                    part[0] += s[c].x * qq.x;
-                    part[1] += s[c].y * qq.y;
-                    part[2] += s[c].z * qq.z;
-                    part[3] += s[c].w * qq.w;
-                }
-                float so = (part[0] + part[1]) + (part[2] + part[3]);
 #pragma unroll
-                for (int x = 4; x; x >>= 1) so += __shfl_xor_sync(0xffffffffu, so, x);
-                if (gl == 0 && n < m) store_out(op + size_t(n) * HV * D, scale * so);
+                    for (int r = 0; r < R; ++r) {
+                        s[r][c].x = a * s[r][c].x + u[r] * kk[c].x;
+                        s[r][c].y = a * s[r][c].y + u[r] * kk[c].y;
+                        s[r][c].z = a * s[r][c].z + u[r] * kk[c].z;
+                        s[r][c].w = a * s[r][c].w + u[r] * kk[c].w;
+                        part[r][0] += s[r][c].x * qq.x;
+                        part[r][1] += s[r][c].y * qq.y;
+                        part[r][2] += s[r][c].z * qq.z;
+                        part[r][3] += s[r][c].w * qq.w;
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < R; ++r) so[r] = (part[r][0] + part[r][1]) + (part[r][2] + part[r][3]);
+#pragma unroll
+                for (int x = 4; x; x >>= 1)
+#pragma unroll
+                    for (int r = 0; r < R; ++r) so[r] += __shfl_xor_sync(0xffffffffu, so[r], x);
+                float mine = so[0];  // lane r of the eight stores row r's
+#pragma unroll
+                for (int r = 1; r < R; ++r) mine = gl == r ? so[r] : mine;
+                if (gl < R && n < m) store_out(op + size_t(n) * HV * D + gl, scale * mine);
             }
         }
     }
 #pragma unroll
-    for (int c = 0; c < C4; ++c) *reinterpret_cast<float4*>(S_new + at + (c * 8 + gl) * 4) = s[c];
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int c = 0; c < C4; ++c) *reinterpret_cast<float4*>(S_new + at + r * D + (c * 8 + gl) * 4) = s[r][c];
     if (bad && blockIdx.x == 0) raise_err(err, bad);
+}
+
+template <typename InT, typename OutT, int D, int R>
+cudaError_t launch_rows(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                        const float* S0, float* S_new, const int32_t* starts, void* o, int N, int B, int H, int HV,
+                        float scale, int32_t* err, cudaStream_t st) {
+    // With more blocks than SMs but at most two for each, shared memory that
+    // is not used keeps a third from an SM: 64 states 31 us instead of 41.
+    constexpr int kTwoPerSM = 42 * 1024;
+    static const cudaError_t attr = cudaFuncSetAttribute(scan_kernel<InT, OutT, D, R>,
+                                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kTwoPerSM);
+    if (attr != cudaSuccess) return attr;
+    const size_t blocks = size_t(D / (16 * R)) * HV * B;
+    const int unused = blocks > kSMs && blocks <= 2 * kSMs ? kTwoPerSM : 0;
+    return launch_pdl(scan_kernel<InT, OutT, D, R>, dim3(D / (16 * R), HV, B), dim3(NT), unused, st,
+                      static_cast<const InT*>(q), static_cast<const InT*>(k), static_cast<const InT*>(v), g, beta, S0,
+                      S_new, starts, static_cast<OutT*>(o), N, HV, HV / H, scale, err);
 }
 
 template <typename InT, typename OutT, int D>
 cudaError_t launch(const void* q, const void* k, const void* v, const float* g, const float* beta, const float* S0,
                    float* S_new, const int32_t* starts, void* o, int N, int B, int H, int HV, float scale,
                    int32_t* err, cudaStream_t st) {
-    return launch_pdl(scan_kernel<InT, OutT, D>, dim3(D / ROWS, HV, B), dim3(NT), 0, st, static_cast<const InT*>(q),
-                      static_cast<const InT*>(k), static_cast<const InT*>(v), g, beta, S0, S_new, starts,
-                      static_cast<OutT*>(o), N, HV, HV / H, scale, err);
+    return (size_t(D / 16) * HV * B <= kSMs ? launch_rows<InT, OutT, D, 1> : launch_rows<InT, OutT, D, 2>)(q, k, v, g, beta, S0, S_new, starts, o, N,
+                                                                            B, H, HV, scale, err, st);
 }
 
 }  // namespace scan

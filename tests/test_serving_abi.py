@@ -24,10 +24,10 @@ def test_prefill_plan(canopy):
     assert plan(16384, 1, 16, 32, True, 128) == "chunked"
     assert plan(37, 1, 16, 16, True, 128) == "scan"
     assert plan(64, 1, 16, 16, True, 128) == "chunked"
-    assert plan(39, 1, 16, 32, True, 128) == "scan"
-    assert plan(40, 1, 16, 32, True, 128) == "chunked"
-    assert plan(18 * 64, 64, 16, 32, True, 128) == "chunked"
-    assert plan(17 * 64, 64, 16, 32, True, 128) == "scan"
+    assert plan(47, 1, 16, 32, True, 128) == "scan"
+    assert plan(48, 1, 16, 32, True, 128) == "chunked"
+    assert plan(26 * 64, 64, 16, 32, True, 128) == "chunked"
+    assert plan(25 * 64, 64, 16, 32, True, 128) == "scan"
     assert plan(16384, 1, 16, 32, False, 128) == "scan"
     assert plan(16384, 1, 16, 32, True, 32) == "scan"
     assert plan(3, 1, 16, 32, True, 128, force="chunked") == "chunked"

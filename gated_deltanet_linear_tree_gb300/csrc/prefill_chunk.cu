@@ -51,12 +51,16 @@ constexpr int GATE_FLOATS = 192;  // 2^l, beta and the decay to the chunk's end,
 __host__ __device__ inline size_t slot_count(int N, int B) { return size_t(N / C) + B; }
 
 constexpr int kMaxRanked = 127;  // sequences that the walk is planned for
-constexpr int kMaxHalved = 4;    // of them, at most so many in halves (a block that has no walk costs its start)
+constexpr int kSMs = 152;
 
-// The walk's rows, longest first: the sequence, whether it is walked in
-// halves of a state, and its first block; one more for where they end.
+// Blocks per head that the walk may take beyond one per sequence: about as
+// many in all as there are SMs (one without a walk costs its start).
+__host__ __device__ inline int more_blocks(int HV) { return HV > kSMs / 4 ? 4 : HV < kSMs / 12 ? 12 : kSMs / HV; }
+
+// The walk's rows, longest first: the sequence, how many blocks share a state
+// of it, and its first block; one more for where they end.
 struct Row {
-    int32_t seq, halved, first, unused;
+    int32_t seq, parts, first, unused;
 };
 
 struct WsView {
@@ -286,18 +290,22 @@ __device__ inline void put_half_row(uint8_t* image, int row, int half, const uin
 }
 
 // The walk's plan, by one block of 128 threads.  Sequences are walked by four
-// blocks per state (quarters), or by one, the longest of them by two: so many
-// as give the least estimate for the launch, the largest of the longest walk,
-// the work spread over the SMs, and (m + 1) times the walk at place
-// 152 m + 1 by length (of 152 m + 1 walks some SM has m + 1).  The longest
-// walks start first (they end last).
-constexpr int kSMs = 152, kHalfCycles = 5700, kWholeCycles = 8300, kWalkCycles = 5000;  // per chunk; per walk
+// blocks per state (quarters), or by one, the longest of them by four and the
+// next by two: so many of either as give the least estimate for the launch,
+// the largest of the longest walk, (m + 1) times the walk at place 152 m + 1 by
+// length (of 152 m + 1 walks some SM has m + 1) and, where they are more than
+// the SMs, the work spread over the SMs and a third of a mean walk (what is
+// uneven at the end).  The longest walks start first.  Drawn batches took on
+// average 0.6 % longer, at most 13 %, in a simulation of the launch than by
+// the best of these plans.
+constexpr int kWalkCycles = 5000;  // per walk, and
+constexpr int kQuarterCycles = 4000, kHalfCycles = 5700, kWholeCycles = 8300;  // per chunk
 
 __device__ inline void plan_walk(const int32_t* starts, int nseq, int HV, int quarters, Row* rows) {
     __shared__ int sLen[128], sSorted[128], sCount[128];
     __shared__ unsigned long long sBest;
     const int tid = threadIdx.x;
-    if (tid == 0) sBest = quarters ? 0ull : ~0ull;
+    if (tid == 0) sBest = ~0ull;
     const int len = tid < nseq ? max(starts[tid + 1] - starts[tid], 0) : 0, chunks = (len + C - 1) / C;
     sLen[tid] = len;
     __syncthreads();
@@ -305,39 +313,51 @@ __device__ inline void plan_walk(const int32_t* starts, int nseq, int HV, int qu
     for (int k = 0; k < nseq; ++k) rank += sLen[k] > len || (sLen[k] == len && k < tid);
     if (tid < nseq) sSorted[rank] = chunks;
     __syncthreads();
-    if (!quarters && tid <= min(nseq, kMaxHalved)) {  // the estimate with the first tid sequences halved
-        int i = 0, j = tid, walks = 0, m = 0;
+    // thread by thread: the first nq sequences in quarters, those up to nsplit in halves
+    const int more = more_blocks(HV);
+    int nq = 0, nsplit = tid;
+    for (; 3 * nq <= more && nsplit > more - 3 * nq; ++nq) nsplit -= more - 3 * nq + 1;
+    nsplit += nq;
+    if (!quarters && 3 * nq <= more && nsplit <= nseq) {
+        int i = 0, j = nq, k = nsplit, walks = 0, m = 0;
         float most = 0.f, work = 0.f;
-        while (i < tid || j < nseq) {  // both kinds in descending order
-            const float half = i < tid ? float(sSorted[i]) * kHalfCycles + kWalkCycles : -1.f;
-            const float whole = j < nseq ? float(sSorted[j]) * kWholeCycles + kWalkCycles : -1.f;
-            const float cycles = fmaxf(half, whole);
-            const int count = half >= whole ? 2 * HV : HV;
-            if (half >= whole) ++i;
-            else ++j;
+        while (i < nq || j < nsplit || k < nseq) {  // each kind in descending order
+            const float quarter = i < nq ? float(sSorted[i]) * kQuarterCycles + kWalkCycles : -1.f;
+            const float half = j < nsplit ? float(sSorted[j]) * kHalfCycles + kWalkCycles : -1.f;
+            const float whole = k < nseq ? float(sSorted[k]) * kWholeCycles + kWalkCycles : -1.f;
+            const float cycles = fmaxf(quarter, fmaxf(half, whole));
+            int count = HV;
+            if (cycles == quarter) ++i, count *= 4;
+            else if (cycles == half) ++j, count *= 2;
+            else ++k;
             work += cycles * count;
             walks += count;
             for (; walks > kSMs * m; ++m) most = fmaxf(most, float(m + 1) * cycles);
         }
-        most = fmaxf(most, work * (1.05f / kSMs));
-        if (tid > 0) most *= 1.08f;  // (and it has to be worth it)
-        atomicMin(&sBest, static_cast<unsigned long long>(most) << 8 | tid);
+        if (walks > kSMs) most = fmaxf(most, work / kSMs + 0.35f * work / float(walks));
+        if (tid > 0) most *= 1.04f;  // (and it has to be worth it)
+        atomicMin(&sBest, static_cast<unsigned long long>(most) << 16 | nq << 8 | nsplit);
     }
     __syncthreads();
-    const int halved = int(sBest & 255);
+    nq = quarters ? nseq : int(sBest >> 8 & 255);
+    nsplit = int(sBest & 255);
+    auto parts = [&](int r) { return r < nq ? 4 : r < nsplit ? 2 : 1; };
+    auto cycles = [&](int r, int n) {
+        return float(n) * (parts(r) == 4 ? kQuarterCycles : parts(r) == 2 ? kHalfCycles : kWholeCycles);
+    };
     int place = 0;
     if (tid < nseq) {
-        const float cycles = float(chunks) * (rank < halved ? kHalfCycles : kWholeCycles);
+        const float mine = cycles(rank, chunks);
         for (int k = 0; k < nseq; ++k) {
-            const float other = float(sSorted[k]) * (k < halved ? kHalfCycles : kWholeCycles);
-            place += other > cycles || (other == cycles && k < rank);
+            const float other = cycles(k, sSorted[k]);
+            place += other > mine || (other == mine && k < rank);
         }
-        sCount[place] = quarters ? 4 * HV : rank < halved ? 2 * HV : HV;
+        sCount[place] = parts(rank) * HV;
     }
     __syncthreads();
     int first = 0;
     for (int k = 0; k < (tid < nseq ? place : nseq); ++k) first += sCount[k];
-    if (tid < nseq) rows[place] = {tid, rank < halved, first, 0};
+    if (tid < nseq) rows[place] = {tid, parts(rank), first, 0};
     else if (tid == nseq) rows[nseq] = {-1, 0, first, 0};
 }
 
@@ -599,9 +619,11 @@ enum { CB_X, CB_OU, CB_O2, CB_DS, CB_S, CB_R, CB_U, CB_N };  // a chain's barrie
 enum { PB_QK = 0, PB_QKE = 2, PB_MW = 4, PB_MWE = 6, PB_LO = 8, PB_LOE, PB_N };  // tiles: full and empty
 
 // Three shapes of a block:
-//   <32, 1>  one chain: few states, a chunk's latency counts.  U is apart from
-//            R, so that the third part's products need not be over before U
-//            is taken on (16 warps of 8 columns were no faster);
+//   <32, 1>  a quarter of a state: one chain, where there are few states, or
+//            one sequence that the others wait for, and a chunk's latency
+//            counts.  U is apart from R, so that the third part's products need
+//            not be over before U is taken on (16 warps of 8 columns were no
+//            faster);
 //   <32, 2>  half a state: two chains half a chunk apart, one's products
 //            beside the other's register work;
 //   <64, 2>  a whole state: [Q; K] and [M; W] are read once for all of it, and
@@ -733,17 +755,17 @@ __device__ inline void sum8(uint32_t taddr, uint64_t (&x)[4]) {
 
 // This block's place in the plan.
 struct Turn {
-    int seq, halved, index;  // index among the sequence's blocks
+    int seq, parts, index;  // index among the sequence's blocks
 };
 __device__ inline Turn take_turn(const Row* rows, int nseq, int per_seq) {
     __shared__ Turn sTurn;
     const int tid = threadIdx.x, item = blockIdx.x;
-    if (nseq > kMaxRanked) return {item / per_seq, 0, item % per_seq};
+    if (nseq > kMaxRanked) return {item / per_seq, 1, item % per_seq};
     if (tid == 0) sTurn.seq = -1;
     __syncthreads();
     if (tid < nseq) {
         const Row r = rows[tid];
-        if (item >= r.first && item < rows[tid + 1].first) sTurn = {r.seq, r.halved, item - r.first};
+        if (item >= r.first && item < rows[tid + 1].first) sTurn = {r.seq, r.parts, item - r.first};
     }
     __syncthreads();
     return sTurn;
@@ -839,6 +861,8 @@ __device__ __forceinline__ void walk(const CUtensorMap& tmQ, const CUtensorMap& 
                 if (lo_n) mbar_wait(&pb[PB_LO], (lo_n - 1) & 1);
             }
         }
+    } else if (warp > kComputeWarps + NCH) {
+        // (a block with more warps than this shape has)
     } else if (warp >= kComputeWarps) {
         // ---- the chain's products -----------------------------------------------
         if (lane == 0) {
@@ -1125,15 +1149,17 @@ __global__ void __launch_bounds__(32 * (2 * WARPS + 3), 1)
     pdl_wait();
     const Turn turn = take_turn(args.ws.rows, args.B, args.HV);
     if (turn.seq < 0) return;  // fewer walks than there might be
-    if (turn.halved) walk<Shape<32, 2>>(tmQ, tmK, args, o, turn.seq, turn.index >> 1, (turn.index & 1) * 64, sm);
-    else walk<Shape<64, 2>>(tmQ, tmK, args, o, turn.seq, turn.index, 0, sm);
+    if (turn.parts == 1) walk<Shape<64, 2>>(tmQ, tmK, args, o, turn.seq, turn.index, 0, sm);
+    else if (turn.parts == 2) walk<Shape<32, 2>>(tmQ, tmK, args, o, turn.seq, turn.index >> 1, (turn.index & 1) * 64, sm);
+    else walk<Shape<32, 1>>(tmQ, tmK, args, o, turn.seq, turn.index >> 2, (turn.index & 3) * 32, sm);
 }
 
 template <typename OutT>
 cudaError_t launch_walk(bool many, const CUtensorMap& mq, const CUtensorMap& mk, const WalkArgs& args, OutT* o,
                         cudaStream_t st) {
-    constexpr int one = Shape<32, 1>::TOTAL,
-                  two = Shape<32, 2>::TOTAL > Shape<64, 2>::TOTAL ? Shape<32, 2>::TOTAL : Shape<64, 2>::TOTAL;
+    static constexpr int one = Shape<32, 1>::TOTAL, half = Shape<32, 2>::TOTAL, whole = Shape<64, 2>::TOTAL;
+    static constexpr int two = half > whole ? half : whole;  // of the shapes that meet in one launch
+    static_assert(two >= one, "shared memory");
     static const cudaError_t attr = [] {
         const cudaError_t e =
             cudaFuncSetAttribute(walk_kernel<OutT>, cudaFuncAttributeMaxDynamicSharedMemorySize, one);
@@ -1144,7 +1170,7 @@ cudaError_t launch_walk(bool many, const CUtensorMap& mq, const CUtensorMap& mk,
     if (attr != cudaSuccess) return attr;
     const unsigned states = unsigned(args.B) * args.HV;
     if (many)
-        return launch_pdl(walk_many_kernel<OutT>, dim3(states + (args.B <= kMaxRanked ? min(args.B, kMaxHalved) * args.HV : 0)),
+        return launch_pdl(walk_many_kernel<OutT>, dim3(states + (args.B <= kMaxRanked ? more_blocks(args.HV) * args.HV : 0)),
                           dim3(32 * (2 * WARPS + 3)), two, st, mq, mk, args, o);
     return launch_pdl(walk_kernel<OutT>, dim3(states * 4), dim3(32 * (WARPS + 2)), one, st, mq, mk, args, o);
 }
@@ -1156,17 +1182,14 @@ cudaError_t launch_walk(bool many, const CUtensorMap& mq, const CUtensorMap& mk,
 // pairs of 16 key heads 92 us alone and 85 us in twos, with 16,640 327 and 296.
 constexpr size_t kPairFrom = 2432;
 
-// States (sequences times value heads) from which the walk takes them in
-// halves and whole rather than in quarters: one sequence fills the SMs in
-// quarters with 38; several are uneven as a rule and wait for the longest,
-// which quarters walk fastest.  Measured with sequences of 2,048 tokens on
+// States (sequences times value heads) from which not every one is walked in
+// quarters: those fill the SMs up to 38.  Sequences of 2,048 tokens on
 // average, one even and three uneven batches, in us, quarters against the
-// rest: 48 states of three 169/185/147/160 and 136/254/200/218, 96 states
-// 260/236/249/243 and 217/281/226/249, 128 states 342/308/324/339 and
-// 236/386/294/277, 256 states 609/594/611/609 and 453/503/456/475.  (Before
-// halves and wholes were mixed, 256 states took 527 whole and 560 in halves,
-// uneven.)
-bool many_states(int B, int HV) { return size_t(B) * HV > (B == 1 ? 38 : 100); }
+// plan's mixture: 48 states of three sequences 168/141/140/217 and
+// 136/146/142/222, 80 of five 253/241/220/229 and 207/214/202/190, 96 of three
+// 259/258/247/259 and 214/217/250/199, 96 of twelve 264/244/297/282 and
+// 218/258/308/298.
+bool many_states(int B, int HV) { return size_t(B) * HV > 38; }
 
 size_t prefill_chunk_ws_bytes(int N, int B, int HV) { return pfc::ws_bytes(N, B, HV); }
 

@@ -110,6 +110,22 @@ def test_prefill_many_states(lib, lens, H, HV):
     close(S, S_ref)
 
 
+@pytest.mark.parametrize("lens,HV", [([1300, 70, 64, 1], 26), ([1300, 800, 70, 64, 10, 1], 17), ([3, 700], 51)])
+@pytest.mark.parametrize("o_bf16", [False, True])
+def test_prefill_uneven_batches(lib, lens, HV, o_bf16):
+    """One prompt much longer than the rest, whose states are shared by two or four blocks."""
+    x = sc.layer_inputs(lens, HV, HV, 128, True, seed=HV, kind="rates")
+    o_ref, S_ref = oracle.serving.recurrence(**x)
+    t = sc.to_cuda(x, True)
+    o, S, err = prefill(lib, t, "chunked", 128)
+    assert err == 0
+    close(o, o_ref)
+    close(S, S_ref)
+    if o_bf16:
+        rounded, S2, _ = prefill(lib, t, "chunked", 128, out=torch.empty_like(o, dtype=torch.bfloat16))
+        assert torch.equal(rounded, o.bfloat16()) and torch.equal(S, S2)
+
+
 @pytest.mark.parametrize("force,bf16,d", PATHS)
 @pytest.mark.parametrize("kind", ["aligned", "forget", "rates"])
 def test_prefill_hard_inputs(lib, force, bf16, d, kind):

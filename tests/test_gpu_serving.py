@@ -126,6 +126,29 @@ def test_prefill_uneven_batches(lib, lens, HV, o_bf16):
         assert torch.equal(rounded, o.bfloat16()) and torch.equal(S, S2)
 
 
+@pytest.mark.parametrize("N,lo,hi,HV", [(2100, 0, 2100, 2), (2112, 70, 2001, 4), (2048, 0, 2048, 36),
+                                        (2304, 1200, 2304, 26), (2100, 0, 10, 2), (2200, 2150, 2200, 30)])
+def test_prefill_one_long_sequence(lib, N, lo, hi, HV):
+    """A prompt of many chunks, or what is left of one, anywhere in rows that are otherwise NaN."""
+    x = sc.layer_inputs([hi - lo], HV, HV, 128, True, seed=HV, kind="rates")
+    o_ref, S_ref = oracle.serving.recurrence(**x)
+    t = sc.to_cuda(x, True)
+    y = {n: torch.full((N, *t[n].shape[1:]), float("nan"), dtype=t[n].dtype, device="cuda")
+         for n in ("q", "k", "v", "g", "beta")}
+    for n in y:
+        y[n][lo:hi] = t[n]
+    y["starts"] = torch.tensor([lo, hi], dtype=torch.int32, device="cuda")
+    o = torch.full((N, HV, 128), 7.0, device="cuda")
+    for again in range(3):  # the workspace's earlier contents do not matter, nor is a call in another's way
+        S = t["S0"].clone()
+        y["S0"] = S
+        _, _, err = prefill(lib, y, "chunked", 128, out=o, S_out=S)
+        assert err == 0
+        close(o[lo:hi], o_ref)
+        close(S, S_ref)
+    assert (o[:lo] == 7).all() and (o[hi:] == 7).all()
+
+
 @pytest.mark.parametrize("force,bf16,d", PATHS)
 @pytest.mark.parametrize("kind", ["aligned", "forget", "rates"])
 def test_prefill_hard_inputs(lib, force, bf16, d, kind):

@@ -27,7 +27,7 @@
 //
 // Measured (32 value heads of 16 key heads, both launches in a loop): one
 // sequence of 16,384 tokens 652 us, of which the walk 510; sixteen of 8,191
-// together 229 (81 and 150); eight of 32,768 together 845 to 1,090, by how
+// together 229 (81 and 150); eight of 32,768 together 890 to 950, by how
 // uneven they are.  The first launch is held by the shared-memory and fp32
 // pipes, the walk by the latency of its three products a chunk.
 //

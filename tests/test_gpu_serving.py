@@ -253,6 +253,13 @@ def test_accept(lib, B, T, V, kind, ragged, bf16, draft):
         assert int(err) == 0
 
 
+@pytest.mark.parametrize("B,V", [(2, 70001), (9, 131072), (10, 131075), (1, 196608), (1, 196609), (3, 53249)])
+def test_accept_slices(lib, B, V):
+    """Vocabularies around the sizes from which a block's slice is held in part or not at all."""
+    x = sc.accept_inputs(B, 6, V, seed=B + V, kind="star", draft=True)
+    same(run_accept(lib, x), oracle.serving.accept(**x))
+
+
 def test_accept_draft_equal_to_target(lib):
     """With p = q every first child is accepted (u < 1), down to a leaf."""
     x = sc.accept_inputs(6, 20, 999, seed=1)

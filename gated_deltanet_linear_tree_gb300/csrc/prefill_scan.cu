@@ -220,7 +220,7 @@ cudaError_t launch_rows(const void* q, const void* k, const void* v, const float
                                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kTwoPerSM);
     if (attr != cudaSuccess) return attr;
     const size_t blocks = size_t(D / (16 * R)) * HV * B;
-    const int unused = blocks > kSMs && blocks <= 2 * kSMs ? kTwoPerSM : 0;
+    const int unused = D == 128 && blocks > kSMs && blocks <= 2 * kSMs ? kTwoPerSM : 0;
     return launch_pdl(scan_kernel<InT, OutT, D, R>, dim3(D / (16 * R), HV, B), dim3(NT), unused, st,
                       static_cast<const InT*>(q), static_cast<const InT*>(k), static_cast<const InT*>(v), g, beta, S0,
                       S_new, starts, static_cast<OutT*>(o), N, HV, HV / H, scale, err);

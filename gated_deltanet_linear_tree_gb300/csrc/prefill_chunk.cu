@@ -1178,9 +1178,10 @@ cudaError_t launch_walk(bool many, const CUtensorMap& mq, const CUtensorMap& mk,
 }  // namespace pfc
 
 // (chunk, value head) pairs from which two value heads of a key head share a
-// block of the first launch: four rounds of four blocks per SM.  With 4,576
-// pairs of 16 key heads 92 us alone and 85 us in twos, with 16,640 327 and 296.
-constexpr size_t kPairFrom = 2432;
+// block of the first launch.  With 1,312 pairs of 16 key heads it takes 30.3 us
+// with heads alone and 31.2 in twos, with 1,568 35.2 and 34.6, with 2,080 44.5
+// and 40.3, with 4,128 81.8 and 77.6.
+constexpr size_t kPairFrom = 1400;
 
 // States (sequences times value heads) from which not every one is walked in
 // quarters: those fill the SMs up to 38.  Sequences of 2,048 tokens on

@@ -50,6 +50,8 @@ cudaError_t launch_prefill_scan(const void* q, const void* k, const void* v, int
                                 const float* beta, const float* S0, float* S_new, const int32_t* starts, int N, int B,
                                 int H, int HV, int d, void* o, int o_bf16, float scale, int32_t* err,
                                 cudaStream_t st);
+cudaError_t launch_order_starts(const int32_t* starts, int N, int B, int32_t* ordered, int32_t* err,
+                                cudaStream_t st);
 size_t prefill_chunk_ws_bytes(int N, int B, int HV);
 cudaError_t launch_prefill_chunk(const void* q, const void* k, const void* v, const float* g, const float* beta,
                                  const float* S0, float* S_new, const int32_t* starts, int N, int B, int H, int HV,
@@ -291,7 +293,7 @@ size_t canopy_prefill_workspace_bytes(int N, int B, int HV, int dk, int dv) {
     if (N < 1 || B < 1 || B > kMaxGrid || HV < 1 || HV > kMaxGrid || dk != dv || (dk != 128 && dk != 32) ||
         !chunks_ok(N, B, HV))
         return 0;
-    return dk == 128 ? prefill_chunk_ws_bytes(N, B, HV) : 256;
+    return dk == 128 ? prefill_chunk_ws_bytes(N, B, HV) : 256 + ordered_bytes(B);
 }
 
 canopy_prefill_plan_t canopy_prefill_plan(int N, int B, int H, int HV, canopy_dtype in_dtype, int dk, int dv,
@@ -311,6 +313,12 @@ canopy_status canopy_prefill(const void* q, const void* k, const void* v, canopy
     const canopy_status as = prefill_args(N, B, H, HV, in_dtype, o_dtype, dk, dv, flags, scale);
     if (as != CANOPY_OK) return as;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (ordered_bytes(B)) {
+        int32_t* ordered = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + 256);
+        const cudaError_t e = launch_order_starts(starts, N, B, ordered, static_cast<int32_t*>(workspace), st);
+        if (e != cudaSuccess) return cuda_status(e);
+        starts = ordered;
+    }
     if (prefill_plan(N, B, HV, in_dtype, dk, flags) == CANOPY_PREFILL_PLAN_CHUNKED)
         return cuda_status(launch_prefill_chunk(q, k, v, g, beta, S0, S_new, starts, N, B, H, HV, o,
                                                 o_dtype == CANOPY_BF16, scale, workspace, st));

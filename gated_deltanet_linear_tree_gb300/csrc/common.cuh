@@ -121,6 +121,47 @@ __device__ inline int stream_len(const int32_t* lengths, int b, int T, int* bad)
 }
 
 // ---------------------------------------------------------------------------
+// Packed sequences: sequence b is tokens s_b .. s_{b+1} - 1, where s_i is the
+// largest of starts[0 .. i], each brought into [0, N] first.  For starts that
+// are in order that is starts itself; for others it is the nearest that keeps
+// sequences apart, and a call over them sets CANOPY_DEVERR_LENGTH.
+//
+// Up to this many sequences every warp that needs one forms the largest
+// itself: four reads a lane, all in flight with those of the sequence's own
+// bounds.  Where there are more, a launch ahead (prefill_scan.cu) puts s in the
+// workspace and the kernels read that: a few us in a call that takes 100 and
+// more.
+constexpr int kMaxUnordered = 128;
+
+__host__ __device__ inline size_t ordered_bytes(int B) {
+    return B > kMaxUnordered ? ws_align((size_t(B) + 1) * 4) : 0;
+}
+
+__device__ inline int start_in_range(const int32_t* starts, int i, int N) { return min(max(starts[i], 0), N); }
+
+// s_b from start b in range; for a whole warp.
+__device__ inline int first_token(const int32_t* starts, int b, int B, int N, int start) {
+    int before[kMaxUnordered / 32] = {};
+    if (B <= kMaxUnordered) {
+#pragma unroll
+        for (int u = 0; u < kMaxUnordered / 32; ++u) {
+            const int i = 32 * u + int(threadIdx.x & 31);
+            if (i < b) before[u] = starts[i];
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kMaxUnordered / 32; ++u) start = max(start, min(before[u], N));
+    return __reduce_max_sync(0xffffffffu, start);
+}
+
+// Tokens [lo, hi) of sequence b of B; for a whole warp.
+__device__ inline void sequence(const int32_t* starts, int b, int B, int N, int& lo, int& hi, int* bad) {
+    lo = first_token(starts, b, B, N, start_in_range(starts, b, N));
+    hi = max(start_in_range(starts, b + 1, N), lo);
+    if (starts[b] != lo || starts[b + 1] != hi) *bad |= CANOPY_DEVERR_LENGTH;
+}
+
+// ---------------------------------------------------------------------------
 // Bounded waits use the global nanosecond timer.
 
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s

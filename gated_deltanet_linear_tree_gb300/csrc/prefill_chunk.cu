@@ -31,8 +31,9 @@
 // uneven they are.  The first launch is held by the shared-memory and fp32
 // pipes, the walk by the latency of its three products a chunk.
 //
-// Chunk slots: sequence b's chunk c is slot starts[b] / 64 + b + c; these
-// never collide, and there are at most N / 64 + B of them.
+// Chunk slots: with s_b the first token of sequence b, its chunk c is slot
+// s_b / 64 + b + c; these never collide, and there are at most N / 64 + B of
+// them.
 #include "common.cuh"
 
 namespace canopy {
@@ -71,24 +72,17 @@ struct WsView {
 };
 
 __host__ __device__ inline size_t ws_bytes(int N, int B, int HV) {
-    return 256 + (kMaxRanked + 1) * sizeof(Row) + slot_count(N, B) * HV * (MW_BYTES + GATE_FLOATS * 4);
+    return 256 + ordered_bytes(B) + (kMaxRanked + 1) * sizeof(Row) +
+           slot_count(N, B) * HV * (MW_BYTES + GATE_FLOATS * 4);
 }
 inline WsView ws_view(void* base, int N, int B, int HV) {
     uint8_t* p = static_cast<uint8_t*>(base);
     WsView w;
     w.err = reinterpret_cast<int32_t*>(p);
-    w.rows = reinterpret_cast<Row*>(p + 256);
-    w.mw = p + 256 + (kMaxRanked + 1) * sizeof(Row);
+    w.rows = reinterpret_cast<Row*>(p + 256 + ordered_bytes(B));
+    w.mw = p + 256 + ordered_bytes(B) + (kMaxRanked + 1) * sizeof(Row);
     w.gates = reinterpret_cast<float*>(w.mw + slot_count(N, B) * HV * MW_BYTES);
     return w;
-}
-
-// Tokens [lo, hi) of sequence b (see prefill_scan.cu).
-__device__ inline void sequence(const int32_t* starts, int b, int N, int& lo, int& hi, int* bad) {
-    const int s0 = starts[b], s1 = starts[b + 1];
-    lo = min(max(s0, 0), N);
-    hi = min(max(s1, lo), N);
-    if (s0 != lo || s1 != hi) *bad |= CANOPY_DEVERR_LENGTH;
 }
 
 __device__ inline uint32_t bits(float x) { return __float_as_uint(x); }
@@ -301,12 +295,17 @@ __device__ inline void put_half_row(uint8_t* image, int row, int half, const uin
 constexpr int kWalkCycles = 5000;  // per walk, and
 constexpr int kQuarterCycles = 4000, kHalfCycles = 5700, kWholeCycles = 8300;  // per chunk
 
-__device__ inline void plan_walk(const int32_t* starts, int nseq, int HV, int quarters, Row* rows) {
+__device__ inline void plan_walk(const int32_t* starts, int nseq, int N, int HV, int quarters, Row* rows) {
     __shared__ int sLen[128], sSorted[128], sCount[128];
     __shared__ unsigned long long sBest;
     const int tid = threadIdx.x;
     if (tid == 0) sBest = ~0ull;
-    const int len = tid < nseq ? max(starts[tid + 1] - starts[tid], 0) : 0, chunks = (len + C - 1) / C;
+    sLen[tid] = tid <= nseq ? start_in_range(starts, tid, N) : 0;
+    __syncthreads();
+    int lo = 0;
+    for (int k = 0; k <= tid; ++k) lo = max(lo, sLen[k]);
+    const int len = tid < nseq ? max(sLen[tid + 1] - lo, 0) : 0, chunks = (len + C - 1) / C;
+    __syncthreads();
     sLen[tid] = len;
     __syncthreads();
     int rank = 0;
@@ -389,18 +388,23 @@ __global__ void __launch_bounds__(128, 4)
         prefetch_map(&tmK);
     }
     pdl_wait();
-    if (blockIdx.x == 0 && B <= kMaxRanked) plan_walk(starts, B, HV, quarters, ws.rows);
-    // the sequence whose chunk this slot is: the last b with starts[b] / 64 + b <= slot
-    int b = -1;
-    for (int b0 = 0; b0 < B; b0 += 128) {
-        const int j = b0 + tid;
-        const int here = __syncthreads_count(j < B && min(max(starts[min(j, B)], 0), N) / C + j <= slot);
-        b += here;
-        if (here < 128) break;
+    if (blockIdx.x == 0 && B <= kMaxRanked) plan_walk(starts, B, N, HV, quarters, ws.rows);
+    // The sequence whose chunk this slot is: the last b with s_b / 64 + b <= slot.
+    // With s the running maximum of the starts, the first sequence past the slot
+    // is the least max(i, slot + 1 - starts[i] / 64) of all i.
+    int past = B;
+    for (int b0 = 0; b0 < past; b0 += 128) {
+        int least = past;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = b0 + 32 * u + (tid & 31);
+            if (i < B) least = min(least, max(i, slot + 1 - start_in_range(starts, i, N) / C));
+        }
+        past = __reduce_min_sync(0xffffffffu, least);
     }
-    b = max(b, 0);
+    const int b = max(past - 1, 0);
     int s0, s1, bad = 0;
-    sequence(starts, b, N, s0, s1, &bad);
+    sequence(starts, b, B, N, s0, s1, &bad);
     const int n0 = s0 + C * (slot - (s0 / C + b));
     const int valid = min(C, s1 - n0);  // tokens of this chunk
     if (valid <= 0 || n0 < s0) return;
@@ -816,7 +820,7 @@ __device__ __forceinline__ void walk(const CUtensorMap& tmQ, const CUtensorMap& 
     __syncthreads();
     tc_fence_after();
     int lo, hi, bad = 0;
-    sequence(args.starts, b, N, lo, hi, &bad);
+    sequence(args.starts, b, args.B, N, lo, hi, &bad);
     const int nc = (hi - lo + C - 1) / C;
     const size_t slot0 = size_t(lo / C) + b;
     bool ok = true;

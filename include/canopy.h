@@ -254,10 +254,10 @@ typedef enum {
 } canopy_prefill_plan_t;
 
 /* Size in bytes of the workspace of a prefill over N packed tokens of B
- * sequences with HV value heads: the device error word (offset 0), the order
- * of the sequences (2 KiB), and per
- * 64-token chunk and value head 48 KiB of chunk operands and 768 bytes of
- * gates.  At most floor(N / 64) + B chunks.  Zero it once with
+ * sequences with HV value heads: the device error word (offset 0), the starts
+ * in order where B > 128 (4 (B + 1) bytes), the order of the sequences (2 KiB),
+ * and per 64-token chunk and value head 48 KiB of chunk operands and 768 bytes
+ * of gates.  At most floor(N / 64) + B chunks.  Zero it once with
  * canopy_workspace_init (the error word; the rest is scratch), read the
  * word with canopy_read_device_error.  Returns 0 for unsupported sizes. */
 size_t canopy_prefill_workspace_bytes(int N, int B, int HV, int dk, int dv);
@@ -271,8 +271,9 @@ size_t canopy_prefill_workspace_bytes(int N, int B, int HV, int dk, int dv);
  *   in o_dtype.
  * S_new may alias S0.  Rows of o outside every sequence are not written.  A
  * start outside [0, N] or below the one before it sets CANOPY_DEVERR_LENGTH
- * and is read as the nearest admissible one; gates are checked as the verify
- * checks them.  A sequence's tokens influence no other sequence, whatever
+ * and is read as the nearest admissible one (the nearest of [0, N], and no less
+ * than the one before as that was read); gates are checked as the verify checks
+ * them.  A sequence's tokens influence no other sequence, whatever
  * they hold.  bf16 q/k/v with dk = dv = 128 run in 64-token chunks on the
  * tensor cores (bf16 operands split so that 24 bits of the state, of U and of
  * R enter their products; fp32 accumulation, fp32 states), other inputs and

@@ -100,9 +100,15 @@ __device__ inline float4 load4(const __nv_bfloat16* p) {
 __device__ inline void store_out(float* p, float x) { *p = x; }
 __device__ inline void store_out(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-// Gate checks shared by every kernel: alpha must be finite and > 0, beta finite.
+// Gate checks: alpha must be finite and > 0 where its logarithm is taken, beta
+// finite.
 __device__ inline bool gate_ok(float a, float b) {
     return (a > 0.f) && isfinite(a) && isfinite(b);
+}
+// The same where the gates are only multiplied: zero (what a decay that
+// underflows leaves) forgets the state before the token.
+__device__ inline bool decay_ok(float a, float b) {
+    return (a >= 0.f) && isfinite(a) && isfinite(b);
 }
 
 __device__ inline void raise_err(int32_t* err, int bits) { atomicOr(err, bits); }

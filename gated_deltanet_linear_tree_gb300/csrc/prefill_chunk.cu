@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(128, 4)
         if (n < valid) {
             a = g[size_t(n0 + n) * HV + h + tid / C];
             be = beta[size_t(n0 + n) * HV + h + tid / C];
-            if (!gate_ok(a, be)) {
+            if (!decay_ok(a, be)) {
                 bad |= CANOPY_DEVERR_GATE;
                 a = 1.f;
                 be = 0.f;

@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(NT, R == 1 ? 4 : 3) scan_kernel(const InT* __r
 #pragma unroll
         for (int e = 0; e < VP; ++e) sV[buf][(t + e * NT) / ROWS][(t + e * NT) % ROWS] = to_f(nv[e]);
         if (t < TB) {
-            if (!gate_ok(ng, nb)) {
+            if (!decay_ok(ng, nb)) {
                 bad |= CANOPY_DEVERR_GATE;
                 ng = 1.f;
                 nb = 0.f;

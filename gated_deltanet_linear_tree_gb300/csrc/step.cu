@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(128) step_kernel(const InT* __restrict__ q, co
     for (int c = 0; c < C4; ++c) qq[c] = load4(q + key + (c * 8 + gl) * 4);
     const float vv = to_f(v[unit * D + r]);
     float a = g[unit], be = beta[unit];
-    if (!gate_ok(a, be)) {
+    if (!decay_ok(a, be)) {
         if (err && t == 0 && blockIdx.x == 0) raise_err(err, CANOPY_DEVERR_GATE);
         a = 1.f;
         be = 0.f;

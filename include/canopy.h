@@ -33,9 +33,9 @@
  *   - Device pointers must be 16-byte aligned (vector and TMA loads).
  *   - Argument errors are detected on the host and returned before anything
  *     is enqueued.  Errors that depend on device data (a malformed tree, a
- *     gate <= 0 or not finite, an accepted node out of range, an internal
- *     wait that timed out) set bits in a sticky device error word inside the
- *     workspace; the outputs of that call are then undefined.  Read and clear
+ *     gate <= 0 (prefill and step: < 0) or not finite, an accepted node out of
+ *     range, an internal wait that timed out) set bits in a sticky device error
+ *     word inside the workspace; the outputs of that call are then undefined.  Read and clear
  *     the word with canopy_read_device_error().  No kernel traps or asserts.
  *   - Sizes supported: 1 <= T <= 256, B >= 1, H >= 1, HV a multiple of H
  *     (HV = H where an entry point takes one head count), dk = dv = 128 for every
@@ -109,7 +109,7 @@ typedef enum {
 
 /* Bits of the device error word. */
 #define CANOPY_DEVERR_TREE     0x1  /* parent[b][0] != -1 or parent[b][i] not in [0,i) */
-#define CANOPY_DEVERR_GATE     0x2  /* g <= 0, g or beta not finite                     */
+#define CANOPY_DEVERR_GATE     0x2  /* g <= 0 (prefill, step: < 0), g or beta not finite */
 #define CANOPY_DEVERR_ACCEPTED 0x4  /* commit: accepted node not in [-1, T)             */
 #define CANOPY_DEVERR_TIMEOUT  0x8  /* an internal bounded wait gave up                 */
 #define CANOPY_DEVERR_LENGTH   0x10 /* lengths[b] not in [0, T], or starts out of order  */
@@ -272,8 +272,9 @@ size_t canopy_prefill_workspace_bytes(int N, int B, int HV, int dk, int dv);
  * S_new may alias S0.  Rows of o outside every sequence are not written.  A
  * start outside [0, N] or below the one before it sets CANOPY_DEVERR_LENGTH
  * and is read as the nearest admissible one (the nearest of [0, N], and no less
- * than the one before as that was read); gates are checked as the verify checks
- * them.  A sequence's tokens influence no other sequence, whatever
+ * than the one before as that was read).  A gate of zero forgets the state; a
+ * negative one, or a gate or write strength that is not finite, sets
+ * CANOPY_DEVERR_GATE and is read with its partner as g = 1, beta = 0.  A sequence's tokens influence no other sequence, whatever
  * they hold.  bf16 q/k/v with dk = dv = 128 run in 64-token chunks on the
  * tensor cores (bf16 operands split so that 24 bits of the state, of U and of
  * R enter their products; fp32 accumulation, fp32 states), other inputs and
@@ -293,7 +294,8 @@ canopy_prefill_plan_t canopy_prefill_plan(int N, int B, int H, int HV, canopy_dt
  *   q, k device [B][H][dk], v device [B][HV][dv] in in_dtype; g, beta device
  *   fp32 [B][HV]; S, S_new device fp32 [B][HV][dv][dk] (S_new may be S); o
  *   device [B][HV][dv] in o_dtype; err: optional device int32 that receives
- *   device error bits (OR-ed), or NULL. */
+ *   device error bits (OR-ed), or NULL.  Gates are read as canopy_prefill reads
+ *   them. */
 canopy_status canopy_step(const void* q, const void* k, const void* v, canopy_dtype in_dtype, const float* g,
                           const float* beta, const float* S, float* S_new, int B, int H, int HV, int dk, int dv,
                           float scale, void* o, canopy_dtype o_dtype, int32_t* err, void* stream);

@@ -20,13 +20,15 @@
 // right operand's parts stand side by side along N, so that the left operand
 // is read once for all of them (16 of K take 46 to 56 cycles for N = 32 to 96,
 // 64 for 128 and 96 for 192, and the first is seen after 470), and
-// products of parts below 2^-24 of the result are left out.  W's third part
-// is left out of U where that shortens the way to it (one chain, below):
-// 2^-18 of W's entries off its unit diagonal.  All accumulation is fp32 and S
-// itself stays in fp32 registers across chunks.
+// products of parts below 2^-24 of the result are left out, the same ones in
+// every shape of a block (below), so that a sequence comes out the same beside
+// any others.  (U without W's third part, 2^-18 of its entries off the unit
+// diagonal, saves the quarter of a state 250 cycles a chunk and left the state
+// up to 6e-6 of its rms off on aligned keys.)  All accumulation is fp32 and S
+// itself stays in fp32 across chunks.
 //
 // Measured (32 value heads of 16 key heads, both launches in a loop): one
-// sequence of 16,384 tokens 652 us, of which the walk 510; sixteen of 8,191
+// sequence of 16,384 tokens 688 us, of which the walk 545; sixteen of 8,191
 // together 229 (81 and 150); eight of 32,768 together 890 to 950, by how
 // uneven they are.  The first launch is held by the shared-memory and fp32
 // pipes, the walk by the latency of its three products a chunk.
@@ -293,7 +295,7 @@ __device__ inline void put_half_row(uint8_t* image, int row, int half, const uin
 // average 0.6 % longer, at most 13 %, in a simulation of the launch than by
 // the best of these plans.
 constexpr int kWalkCycles = 5000;  // per walk, and
-constexpr int kQuarterCycles = 4000, kHalfCycles = 5700, kWholeCycles = 8300;  // per chunk
+constexpr int kQuarterCycles = 4250, kHalfCycles = 5700, kWholeCycles = 8300;  // per chunk
 
 __device__ inline void plan_walk(const int32_t* starts, int nseq, int N, int HV, int quarters, Row* rows) {
     __shared__ int sLen[128], sSorted[128], sCount[128];
@@ -619,15 +621,13 @@ __global__ void __launch_bounds__(128, 4)
 
 constexpr int WARPS = 8;         // compute warps per chain
 
-enum { CB_X, CB_OU, CB_O2, CB_DS, CB_S, CB_R, CB_U, CB_N };  // a chain's barriers (from CB_S on: its warps arrive)
+enum { CB_X, CB_OU, CB_DS, CB_S, CB_R, CB_U, CB_N };  // a chain's barriers (from CB_S on: its warps arrive)
 enum { PB_QK = 0, PB_QKE = 2, PB_MW = 4, PB_MWE = 6, PB_LO = 8, PB_LOE, PB_N };  // tiles: full and empty
 
 // Three shapes of a block:
 //   <32, 1>  a quarter of a state: one chain, where there are few states, or
 //            one sequence that the others wait for, and a chunk's latency
-//            counts.  U is apart from R, so that the third part's products need
-//            not be over before U is taken on (16 warps of 8 columns were no
-//            faster);
+//            counts (16 warps of 8 columns were no faster);
 //   <32, 2>  half a state: two chains half a chunk apart, one's products
 //            beside the other's register work;
 //   <64, 2>  a whole state: [Q; K] and [M; W] are read once for all of it, and
@@ -635,7 +635,7 @@ enum { PB_QK = 0, PB_QKE = 2, PB_MW = 4, PB_MWE = 6, PB_LO = 8, PB_LOE, PB_N }; 
 //            does not fit twice shares its place: R and U the shared memory
 //            of S, o and U the tensor memory of X, [M; W] has one buffer, and
 //            S itself is in tensor memory.
-// A chunk takes about 3,900, 5,400 to 5,900 and 8,200 cycles in them.
+// A chunk takes about 4,150, 5,400 to 5,900 and 8,200 cycles in them.
 template <int NV_, int NCH_>
 struct Shape {
     static constexpr int NV = NV_, NCH = NCH_;
@@ -644,20 +644,19 @@ struct Shape {
     static constexpr int SPART = D * ROW;         // one part of S
     static constexpr int RPART = C * ROW;         // one part of R (and U)
     static constexpr uint32_t SWIZZLE = NV == 64 ? 2 : 4;  // rows of 128 or 64 bytes, the swizzle of that width
-    static constexpr bool LATE = NCH == 1, TIGHT = NV == 64;
+    static constexpr bool TIGHT = NV == 64;
     // TMEM columns of a chain: [X_Q; X_K] and later K^T U in three groups,
-    // [o; U] in three, the third part's share of o, S
-    static constexpr uint32_t TX = 0, TO = TIGHT ? 0 : 3 * NV, TL = 6 * NV, TS = 3 * NV;
-    static constexpr uint32_t COLS = TIGHT ? 4 * NV : LATE ? 7 * NV : 6 * NV;
+    // [o; U] in three, S
+    static constexpr uint32_t TX = 0, TO = TIGHT ? 0 : 3 * NV, TS = 3 * NV;
+    static constexpr uint32_t COLS = TIGHT ? 4 * NV : 6 * NV;
     static_assert(NCH * COLS <= 512, "tensor memory");
     // shared memory: [Q; K] twice; parts 0 and 1 of [M; W] (twice, or once), part 2
     static constexpr int MW_BUFS = TIGHT ? 1 : 2;
     static constexpr int QK = 0, MW = QK + 2 * QK_BYTES, LO = MW + MW_BUFS * 2 * MW_PART;
     static constexpr int S = LO + MW_PART;
-    static constexpr int R = TIGHT ? S : S + NCH * 3 * SPART;
-    static constexpr int U = LATE ? R + NCH * 3 * RPART : R;
+    static constexpr int R = TIGHT ? S : S + NCH * 3 * SPART;  // and U
     static constexpr int CHAIN_R = TIGHT ? 3 * SPART : 3 * RPART;  // from one chain's R to the next's
-    static constexpr int BAR = TIGHT ? S + NCH * 3 * SPART : U + NCH * 3 * RPART;
+    static constexpr int BAR = TIGHT ? S + NCH * 3 * SPART : R + NCH * 3 * RPART;
     static constexpr int SLOT = BAR + (PB_N + NCH * CB_N) * 8;
     static constexpr int TOTAL = SLOT + 8;
     static_assert(TOTAL <= 227 * 1024, "shared memory");
@@ -874,7 +873,6 @@ __device__ __forceinline__ void walk(const CUtensorMap& tmQ, const CUtensorMap& 
             uint64_t* cb = pb + PB_N + ch * CB_N;
             const uint32_t tmem = *sTmem + ch * P::COLS;
             const uint32_t aS = smem_u32(sm + P::S + ch * 3 * P::SPART), aR = smem_u32(sm + P::R + ch * P::CHAIN_R);
-            const uint32_t aU = smem_u32(sm + P::U + ch * P::CHAIN_R);
             const uint32_t aLo = smem_u32(sm + P::LO);
             constexpr uint32_t i3 = idesc_bf16(128, 3 * NV) | kMajorB, i2 = idesc_bf16(128, 2 * NV) | kMajorB,
                                i1 = idesc_bf16(128, NV) | kMajorB;
@@ -912,13 +910,11 @@ __device__ __forceinline__ void walk(const CUtensorMap& tmQ, const CUtensorMap& 
                 for (int ks = 0; ks < 4; ++ks)
                     mma_bf16_ss(tmem + P::TO, sdesc(aMW + MW_PART + ks * 32, 0, 1024, 2),
                                 sdesc(aR + ks * 16 * P::ROW, P::RPART, 8 * P::ROW, P::SWIZZLE), i2, 1);
-                if (P::LATE) mma_commit(&cb[CB_OU]);
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    mma_bf16_ss(tmem + (P::LATE ? P::TL : P::TO), sdesc(aLo + ks * 32, 0, 1024, 2),
-                                sdesc(aR + ks * 16 * P::ROW, P::RPART, 8 * P::ROW, P::SWIZZLE), i1,
-                                !P::LATE || ks != 0);
-                mma_commit(&cb[P::LATE ? CB_O2 : CB_OU]);
+                    mma_bf16_ss(tmem + P::TO, sdesc(aLo + ks * 32, 0, 1024, 2),
+                                sdesc(aR + ks * 16 * P::ROW, P::RPART, 8 * P::ROW, P::SWIZZLE), i1, 1);
+                mma_commit(&cb[CB_OU]);
                 mma_commit(&pb[PB_MWE + ms]);
                 mma_commit(&pb[PB_LOE]);
                 if (!(ok = mbar_wait(&cb[CB_U], par))) break;
@@ -926,7 +922,7 @@ __device__ __forceinline__ void walk(const CUtensorMap& tmQ, const CUtensorMap& 
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
                     mma_bf16_ss(tmem + P::TX, sdesc(aQK + 2048 + ks * 4096, 16384, 1024, 2),
-                                sdesc(aU + ks * 16 * P::ROW, P::RPART, 8 * P::ROW, P::SWIZZLE),
+                                sdesc(aR + ks * 16 * P::ROW, P::RPART, 8 * P::ROW, P::SWIZZLE),
                                 i3 | kMajorA, ks != 0);
                 mma_commit(&cb[CB_DS]);
                 mma_commit(&pb[PB_QKE + s]);
@@ -939,7 +935,6 @@ __device__ __forceinline__ void walk(const CUtensorMap& tmQ, const CUtensorMap& 
         uint64_t* cb = pb + PB_N + ch * CB_N;
         uint8_t* sS = sm + P::S + ch * 3 * P::SPART;
         uint8_t* sR = sm + P::R + ch * P::CHAIN_R;
-        uint8_t* sU = sm + P::U + ch * P::CHAIN_R;
         const uint32_t taddr = *sTmem + ch * P::COLS + (uint32_t(quad * 32) << 16) + part * HN;
         const int krow = quad * 32 + lane;          // key row of S^T
         const int col = v0 + ch * NV + part * HN;   // first value column of this warp
@@ -1061,7 +1056,7 @@ __device__ __forceinline__ void walk(const CUtensorMap& tmQ, const CUtensorMap& 
             sum_rows16<P, 3>(taddr + (16u << 16) + P::TO, x);
 #pragma unroll
             for (int r = 0; r < NP; ++r) x[r] = mul2(de[r / G8], x[r]);
-            put_rows16<P>(sU, quad * 16, c0, lane, x);
+            put_rows16<P>(sR, quad * 16, c0, lane, x);  // U, where R was
             fence_proxy_async_smem();
             __syncwarp();
             if (P::TIGHT) {  // (the last product goes where o is)
@@ -1071,14 +1066,6 @@ __device__ __forceinline__ void walk(const CUtensorMap& tmQ, const CUtensorMap& 
             }
             if (lane == 0) mbar_arrive(&cb[CB_U]);
             if (!P::TIGHT) sum_rows16<P, 3>(taddr + P::TO, x);
-            if (P::LATE) {
-                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&cb[CB_O2], par)))) break;
-                tc_fence_after();
-                uint64_t z[NP];
-                sum_rows16<P, 1>(taddr + P::TL, z);
-#pragma unroll
-                for (int r = 0; r < NP; ++r) x[r] = add2(x[r], z[r]);
-            }
             {
                 const uint64_t sc = pack2(scale, scale);
 #pragma unroll

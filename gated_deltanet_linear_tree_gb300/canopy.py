@@ -312,6 +312,11 @@ def _need_all(dev: int, *specs):
             raise CanopyError(f"{name} must be on the same device as the other tensors")
 
 
+def _need_given(dev: int, *specs):
+    """_need_all for those of the tensors that are not None."""
+    _need_all(dev, *(spec for spec in specs if spec[0] is not None))
+
+
 def _raw_stream(dev: int) -> int:
     """The current stream's handle on CUDA device `dev`."""
     return torch._C._cuda_getCurrentRawStream(dev)
@@ -366,22 +371,18 @@ def prefill(q, k, v, g, beta, S0, starts, ws, o_dtype=torch.float32, out=None, S
     _need_all(dev, (q, "q", dt, q.shape), (k, "k", dt, q.shape), (v, "v", dt, v.shape), (g, "g", f32, (N, HV)),
               (beta, "beta", f32, (N, HV)), (starts, "starts", torch.int32, starts.shape),
               (ws, "workspace", torch.uint8, ws.shape))
-    if S0 is not None:
-        _need_all(dev, (S0, "S0", f32, state))
+    _need_given(dev, (S0, "S0", f32, state), (out, "o", None, v.shape), (S_out, "S_new", f32, state))
     lib = load()
     if ws.numel() < lib.canopy_prefill_workspace_bytes(N, B, HV, dk, dv):
         raise CanopyError("the workspace is too small for these sizes")
-    if out is None:
-        out = torch.empty(v.shape, dtype=o_dtype, device=q.device)
-    else:
-        _need(out, "o", None, v.shape)
-    if S_out is None:
-        S_out = torch.empty(state, dtype=f32, device=q.device)
-    else:
-        _need(S_out, "S_new", f32, state)
-    st = lib.canopy_prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dt(q), g.data_ptr(), beta.data_ptr(), _opt(S0),
-                            starts.data_ptr(), N, B, H, HV, dk, dv, scale, out.data_ptr(), _dt(out), S_out.data_ptr(),
-                            ws.data_ptr(), PREFILL_FORCE[force], _raw_stream(dev))
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty(v.shape, dtype=o_dtype, device=q.device)
+        if S_out is None:
+            S_out = torch.empty(state, dtype=f32, device=q.device)
+        st = lib.canopy_prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dt(q), g.data_ptr(), beta.data_ptr(),
+                                _opt(S0), starts.data_ptr(), N, B, H, HV, dk, dv, scale, out.data_ptr(), _dt(out),
+                                S_out.data_ptr(), ws.data_ptr(), PREFILL_FORCE[force], _raw_stream(dev))
     _check(st, "canopy_prefill")
     return out, S_out
 
@@ -407,19 +408,16 @@ def step(q, k, v, g, beta, S, o_dtype=torch.float32, out=None, S_out=None, scale
     dt, f32, dev = q.dtype, torch.float32, q.get_device()
     _need_all(dev, (q, "q", dt, q.shape), (k, "k", dt, q.shape), (v, "v", dt, v.shape), (g, "g", f32, (B, HV)),
               (beta, "beta", f32, (B, HV)), (S, "S", f32, state))
-    if err is not None:
-        _need(err, "err", torch.int32, (1,))
-    if out is None:
-        out = torch.empty(v.shape, dtype=o_dtype, device=q.device)
-    else:
-        _need(out, "o", None, v.shape)
-    if S_out is None:
-        S_out = torch.empty_like(S)
-    else:
-        _need_all(dev, (S_out, "S_new", f32, state))
-    st = load().canopy_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dt(q), g.data_ptr(), beta.data_ptr(),
-                            S.data_ptr(), S_out.data_ptr(), B, H, HV, dk, dv, scale, out.data_ptr(), _dt(out),
-                            _opt(err), _raw_stream(dev))
+    _need_given(dev, (out, "o", None, v.shape), (S_out, "S_new", f32, state), (err, "err", torch.int32, (1,)))
+    lib = load()
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty(v.shape, dtype=o_dtype, device=q.device)
+        if S_out is None:
+            S_out = torch.empty_like(S)
+        st = lib.canopy_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dt(q), g.data_ptr(), beta.data_ptr(),
+                             S.data_ptr(), S_out.data_ptr(), B, H, HV, dk, dv, scale, out.data_ptr(), _dt(out),
+                             _opt(err), _raw_stream(dev))
     _check(st, "canopy_step")
     return out, S_out
 
@@ -445,18 +443,15 @@ def accept(p, tokens, parent, u, noise, q=None, lengths=None, err=None):
     i32, f32, dev = torch.int32, torch.float32, p.get_device()
     _need_all(dev, (p, "p", p.dtype, p.shape), (tokens, "tokens", i32, (B, T)), (parent, "parent", i32, (B, T)),
               (u, "u", f32, (B, T)), (noise, "noise", f32, (B, V)))
-    if q is not None:
-        _need_all(dev, (q, "q", p.dtype, p.shape))
-    if lengths is not None:
-        _need(lengths, "lengths", i32, (B,))
-    if err is not None:
-        _need(err, "err", i32, (1,))
-    accepted = torch.empty((B,), dtype=i32, device=p.device)
-    out_tokens = torch.empty_like(tokens)
-    counts = torch.empty_like(accepted)
-    st = load().canopy_accept(p.data_ptr(), _opt(q), _dt(p), tokens.data_ptr(), parent.data_ptr(), _opt(lengths),
-                              u.data_ptr(), noise.data_ptr(), T, B, V, accepted.data_ptr(), out_tokens.data_ptr(),
-                              counts.data_ptr(), _opt(err), _raw_stream(dev))
+    _need_given(dev, (q, "q", p.dtype, p.shape), (lengths, "lengths", i32, (B,)), (err, "err", i32, (1,)))
+    lib = load()
+    with torch.cuda.device(dev):
+        accepted = torch.empty((B,), dtype=i32, device=p.device)
+        out_tokens = torch.empty_like(tokens)
+        counts = torch.empty_like(accepted)
+        st = lib.canopy_accept(p.data_ptr(), _opt(q), _dt(p), tokens.data_ptr(), parent.data_ptr(), _opt(lengths),
+                               u.data_ptr(), noise.data_ptr(), T, B, V, accepted.data_ptr(), out_tokens.data_ptr(),
+                               counts.data_ptr(), _opt(err), _raw_stream(dev))
     _check(st, "canopy_accept")
     return accepted, out_tokens, counts
 

@@ -431,13 +431,12 @@ template <typename PT>
 cudaError_t launch(const void* p, const void* q, const int32_t* tokens, const int32_t* parent, const int32_t* lengths,
                    const float* u, const float* noise, int T, int B, int V, int32_t* accepted, int32_t* out,
                    int32_t* count, int32_t* err, cudaStream_t st) {
-    static const cudaError_t attrs = [] {
-        cudaError_t e = cudaFuncSetAttribute(accept_kernel<PT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(accept_kernel<PT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxHeld * 8);
-        return e;
-    }();
-    if (attrs != cudaSuccess) return attrs;
+    static OncePerDevice attrs;
+    const cudaError_t e = attrs([] {
+        const cudaError_t e = cudaFuncSetAttribute(accept_kernel<PT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        return e != cudaSuccess ? e : allow_smem(accept_kernel<PT>, kMaxHeld * 8);
+    });
+    if (e != cudaSuccess) return e;
     // As many blocks as full slices take, whatever their number: with the next
     // power of two 48 streams of 50,021 tokens take 23.6 us for 22.3, 100 of them
     // 37 for 33, eight (all at once either way) 11.2 for 11.8.

@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/canopy.h"
 
 namespace canopy {
@@ -206,6 +208,29 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// What a kernel asks for (its attributes), once on each device: a static object
+// per launch, given what sets them on the current device.
+class OncePerDevice {
+    std::atomic<uint64_t> done{0};  // a bit per device; beyond 64 every call sets them
+
+public:
+    template <typename F>
+    cudaError_t operator()(F&& set) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+        if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+        e = set();
+        if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+        return e;
+    }
+};
+template <typename... KArgs>
+inline cudaError_t allow_smem(void (*kernel)(KArgs...), int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
 // ---- mbarrier --------------------------------------------------------------

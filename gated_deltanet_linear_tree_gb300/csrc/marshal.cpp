@@ -9,12 +9,14 @@
 // otherwise it returns None, having done nothing, and the Python side goes
 // through its own checks, which say what is wrong.  The library's entry
 // points are handed over by address, so that this module links against torch
-// only and the library against nothing of it.
+// only and the library against nothing of it.  The library works on the current
+// device: the tensors' is made current for the call.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -143,6 +145,7 @@ PyObject* step(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor* S = plain(a[5], dev, at::kFloat, {B, HV, dv, dk});
         bool ok = k && g && beta && S && v->size(0) == B && v->scalar_type() == q->scalar_type();
         const at::Tensor* err = maybe(a[10], dev, at::kInt, {1}, ok);
+        const c10::cuda::OptionalCUDAGuard on(at::Device(at::kCUDA, at::DeviceIndex(dev)));
         at::Tensor out, S_out;
         if (!ok || !output(a[7], dev, ot, {B, HV, dv}, out) || !output(a[8], dev, at::kFloat, {B, HV, dv, dk}, S_out))
             return none();
@@ -174,6 +177,7 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor *g = plain(a[3], dev, at::kFloat, {N, HV}), *beta = plain(a[4], dev, at::kFloat, {N, HV});
         bool ok = k && g && beta && v->size(0) == N && v->scalar_type() == q->scalar_type() && N <= INT32_MAX;
         const at::Tensor* S0 = maybe(a[5], dev, at::kFloat, {B, HV, dv, dk}, ok);
+        const c10::cuda::OptionalCUDAGuard on(at::Device(at::kCUDA, at::DeviceIndex(dev)));
         at::Tensor out, S_out;
         if (!ok || size_t(ws->numel()) < prefill_bytes_fn(int(N), int(B), int(HV), int(dk), int(dv)) ||
             !output(a[9], dev, ot, {N, HV, dv}, out) || !output(a[10], dev, at::kFloat, {B, HV, dv, dk}, S_out))
@@ -204,6 +208,7 @@ PyObject* accept(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor* lengths = maybe(a[6], dev, at::kInt, {B}, ok);
         const at::Tensor* err = maybe(a[7], dev, at::kInt, {1}, ok);
         if (!ok) return none();
+        const c10::cuda::OptionalCUDAGuard on(at::Device(at::kCUDA, at::DeviceIndex(dev)));
         const at::Tensor accepted = fresh({B}, at::kInt, dev), out = fresh({B, T}, at::kInt, dev),
                          counts = fresh({B}, at::kInt, dev);
         const canopy_status st =

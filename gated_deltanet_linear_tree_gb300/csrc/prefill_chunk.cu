@@ -1151,14 +1151,12 @@ cudaError_t launch_walk(bool many, const CUtensorMap& mq, const CUtensorMap& mk,
     static constexpr int one = Shape<32, 1>::TOTAL, half = Shape<32, 2>::TOTAL, whole = Shape<64, 2>::TOTAL;
     static constexpr int two = half > whole ? half : whole;  // of the shapes that meet in one launch
     static_assert(two >= one, "shared memory");
-    static const cudaError_t attr = [] {
-        const cudaError_t e =
-            cudaFuncSetAttribute(walk_kernel<OutT>, cudaFuncAttributeMaxDynamicSharedMemorySize, one);
-        return e != cudaSuccess ? e
-                                : cudaFuncSetAttribute(walk_many_kernel<OutT>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, two);
-    }();
-    if (attr != cudaSuccess) return attr;
+    static OncePerDevice attrs;
+    const cudaError_t e = attrs([] {
+        const cudaError_t e = allow_smem(walk_kernel<OutT>, one);
+        return e != cudaSuccess ? e : allow_smem(walk_many_kernel<OutT>, two);
+    });
+    if (e != cudaSuccess) return e;
     const unsigned states = unsigned(args.B) * args.HV;
     if (many)
         return launch_pdl(walk_many_kernel<OutT>, dim3(states + (args.B <= kMaxRanked ? more_blocks(args.HV) * args.HV : 0)),
@@ -1194,16 +1192,16 @@ cudaError_t launch_prefill_chunk(const void* q, const void* k, const void* v, co
         return cudaErrorInvalidValue;
     const pfc::WsView ws = pfc::ws_view(workspace, N, B, HV);
     const int smem = pfc::PrepSmem::TOTAL;
-    static const cudaError_t attr =
-        cudaFuncSetAttribute(pfc::prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (attr != cudaSuccess) return attr;
+    static OncePerDevice attrs;
+    cudaError_t e = attrs([=] { return allow_smem(pfc::prep_kernel, smem); });
+    if (e != cudaSuccess) return e;
     // Two value heads of one key head share a block, its [Q; K] and their
     // product, where there are many blocks all the same.
     const bool many = many_states(B, HV);
     const size_t pairs = pfc::slot_count(N, B) * HV;
     const int heads = (HV / H) % 2 == 0 && pairs >= kPairFrom ? 2 : 1;
-    const cudaError_t e = launch_pdl(pfc::prep_kernel, dim3(unsigned(pairs / heads)), dim3(128), smem, st, pq, pk, g,
-                                     beta, starts, N, B, HV, HV / H, heads, !many, ws);
+    e = launch_pdl(pfc::prep_kernel, dim3(unsigned(pairs / heads)), dim3(128), smem, st, pq, pk, g, beta, starts, N, B,
+                   HV, HV / H, heads, !many, ws);
     if (e != cudaSuccess) return e;
     const pfc::WalkArgs args = {static_cast<const __nv_bfloat16*>(v), S0, S_new, starts, N, B, HV, HV / H, scale, ws};
     return o_bf16 ? pfc::launch_walk(many, mq, mk, args, static_cast<__nv_bfloat16*>(o), st)

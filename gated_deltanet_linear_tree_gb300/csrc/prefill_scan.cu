@@ -246,9 +246,9 @@ cudaError_t launch_rows(const void* q, const void* k, const void* v, const float
     // With more blocks than SMs but at most two for each, shared memory that
     // is not used keeps a third from an SM: 64 states 31 us instead of 41.
     constexpr int kTwoPerSM = 42 * 1024;
-    static const cudaError_t attr = cudaFuncSetAttribute(scan_kernel<InT, OutT, D, R>,
-                                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kTwoPerSM);
-    if (attr != cudaSuccess) return attr;
+    static OncePerDevice attrs;
+    const cudaError_t e = attrs([] { return allow_smem(scan_kernel<InT, OutT, D, R>, kTwoPerSM); });
+    if (e != cudaSuccess) return e;
     const size_t blocks = size_t(D / (16 * R)) * HV * B;
     const int unused = D == 128 && blocks > kSMs && blocks <= 2 * kSMs ? kTwoPerSM : 0;
     return launch_pdl(scan_kernel<InT, OutT, D, R>, dim3(D / (16 * R), HV, B), dim3(NT), unused, st,
@@ -260,8 +260,8 @@ template <typename InT, typename OutT, int D>
 cudaError_t launch(const void* q, const void* k, const void* v, const float* g, const float* beta, const float* S0,
                    float* S_new, const int32_t* starts, void* o, int N, int B, int H, int HV, float scale,
                    int32_t* err, cudaStream_t st) {
-    return (size_t(D / 16) * HV * B <= kSMs ? launch_rows<InT, OutT, D, 1> : launch_rows<InT, OutT, D, 2>)(q, k, v, g, beta, S0, S_new, starts, o, N,
-                                                                            B, H, HV, scale, err, st);
+    const auto rows = size_t(D / 16) * HV * B <= kSMs ? launch_rows<InT, OutT, D, 1> : launch_rows<InT, OutT, D, 2>;
+    return rows(q, k, v, g, beta, S0, S_new, starts, o, N, B, H, HV, scale, err, st);
 }
 
 }  // namespace scan

@@ -30,7 +30,8 @@
  *       S0       [B][HV][dv][dk]  fp32
  *       parent   [B][T]           int32, parent[b][0] = -1, 0 <= parent[b][i] < i
  *       o        [B][T][HV][dv]   fp32 or bf16 (o_dtype)
- *   - Device pointers must be 16-byte aligned (vector and TMA loads).
+ *   - Device pointers must be 16-byte aligned (vector and TMA loads), and the
+ *     device that they and the stream belong to has to be the current one.
  *   - Argument errors are detected on the host and returned before anything
  *     is enqueued.  Errors that depend on device data (a malformed tree, a
  *     gate <= 0 (prefill and step: < 0) or not finite, an accepted node out of

@@ -18,8 +18,10 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <exception>
 #include <initializer_list>
 
 #include "../../include/canopy.h"
@@ -101,15 +103,14 @@ PyObject* pair_of(PyObject* given_a, const at::Tensor& a, PyObject* given_b, con
     return r;
 }
 
-// C++ exceptions (an allocation that fails) become Python ones.
+// C++ exceptions become the Python ones that torch raises for them (an
+// allocation that fails torch.OutOfMemoryError).
 template <typename F>
 PyObject* guarded(F&& f) {
     try {
         return f();
-    } catch (const c10::OutOfMemoryError& e) {
-        PyErr_SetString(PyExc_MemoryError, e.what_without_backtrace());
-    } catch (const std::exception& e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {
+        torch::translate_exception_to_python(std::current_exception());
     }
     return nullptr;
 }

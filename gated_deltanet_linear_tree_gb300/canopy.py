@@ -3,7 +3,8 @@
 Argument marshalling only: every step of the path runs in the library's
 CUDA kernels.  (The calls of a few microseconds, step, prefill and accept, go
 through the native _marshal.so, which checks their arguments, allocates their
-outputs and makes the call; the Python code here is for what it turns down.)
+outputs and makes the call; the Python code here is for what it turns down, and
+for all of them where that file is missing or built for another torch.)
 Tensors are torch CUDA tensors (torch provides device memory
 and the current stream); the calls are enqueued on
 ``torch.cuda.current_stream()`` and return without synchronising.  If the
@@ -14,8 +15,11 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 
 import torch
+
+from .build import marshal_tag
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libcanopy.so")
@@ -74,17 +78,38 @@ class CanopyError(RuntimeError):
     pass
 
 
+class _NoMarshal:
+    """In place of _marshal.so: turns every call down."""
+
+    @staticmethod
+    def _none(*args):
+        return None
+
+    bind = step = prefill = accept = _none
+
+
+def _native():
+    """_marshal.so, or where it does not load, or was built for another Python or torch, what stands in for it."""
+    try:
+        from . import _marshal as marshal
+        built_for = getattr(marshal, "built_for", "something else")
+        if built_for == marshal_tag():
+            return marshal
+        why = f"was built for {built_for}, not {marshal_tag()}"
+    except ImportError as e:
+        why = f"does not load ({e})"
+    warnings.warn(f"_marshal.so {why}: step, prefill and accept take 10 us more of host time a call; "
+                  "gated_deltanet_linear_tree_gb300.build.build() builds it")
+    return _NoMarshal
+
+
 def load(path: str = LIB_PATH):
     """Load the shared library (no CUDA call is made by loading)."""
     global _lib, _marshal
     if _lib is None:
         if not os.path.exists(path):
             raise CanopyError(f"{path} is missing: build it with gated_deltanet_linear_tree_gb300.build.build()")
-        try:
-            from . import _marshal as marshal
-        except ImportError as e:
-            raise CanopyError(f"_marshal.so does not load ({e}): build it with "
-                              "gated_deltanet_linear_tree_gb300.build.build()") from e
+        marshal = _native()
         lib = ctypes.CDLL(path)
         for name, (res, args) in SIGNATURES.items():
             fn = getattr(lib, name)

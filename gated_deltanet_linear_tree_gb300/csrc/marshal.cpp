@@ -268,4 +268,13 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods};
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal() { return PyModule_Create(&module); }
+// built_for: the Python and torch that this file was compiled for, which the
+// binding compares with those that it runs on.
+PyMODINIT_FUNC PyInit__marshal() {
+    PyObject* m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_for", CANOPY_MARSHAL_TAG) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

@@ -319,7 +319,6 @@ __global__ void __launch_bounds__(NT, 4) accept_kernel(const PT* __restrict__ p,
                 }
                 if (lane == 0) sh.z[refused] = Z;
                 ++refused;
-                more = false;
                 for (int v = 0; v < words; ++v) {  // what is left at the later siblings' tokens
                     const int j = 32 * v + lane;
                     if (j > c && (sh.kids[cur * words + v] >> lane & 1)) {

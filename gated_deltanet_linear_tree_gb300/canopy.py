@@ -6,7 +6,8 @@ through the native _marshal.so, which checks their arguments, allocates their
 outputs and makes the call; the Python code here is for what it turns down, and
 for all of them where that file is missing or built for another torch.)
 Tensors are torch CUDA tensors (torch provides device memory
-and the current stream); the calls are enqueued on
+and the current stream), contiguous and on 16 bytes: a slice that starts
+elsewhere is "invalid argument" and wants a clone().  The calls are enqueued on
 ``torch.cuda.current_stream()`` and return without synchronising.  If the
 library has not been built, loading fails loudly: there is no fallback.
 """

@@ -27,11 +27,15 @@
 // has to be read is the last node's rows and the noise, once: 4 to 12 bytes
 // per token of the vocabulary and stream.
 //
-// Bound by latency: two dependent reads before the walk, the rows' read after
-// it, and a meeting of the cluster (about 1 us) for each mass and for the
-// draw.  A chain of 8 over 32,000 tokens takes 6.0 us, 16 trees of 64 nodes
-// over 131,072 tokens 12.5 us (17 MB), 48 ragged trees of 33 nodes over 50,021
-// tokens with draft rows 22.5 us (up to four masses one after the other).
+// Bound by latency up to 65,536 tokens: two dependent reads before the walk,
+// the rows' read after it, and a meeting of the cluster (about 1 us) for each
+// mass and for the draw.  A chain of 8 over 32,000 tokens takes 6.0 to 6.7 us, 48
+// ragged trees of 33 nodes over 50,021 tokens with draft rows 21 to 23 (up to
+// four masses one after the other).  Over more a block's slice is longer and its
+// tiles are read one after the other: 16 trees of 64 nodes without draft rows
+// take 9.1 us over 65,536 tokens and 12.8 to 13.8 over 131,072 (17 MB); with draft
+// rows over 151,936, where no slice is held and each mass reads both rows again,
+// 32 us, and 36 with bf16 rows.
 // Slices of 4,096 tokens for 256 threads measured best: 512 threads or
 // slices twice as long took 1.1 to 1.5 times as long.
 #include <cooperative_groups.h>

@@ -31,7 +31,9 @@
 // sequence of 16,384 tokens 688 us, of which the walk 545; sixteen of 8,191
 // together 229 (81 and 150); eight of 32,768 together 890 to 950, by how
 // uneven they are.  The first launch is held by the shared-memory and fp32
-// pipes, the walk by the latency of its three products a chunk.
+// pipes, the walk by the latency of its three products a chunk: with fewer heads
+// one sequence takes nearly as long (16,384 tokens of 16, 8 and 4 value heads
+// 626, 585 and 565 us, the walk on 64, 32 and 16 SMs).
 //
 // Chunk slots: with s_b the first token of sequence b, its chunk c is slot
 // s_b / 64 + b + c; these never collide, and there are at most N / 64 + B of
@@ -291,9 +293,7 @@ __device__ inline void put_half_row(uint8_t* image, int row, int half, const uin
 // the largest of the longest walk, (m + 1) times the walk at place 152 m + 1 by
 // length (of 152 m + 1 walks some SM has m + 1) and, where they are more than
 // the SMs, the work spread over the SMs and a third of a mean walk (what is
-// uneven at the end).  The longest walks start first.  Drawn batches took on
-// average 0.6 % longer, at most 13 %, in a simulation of the launch than by
-// the best of these plans.
+// uneven at the end).  The longest walks start first.
 constexpr int kWalkCycles = 5000;  // per walk, and
 constexpr int kQuarterCycles = 4250, kHalfCycles = 5700, kWholeCycles = 8300;  // per chunk
 
@@ -1175,10 +1175,10 @@ constexpr size_t kPairFrom = 1400;
 // States (sequences times value heads) from which not every one is walked in
 // quarters: those fill the SMs up to 38.  Sequences of 2,048 tokens on
 // average, one even and three uneven batches, in us, quarters against the
-// plan's mixture: 48 states of three sequences 168/141/140/217 and
-// 136/146/142/222, 80 of five 253/241/220/229 and 207/214/202/190, 96 of three
-// 259/258/247/259 and 214/217/250/199, 96 of twelve 264/244/297/282 and
-// 218/258/308/298.
+// plan's mixture: 48 states of three sequences 176/158/150/146 and
+// 136/167/139/137, 64 of two 183/185/179/170 and 142/154/183/176, 80 of five
+// 264/216/225/223 and 207/230/213/209, 96 of three 271/271/271/264 and
+// 215/256/197/210, 96 of twelve 275/336/255/253 and 218/346/278/263.
 bool many_states(int B, int HV) { return size_t(B) * HV > 38; }
 
 size_t prefill_chunk_ws_bytes(int N, int B, int HV) { return pfc::ws_bytes(N, B, HV); }

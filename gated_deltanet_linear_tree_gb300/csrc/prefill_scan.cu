@@ -20,7 +20,8 @@
 // 16 states 18 / 21, 32 states 25 / 21, 64 states 40 / 31, 128 states 70 / 59,
 // 512 states 260 / 187.  Four rows a lane: 30, 31 (32, 64 states), 191 (512).
 // Sixteen or 32 lanes per row, and blocks of 2 or 4 tokens in closed form,
-// were slower or no faster.
+// were slower or no faster.  Long prompts take as long per token: 16,384 of fp32
+// 2.6 ms with 16 value heads and 3.2 with 32, bf16 ones of d = 32 1.7.
 #include "common.cuh"
 
 namespace canopy {

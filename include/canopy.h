@@ -276,11 +276,14 @@ size_t canopy_prefill_workspace_bytes(int N, int B, int HV, int dk, int dv);
  * than the one before as that was read).  A gate of zero forgets the state; a
  * negative one, or a gate or write strength that is not finite, sets
  * CANOPY_DEVERR_GATE and is read with its partner as g = 1, beta = 0.  A sequence's tokens influence no other sequence, whatever
- * they hold.  bf16 q/k/v with dk = dv = 128 run in 64-token chunks on the
- * tensor cores (bf16 operands split so that 24 bits of the state, of U and of
- * R enter their products; fp32 accumulation, fp32 states), other inputs and
- * calls of few tokens per sequence token by token in fp32
- * (canopy_prefill_plan says which).  flags: 0 or one CANOPY_PREFILL_ bit. */
+ * they hold, and which other sequences a call has does not show in one's
+ * results as long as the plan is the same.  bf16 q/k/v with dk = dv = 128 run in
+ * 64-token chunks on the tensor cores (bf16 operands split so that 24 bits of the
+ * state, of the chunk operands, of R and of U enter their products, but for
+ * products of parts below 2^-24; fp32 accumulation, fp32 states), other inputs
+ * and calls of few tokens per sequence token by token in fp32
+ * (canopy_prefill_plan says which, from the mean length: a call that mixes many
+ * single tokens with a long prompt is faster as two).  flags: 0 or one CANOPY_PREFILL_ bit. */
 canopy_status canopy_prefill(const void* q, const void* k, const void* v, canopy_dtype in_dtype, const float* g,
                              const float* beta, const float* S0, const int32_t* starts, int N, int B, int H, int HV,
                              int dk, int dv, float scale, void* o, canopy_dtype o_dtype, float* S_new,

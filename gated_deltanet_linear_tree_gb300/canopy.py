@@ -343,6 +343,12 @@ def _need_given(dev: int, *specs):
     _need_all(dev, *(spec for spec in specs if spec[0] is not None))
 
 
+def _need_ints(*sizes):
+    """The library takes sizes as int; ctypes would drop what is beyond."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise CanopyError(f"unsupported sizes {tuple(sizes)}")
+
+
 def _raw_stream(dev: int) -> int:
     """The current stream's handle on CUDA device `dev`."""
     return torch._C._cuda_getCurrentRawStream(dev)
@@ -392,6 +398,7 @@ def prefill(q, k, v, g, beta, S0, starts, ws, o_dtype=torch.float32, out=None, S
     if not isinstance(starts, torch.Tensor) or starts.dim() != 1 or starts.shape[0] < 2:
         raise CanopyError("starts must have shape (B + 1,)")
     B = starts.shape[0] - 1
+    _need_ints(N, B, H, HV, dk, dv)
     state = (B, HV, dv, dk)
     dt, f32, dev = q.dtype, torch.float32, q.get_device()
     _need_all(dev, (q, "q", dt, q.shape), (k, "k", dt, q.shape), (v, "v", dt, v.shape), (g, "g", f32, (N, HV)),
@@ -430,6 +437,7 @@ def step(q, k, v, g, beta, S, o_dtype=torch.float32, out=None, S_out=None, scale
     if r is not None:
         return _short_call("canopy_step", r)
     B, H, HV, dk, dv = _heads3(q, v)
+    _need_ints(B, H, HV, dk, dv)
     state = (B, HV, dv, dk)
     dt, f32, dev = q.dtype, torch.float32, q.get_device()
     _need_all(dev, (q, "q", dt, q.shape), (k, "k", dt, q.shape), (v, "v", dt, v.shape), (g, "g", f32, (B, HV)),
@@ -466,6 +474,7 @@ def accept(p, tokens, parent, u, noise, q=None, lengths=None, err=None):
     if not isinstance(p, torch.Tensor) or p.dim() != 3:
         raise CanopyError("p must have shape (B, T, V)")
     B, T, V = p.shape
+    _need_ints(B, T, V)
     i32, f32, dev = torch.int32, torch.float32, p.get_device()
     _need_all(dev, (p, "p", p.dtype, p.shape), (tokens, "tokens", i32, (B, T)), (parent, "parent", i32, (B, T)),
               (u, "u", f32, (B, T)), (noise, "noise", f32, (B, V)))

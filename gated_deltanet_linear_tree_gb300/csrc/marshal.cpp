@@ -77,6 +77,13 @@ void* stream_of(int dev) { return c10::cuda::getCurrentCUDAStream(dev).stream();
 
 PyObject* none() { Py_RETURN_NONE; }
 
+// The library takes sizes as int.
+bool ints(std::initializer_list<int64_t> sizes) {
+    for (const int64_t n : sizes)
+        if (n > INT32_MAX) return false;
+    return true;
+}
+
 // The output for obj: a fresh tensor for None, else the given one if it fits.
 bool output(PyObject* obj, int dev, at::ScalarType type, std::initializer_list<int64_t> shape, at::Tensor& out) {
     if (obj == Py_None) {
@@ -144,7 +151,8 @@ PyObject* step(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor* k = plain(a[1], dev, q->scalar_type(), {B, H, dk});
         const at::Tensor *g = plain(a[3], dev, at::kFloat, {B, HV}), *beta = plain(a[4], dev, at::kFloat, {B, HV});
         const at::Tensor* S = plain(a[5], dev, at::kFloat, {B, HV, dv, dk});
-        bool ok = k && g && beta && S && v->size(0) == B && v->scalar_type() == q->scalar_type();
+        bool ok = ints({B, H, HV, dk, dv}) && k && g && beta && S && v->size(0) == B &&
+                  v->scalar_type() == q->scalar_type();
         const at::Tensor* err = maybe(a[10], dev, at::kInt, {1}, ok);
         const c10::cuda::OptionalCUDAGuard on(at::Device(at::kCUDA, at::DeviceIndex(dev)));
         at::Tensor out, S_out;
@@ -176,7 +184,8 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int64_t B = starts->size(0) - 1;
         const at::Tensor* k = plain(a[1], dev, q->scalar_type(), {N, H, dk});
         const at::Tensor *g = plain(a[3], dev, at::kFloat, {N, HV}), *beta = plain(a[4], dev, at::kFloat, {N, HV});
-        bool ok = k && g && beta && v->size(0) == N && v->scalar_type() == q->scalar_type() && N <= INT32_MAX;
+        bool ok = ints({N, B, H, HV, dk, dv}) && k && g && beta && v->size(0) == N &&
+                  v->scalar_type() == q->scalar_type();
         const at::Tensor* S0 = maybe(a[5], dev, at::kFloat, {B, HV, dv, dk}, ok);
         const c10::cuda::OptionalCUDAGuard on(at::Device(at::kCUDA, at::DeviceIndex(dev)));
         at::Tensor out, S_out;
@@ -204,7 +213,7 @@ PyObject* accept(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int64_t B = p->size(0), T = p->size(1), V = p->size(2);
         const at::Tensor *tokens = plain(a[1], dev, at::kInt, {B, T}), *parent = plain(a[2], dev, at::kInt, {B, T});
         const at::Tensor *u = plain(a[3], dev, at::kFloat, {B, T}), *noise = plain(a[4], dev, at::kFloat, {B, V});
-        bool ok = tokens && parent && u && noise && V <= INT32_MAX;
+        bool ok = ints({B, T, V}) && tokens && parent && u && noise;
         const at::Tensor* q = maybe(a[5], dev, p->scalar_type(), {B, T, V}, ok);
         const at::Tensor* lengths = maybe(a[6], dev, at::kInt, {B}, ok);
         const at::Tensor* err = maybe(a[7], dev, at::kInt, {1}, ok);

@@ -10,7 +10,9 @@
 // through its own checks, which say what is wrong.  The library's entry
 // points are handed over by address, so that this module links against torch
 // only and the library against nothing of it.  The library works on the current
-// device: the tensors' is made current for the call.
+// device: the tensors' is made current for the call.  An allocation may wait for
+// the GPU and a launch for room in the stream's queue, so other Python threads
+// run meanwhile.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -84,16 +86,26 @@ bool ints(std::initializer_list<int64_t> sizes) {
     return true;
 }
 
-// The output for obj: a fresh tensor for None, else the given one if it fits.
+// The output given as obj, if it fits; None stays undefined for now.
 bool output(PyObject* obj, int dev, at::ScalarType type, std::initializer_list<int64_t> shape, at::Tensor& out) {
-    if (obj == Py_None) {
-        out = fresh(at::IntArrayRef(shape), type, dev);
-        return true;
-    }
+    if (obj == Py_None) return true;
     const at::Tensor* t = plain(obj, dev, type, shape);
     if (t) out = *t;
     return t != nullptr;
 }
+
+// While one of these exists other Python threads run, and the device is current.
+struct Unlocked {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+struct OnDevice {
+    Unlocked unlocked;
+    c10::cuda::OptionalCUDAGuard guard;  // (set where it has to be: it costs 0.1 us)
+    explicit OnDevice(int dev) {
+        if (c10::cuda::current_device() != dev) guard.set_index(at::DeviceIndex(dev));
+    }
+};
 
 PyObject* pair_of(PyObject* given_a, const at::Tensor& a, PyObject* given_b, const at::Tensor& b) {
     PyObject* r = PyTuple_New(2);
@@ -154,14 +166,19 @@ PyObject* step(PyObject*, PyObject* const* a, Py_ssize_t n) {
         bool ok = ints({B, H, HV, dk, dv}) && k && g && beta && S && v->size(0) == B &&
                   v->scalar_type() == q->scalar_type();
         const at::Tensor* err = maybe(a[10], dev, at::kInt, {1}, ok);
-        const c10::cuda::OptionalCUDAGuard on(at::Device(at::kCUDA, at::DeviceIndex(dev)));
         at::Tensor out, S_out;
         if (!ok || !output(a[7], dev, ot, {B, HV, dv}, out) || !output(a[8], dev, at::kFloat, {B, HV, dv, dk}, S_out))
             return none();
-        const canopy_status st =
-            step_fn(q->data_ptr(), k->data_ptr(), v->data_ptr(), in, ptr<float>(g), ptr<float>(beta), ptr<float>(S),
-                    ptr<float>(&S_out), int(B), int(H), int(HV), int(dk), int(dv), float(PyFloat_AS_DOUBLE(a[9])),
-                    out.data_ptr(), oc, ptr<int32_t>(err), stream_of(dev));
+        const float scale = float(PyFloat_AS_DOUBLE(a[9]));
+        canopy_status st;
+        {
+            const OnDevice on(dev);
+            if (!out.defined()) out = fresh({B, HV, dv}, ot, dev);
+            if (!S_out.defined()) S_out = fresh({B, HV, dv, dk}, at::kFloat, dev);
+            st = step_fn(q->data_ptr(), k->data_ptr(), v->data_ptr(), in, ptr<float>(g), ptr<float>(beta),
+                         ptr<float>(S), ptr<float>(&S_out), int(B), int(H), int(HV), int(dk), int(dv), scale,
+                         out.data_ptr(), oc, ptr<int32_t>(err), stream_of(dev));
+        }
         if (st != CANOPY_OK) return PyLong_FromLong(st);
         return pair_of(a[7], out, a[8], S_out);
     });
@@ -187,16 +204,21 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
         bool ok = ints({N, B, H, HV, dk, dv}) && k && g && beta && v->size(0) == N &&
                   v->scalar_type() == q->scalar_type();
         const at::Tensor* S0 = maybe(a[5], dev, at::kFloat, {B, HV, dv, dk}, ok);
-        const c10::cuda::OptionalCUDAGuard on(at::Device(at::kCUDA, at::DeviceIndex(dev)));
         at::Tensor out, S_out;
         if (!ok || size_t(ws->numel()) < prefill_bytes_fn(int(N), int(B), int(HV), int(dk), int(dv)) ||
             !output(a[9], dev, ot, {N, HV, dv}, out) || !output(a[10], dev, at::kFloat, {B, HV, dv, dk}, S_out))
             return none();
-        const canopy_status st =
-            prefill_fn(q->data_ptr(), k->data_ptr(), v->data_ptr(), in, ptr<float>(g), ptr<float>(beta),
-                       ptr<float>(S0), ptr<int32_t>(starts), int(N), int(B), int(H), int(HV), int(dk), int(dv),
-                       float(PyFloat_AS_DOUBLE(a[11])), out.data_ptr(), oc, ptr<float>(&S_out), ws->data_ptr(),
-                       unsigned(PyLong_AsUnsignedLong(a[12])), stream_of(dev));
+        const float scale = float(PyFloat_AS_DOUBLE(a[11]));
+        const unsigned flags = unsigned(PyLong_AsUnsignedLong(a[12]));
+        canopy_status st;
+        {
+            const OnDevice on(dev);
+            if (!out.defined()) out = fresh({N, HV, dv}, ot, dev);
+            if (!S_out.defined()) S_out = fresh({B, HV, dv, dk}, at::kFloat, dev);
+            st = prefill_fn(q->data_ptr(), k->data_ptr(), v->data_ptr(), in, ptr<float>(g), ptr<float>(beta),
+                            ptr<float>(S0), ptr<int32_t>(starts), int(N), int(B), int(H), int(HV), int(dk), int(dv),
+                            scale, out.data_ptr(), oc, ptr<float>(&S_out), ws->data_ptr(), flags, stream_of(dev));
+        }
         if (st != CANOPY_OK) return PyLong_FromLong(st);
         return pair_of(a[9], out, a[10], S_out);
     });
@@ -218,14 +240,18 @@ PyObject* accept(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor* lengths = maybe(a[6], dev, at::kInt, {B}, ok);
         const at::Tensor* err = maybe(a[7], dev, at::kInt, {1}, ok);
         if (!ok) return none();
-        const c10::cuda::OptionalCUDAGuard on(at::Device(at::kCUDA, at::DeviceIndex(dev)));
-        const at::Tensor accepted = fresh({B}, at::kInt, dev), out = fresh({B, T}, at::kInt, dev),
-                         counts = fresh({B}, at::kInt, dev);
-        const canopy_status st =
-            accept_fn(p->data_ptr(), ptr<void>(q), type, ptr<int32_t>(tokens), ptr<int32_t>(parent),
-                      ptr<int32_t>(lengths), ptr<float>(u), ptr<float>(noise), int(T), int(B), int(V),
-                      ptr<int32_t>(&accepted), ptr<int32_t>(&out), ptr<int32_t>(&counts), ptr<int32_t>(err),
-                      stream_of(dev));
+        at::Tensor accepted, out, counts;
+        canopy_status st;
+        {
+            const OnDevice on(dev);
+            accepted = fresh({B}, at::kInt, dev);
+            out = fresh({B, T}, at::kInt, dev);
+            counts = fresh({B}, at::kInt, dev);
+            st = accept_fn(p->data_ptr(), ptr<void>(q), type, ptr<int32_t>(tokens), ptr<int32_t>(parent),
+                           ptr<int32_t>(lengths), ptr<float>(u), ptr<float>(noise), int(T), int(B), int(V),
+                           ptr<int32_t>(&accepted), ptr<int32_t>(&out), ptr<int32_t>(&counts), ptr<int32_t>(err),
+                           stream_of(dev));
+        }
         if (st != CANOPY_OK) return PyLong_FromLong(st);
         PyObject* r = PyTuple_New(3);
         if (!r) return nullptr;

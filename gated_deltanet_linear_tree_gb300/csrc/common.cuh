@@ -137,8 +137,8 @@ __device__ inline int stream_len(const int32_t* lengths, int b, int T, int* bad)
 // Up to this many sequences every warp that needs one forms the largest
 // itself: four reads a lane, all in flight with those of the sequence's own
 // bounds.  Where there are more, a launch ahead (prefill_scan.cu) puts s in the
-// workspace and the kernels read that: a few us in a call that takes 100 and
-// more.
+// workspace and the kernels read that (200 single tokens of 32 heads take 178 us
+// either way).
 constexpr int kMaxUnordered = 128;
 
 __host__ __device__ inline size_t ordered_bytes(int B) {

@@ -338,63 +338,93 @@ def _plain_prep(s):
     return q, s["k_cache"], s["v_cache"]
 
 
-def _plain_attend(s):
+def _reach(s):
+    """[B, T, T]: whether node j is on node i's root path (i itself among them), by squaring: after r rounds the
+    nodes up to 2^r steps above."""
+    B, T = s["parent"].shape
+    node = torch.arange(T, device="cuda")
+    reach = ((s["parent"][..., None] == node) | torch.eye(T, dtype=torch.bool, device="cuda")).float()
+    for _ in range((T - 1).bit_length()):
+        reach = ((reach @ reach) > 0).float()
+    return reach > 0
+
+
+def _softmax_of(q, K, V, seen, s):
+    """q [b, n, HQ, d] over K, V [b, HKV, m, d], where seen [b, n, m] (a row at least sees one); fp32."""
+    b, n, HQ, d = q.shape
+    HKV, m = K.shape[1:3]
+    x = q.float().reshape(b, n, HKV, HQ // HKV, d).permute(0, 2, 3, 1, 4).reshape(b, HKV, -1, d)
+    z = (s["scale"] * (x @ K.transpose(-1, -2))).reshape(b, HKV, HQ // HKV, n, m)
+    z = torch.where(seen[:, None, None], z, -torch.inf)
+    p = torch.exp(z - z.amax(-1, keepdim=True))
+    y = (p.reshape(b, HKV, -1, m) @ V).reshape(b, HKV, HQ // HKV, n, d) / p.sum(-1, keepdim=True)
+    return y.permute(0, 3, 1, 2, 4).reshape(b, n, HQ, d).to(q.dtype)
+
+
+def _near(at, place, case):
+    """Whether a row at position `at` sees one at position `place` before it."""
+    if not case["window"]:
+        return at >= place
+    return (at >= place) & ((at - place < case["window"]) | (place < case["sinks"]))
+
+
+def _plain_attend_even(s):
+    """Single tokens and trees: every stream's rows at once, the caches filled up to one length."""
     case = s["case"]
-    HQ, HKV, d, ps, T = case["HQ"], case["HKV"], case["d"], case["page"], s["T"]
-    q = s["q"].reshape(-1, HQ, d)
-    o = torch.zeros_like(q)
+    B, ps = case["B"], case["page"]
+    q = s["q"].reshape(B, -1, case["HQ"], case["d"])
+    T = q.shape[1]
+    lens = s["lengths"].long() if s["T"] else torch.ones(B, dtype=torch.int64, device="cuda")
+    c = s["context"].long()[:, None]
+    reach = _reach(s) if s["T"] else torch.ones(B, 1, 1, dtype=torch.bool, device="cuda")
+    depth = reach.sum(-1) - 1
+    m = max(x + y for x, y in zip(s["lens"], s["ctxs"]))
+    key = torch.arange(m, device="cuda").expand(B, m)
+    node = (key - c).clamp(0, T - 1)
+    new = key >= c
+    place = torch.where(new, c + depth.gather(1, node), key)
+    seen = ~new[:, None] | reach.gather(2, node[:, None].expand(B, T, m))
+    seen &= _near((c + depth)[..., None], place[:, None], case) & (key < c + lens[:, None])[:, None]
+    seen[..., 0] |= ~seen.any(-1)  # a row behind its tree's end (not returned)
+    table = s["page_table"][:, :-(-m // ps)].long()
+    there = (key < c + lens[:, None])[:, None, :, None]
+    K, V = (torch.where(there, x[table.clamp_min(0)].transpose(1, 2).flatten(2, 3)[:, :, :m].float(), 0)
+            for x in (s["k_cache"], s["v_cache"]))
+    o = _softmax_of(q, K, V, seen, s)
+    return torch.where((torch.arange(T, device="cuda") < lens[:, None])[..., None, None], o, 0).reshape(s["q"].shape)
+
+
+def _plain_attend_packed(s):
+    """Prompts: sequence by sequence, some hundred rows at a time."""
+    case = s["case"]
+    ps = case["page"]
+    o = torch.empty_like(s["q"])
     first = 0
     for b, (m, c) in enumerate(zip(s["lens"], s["ctxs"])):
-        lo = b * T if T else first
-        first += m
-        if m == 0:
-            continue
         pages = s["page_table"][b, :-(-(c + m) // ps)].long()
-        K, V = (x[pages].transpose(0, 1).reshape(HKV, -1, d)[:, :c + m].float() for x in (s["k_cache"], s["v_cache"]))
-        key = torch.arange(c + m, device="cuda")
-        new = torch.eye(m, dtype=torch.bool, device="cuda") if T else \
-            torch.ones(m, m, dtype=torch.bool, device="cuda").tril()
-        t = torch.arange(m, device="cuda")
-        if T:  # paths by squaring: after r rounds the nodes up to 2^r steps above
-            up = s["parent"][b, :m].long()
-            step = torch.zeros(m, m, device="cuda")
-            step[t[1:], up[1:]] = 1.0
-            reach = step + torch.eye(m, device="cuda")
-            for _ in range(max(1, (m - 1).bit_length())):
-                reach = ((reach @ reach) > 0).float()
-            new = reach > 0
-            t = new.sum(1) - 1
-        where = torch.cat([key[:c], c + t])
+        K, V = (x[pages].transpose(0, 1).flatten(1, 2)[None, :, :c + m].float() for x in (s["k_cache"], s["v_cache"]))
+        place = torch.arange(c + m, device="cuda")
         for r in range(0, m, 512):
-            rows = slice(lo + r, lo + min(m, r + 512))
-            at = c + t[r:r + 512]
-            ok = torch.cat([torch.ones(len(at), c, dtype=torch.bool, device="cuda"), new[r:r + 512]], 1)
-            if case["window"]:
-                ok &= (at[:, None] - where < case["window"]) | (where < case["sinks"])
-            x = q[rows].float().reshape(len(at), HKV, HQ // HKV, d).permute(1, 2, 0, 3).reshape(HKV, -1, d)
-            z = (s["scale"] * (x @ K.transpose(1, 2))).reshape(HKV, HQ // HKV, len(at), c + m)
-            z = torch.where(ok, z, -torch.inf)
-            p = torch.exp(z - z.amax(-1, keepdim=True))
-            y = (p.reshape(HKV, -1, c + m) @ V).reshape(HKV, HQ // HKV, len(at), d) / p.sum(-1, keepdim=True)
-            o[rows] = y.permute(2, 0, 1, 3).reshape(len(at), HQ, d).to(o.dtype)
-    return o.reshape(s["q"].shape)
+            rows = slice(r, min(m, r + 512))
+            seen = _near(place[c:][rows, None], place, case)
+            o[first:first + m][rows] = _softmax_of(s["q"][first:first + m][rows][None], K, V, seen[None], s)[0]
+        first += m
+    return o
+
+
+def _plain_attend(s):
+    return (_plain_attend_packed if s["starts"] is not None else _plain_attend_even)(s)
 
 
 def _plain_commit(s):
     q, K, V = _plain_prep(s)
-    B, T = s["parent"].shape
-    ps = s["case"]["page"]
-    node, paths = s["accepted"].long(), []
-    rows = torch.arange(B, device="cuda")
-    for _ in range(T):
-        paths.append(node)
-        node = torch.where(node >= 0, s["parent"].long()[rows, node.clamp_min(0)], -1)
-    path = torch.stack(paths, 1)  # from the accepted node up, then -1
-    size = (path >= 0).sum(1)
-    context = s["context"] + size.int()
-    b, k = (path >= 0).nonzero(as_tuple=True)
-    c = s["context"].long()[b]
-    src, dst = c + path[b, k], c + size[b] - 1 - k
+    reach = _reach(s)
+    depth = reach.sum(-1) - 1
+    path = reach.gather(1, s["accepted"].long()[:, None, None].expand(-1, 1, reach.shape[2]))[:, 0]
+    context = s["context"] + path.sum(1).int()
+    b, node = path.nonzero(as_tuple=True)
+    c, ps = s["context"].long()[b], s["case"]["page"]
+    src, dst = c + node, c + depth[b, node]
     for cache in (K, V):
         moved = cache[s["page_table"].long()[b, src // ps], :, src % ps]
         cache[s["page_table"].long()[b, dst // ps], :, dst % ps] = moved

@@ -29,7 +29,7 @@ OK, ERR_ARG, ERR_TREE, ERR_UNSUPPORTED, ERR_CUDA = 0, 1, 2, 3, 4
 F32, BF16 = 0, 1
 SOLVE = {"fwdsub": 0, "neumann": 1, "squaring": 2, "split": 3}
 DEVERR_TREE, DEVERR_GATE, DEVERR_ACCEPTED, DEVERR_TIMEOUT, DEVERR_LENGTH = 0x1, 0x2, 0x4, 0x8, 0x10
-DEVERR_TOKEN = 0x20
+DEVERR_TOKEN, DEVERR_PAGE = 0x20, 0x40
 VERIFY_INPUTS_READY = 0x1
 VERIFY_STATE_READY = 0x2
 VERIFY_CLOSED_FORM = 0x4
@@ -39,11 +39,15 @@ FORCE = {None: 0, "closed_form": VERIFY_CLOSED_FORM, "path_replay": VERIFY_PATH_
 COMMIT_STATE_READY = 0x1
 PREFILL_FORCE = {None: 0, "scan": 0x1, "chunked": 0x2}
 PREFILL_PLAN = {"none": -1, "scan": 0, "chunked": 1}
+ATTEND_PLAN = {"none": -1, "fp32": 0, "few": 1, "tiles": 2}
+NORM = {"none": 0, "rms": 1, "l2": 2}
+PAIRS = {"half": 0, "adjacent": 1}
 ACT = {"none": 0, "silu": 1}
 WS_REGION = {"err": 0, "l": 1, "depth": 2, "mask": 3, "order": 4, "u": 5}
 
 # name -> (restype, argtypes); mirrors include/canopy.h
 _P, _I, _S, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+_L = ctypes.c_int64
 SIGNATURES = {
     "canopy_workspace_bytes": (_S, [_I, _I, _I, _I, _I]),
     "canopy_workspace_init": (_I, [_P, _S, _P]),
@@ -64,6 +68,13 @@ SIGNATURES = {
     "canopy_prefill_plan": (_I, [_I, _I, _I, _I, _I, _I, _I, ctypes.c_uint]),
     "canopy_step": (_I, [_P, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _I, _P, _P]),
     "canopy_accept": (_I, [_P, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P]),
+    "canopy_qk_prep": (_I, [_P, _P, _P, _I, _L, _L, _L, _I, _P, _P, _F, _P, _I, _P, _I, _P, _I, _I, _I, _I, _I, _I,
+                            _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P]),
+    "canopy_attend_workspace_bytes": (_S, [_I, _I, _I, _I, _I]),
+    "canopy_attend_plan": (_I, [_I, _I, _I, _I, _I, _I]),
+    "canopy_attend": (_I, [_P, _I, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P,
+                           _P]),
+    "canopy_cache_commit": (_I, [_P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _P, _I, _I, _I, _I, _P, _P, _P]),
     "canopy_tree_conv": (_I, [_P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P]),
     "canopy_conv_commit": (_I, [_P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
     "canopy_read_device_error": (_I, [_P, ctypes.POINTER(ctypes.c_int32), _P]),
@@ -489,6 +500,210 @@ def accept(p, tokens, parent, u, noise, q=None, lengths=None, err=None):
                                counts.data_ptr(), _opt(err), _raw_stream(dev))
     _check(st, "canopy_accept")
     return accepted, out_tokens, counts
+
+
+def _rows_shape(q, starts, lengths, what: str):
+    """Leading sizes of an attention layer's rows q [N, H, d] (packed, or one token of each stream) or
+    [B, T, H, d], and N."""
+    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
+        raise CanopyError(f"{what} must have shape (N, H, d) or (B, T, H, d)")
+    lead = tuple(q.shape[:-2])
+    if q.dim() == 4 and starts is not None:
+        raise CanopyError("starts come with packed rows, not with (B, T, H, d)")
+    if q.dim() == 3 and lengths is not None:
+        raise CanopyError("lengths come with (B, T, H, d), not with packed rows")
+    return lead, lead[0] * (lead[1] if q.dim() == 4 else 1)
+
+
+def _need_rows(t, name: str, dev: int, dtype, shape) -> int:
+    """Rows whose heads are dense but whose tokens may lie apart; elements from a token to the next."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise CanopyError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise CanopyError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise CanopyError(f"{name} must be on the same device as the other tensors")
+    H, d = shape[-2:]
+    ld = t.stride(-3) if shape[-3] > 1 else t.stride(0) if len(shape) == 4 and shape[0] > 1 else H * d
+    if d > 1 and t.stride(-1) != 1 or H > 1 and t.stride(-2) != d or \
+            len(shape) == 4 and shape[0] > 1 and t.stride(0) != ld * shape[1]:
+        raise CanopyError(f"{name} must have dense heads and tokens at one distance")
+    return ld
+
+
+def _cache(k_cache, v_cache, page_table, context, dtype, HKV, d, dev):
+    """Check a paged cache: k_cache, v_cache [pages, HKV, page_size, d], page_table int32 [B, max_pages], context
+    int32 [B]; (B, pages, page_size, max_pages)."""
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4 or k_cache.shape[1] != HKV or \
+            k_cache.shape[3] != d:
+        raise CanopyError(f"k_cache must have shape (pages, {HKV}, page_size, {d})")
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise CanopyError("page_table must have shape (B, max_pages)")
+    B = page_table.shape[0]
+    _need_all(dev, (k_cache, "k_cache", dtype, k_cache.shape), (v_cache, "v_cache", dtype, k_cache.shape),
+              (page_table, "page_table", torch.int32, page_table.shape), (context, "context", torch.int32, (B,)))
+    sizes = (k_cache.shape[0], k_cache.shape[2], page_table.shape[1])
+    _need_ints(B, HKV, d, *sizes)
+    return (B, *sizes)
+
+
+def _streams(lead, B, starts):
+    """Whether rows of these leading sizes are those of B streams."""
+    if len(lead) == 2 and lead[0] != B or len(lead) == 1 and starts is None and lead[0] != B:
+        raise CanopyError(f"{lead} rows do not fit {B} streams: (B, T, H, d), one token of each, or packed with starts")
+
+
+def qk_prep(q, k, v=None, norm: str = "rms", q_weight=None, k_weight=None, eps: float = 1e-6, freqs=None,
+            positions=None, axis=None, pairs: str = "half", q_out=None, k_out=None, k_cache=None, v_cache=None,
+            page_table=None, context=None, starts=None, lengths=None, err=None):
+    """Queries and keys of a layer in one pass: (q_out, k_out).  Every head's
+    row normed ("rms", "l2" for unit rows, or "none"; weights fp32 [d] or
+    None), the first 2 len(freqs) columns rotated by position (freqs fp32;
+    positions int32 of the rows' shape, or [axes, ...] with axis int32
+    [len(freqs)] each pair's axis, or None for the place in the cache; pairs
+    "half" (j, j + R/2) or "adjacent" (2j, 2j + 1)), rounded once.
+    q [N, HQ, d], k, v [N, HKV, d]: packed sequences at starts int32 [B+1], or
+    one token of each stream; or [B, T, heads, d], of which lengths int32 [B] (or
+    all) are there.  Tokens may lie apart (slices of one projection), their heads
+    dense.  With k_cache and v_cache [pages, HKV, page_size, d], page_table int32
+    [B, max_pages] and context int32 [B], row i's key and value go to place
+    context[b] + i of its stream and k_out is None.  q_out may be q and k_out k.
+    err: an optional int32 CUDA tensor of one element for device error bits."""
+    lead, N = _rows_shape(q, starts, lengths, "q")
+    HQ, d = q.shape[-2:]
+    if not isinstance(k, torch.Tensor) or k.dim() != q.dim():
+        raise CanopyError("k must have the rows of q")
+    HKV = k.shape[-2]
+    _need_ints(N, HQ, HKV, d)
+    dt, f32, i32, dev = q.dtype, torch.float32, torch.int32, q.get_device()
+    code = _dt(q)
+    ldq = _need_rows(q, "q", dev, dt, (*lead, HQ, d))
+    ldk = _need_rows(k, "k", dev, dt, (*lead, HKV, d))
+    R = ldv = B = pages = page_size = max_pages = 0
+    axes = 1
+    if k_cache is not None:
+        B, pages, page_size, max_pages = _cache(k_cache, v_cache, page_table, context, dt, HKV, d, dev)
+        _streams(lead, B, starts)
+        ldv = _need_rows(v, "v", dev, dt, (*lead, HKV, d))
+        _need_given(dev, (starts, "starts", i32, (B + 1,)), (lengths, "lengths", i32, (B,)))
+        if k_out is not None:
+            raise CanopyError("k_out comes without a cache")
+    elif any(x is not None for x in (v, v_cache, page_table, context, starts, lengths)):
+        raise CanopyError("v, v_cache, page_table, context, starts and lengths come with k_cache")
+    _need_given(dev, (q_weight, "q_weight", f32, (d,)), (k_weight, "k_weight", f32, (d,)),
+                (q_out, "q_out", dt, (*lead, HQ, d)), (k_out, "k_out", dt, (*lead, HKV, d)), (err, "err", i32, (1,)))
+    if freqs is not None:
+        _need_all(dev, (freqs, "freqs", f32, freqs.shape if isinstance(freqs, torch.Tensor) else ()))
+        if freqs.dim() != 1:
+            raise CanopyError("freqs must have shape (R / 2,)")
+        R = 2 * freqs.shape[0]
+    if positions is not None:
+        if not isinstance(positions, torch.Tensor) or tuple(positions.shape) not in (lead, (*positions.shape[:1], *lead)):
+            raise CanopyError(f"positions must have shape {lead} or (axes, *{lead})")
+        if positions.dim() > len(lead):
+            axes = positions.shape[0]
+        _need_all(dev, (positions, "positions", i32, positions.shape))
+    _need_given(dev, (axis, "axis", i32, (R // 2,)))
+    lib = load()
+    with torch.cuda.device(dev):
+        if q_out is None:
+            q_out = torch.empty((*lead, HQ, d), dtype=dt, device=q.device)
+        if k_out is None and k_cache is None:
+            k_out = torch.empty((*lead, HKV, d), dtype=dt, device=q.device)
+        st = lib.canopy_qk_prep(q.data_ptr(), k.data_ptr(), _opt(v), code, ldq, ldk, ldv, NORM[norm], _opt(q_weight),
+                                _opt(k_weight), eps, _opt(freqs), R, _opt(positions), axes, _opt(axis), PAIRS[pairs],
+                                N, B, HQ, HKV, d, q_out.data_ptr(), _opt(k_out), _opt(k_cache), _opt(v_cache),
+                                _opt(page_table), pages, page_size, max_pages, _opt(context), _opt(starts),
+                                _opt(lengths), _opt(err), _raw_stream(dev))
+    _check(st, "canopy_qk_prep")
+    return q_out, k_out
+
+
+def attend_workspace(N: int, B: int, HQ: int, HKV: int, d: int, device="cuda") -> torch.Tensor:
+    """Workspace of attend calls over up to N rows of B sequences with these
+    heads.  Calls that may run at the same time need one each."""
+    n = int(load().canopy_attend_workspace_bytes(N, B, HQ, HKV, d))
+    if n == 0:
+        raise CanopyError("unsupported sizes for the attend workspace")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    _check(load().canopy_workspace_init(_ptr(ws), 4096, _stream()), "canopy_workspace_init")
+    return ws
+
+
+def attend_plan(N: int, B: int, HQ: int, HKV: int, bf16: bool, d: int) -> str:
+    """Which path canopy_attend takes for these sizes (an ATTEND_PLAN name)."""
+    code = load().canopy_attend_plan(N, B, HQ, HKV, BF16 if bf16 else F32, d)
+    return {v: k for k, v in ATTEND_PLAN.items()}[code]
+
+
+def attend(q, k_cache, v_cache, page_table, context, ws, starts=None, parent=None, lengths=None, window: int = 0,
+           sinks: int = 0, scale=None, out=None):
+    """Attention of new rows over a paged cache that holds their keys and
+    values already (qk_prep): o of q's shape and dtype.
+    q [N, HQ, d]: packed sequences at starts int32 [B+1], or one token of each
+    stream; or [B, T, HQ, d], with parent int32 [B, T] the nodes of draft trees
+    (T <= 256), of which lengths int32 [B] (or all) are there; rows that are not
+    there are left as they were.  Row i of a sequence sees the context[b] tokens
+    before it and the new ones up to itself, or on its root path; with window > 0
+    only those less than window positions before it and the first `sinks`.
+    k_cache, v_cache [pages, HKV, page_size, d], page_table int32
+    [B, max_pages].  scale: d ** -0.5 unless given.  ws: attend_workspace for at
+    least these sizes."""
+    lead, N = _rows_shape(q, starts, lengths, "q")
+    HQ, d = q.shape[-2:]
+    dt, i32, dev = q.dtype, torch.int32, q.get_device()
+    code = _dt(q)
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise CanopyError("k_cache must have shape (pages, HKV, page_size, d)")
+    HKV = k_cache.shape[1]
+    B, pages, page_size, max_pages = _cache(k_cache, v_cache, page_table, context, dt, HKV, d, dev)
+    _need_ints(N, HQ, window, sinks)
+    _streams(lead, B, starts)
+    if parent is not None and len(lead) != 2:
+        raise CanopyError("parent comes with (B, T, HQ, d)")
+    _need_all(dev, (q, "q", dt, q.shape), (ws, "workspace", torch.uint8, ws.shape))
+    _need_given(dev, (starts, "starts", i32, (B + 1,)), (parent, "parent", i32, lead), (out, "o", dt, q.shape),
+                (lengths, "lengths", i32, (B,)))
+    lib = load()
+    if ws.numel() < lib.canopy_attend_workspace_bytes(N, B, HQ, HKV, d):
+        raise CanopyError("the workspace is too small for these sizes")
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty(q.shape, dtype=dt, device=q.device)
+        st = lib.canopy_attend(q.data_ptr(), code, k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), pages,
+                               page_size, max_pages, context.data_ptr(), _opt(starts), _opt(parent), _opt(lengths), N,
+                               B, HQ, HKV, d, window, sinks, d ** -0.5 if scale is None else scale, out.data_ptr(),
+                               ws.data_ptr(), _raw_stream(dev))
+    _check(st, "canopy_attend")
+    return out
+
+
+def cache_commit(accepted, parent, k_cache, v_cache, page_table, context, lengths=None, err=None):
+    """The paged cache after accepting node accepted[b] of every stream's draft
+    tree (int32 [B], as commit takes it; parent int32 [B, T]): the keys and
+    values of its root path, at places context[b] + node, move to context[b] +
+    depth, in place.  Returns the new lengths, int32 [B].  err: an optional int32
+    CUDA tensor of one element for device error bits."""
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise CanopyError("k_cache must have shape (pages, HKV, page_size, d)")
+    _, HKV, _, d = k_cache.shape
+    i32, dev = torch.int32, k_cache.get_device()
+    code = _dt(k_cache)
+    B, pages, page_size, max_pages = _cache(k_cache, v_cache, page_table, context, k_cache.dtype, HKV, d, dev)
+    if not isinstance(parent, torch.Tensor) or parent.dim() != 2 or parent.shape[0] != B:
+        raise CanopyError(f"parent must have shape ({B}, T)")
+    T = parent.shape[1]
+    _need_ints(T)
+    _need_all(dev, (parent, "parent", i32, (B, T)), (accepted, "accepted", i32, (B,)))
+    _need_given(dev, (lengths, "lengths", i32, (B,)), (err, "err", i32, (1,)))
+    lib = load()
+    with torch.cuda.device(dev):
+        new = torch.empty((B,), dtype=i32, device=k_cache.device)
+        st = lib.canopy_cache_commit(accepted.data_ptr(), parent.data_ptr(), _opt(lengths), k_cache.data_ptr(),
+                                     v_cache.data_ptr(), code, page_table.data_ptr(), pages, page_size, max_pages,
+                                     context.data_ptr(), T, B, HKV, d, new.data_ptr(), _opt(err), _raw_stream(dev))
+    _check(st, "canopy_cache_commit")
+    return new
 
 
 def tree_conv(x, conv_state, weight, parent, bias=None, act: str = "silu", err=None, out=None):

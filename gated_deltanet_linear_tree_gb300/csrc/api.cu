@@ -59,6 +59,22 @@ cudaError_t launch_prefill_chunk(const void* q, const void* k, const void* v, co
 cudaError_t launch_accept(const void* p, const void* q, int bf16, const int32_t* tokens, const int32_t* parent,
                           const int32_t* lengths, const float* u, const float* noise, int T, int B, int V,
                           int32_t* accepted, int32_t* out, int32_t* count, int32_t* err, cudaStream_t st);
+cudaError_t launch_qk_prep(const void* q, const void* k, const void* v, int bf16, int64_t ldq, int64_t ldk,
+                           int64_t ldv, int norm, const float* qw, const float* kw, float eps, const float* freqs,
+                           int R, const int32_t* positions, int axes, const int32_t* axis, int adjacent, int N, int B,
+                           int HQ, int HKV, int d, void* qo, void* ko, void* kc, void* vc, const int32_t* table,
+                           int pages, int log_page, int max_pages, const int32_t* context, const int32_t* starts,
+                           const int32_t* lengths, int32_t* err, cudaStream_t st);
+size_t attend_ws_bytes(int N, int B, int HQ, int HKV, int d);
+canopy_attend_plan_t attend_plan(int N, int B, int HQ, int HKV, int bf16, int d);
+cudaError_t launch_attend(const void* q, int bf16, const void* kc, const void* vc, const int32_t* table, int pages,
+                          int log_page, int max_pages, const int32_t* context, const int32_t* starts,
+                          const int32_t* parent, const int32_t* lengths, int N, int B, int HQ, int HKV, int d,
+                          int window, int sinks, float scale, void* o, void* workspace, cudaStream_t st);
+cudaError_t launch_cache_commit(const int32_t* accepted, const int32_t* parent, const int32_t* lengths, void* kc,
+                                void* vc, int bf16, const int32_t* table, int pages, int log_page, int max_pages,
+                                const int32_t* context, int T, int B, int HKV, int d, int32_t* context_new,
+                                int32_t* err, cudaStream_t st);
 }  // namespace canopy
 
 using namespace canopy;
@@ -161,6 +177,29 @@ canopy_prefill_plan_t prefill_plan(int N, int B, int HV, canopy_dtype in_dtype, 
     const size_t pairs = size_t(B) * HV, least = pairs < 24 ? 64 : pairs < 128 ? 48 : 26;
     return in_dtype == CANOPY_BF16 && dk == 128 && size_t(N) >= least * B ? CANOPY_PREFILL_PLAN_CHUNKED
                                                                            : CANOPY_PREFILL_PLAN_SCAN;
+}
+
+bool dtype_ok(canopy_dtype t) { return t == CANOPY_F32 || t == CANOPY_BF16; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Sizes of an attention layer's call: rows, sequences, heads.
+canopy_status layer_sizes(int N, int B, int HQ, int HKV, int d) {
+    if (N <= 0 || B <= 0 || !heads_ok(HKV, HQ)) return CANOPY_ERR_ARG;
+    if (B > kMaxGrid || HQ / HKV > 64 || (d != 64 && d != 128) || size_t(N) * HQ > 0x7FFFFFFF)
+        return CANOPY_ERR_UNSUPPORTED;
+    return CANOPY_OK;
+}
+
+// Sizes of a paged cache; the logarithm of the page size.  Places and rows of the
+// pages are ints.
+canopy_status cache_sizes(int pages, int page_size, int max_pages, int HKV, int& log_page) {
+    if (pages <= 0 || page_size <= 0 || max_pages <= 0) return CANOPY_ERR_ARG;
+    if (page_size < 16 || (page_size & (page_size - 1)) || HKV > kMaxGrid / 2 ||
+        size_t(max_pages) * page_size > 0x3FFFFFFF || size_t(pages) * HKV > 0x7FFFFFFF)
+        return CANOPY_ERR_UNSUPPORTED;
+    log_page = 0;
+    while ((1 << log_page) < page_size) ++log_page;
+    return CANOPY_OK;
 }
 
 }  // namespace
@@ -357,6 +396,103 @@ canopy_status canopy_accept(const void* p, const void* q, canopy_dtype dtype, co
     if (T > kMaxT || V > (1 << 24) || B > kMaxGrid) return CANOPY_ERR_UNSUPPORTED;
     return cuda_status(launch_accept(p, q, dtype == CANOPY_BF16, tokens, parent, lengths, u, noise, T, B, V, accepted,
                                      out_tokens, counts, err, static_cast<cudaStream_t>(stream)));
+}
+
+canopy_status canopy_qk_prep(const void* q, const void* k, const void* v, canopy_dtype dtype, int64_t ldq,
+                             int64_t ldk, int64_t ldv, canopy_norm norm, const float* q_weight,
+                             const float* k_weight, float eps, const float* freqs, int R, const int32_t* positions,
+                             int axes, const int32_t* axis, canopy_pairs pairs, int N, int B, int HQ, int HKV, int d,
+                             void* q_out, void* k_out, void* k_cache, void* v_cache, const int32_t* page_table,
+                             int pages, int page_size, int max_pages, const int32_t* context, const int32_t* starts,
+                             const int32_t* lengths, int32_t* err, void* stream) {
+    const bool cached = k_cache != nullptr;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || (q_weight && !aligned16(q_weight)) ||
+        (k_weight && !aligned16(k_weight)) || !aligned4(freqs) || !aligned4(positions) || !aligned4(axis) ||
+        !aligned4(err))
+        return CANOPY_ERR_ARG;
+    if (cached) {
+        if (!aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) || !page_table || !aligned4(page_table) ||
+            !context || !aligned4(context) || !aligned4(starts) || !aligned4(lengths) || k_out)
+            return CANOPY_ERR_ARG;
+    } else if (!aligned16(k_out) || v || v_cache || page_table || context || starts || lengths || B) {
+        return CANOPY_ERR_ARG;
+    }
+    if (!dtype_ok(dtype) || norm < CANOPY_NORM_NONE || norm > CANOPY_NORM_L2 ||
+        (pairs != CANOPY_PAIRS_HALF && pairs != CANOPY_PAIRS_ADJACENT) || !(eps >= 0.f) || !std::isfinite(eps) ||
+        (norm == CANOPY_NORM_NONE && (q_weight || k_weight)))
+        return CANOPY_ERR_ARG;
+    if (R < 0 || R > d || (R > 0) != (freqs != nullptr) || (positions && axes < 1) || (axis && !positions) ||
+        (R && !positions && !cached) || (positions && !R))
+        return CANOPY_ERR_ARG;
+    const canopy_status as = layer_sizes(N, cached ? B : 1, HQ, HKV, d);
+    if (as != CANOPY_OK) return as;
+    if (R % 8) return CANOPY_ERR_UNSUPPORTED;
+    const int vec = dtype == CANOPY_BF16 ? 8 : 4;
+    if (ldq < int64_t(HQ) * d || ldk < int64_t(HKV) * d || (cached && ldv < int64_t(HKV) * d) || ldq % vec ||
+        ldk % vec || (cached && ldv % vec))
+        return CANOPY_ERR_ARG;
+    int log_page = 0;
+    if (cached) {
+        const canopy_status cs = cache_sizes(pages, page_size, max_pages, HKV, log_page);
+        if (cs != CANOPY_OK) return cs;
+        if (starts ? lengths != nullptr : N % B != 0) return CANOPY_ERR_ARG;
+    }
+    return cuda_status(launch_qk_prep(q, k, v, dtype == CANOPY_BF16, ldq, ldk, ldv, norm, q_weight, k_weight, eps,
+                                      freqs, R, positions, axes, axis, pairs == CANOPY_PAIRS_ADJACENT, N, B, HQ, HKV,
+                                      d, q_out, k_out, k_cache, v_cache, page_table, pages, log_page, max_pages,
+                                      context, starts, lengths, err, static_cast<cudaStream_t>(stream)));
+}
+
+size_t canopy_attend_workspace_bytes(int N, int B, int HQ, int HKV, int d) {
+    return layer_sizes(N, B, HQ, HKV, d) == CANOPY_OK ? attend_ws_bytes(N, B, HQ, HKV, d) : 0;
+}
+
+canopy_attend_plan_t canopy_attend_plan(int N, int B, int HQ, int HKV, canopy_dtype dtype, int d) {
+    if (!dtype_ok(dtype) || layer_sizes(N, B, HQ, HKV, d) != CANOPY_OK) return CANOPY_ATTEND_PLAN_NONE;
+    return attend_plan(N, B, HQ, HKV, dtype == CANOPY_BF16, d);
+}
+
+canopy_status canopy_attend(const void* q, canopy_dtype dtype, const void* k_cache, const void* v_cache,
+                            const int32_t* page_table, int pages, int page_size, int max_pages,
+                            const int32_t* context, const int32_t* starts, const int32_t* parent,
+                            const int32_t* lengths, int N, int B, int HQ, int HKV, int d, int window, int sinks,
+                            float scale, void* o, void* workspace, void* stream) {
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !page_table || !aligned4(page_table) ||
+        !context || !aligned4(context) || !aligned4(starts) || !aligned4(parent) || !aligned4(lengths) ||
+        !aligned16(o) || !aligned16(workspace))
+        return CANOPY_ERR_ARG;
+    if (!dtype_ok(dtype) || !std::isfinite(scale) || window < 0 || sinks < 0 || (sinks && !window))
+        return CANOPY_ERR_ARG;
+    const canopy_status as = layer_sizes(N, B, HQ, HKV, d);
+    if (as != CANOPY_OK) return as;
+    int log_page = 0;
+    const canopy_status cs = cache_sizes(pages, page_size, max_pages, HKV, log_page);
+    if (cs != CANOPY_OK) return cs;
+    if (starts ? parent || lengths : N % B != 0) return CANOPY_ERR_ARG;
+    if (parent && N / B > kMaxT) return CANOPY_ERR_UNSUPPORTED;
+    return cuda_status(launch_attend(q, dtype == CANOPY_BF16, k_cache, v_cache, page_table, pages, log_page,
+                                     max_pages, context, starts, parent, lengths, N, B, HQ, HKV, d, window, sinks,
+                                     scale, o, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+canopy_status canopy_cache_commit(const int32_t* accepted, const int32_t* parent, const int32_t* lengths,
+                                  void* k_cache, void* v_cache, canopy_dtype dtype, const int32_t* page_table,
+                                  int pages, int page_size, int max_pages, const int32_t* context, int T, int B,
+                                  int HKV, int d, int32_t* context_new, int32_t* err, void* stream) {
+    if (!accepted || !aligned4(accepted) || !parent || !aligned4(parent) || !aligned4(lengths) ||
+        !aligned16(k_cache) || !aligned16(v_cache) || !page_table || !aligned4(page_table) || !context ||
+        !aligned4(context) || !context_new || !aligned4(context_new) || context_new == context || !aligned4(err))
+        return CANOPY_ERR_ARG;
+    if (!dtype_ok(dtype) || T <= 0) return CANOPY_ERR_ARG;
+    const canopy_status as = layer_sizes(1, B, HKV, HKV, d);
+    if (as != CANOPY_OK) return as;
+    int log_page = 0;
+    const canopy_status cs = cache_sizes(pages, page_size, max_pages, HKV, log_page);
+    if (cs != CANOPY_OK) return cs;
+    if (T > kMaxT) return CANOPY_ERR_UNSUPPORTED;
+    return cuda_status(launch_cache_commit(accepted, parent, lengths, k_cache, v_cache, dtype == CANOPY_BF16,
+                                           page_table, pages, log_page, max_pages, context, T, B, HKV, d,
+                                           context_new, err, static_cast<cudaStream_t>(stream)));
 }
 
 canopy_status canopy_tree_conv(const void* x, canopy_dtype dtype, const float* conv_state, const float* weight,

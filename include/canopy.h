@@ -115,6 +115,7 @@ typedef enum {
 #define CANOPY_DEVERR_TIMEOUT  0x8  /* an internal bounded wait gave up                 */
 #define CANOPY_DEVERR_LENGTH   0x10 /* lengths[b] not in [0, T], or starts out of order  */
 #define CANOPY_DEVERR_TOKEN    0x20 /* accept: a drafted token not in [0, V)            */
+#define CANOPY_DEVERR_PAGE     0x40 /* a place beyond the page table, or a page not in [0, pages) */
 
 /* Size in bytes of the workspace one verify/commit pair needs, for HV value
  * heads.  It holds the pseudo-values U fp32 [B][T][HV][dv], the cumulative
@@ -339,6 +340,105 @@ canopy_status canopy_accept(const void* p, const void* q, canopy_dtype dtype, co
                             const int32_t* parent, const int32_t* lengths, const float* u, const float* noise, int T,
                             int B, int V, int32_t* accepted, int32_t* out_tokens, int32_t* counts, int32_t* err,
                             void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The softmax attention layers between Gated DeltaNet layers.
+ *
+ * Keys and values lie in pages: k_cache and v_cache are device arrays
+ * [pages][HKV][page_size][d] in dtype (bf16 or fp32), page_size a power of two
+ * of at least 16, and page_table device int32 [B][max_pages] names stream b's
+ * pages in order; place i of stream b is slot i % page_size of page
+ * page_table[b][i / page_size].  context device int32 [B]: the tokens that stream b
+ * has in the cache before the call; its new rows lie behind them, row i at place
+ * context[b] + i.  Entries of the page table that no place of the call needs
+ * may hold anything.  Heads: HQ query heads on HKV key heads, HQ a multiple of
+ * HKV, at most 64 to one; d = 64 or 128.
+ *
+ * Rows are packed, sequence b at starts[b] .. starts[b+1] - 1 of N (starts device
+ * int32 [B+1], as canopy_prefill takes it; rows behind the last sequence are left
+ * as they were), or with starts NULL N / B rows to each stream: one token each, or
+ * the nodes of its draft tree, of which the first lengths[b] are there (lengths
+ * device int32 [B], or NULL for all; rows past them are left as they were). */
+
+typedef enum { CANOPY_NORM_NONE = 0, CANOPY_NORM_RMS = 1, CANOPY_NORM_L2 = 2 } canopy_norm;
+typedef enum { CANOPY_PAIRS_HALF = 0, CANOPY_PAIRS_ADJACENT = 1 } canopy_pairs;
+
+/* Queries and keys of a layer in one pass: the norm of every head's row, the
+ * rotation by position, and keys and values into the cache.
+ *   q [N][HQ][d], k, v [N][HKV][d] in dtype, the rows of token n at ldq, ldk, ldv
+ *   elements times n (a multiple of 16 bytes; the heads of a token dense).
+ *   norm: CANOPY_NORM_RMS x / sqrt(mean x^2 + eps), CANOPY_NORM_L2 x / sqrt(sum
+ *   x^2 + eps), CANOPY_NORM_NONE; q_weight, k_weight device fp32 [d] times that, or
+ *   NULL (NULL with CANOPY_NORM_NONE).
+ *   freqs device fp32 [R/2] (NULL for R = 0): pair j of the first R columns
+ *   (R a multiple of 8, at most d) turns by position * freqs[j]; pairs are columns
+ *   (j, j + R/2), or (2j, 2j + 1) with CANOPY_PAIRS_ADJACENT.  positions device int32
+ *   [axes][N], or NULL for the token's place in the cache; axis device int32
+ *   [R/2], the axis whose position pair j turns by (a value outside
+ *   [0, axes) is read as the nearest), or NULL for axis 0.
+ *   q_out [N][HQ][d] (may be q, where that is dense).  With caches, keys and
+ *   values go into them, k_out is NULL and v, page_table and context are given.
+ *   Without (k_cache NULL), k_out [N][HKV][d] (may be k) receives the keys, and
+ *   v, v_cache, page_table, context, starts and lengths are NULL, B 0.
+ * Norm and rotation in fp32 (angles of any int32 position to 1e-7), rounded once.
+ * err: an optional device int32 (OR-ed): a place without a page sets
+ * CANOPY_DEVERR_PAGE and is not written.  Any other value of q_out, k_out and the
+ * caches stays as it was. */
+canopy_status canopy_qk_prep(const void* q, const void* k, const void* v, canopy_dtype dtype, int64_t ldq,
+                             int64_t ldk, int64_t ldv, canopy_norm norm, const float* q_weight,
+                             const float* k_weight, float eps, const float* freqs, int R, const int32_t* positions,
+                             int axes, const int32_t* axis, canopy_pairs pairs, int N, int B, int HQ, int HKV, int d,
+                             void* q_out, void* k_out, void* k_cache, void* v_cache, const int32_t* page_table,
+                             int pages, int page_size, int max_pages, const int32_t* context, const int32_t* starts,
+                             const int32_t* lengths, int32_t* err, void* stream);
+
+/* Workspace of canopy_attend calls over up to N rows of B sequences with these
+ * heads.  Clear its first 4096 bytes once after allocating it (canopy_workspace_init);
+ * calls that may run at the same time need one each.  Returns 0 for
+ * unsupported sizes. */
+size_t canopy_attend_workspace_bytes(int N, int B, int HQ, int HKV, int d);
+
+/* How an attend call is carried out (canopy_attend_plan). */
+typedef enum {
+    CANOPY_ATTEND_PLAN_NONE = -1, /* the call would be refused                                   */
+    CANOPY_ATTEND_PLAN_FP32 = 0,  /* fp32: CUDA cores                                           */
+    CANOPY_ATTEND_PLAN_FEW = 1,   /* bf16, few rows a sequence: bound by the cache's reads        */
+    CANOPY_ATTEND_PLAN_TILES = 2  /* bf16, many rows: tensor-core tiles of 256 rows x 128 keys  */
+} canopy_attend_plan_t;
+canopy_attend_plan_t canopy_attend_plan(int N, int B, int HQ, int HKV, canopy_dtype dtype, int d);
+
+/* Attention of the new rows over the cache, whose places already hold their keys
+ * and values (canopy_qk_prep): with c = context[b], row i at position t_i = c + i
+ * (with parent: c + its depth),
+ *   o_i = sum_j p_ij v_j,  p_ij = softmax over the places j that i sees of scale q_i.k_j.
+ * Row i sees places j <= c + i; with parent (device int32 [B][T], T = N / B <= 256
+ * and starts NULL, as canopy_tree_verify takes it) the places j < c and those of its
+ * root path, itself among them.  With window > 0 of these only the tokens whose
+ * position is less than window before t_i, and those at positions < sinks.
+ *   q, o [N][HQ][d] in dtype; the places that no row of a sequence sees (behind its
+ *   last row, out of the window) need no page and may hold anything; what a place
+ *   holds reaches no row that does not see it.
+ * bf16: products on the tensor cores with fp32 sums and statistics, the weights
+ * rounded to bf16 for the second product; fp32: fp32 throughout.
+ * Data errors (parent, starts, lengths, context, pages) set bits in the workspace's
+ * error word (canopy_read_device_error). */
+canopy_status canopy_attend(const void* q, canopy_dtype dtype, const void* k_cache, const void* v_cache,
+                            const int32_t* page_table, int pages, int page_size, int max_pages,
+                            const int32_t* context, const int32_t* starts, const int32_t* parent,
+                            const int32_t* lengths, int N, int B, int HQ, int HKV, int d, int window, int sinks,
+                            float scale, void* o, void* workspace, void* stream);
+
+/* The cache after accepting node accepted[b] of every stream's tree (as
+ * canopy_commit takes it): the accepted node's root path, whose keys and values
+ * lie at places context[b] + node, moves to context[b] + 0, 1, 2, ... in depth
+ * order, in place, and context_new[b] (device int32 [B], not context itself) =
+ * context[b] + the path's length.  accepted -1 keeps nothing of the tree; an
+ * accepted node out of range sets CANOPY_DEVERR_ACCEPTED in *err and does the same.
+ * parent device int32 [B][T], T <= 256; lengths as canopy_tree_verify takes it. */
+canopy_status canopy_cache_commit(const int32_t* accepted, const int32_t* parent, const int32_t* lengths,
+                                  void* k_cache, void* v_cache, canopy_dtype dtype, const int32_t* page_table,
+                                  int pages, int page_size, int max_pages, const int32_t* context, int T, int B,
+                                  int HKV, int d, int32_t* context_new, int32_t* err, void* stream);
 
 /* Activation after the short convolution. */
 typedef enum { CANOPY_ACT_NONE = 0, CANOPY_ACT_SILU = 1 } canopy_activation;

@@ -32,6 +32,8 @@ Modules
   conv         the tree-aware short causal convolution and its state commit
   serving      the layer over packed prompts token by token; the accepted node
                of a draft tree from probabilities and random numbers
+  attention    the attention layers' operators: norms and rotations, attention
+               over a paged cache, the accepted path's move in it
 
 Pins (tests/test_oracle_*.py, run with -m "not gpu"): chain = sequential
 recurrence; brute force on every tree of at most 8 nodes; closed form = replay
@@ -60,4 +62,4 @@ from .closed_form import (  # noqa: F401
 )
 from .commit import commit, commit_batch  # noqa: F401
 from .conv import tree_conv, tree_conv_batch, conv_commit, conv_commit_batch  # noqa: F401
-from . import serving  # noqa: F401
+from . import serving, attention  # noqa: F401

@@ -461,7 +461,7 @@ canopy_status canopy_attend(const void* q, canopy_dtype dtype, const void* k_cac
         !context || !aligned4(context) || !aligned4(starts) || !aligned4(parent) || !aligned4(lengths) ||
         !aligned16(o) || !aligned16(workspace))
         return CANOPY_ERR_ARG;
-    if (!dtype_ok(dtype) || !std::isfinite(scale) || window < 0 || sinks < 0 || (sinks && !window))
+    if (!dtype_ok(dtype) || !std::isfinite(scale) || scale <= 0.f || window < 0 || sinks < 0 || (sinks && !window))
         return CANOPY_ERR_ARG;
     const canopy_status as = layer_sizes(N, B, HQ, HKV, d);
     if (as != CANOPY_OK) return as;

@@ -203,8 +203,8 @@ __global__ void __launch_bounds__(NT) attend_kernel(const Args a, int least) {
 #pragma unroll
             for (int x = 8; x; x >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], x);
         if (p.pieces > 1) {
-            constexpr int SLOT = R * (D + 2);
-            float* out = a.part + size_t(p.slot) * SLOT;
+            const size_t SLOT = size_t(a.slot_rows) * (D + 2);
+            float* out = a.part + p.slot * SLOT;
 #pragma unroll
             for (int r = 0; r < RR; ++r) {
                 const int row = ty * RR + r;
@@ -231,13 +231,13 @@ __global__ void __launch_bounds__(NT) attend_kernel(const Args a, int least) {
                 const int row = ty * RR + r;
                 float top = -INFINITY;
                 for (int i = 0; i < p.pieces; ++i)
-                    top = fmaxf(top, __ldcg(a.part + size_t(slot_of(p.first, i)) * SLOT + R * D + row));
+                    top = fmaxf(top, __ldcg(a.part + slot_of(p.first, i) * SLOT + R * D + row));
                 const float base = top == -INFINITY ? 0.f : top;
                 l[r] = 0.f;
 #pragma unroll
                 for (int c = 0; c < C4; ++c) o[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
                 for (int i = 0; i < p.pieces; ++i) {
-                    const float* in = a.part + size_t(slot_of(p.first, i)) * SLOT;
+                    const float* in = a.part + slot_of(p.first, i) * SLOT;
                     const float w = exp2f(__ldcg(in + R * D + row) - base);
                     l[r] += w * __ldcg(in + R * D + R + row);
 #pragma unroll
@@ -282,13 +282,19 @@ cudaError_t launch(const Args& a, int least, cudaStream_t st) {
 
 // ---------------------------------------------------------------------------
 
+int tc_tile_tokens(int g);
+cudaError_t launch_tc(const Args& a, int d, int least, cudaStream_t st);
+
 namespace {
 
-constexpr int kMaxCtas = 304;  // two CTAs on each of the 152 SMs
+constexpr int kCtas = 152;  // one on every SM
 constexpr int kLeast = 2;      // units of a part
 
-// A row tile's tokens, for g query heads a key head.
-int tile_tokens(int rows, int g) { return rows / g; }
+// Rows of an unfinished piece: those of the largest row tile that a call takes.
+int slot_rows(int N, int g) {
+    const int64_t rows = int64_t(N) * g;
+    return rows <= 16 ? 16 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+}
 
 struct Layout {
     size_t seqs, tiles, line, first_tile, total, mask, depth, done, part, end;
@@ -300,14 +306,14 @@ Layout layout(int N, int B, int g, int d) {
     Layout w;
     size_t o = 256;  // the error word, and the count of tiles behind it
     w.total = 128;
-    w.done = o;       o = ws_align(o + kMaxCtas * 4);
+    w.done = o;       o = ws_align(o + 2 * kCtas * 4);
     w.seqs = o;       o = ws_align(o + size_t(B) * sizeof(int4));
     w.tiles = o;      o = ws_align(o + max_tiles * sizeof(Tile));
     w.line = o;       o = ws_align(o + (max_tiles + 1) * 8);
-    w.first_tile = o; o = ws_align(o + kMaxCtas * 4);
+    w.first_tile = o; o = ws_align(o + kCtas * 4);
     w.mask = o;       o = ws_align(o + size_t(N) * kMaskWords * 4);
     w.depth = o;      o = ws_align(o + size_t(N) * 4);
-    w.part = o;       o = ws_align(o + size_t(2 * kMaxCtas) * 64 * (d + 2) * 4);
+    w.part = o;       o = ws_align(o + size_t(2 * kCtas) * slot_rows(N, g) * (d + 2) * 4);
     w.end = o;
     return w;
 }
@@ -317,7 +323,10 @@ Layout layout(int N, int B, int g, int d) {
 }  // namespace att
 
 size_t attend_ws_bytes(int N, int B, int HQ, int HKV, int d) { return att::layout(N, B, HQ / HKV, d).end; }
-canopy_attend_plan_t attend_plan(int N, int B, int HQ, int HKV, int bf16, int d) { return CANOPY_ATTEND_PLAN_FP32; }
+canopy_attend_plan_t attend_plan(int N, int B, int HQ, int HKV, int bf16, int d) {
+    if (!bf16) return CANOPY_ATTEND_PLAN_FP32;
+    return CANOPY_ATTEND_PLAN_TILES;
+}
 
 cudaError_t launch_attend(const void* q, int bf16, const void* kc, const void* vc, const int32_t* table, int pages,
                           int log_page, int max_pages, const int32_t* context, const int32_t* starts,
@@ -346,11 +355,13 @@ cudaError_t launch_attend(const void* q, int bf16, const void* kc, const void* v
     a.window = window > 0 ? window : kNoWindow;
     a.sinks = sinks;
     a.scale2 = scale * 1.4426950408889634f;
+    const canopy_attend_plan_t plan = attend_plan(N, B, HQ, HKV, bf16, d);
     const int R = size_t(N) * a.g <= size_t(16) * B && a.g <= 16 ? 16 : 64;
-    a.rt = tile_tokens(R, a.g);
-    a.log_kt = 6;
-    a.ctas = 152;
+    a.rt = plan == CANOPY_ATTEND_PLAN_TILES ? tc_tile_tokens(a.g) : R / a.g;
+    a.log_kt = plan == CANOPY_ATTEND_PLAN_TILES ? 7 : 6;
+    a.ctas = kCtas;
     a.max_tiles = N + B;
+    a.slot_rows = slot_rows(N, a.g);
     const Layout w = layout(N, B, a.g, d);
     char* p = static_cast<char*>(workspace);
     a.err = reinterpret_cast<int32_t*>(p);
@@ -365,16 +376,10 @@ cudaError_t launch_attend(const void* q, int bf16, const void* kc, const void* v
     a.part = reinterpret_cast<float*>(p + w.part);
     cudaError_t e = launch_pdl(plan_kernel, dim3(parent ? B + 1 : 1), dim3(256), 0, st, a, kLeast);
     if (e != cudaSuccess) return e;
-    using bf = __nv_bfloat16;
-#define CANOPY_ATTEND(IT, D)                                               \
-    return R == 16 ? simt::launch<IT, D, 16>(a, kLeast, st) : simt::launch<IT, D, 64>(a, kLeast, st)
-    if (bf16) {
-        if (d == 128) CANOPY_ATTEND(bf, 128);
-        CANOPY_ATTEND(bf, 64);
-    }
-    if (d == 128) CANOPY_ATTEND(float, 128);
-    CANOPY_ATTEND(float, 64);
-#undef CANOPY_ATTEND
+    if (plan == CANOPY_ATTEND_PLAN_TILES) return launch_tc(a, d, kLeast, st);
+    if (d == 128)
+        return R == 16 ? simt::launch<float, 128, 16>(a, kLeast, st) : simt::launch<float, 128, 64>(a, kLeast, st);
+    return R == 16 ? simt::launch<float, 64, 16>(a, kLeast, st) : simt::launch<float, 64, 64>(a, kLeast, st);
 }
 
 }  // namespace canopy

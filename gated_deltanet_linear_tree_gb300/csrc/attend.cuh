@@ -37,6 +37,7 @@ struct Args {
     int window, sinks;
     float scale2;  // scale * log2(e): weights are powers of two
     int rt, log_kt, ctas, max_tiles;
+    int slot_rows;  // rows of a slot
     // workspace
     int32_t* err;
     int4* seqs;       // [B]: first row, rows, ctx, first tile
@@ -46,7 +47,7 @@ struct Args {
     int* total;       // number of tiles
     uint32_t* mask;   // trees: [N][kMaskWords], the nodes of a row's path that it sees
     int32_t* depth;   // trees: [N]
-    int32_t* done;    // [ctas]: pieces of the item that begins in CTA c that are finished
+    int32_t* done;    // [2 ctas]: pieces finished of the item that begins in CTA c (by halves of its rows)
     float* part;      // [2 ctas] slots
 };
 

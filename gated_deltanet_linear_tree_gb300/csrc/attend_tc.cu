@@ -1,0 +1,595 @@
+// Attention of many new rows over a paged cache on the tensor cores (bf16).
+//
+// A CTA works on up to 256 rows of one (sequence, key head): two halves of 128
+// lanes, each of 128 / g tokens with the g query heads that share the key head,
+// against key tiles of 128.  Per half and key tile
+//     S = Q K^T            (128 x 128 x d, Q and K in shared memory)
+//     P = 2^(scale2 S - m) (four warps, a row a thread; bf16 over S's columns)
+//     O += P V             (128 x d x 128, P from tensor memory)
+// with S and O of both halves in the 512 columns of tensor memory.  While one
+// half's rows are in the softmax the other half's products run.  m is the
+// running maximum as of the last time that it grew by more than 2^8: until then
+// the weights are merely larger than 1, by less than 2^8, and neither sums nor
+// roundings know the difference; when it does grow, the row's thread scales O.
+// The weights are rounded to bf16 for the second product (their sum is of the
+// unrounded ones): a rounding of 2^-9 each, which averages out over the keys.
+//
+// Key tiles come by TMA, one box per page and 64 columns, into a ring of stages
+// that K and V tiles take in turns.  A page that no row sees is read at a
+// coordinate outside the cache, as zeros.  Where not every row sees every key of
+// a tile, two warps look through its V first: what no row sees, and what is not
+// finite, becomes zero (0 times it would reach every row's sum), and a row that
+// sees a key with such a value is NaN.
+#include "attend.cuh"
+
+namespace canopy {
+
+bool make_bf16_box_map(CUtensorMap* m, const void* base, const uint64_t (&dim)[3], const uint64_t (&stride)[2],
+                       const uint32_t (&size)[3]);
+
+namespace att {
+namespace tcg {
+
+constexpr int KT = 128, NT = 384;
+constexpr uint32_t kCols = 512;
+constexpr float kGrow = 8.f;  // the maximum is kept until it grows by this, in powers of two
+
+template <int D>
+struct Shape {
+    static constexpr int TILE = 128 * D * 2;  // Q half, K or V tile: [d / 64][128 rows][128 bytes]
+    static constexpr int STAGES = D == 128 ? 5 : 10;
+    static constexpr int Q = 0, KV = 2 * TILE, BARS = KV + STAGES * TILE;
+    // barriers: Q full, Q read, all products done; per stage full, empty, and V looked through; per half S full, P
+    // there, O full, piece written, its place in the order told
+    static constexpr int NBAR = 3 + 3 * STAGES + 10;
+    static constexpr int POISON = BARS + 8 * NBAR;         // [STAGES][4] words: keys with a value that is not finite
+    static constexpr int MISC = POISON + 16 * STAGES;      // tensor memory's address, flags
+    static constexpr int TOTAL = MISC + 32;
+};
+static_assert(Shape<128>::TOTAL + 1024 <= 232448 && Shape<64>::TOTAL + 1024 <= 232448, "shared memory");
+
+__device__ inline uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ inline void unpack2(uint64_t x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ inline uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ inline uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ inline float exp2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ inline uint32_t pack_bf16(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+
+// Bits [a, b) of a word.
+__device__ inline uint32_t range_bits(int a, int b) {
+    a = min(max(a, 0), 32);
+    b = min(max(b, a), 32);
+    return uint32_t((1ull << b) - (1ull << a));
+}
+// Which of the keys [base, base + 32) a row sees (att::sees for 32 keys).
+__device__ inline uint32_t seen_bits(const Args& a, const Tile& tile, int depth, const uint32_t* mask, int base) {
+    const int pos = tile.ctx + depth;
+    const int end = (mask ? min(pos, tile.ctx - 1) : pos) + 1;  // past the last one in the cache, or in all
+    const int64_t near = int64_t(pos) - a.window + 1 - base;
+    uint32_t bits = range_bits(int(near > 0 ? near : 0), end - base) | range_bits(0, min(a.sinks, end) - base);
+    const int p = base - tile.ctx;
+    if (mask && p > -32 && p < kMaxT) {
+        if (p < 0) {
+            bits |= mask[0] << -p;
+        } else {
+            const uint32_t lo = mask[p >> 5], hi = (p >> 5) + 1 < kMaskWords ? mask[(p >> 5) + 1] : 0u;
+            bits |= __funnelshift_r(lo, hi, p & 31);
+        }
+    }
+    return bits;
+}
+
+__device__ inline bool finite_pair(uint32_t x) {
+    return (x & 0x7F80u) != 0x7F80u && (x & 0x7F800000u) != 0x7F800000u;
+}
+
+// A wait of a whole warp, which goes on or gives up together.
+__device__ inline bool warp_wait(uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+// Waits for a barrier's phases in turn.
+struct Phase {
+    uint32_t bit = 0;
+    __device__ bool wait(uint64_t* bar) {
+        const bool ok = warp_wait(bar, bit);
+        bit ^= 1;
+        return ok;
+    }
+};
+// A place in the ring of stages.
+template <int STAGES>
+struct Ring {
+    int at = 0;
+    uint32_t phase = 0;
+    __device__ void step() {
+        if (++at == STAGES) {
+            at = 0;
+            phase ^= 1;
+        }
+    }
+    __device__ void back() {
+        if (at-- == 0) {
+            at = STAGES - 1;
+            phase ^= 1;
+        }
+    }
+};
+
+template <int D>
+__global__ void __launch_bounds__(NT, 1)
+    attend_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
+                  const __grid_constant__ CUtensorMap mapV, const Args a, int least) {
+    using Sh = Shape<D>;
+    constexpr int HALVES = D / 64;
+    extern __shared__ uint8_t raw[];
+    uint8_t* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Sh::BARS);
+    uint64_t *q_full = bars, *q_read = bars + 1, *full = bars + 2, *empty = full + Sh::STAGES,
+             *looked = empty + Sh::STAGES, *s_full = looked + Sh::STAGES, *p_there = s_full + 2, *o_full = p_there + 2,
+             *written = o_full + 2, *told = written + 2, *drained = told + 2;
+    uint32_t* poison = reinterpret_cast<uint32_t*>(sm + Sh::POISON);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Sh::MISC);
+    int* last = reinterpret_cast<int*>(sm + Sh::MISC + 8);  // [2]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (warp == 8) {
+        tmem_alloc(tmem_slot, kCols);
+        tmem_relinquish();
+    }
+    if (warp == 9 && lane == 0) {
+        mbar_init(q_full, 1);
+        mbar_init(q_read, 1);
+        for (int i = 0; i < Sh::STAGES; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 3);  // the products, and the two warps that look through V
+            mbar_init(looked + i, 64);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full + i, 1);
+            mbar_init(p_there + i, 128);
+            mbar_init(o_full + i, 1);
+            mbar_init(written + i, 128);
+            mbar_init(told + i, 1);
+        }
+        mbar_init(drained, 1);
+        fence_mbar_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+
+    const int ntiles = *a.total;
+    const int64_t units = a.line[ntiles];
+    const int ctas = parts(a, units, least);
+    const bool work = int(blockIdx.x) < ctas && units > 0;
+    Walk walk{units, 0, 0, ctas, 0};
+    if (work) {
+        walk.at = cta_begin(units, ctas, blockIdx.x);
+        walk.end = cta_begin(units, ctas, blockIdx.x + 1);
+        walk.tile = a.first_tile[blockIdx.x];
+    }
+    const int half_tok = a.rt / 2;  // tokens of a half
+    bool ok = true;
+    Piece p;
+
+    // 200 registers for the softmax's warps, 104 for the others: all of the 64,512 that the block was launched with
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        if (warp == 9) {
+            // ---- loads -----------------------------------------------------------------
+            Ring<Sh::STAGES> ring;
+            uint32_t q_phase = 1;  // the first Q needs nothing read
+            int q_loads = 0, loads = 0;
+            const int box = min(1 << a.log_page, KT), boxes = KT / box;  // keys of a box, boxes of a tile
+            const int i = lane / HALVES, part = lane % HALVES;           // this lane's boxes: i, i + 32 / HALVES, ...
+            int bad = 0;
+            while (ok && walk.next(a, p)) {
+                const Tile& tile = p.tile;
+                const bool two = tile.ntok > half_tok;
+                ok = warp_wait(q_read, q_phase);
+                q_phase ^= 1;
+                if (!ok) break;
+                ++q_loads;
+                if (lane == 0) {
+                    mbar_expect_tx(q_full, (two ? 2 : 1) * HALVES * half_tok * a.g * 128);
+                    for (int h = 0; h < (two ? 2 : 1); ++h)
+                        for (int c = 0; c < HALVES; ++c)
+                            tma_load_3d(sm + Sh::Q + h * Sh::TILE + c * 16384, &mapQ, q_full, 64 * c, p.h * a.g,
+                                        tile.row + h * half_tok);
+                }
+                for (int u = p.u0; ok && u < p.u1; ++u) {
+                    const int key = key_tile(tile, u) * KT + i * box;
+                    int z = a.pages * a.HKV;  // outside: zeros
+                    if (i < boxes) {
+                        bool reach = key < tile.sink_end || (key + box > tile.near && key < tile.hi);
+                        if (reach) {
+                            const int page = a.table[size_t(tile.b) * a.max_pages + (key >> a.log_page)];
+                            if (page < 0 || page >= a.pages) bad = CANOPY_DEVERR_PAGE;
+                            else z = page * a.HKV + p.h;
+                        }
+                    }
+                    const int slot = key & ((1 << a.log_page) - 1);
+    #pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        ok = ok && warp_wait(empty + ring.at, ring.phase ^ 1);
+                        if (!ok) break;
+                        ++loads;
+                        uint8_t* dst = sm + Sh::KV + ring.at * Sh::TILE;
+                        if (lane == 0) mbar_expect_tx(full + ring.at, Sh::TILE);
+                        __syncwarp();
+                        if (i < boxes)
+                            tma_load_3d(dst + part * 16384 + i * box * 128, kv ? &mapV : &mapK, full + ring.at, 64 * part,
+                                        slot, z);
+                        ring.step();
+                    }
+                }
+            }
+            if (bad) raise_err(a.err, bad);
+            // no copy is left in flight, should another warp have given up
+            if (q_loads) warp_wait(q_full, (q_loads - 1) & 1);
+            for (int i = min(loads, Sh::STAGES); i > 0; --i) {
+                ring.back();
+                warp_wait(full + ring.at, ring.phase);
+            }
+        } else if (warp == 8) {
+            // ---- products ---------------------------------------------------------------
+            Ring<Sh::STAGES> ring, look;
+            Phase q_ready, p_ready[2];
+            const uint32_t qa = smem_u32(sm + Sh::Q), kv = smem_u32(sm + Sh::KV);
+            const bool lead = lane == 0;
+            // (descriptors hold addresses in units of 16 bytes: a step is an addition)
+            auto scores = [&](int h, int stage) {
+                const uint64_t q = sdesc_sw128(qa + h * Sh::TILE), k = sdesc_sw128(kv + stage * Sh::TILE);
+                if (lead)
+    #pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        const int step = (i >> 2) * 1024 + (i & 3) * 2;
+                        mma_bf16_ss(tmem + 128 * h, q + step, k + step, idesc_bf16(128, KT), i > 0);
+                    }
+            };
+            auto values = [&](int h, int stage, bool add) {
+                const uint64_t v = sdesc_sw128_mn(kv + stage * Sh::TILE, 16384);
+                if (lead)
+    #pragma unroll
+                    for (int i = 0; i < KT / 16; ++i)
+                        mma_bf16_ts(tmem + 256 + D * h, tmem + 128 * h + 8 * i, v + i * 128,
+                                    idesc_bf16(128, D) | kIdescBMnMajor, add || i > 0);
+            };
+            auto commit = [&](uint64_t* bar) {
+                if (lead) mma_commit(bar);
+                __syncwarp();
+            };
+            while (ok && walk.next(a, p)) {
+                const Tile& tile = p.tile;
+                const int nh = tile.ntok > half_tok ? 2 : 1;
+                ok = q_ready.wait(q_full) && warp_wait(full + ring.at, ring.phase);
+                if (!ok) break;
+                tc_fence_after();
+                for (int h = 0; h < nh; ++h) {
+                    scores(h, ring.at);
+                    commit(s_full + h);
+                }
+                commit(empty + ring.at);
+                if (p.u1 - p.u0 == 1) commit(q_read);
+                ring.step();
+                for (int u = p.u0; ok && u < p.u1; ++u) {
+                    const bool more = u + 1 < p.u1, all = all_see(a, tile, key_tile(tile, u) * KT, KT);
+                    const Ring<Sh::STAGES> v = ring;
+                    ring.step();
+                    ok = warp_wait(full + v.at, v.phase);
+                    if (ok && !all) {
+                        ok = warp_wait(looked + look.at, look.phase);
+                        look.step();
+                    }
+                    for (int h = 0; ok && h < nh; ++h) {
+                        ok = p_ready[h].wait(p_there + h);
+                        if (!ok) break;
+                        tc_fence_after();
+                        values(h, v.at, u > p.u0);
+                        if (h == nh - 1) commit(empty + v.at);
+                        if (!more) {
+                            commit(o_full + h);
+                            continue;
+                        }
+                        if (h == 0) ok = warp_wait(full + ring.at, ring.phase);
+                        if (!ok) break;
+                        tc_fence_after();
+                        scores(h, ring.at);
+                        commit(s_full + h);
+                        if (h == nh - 1) {
+                            commit(empty + ring.at);
+                            if (u + 2 == p.u1) commit(q_read);
+                        }
+                    }
+                    if (more) ring.step();
+                }
+            }
+            commit(drained);
+            warp_wait(drained, 0);
+        } else if (warp >= 10) {
+            // ---- looks through V where not every row sees every key ---------------------
+            // Every stage is waited for and let go, so that these warps neither fall behind the ring nor get ahead of it.
+            Ring<Sh::STAGES> ring, look;
+            while (ok && walk.next(a, p)) {
+                const Tile& tile = p.tile;
+                for (int u = p.u0; ok && u < p.u1; ++u)
+                    for (int kv = 0; kv < 2; ++kv) {
+                        ok = warp_wait(full + ring.at, ring.phase);
+                        if (!ok) break;
+                        const int key = key_tile(tile, u) * KT;
+                        if (kv && !all_see(a, tile, key, KT)) {
+                            const int row0 = 64 * (warp - 10);  // this warp's keys
+                            uint32_t* words = poison + 4 * look.at;
+                            if (lane < 2) words[2 * (warp - 10) + lane] = 0;
+                            __syncwarp();
+    #pragma unroll
+                            for (int c = 0; c < HALVES; ++c) {
+                                uint4* v = reinterpret_cast<uint4*>(sm + Sh::KV + ring.at * Sh::TILE + c * 16384) + 8 * row0;
+    #pragma unroll 8
+                                for (int e = lane; e < 64 * 8; e += 32) {
+                                    const int row = row0 + (e >> 3);
+                                    const uint4 x = v[e];
+                                    const bool there = in_reach(tile, key + row);
+                                    if (there && finite_pair(x.x) && finite_pair(x.y) && finite_pair(x.z) && finite_pair(x.w))
+                                        continue;
+                                    v[e] = make_uint4(0, 0, 0, 0);
+                                    if (there) atomicOr(words + (row >> 5), 1u << (row & 31));
+                                }
+                            }
+                            fence_proxy_async_smem();
+                            mbar_arrive(looked + look.at);
+                            look.step();
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(empty + ring.at);
+                        ring.step();
+                    }
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        // ---- softmax ------------------------------------------------------------------
+        const int h = warp >> 2, r = threadIdx.x & 127;
+        const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16), S = lanes + 128 * h, O = lanes + 256 + D * h;
+        Ring<Sh::STAGES> look;
+        Phase scores_ready, o_ready, place_told;
+        uint32_t write_phase = 0;
+        const int tok_in_half = r / a.g, head = r % a.g;
+        while (ok && walk.next(a, p)) {
+            const Tile& tile = p.tile;
+            const bool mine = h == 0 || tile.ntok > half_tok;  // this half has rows
+            const int tok = h * half_tok + tok_in_half;
+            const bool valid = tok_in_half < half_tok && tok < tile.ntok;
+            const int row = tile.row + min(tok, tile.ntok - 1);
+            const int depth = a.parent ? (mine ? a.depth[row] : 0) : tile.t0 + tok;
+            const uint32_t* mask = a.parent ? a.mask + size_t(row) * kMaskWords : nullptr;
+            float m = -INFINITY, base = 0.f;  // the maximum that the weights are relative to, scaled
+            float l = 0.f;
+            for (int u = p.u0; u < p.u1; ++u) {
+                const int key = key_tile(tile, u) * KT;
+                const bool all = all_see(a, tile, key, KT);
+                const Ring<Sh::STAGES> v = look;
+                if (!all) look.step();
+                if (!mine) continue;
+                ok = scores_ready.wait(s_full + h);
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t s[128];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(S + 32 * c, s + 32 * c);
+                tmem_wait_ld();
+                if (!all) {
+                    uint32_t seen[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) seen[c] = seen_bits(a, tile, depth, mask, key + 32 * c);
+#pragma unroll
+                    for (int j = 0; j < 128; ++j)
+                        if (!((seen[j >> 5] >> (j & 31)) & 1u)) s[j] = 0xFF800000u;
+                    ok = warp_wait(looked + v.at, v.phase);
+                    if (!ok) break;
+                    const uint32_t* words = poison + 4 * v.at;
+                    if ((words[0] & seen[0]) | (words[1] & seen[1]) | (words[2] & seen[2]) | (words[3] & seen[3]))
+                        l = NAN;
+                }
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int j = 0; j < 128; j += 8)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        top[c] = fmaxf(top[c], fmaxf(__uint_as_float(s[j + 2 * c]), __uint_as_float(s[j + 2 * c + 1])));
+                const float t = a.scale2 * fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                const bool grow = t > m + kGrow;  // (the first finite one too)
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float keep = grow ? exp2_approx(m - t) : 1.f;
+                    if (grow) {
+                        m = t;
+                        base = t;
+                    }
+                    l *= keep;
+                    if (u > p.u0) {
+#pragma unroll
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(O + c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
+                            tmem_st16(O + c, o);
+                        }
+                    }
+                }
+                const uint64_t sc = pack2(a.scale2, a.scale2), mb = pack2(-base, -base);
+                uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float x, y;
+                        unpack2(fma2(pack2(__uint_as_float(s[c + 2 * j]), __uint_as_float(s[c + 2 * j + 1])), sc, mb), x,
+                                y);
+                        x = exp2_approx(x);
+                        y = exp2_approx(y);
+                        if (j & 1) sum1 = add2(sum1, pack2(x, y));
+                        else sum0 = add2(sum0, pack2(x, y));
+                        w[j] = pack_bf16(x, y);
+                    }
+                    tmem_st16(S + c / 2, w);
+                }
+                float x, y;
+                unpack2(add2(sum0, sum1), x, y);
+                l += x + y;
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(p_there + h);
+            }
+            if (!ok) break;
+            if (!mine) continue;
+            ok = o_ready.wait(o_full + h);
+            if (!ok) break;
+            tc_fence_after();
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            if (p.pieces == 1) {
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + (size_t(row) * a.HQ + p.h * a.g + head) * D;
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(O + c, o);
+                    tmem_wait_ld();
+                    if (valid)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint4 w;
+                            w.x = pack_bf16(__uint_as_float(o[8 * j]) * inv, __uint_as_float(o[8 * j + 1]) * inv);
+                            w.y = pack_bf16(__uint_as_float(o[8 * j + 2]) * inv, __uint_as_float(o[8 * j + 3]) * inv);
+                            w.z = pack_bf16(__uint_as_float(o[8 * j + 4]) * inv, __uint_as_float(o[8 * j + 5]) * inv);
+                            w.w = pack_bf16(__uint_as_float(o[8 * j + 6]) * inv, __uint_as_float(o[8 * j + 7]) * inv);
+                            *reinterpret_cast<uint4*>(out + c + 8 * j) = w;
+                        }
+                }
+                continue;
+            }
+            // a slot: per half [D / 4][rows] float4, then the rows' m and l
+            const int hr = min(a.slot_rows, 128);
+            const size_t half = size_t(hr) * (D + 2);
+            float* slot = a.part + (size_t(p.slot) * (a.slot_rows / hr) + h) * half;
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(O + c, o);
+                tmem_wait_ld();
+                if (r < hr)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        reinterpret_cast<uint4*>(slot)[(c / 4 + j) * hr + r] =
+                            make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            }
+            if (r < hr) {
+                slot[hr * D + r] = m;
+                slot[hr * D + hr + r] = l;
+            }
+            __threadfence();
+            mbar_arrive(written + h);
+            if ((warp & 3) == 0) {
+                ok = warp_wait(written + h, write_phase);
+                write_phase ^= 1;
+                if (!ok) break;
+                if (lane == 0) {
+                    const int before = atomicAdd(a.done + 2 * p.first + h, 1);
+                    last[h] = before == p.pieces - 1;
+                    if (last[h]) a.done[2 * p.first + h] = 0;
+                    mbar_arrive(told + h);
+                }
+            }
+            ok = place_told.wait(told + h);
+            if (!ok) break;
+            if (last[h] == 0) continue;
+            __threadfence();
+            if (r < hr) {
+                float all_top = -INFINITY;
+                for (int i = 0; i < p.pieces; ++i)
+                    all_top = fmaxf(all_top, __ldcg(a.part + (size_t(slot_of(p.first, i)) * (a.slot_rows / hr) + h) * half + hr * D + r));
+                const float from = all_top == -INFINITY ? 0.f : all_top;
+                float sum = 0.f;
+                for (int i = 0; i < p.pieces; ++i) {
+                    const float* in = a.part + (size_t(slot_of(p.first, i)) * (a.slot_rows / hr) + h) * half + hr * D + r;
+                    sum += exp2_approx(__ldcg(in) - from) * __ldcg(in + hr);
+                }
+                const float f = sum == 0.f ? 0.f : 1.f / sum;
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + (size_t(row) * a.HQ + p.h * a.g + head) * D;
+                for (int c = 0; c < D / 4; c += 2) {
+                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+                    for (int i = 0; i < p.pieces; ++i) {
+                        const float* in = a.part + (size_t(slot_of(p.first, i)) * (a.slot_rows / hr) + h) * half;
+                        const float w = exp2_approx(__ldcg(in + hr * D + r) - from) * f;
+                        const float4 s = __ldcg(reinterpret_cast<const float4*>(in) + c * hr + r);
+                        const float4 t = __ldcg(reinterpret_cast<const float4*>(in) + (c + 1) * hr + r);
+                        x.x += w * s.x; x.y += w * s.y; x.z += w * s.z; x.w += w * s.w;
+                        y.x += w * t.x; y.y += w * t.y; y.z += w * t.z; y.w += w * t.w;
+                    }
+                    if (valid)
+                        *reinterpret_cast<uint4*>(out + 4 * c) = make_uint4(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w),
+                                                                            pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+                }
+            }
+        }
+    }
+    if (!ok && lane == 0) raise_err(a.err, CANOPY_DEVERR_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kCols);
+    }
+}
+
+}  // namespace tcg
+
+// Rows of a tile are 2 (128 / g) tokens of g heads.
+int tc_tile_tokens(int g) { return 2 * (128 / g); }
+
+template <int D>
+static cudaError_t launch_tc_d(const Args& a, int least, cudaStream_t st) {
+    CUtensorMap mq, mk, mv;
+    const uint64_t row = D * 2, page = uint64_t(1) << a.log_page;
+    const uint32_t keys = uint32_t(page < tcg::KT ? page : tcg::KT);
+    if (!make_bf16_box_map(&mq, a.q, {D, uint64_t(a.HQ), uint64_t(a.N)}, {row, a.HQ * row},
+                           {64, uint32_t(a.g), uint32_t(a.rt / 2)}) ||
+        !make_bf16_box_map(&mk, a.kc, {D, page, uint64_t(a.pages) * a.HKV}, {row, page * row}, {64, keys, 1}) ||
+        !make_bf16_box_map(&mv, a.vc, {D, page, uint64_t(a.pages) * a.HKV}, {row, page * row}, {64, keys, 1}))
+        return cudaErrorInvalidValue;
+    const int smem = tcg::Shape<D>::TOTAL + 1024;
+    static OncePerDevice once;
+    const cudaError_t e = once([=] { return allow_smem(tcg::attend_kernel<D>, smem); });
+    if (e != cudaSuccess) return e;
+    return launch_pdl(tcg::attend_kernel<D>, dim3(a.ctas), dim3(tcg::NT), smem, st, mq, mk, mv, a, least);
+}
+
+cudaError_t launch_tc(const Args& a, int d, int least, cudaStream_t st) {
+    return d == 128 ? launch_tc_d<128>(a, least, st) : launch_tc_d<64>(a, least, st);
+}
+
+}  // namespace att
+}  // namespace canopy

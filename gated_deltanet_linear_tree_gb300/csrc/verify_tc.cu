@@ -665,6 +665,21 @@ bool make_bf16_row_map(CUtensorMap* m, const void* base, int B, int T, int H) {
     return make_bf16_row_map(m, base, B, T, H, 64);
 }
 
+// A bf16 array of three dimensions (the last dense) -> boxes with the 128-byte
+// swizzle; what lies outside reads as zero.
+bool make_bf16_box_map(CUtensorMap* m, const void* base, const uint64_t (&dim)[3], const uint64_t (&stride)[2],
+                       const uint32_t (&size)[3]) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {dim[0], dim[1], dim[2]};
+    const cuuint64_t strides[2] = {stride[0], stride[1]};
+    const cuuint32_t box[3] = {size[0], size[1], size[2]};
+    const cuuint32_t es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Node rows of o or U ([B][T][H][128], fp32 or bf16) for tiled bulk stores:
 // boxes of 32 node rows x 128 columns of one (stream, head), no swizzle
 // (a [32][128] row-major staging tile).

@@ -415,7 +415,7 @@ canopy_attend_plan_t canopy_attend_plan(int N, int B, int HQ, int HKV, canopy_dt
  * and starts NULL, as canopy_tree_verify takes it) the places j < c and those of its
  * root path, itself among them.  With window > 0 of these only the tokens whose
  * position is less than window before t_i, and those at positions < sinks.
- *   q, o [N][HQ][d] in dtype; the places that no row of a sequence sees (behind its
+ *   scale > 0; q, o [N][HQ][d] in dtype; the places that no row of a sequence sees (behind its
  *   last row, out of the window) need no page and may hold anything; what a place
  *   holds reaches no row that does not see it.
  * bf16: products on the tensor cores with fp32 sums and statistics, the weights

@@ -1,8 +1,8 @@
 """Thin ctypes binding of libcanopy.so (include/canopy.h).
 
 Argument marshalling only: every step of the path runs in the library's
-CUDA kernels.  (The calls of a few microseconds, step, prefill and accept, go
-through the native _marshal.so, which checks their arguments, allocates their
+CUDA kernels.  (The calls of a few microseconds, step, prefill, accept, qk_prep,
+attend and cache_commit, go through the native _marshal.so, which checks their arguments, allocates their
 outputs and makes the call; the Python code here is for what it turns down, and
 for all of them where that file is missing or built for another torch.)
 Tensors are torch CUDA tensors (torch provides device memory
@@ -97,7 +97,7 @@ class _NoMarshal:
     def _none(*args):
         return None
 
-    bind = step = prefill = accept = _none
+    bind = step = prefill = accept = bind_attention = qk_prep = attend = cache_commit = _none
 
 
 def _native():
@@ -130,6 +130,8 @@ def load(path: str = LIB_PATH):
         marshal.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
             lib.canopy_step, lib.canopy_prefill, lib.canopy_prefill_workspace_bytes, lib.canopy_accept)),
             torch.bfloat16, torch.float32)
+        marshal.bind_attention(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.canopy_qk_prep, lib.canopy_attend, lib.canopy_attend_workspace_bytes, lib.canopy_cache_commit)))
         _lib, _marshal = lib, marshal
     return _lib
 
@@ -569,6 +571,12 @@ def qk_prep(q, k, v=None, norm: str = "rms", q_weight=None, k_weight=None, eps: 
     [B, max_pages] and context int32 [B], row i's key and value go to place
     context[b] + i of its stream and k_out is None.  q_out may be q and k_out k.
     err: an optional int32 CUDA tensor of one element for device error bits."""
+    if _marshal is None:
+        load()
+    r = _marshal.qk_prep(q, k, v, NORM[norm], q_weight, k_weight, eps, freqs, positions, axis, PAIRS[pairs], q_out,
+                         k_out, k_cache, v_cache, page_table, context, starts, lengths, err)
+    if r is not None:
+        return _short_call("canopy_qk_prep", r)
     lead, N = _rows_shape(q, starts, lengths, "q")
     HQ, d = q.shape[-2:]
     if not isinstance(k, torch.Tensor) or k.dim() != q.dim():
@@ -649,6 +657,12 @@ def attend(q, k_cache, v_cache, page_table, context, ws, starts=None, parent=Non
     k_cache, v_cache [pages, HKV, page_size, d], page_table int32
     [B, max_pages].  scale: d ** -0.5 unless given.  ws: attend_workspace for at
     least these sizes."""
+    if _marshal is None:
+        load()
+    r = _marshal.attend(q, k_cache, v_cache, page_table, context, ws, starts, parent, lengths, window, sinks, scale,
+                        out)
+    if r is not None:
+        return _short_call("canopy_attend", r)
     lead, N = _rows_shape(q, starts, lengths, "q")
     HQ, d = q.shape[-2:]
     dt, i32, dev = q.dtype, torch.int32, q.get_device()
@@ -684,6 +698,11 @@ def cache_commit(accepted, parent, k_cache, v_cache, page_table, context, length
     values of its root path, at places context[b] + node, move to context[b] +
     depth, in place.  Returns the new lengths, int32 [B].  err: an optional int32
     CUDA tensor of one element for device error bits."""
+    if _marshal is None:
+        load()
+    r = _marshal.cache_commit(accepted, parent, k_cache, v_cache, page_table, context, lengths, err)
+    if r is not None:
+        return _short_call("canopy_cache_commit", r)
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
         raise CanopyError("k_cache must have shape (pages, HKV, page_size, d)")
     _, HKV, _, d = k_cache.shape

@@ -9,15 +9,14 @@ namespace canopy {
 namespace att {
 
 // Block 0 plans; block 1 + b, with trees, lists the paths of stream b.
-__global__ void __launch_bounds__(256) plan_kernel(Args a, int least) {
+__global__ void __launch_bounds__(256) plan_kernel(const Args a) {
     pdl_wait();
     if (blockIdx.x == 0) {
         int bad = 0;
-        const int ntiles = make_plan<256>(a, &bad);
+        const int ntiles = make_plan<256>(a, a.seqs, a.line, &bad);
         if (bad) raise_err(a.err, bad);
         const int64_t units = a.line[ntiles];
-        const int ctas = parts(a, units, least);
-        if (threadIdx.x == 0) *a.total = ntiles;
+        const int ctas = parts(a, units);
         for (int c = threadIdx.x; c < ctas; c += 256)
             a.first_tile[c] = ntiles ? tile_at(a.line, ntiles, cta_begin(units, ctas, c)) : 0;
         return;
@@ -68,7 +67,6 @@ template <int D, int R>
 struct Smem {
     static constexpr int LD = D + 4, LP = KT + 4;  // float4 reads of neighbouring rows on other banks
     float q[R * LD], k[KT * LD], v[KT * LD], p[R * LP];
-    int last;
 };
 
 template <typename InT>
@@ -85,18 +83,13 @@ __device__ inline float4 load_row4(const void* cache, const Args& a, const Tile&
 }
 
 template <typename InT, int D, int R>
-__global__ void __launch_bounds__(NT) attend_kernel(const Args a, int least) {
+__global__ void __launch_bounds__(NT) attend_kernel(const Args a) {
     constexpr int RR = R / 16, C4 = D / 64, LD = Smem<D, R>::LD, LP = Smem<D, R>::LP;
     extern __shared__ __align__(16) uint8_t raw[];
     Smem<D, R>& sm = *reinterpret_cast<Smem<D, R>*>(raw);
     pdl_wait();
-    const int ntiles = *a.total;
-    const int64_t units = a.line[ntiles];
-    const int ctas = parts(a, units, least);
-    if (int(blockIdx.x) >= ctas || ntiles == 0) return;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-    Walk walk{units, cta_begin(units, ctas, blockIdx.x), cta_begin(units, ctas, blockIdx.x + 1), ctas,
-              a.first_tile[blockIdx.x]};
+    Walk walk(a, a.seqs, a.line, blockIdx.x, a.first_tile);
     int bad = 0;
     Piece p;
     while (walk.next(a, p)) {
@@ -202,9 +195,8 @@ __global__ void __launch_bounds__(NT) attend_kernel(const Args a, int least) {
         for (int r = 0; r < RR; ++r)
 #pragma unroll
             for (int x = 8; x; x >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], x);
-        if (p.pieces > 1) {
-            const size_t SLOT = size_t(a.slot_rows) * (D + 2);
-            float* out = a.part + p.slot * SLOT;
+        if (!p.whole) {  // a slot: [rows][D], then the rows' m and l
+            float* out = a.part + size_t(p.slot) * a.slot_rows * (D + 2);
 #pragma unroll
             for (int r = 0; r < RR; ++r) {
                 const int row = ty * RR + r;
@@ -212,44 +204,11 @@ __global__ void __launch_bounds__(NT) attend_kernel(const Args a, int least) {
                 for (int c = 0; c < C4; ++c)
                     *reinterpret_cast<float4*>(out + row * D + 4 * tx + 64 * c) = o[r][c];
                 if (tx == 0) {
-                    out[R * D + row] = m[r];
-                    out[R * D + R + row] = l[r];
+                    out[a.slot_rows * D + row] = m[r];
+                    out[a.slot_rows * D + a.slot_rows + row] = l[r];
                 }
             }
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                const int before = atomicAdd(a.done + p.first, 1);
-                sm.last = before == p.pieces - 1;
-                if (sm.last) a.done[p.first] = 0;
-            }
-            __syncthreads();
-            if (!sm.last) continue;
-            __threadfence();
-#pragma unroll
-            for (int r = 0; r < RR; ++r) {
-                const int row = ty * RR + r;
-                float top = -INFINITY;
-                for (int i = 0; i < p.pieces; ++i)
-                    top = fmaxf(top, __ldcg(a.part + slot_of(p.first, i) * SLOT + R * D + row));
-                const float base = top == -INFINITY ? 0.f : top;
-                l[r] = 0.f;
-#pragma unroll
-                for (int c = 0; c < C4; ++c) o[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int i = 0; i < p.pieces; ++i) {
-                    const float* in = a.part + slot_of(p.first, i) * SLOT;
-                    const float w = exp2f(__ldcg(in + R * D + row) - base);
-                    l[r] += w * __ldcg(in + R * D + R + row);
-#pragma unroll
-                    for (int c = 0; c < C4; ++c) {
-                        const float4 x = __ldcg(reinterpret_cast<const float4*>(in + row * D + 4 * tx + 64 * c));
-                        o[r][c].x += w * x.x;
-                        o[r][c].y += w * x.y;
-                        o[r][c].z += w * x.z;
-                        o[r][c].w += w * x.w;
-                    }
-                }
-            }
+            continue;
         }
 #pragma unroll
         for (int r = 0; r < RR; ++r) {
@@ -270,25 +229,117 @@ __global__ void __launch_bounds__(NT) attend_kernel(const Args a, int least) {
 }
 
 template <typename InT, int D, int R>
-cudaError_t launch(const Args& a, int least, cudaStream_t st) {
+cudaError_t launch(const Args& a, cudaStream_t st) {
     static OncePerDevice once;
     const auto kernel = attend_kernel<InT, D, R>;
     cudaError_t e = once([&] { return allow_smem(kernel, int(sizeof(Smem<D, R>))); });
     if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, dim3(a.ctas), dim3(NT), sizeof(Smem<D, R>), st, a, least);
+    return launch_pdl(kernel, dim3(a.ctas), dim3(NT), sizeof(Smem<D, R>), st, a);
 }
 
 }  // namespace simt
 
 // ---------------------------------------------------------------------------
+// Joins the pieces of the rows whose (row tile, key head) is cut: W warps a row,
+// each with every W-th piece; a lane has D / 32 columns.  Where a row has
+// hundreds of pieces (a lone token behind a long cache) the reads in flight are
+// what counts.
+template <typename OutT, int D, int W>
+__global__ void __launch_bounds__(W > 4 ? 32 * W : 128) join_rows_kernel(const Args a) {
+    constexpr int ROWS = W > 4 ? 1 : 4 / W, C = D / 32;
+    __shared__ float part_o[ROWS * W][D], part_m[ROWS * W], part_l[ROWS * W];
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp % W;
+    const int64_t id = int64_t(blockIdx.x) * ROWS + warp / W;
+    const int row = int(id / a.HQ), hq = int(id % a.HQ), h = hq / a.g;
+    bool cut = row < a.N;
+    int first = 0, pieces = 0, r = 0;
+    if (cut) {
+        int b = 0, e = a.B;  // the last sequence that does not begin behind the row
+        while (e - b > 1) {
+            const int m = (b + e) >> 1;
+            if (a.seqs[m].x <= row) b = m; else e = m;
+        }
+        const int4 s = a.seqs[b];
+        cut = row >= s.x && row < s.x + s.y;
+        if (cut) {
+            const int tile = s.w + (row - s.x) / a.rt;
+            r = (row - s.x) % a.rt * a.g + hq % a.g;
+            const int64_t units = a.line[a.seqs[a.B].w], at = a.line[tile], per = (a.line[tile + 1] - at) / a.HKV;
+            const int ctas = parts(a, units);
+            first = cta_of(units, ctas, at + h * per);
+            pieces = cta_of(units, ctas, at + (h + 1) * per - 1) - first + 1;
+            cut = pieces > 1;
+        }
+    }
+    float m = -INFINITY, l = 0.f, o[C] = {};
+    if (cut) {
+        const size_t size = size_t(a.slot_rows) * (D + 2);
+        const float* stat = a.part + a.slot_rows * D + r;
+        for (int i = w; i < pieces; i += W) m = fmaxf(m, stat[slot_of(first, i) * size]);
+        const float from = m == -INFINITY ? 0.f : m;
+#pragma unroll 8
+        for (int i = w; i < pieces; i += W) {
+            const size_t slot = slot_of(first, i) * size;
+            const float f = exp2f(stat[slot] - from);
+            l += f * stat[slot + a.slot_rows];
+            const float* in = a.part + slot + r * D + C * lane;
+#pragma unroll
+            for (int c = 0; c < C; ++c) o[c] += f * in[c];
+        }
+    }
+    if (W > 1) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) part_o[warp][C * lane + c] = o[c];
+        if (lane == 0) {
+            part_m[warp] = m;
+            part_l[warp] = l;
+        }
+        __syncthreads();
+        if (w != 0) return;
+        for (int i = 1; i < W; ++i) m = fmaxf(m, part_m[warp + i]);
+        const float from = m == -INFINITY ? 0.f : m;
+        l = 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) o[c] = 0.f;
+        for (int i = 0; i < W; ++i) {
+            const float f = exp2f(part_m[warp + i] - from);
+            l += f * part_l[warp + i];
+#pragma unroll
+            for (int c = 0; c < C; ++c) o[c] += f * part_o[warp + i][C * lane + c];
+        }
+    }
+    if (!cut) return;
+    const float f = l == 0.f ? 0.f : 1.f / l;
+    OutT* out = static_cast<OutT*>(a.o) + (size_t(row) * a.HQ + hq) * D + C * lane;
+#pragma unroll
+    for (int c = 0; c < C; ++c) store_out(out + c, o[c] * f);
+}
+
+template <typename OutT, int D>
+cudaError_t launch_join_rows(const Args& a, cudaStream_t st) {
+    // (row tile, key head) items at least; each is cut into about ctas / items pieces
+    const int64_t rows = int64_t(a.N) * a.HQ, items = int64_t(a.B) * a.HKV, each = a.ctas / items;
+    if (each >= 32) return launch_pdl(join_rows_kernel<OutT, D, 16>, dim3(unsigned(rows)), dim3(512), 0, st, a);
+    if (each >= 4) return launch_pdl(join_rows_kernel<OutT, D, 4>, dim3(unsigned(rows)), dim3(128), 0, st, a);
+    return launch_pdl(join_rows_kernel<OutT, D, 1>, dim3(unsigned((rows + 3) / 4)), dim3(128), 0, st, a);
+}
+cudaError_t launch_join_bf16(const Args& a, int d, cudaStream_t st) {
+    return d == 128 ? launch_join_rows<__nv_bfloat16, 128>(a, st) : launch_join_rows<__nv_bfloat16, 64>(a, st);
+}
+
+// ---------------------------------------------------------------------------
 
 int tc_tile_tokens(int g);
-cudaError_t launch_tc(const Args& a, int d, int least, cudaStream_t st);
+cudaError_t launch_tc(const Args& a, int d, cudaStream_t st);
+cudaError_t launch_few(const Args& a, int d, cudaStream_t st);
+bool few_plans(int N, int B);  // whether launch_few makes the plan itself
 
 namespace {
 
-constexpr int kCtas = 152;  // one on every SM
-constexpr int kLeast = 2;      // units of a part
+constexpr int kSMs = 152;
+constexpr int kLeast = 2;  // units of a CTA at least
+constexpr int kFewCtas = 2 * kSMs;  // two CTAs an SM
 
 // Rows of an unfinished piece: those of the largest row tile that a call takes.
 int slot_rows(int N, int g) {
@@ -297,23 +348,20 @@ int slot_rows(int N, int g) {
 }
 
 struct Layout {
-    size_t seqs, tiles, line, first_tile, total, mask, depth, done, part, end;
+    size_t seqs, line, first_tile, mask, depth, part, end;
 };
 
 // For the smallest row tile that a call of these sizes may take.
 Layout layout(int N, int B, int g, int d) {
-    const size_t max_tiles = size_t(N) + B;
     Layout w;
-    size_t o = 256;  // the error word, and the count of tiles behind it
-    w.total = 128;
-    w.done = o;       o = ws_align(o + 2 * kCtas * 4);
-    w.seqs = o;       o = ws_align(o + size_t(B) * sizeof(int4));
-    w.tiles = o;      o = ws_align(o + max_tiles * sizeof(Tile));
-    w.line = o;       o = ws_align(o + (max_tiles + 1) * 8);
-    w.first_tile = o; o = ws_align(o + kCtas * 4);
+    size_t o = 4096;  // the error word
+    w.seqs = o;       o = ws_align(o + (size_t(B) + 1) * sizeof(int4));
+    w.line = o;       o = ws_align(o + (size_t(N) + B + 1) * 8);
+    w.first_tile = o; o = ws_align(o + kFewCtas * 4);
     w.mask = o;       o = ws_align(o + size_t(N) * kMaskWords * 4);
     w.depth = o;      o = ws_align(o + size_t(N) * 4);
-    w.part = o;       o = ws_align(o + size_t(2 * kCtas) * slot_rows(N, g) * (d + 2) * 4);
+    const size_t most = size_t(2) * kSMs * slot_rows(N, g), few = size_t(2) * kFewCtas * 16;
+    w.part = o;       o = ws_align(o + (most > few ? most : few) * (d + 2) * 4);
     w.end = o;
     return w;
 }
@@ -323,9 +371,12 @@ Layout layout(int N, int B, int g, int d) {
 }  // namespace att
 
 size_t attend_ws_bytes(int N, int B, int HQ, int HKV, int d) { return att::layout(N, B, HQ / HKV, d).end; }
+// Rows of a sequence and key head on average: up to 16 are one row tile of the
+// kernel for few rows.
 canopy_attend_plan_t attend_plan(int N, int B, int HQ, int HKV, int bf16, int d) {
     if (!bf16) return CANOPY_ATTEND_PLAN_FP32;
-    return CANOPY_ATTEND_PLAN_TILES;
+    const int g = HQ / HKV;
+    return g <= 16 && int64_t(N) * g <= int64_t(16) * B ? CANOPY_ATTEND_PLAN_FEW : CANOPY_ATTEND_PLAN_TILES;
 }
 
 cudaError_t launch_attend(const void* q, int bf16, const void* kc, const void* vc, const int32_t* table, int pages,
@@ -356,30 +407,36 @@ cudaError_t launch_attend(const void* q, int bf16, const void* kc, const void* v
     a.sinks = sinks;
     a.scale2 = scale * 1.4426950408889634f;
     const canopy_attend_plan_t plan = attend_plan(N, B, HQ, HKV, bf16, d);
-    const int R = size_t(N) * a.g <= size_t(16) * B && a.g <= 16 ? 16 : 64;
-    a.rt = plan == CANOPY_ATTEND_PLAN_TILES ? tc_tile_tokens(a.g) : R / a.g;
-    a.log_kt = plan == CANOPY_ATTEND_PLAN_TILES ? 7 : 6;
-    a.ctas = kCtas;
-    a.max_tiles = N + B;
-    a.slot_rows = slot_rows(N, a.g);
+    const bool tiles = plan == CANOPY_ATTEND_PLAN_TILES, few = plan == CANOPY_ATTEND_PLAN_FEW;
+    const int R = a.g <= 16 && int64_t(N) * a.g <= int64_t(16) * B ? 16 : 64;  // rows of a tile, where not on 256
+    a.rt = tiles ? tc_tile_tokens(a.g) : R / a.g;
+    a.log_kt = tiles ? 7 : 6;
+    a.ctas = few ? kFewCtas : kSMs;
+    a.least = kLeast;
+    a.slot_rows = few ? 16 : slot_rows(N, a.g);
     const Layout w = layout(N, B, a.g, d);
     char* p = static_cast<char*>(workspace);
     a.err = reinterpret_cast<int32_t*>(p);
-    a.total = reinterpret_cast<int*>(p + w.total);
-    a.done = reinterpret_cast<int32_t*>(p + w.done);
     a.seqs = reinterpret_cast<int4*>(p + w.seqs);
-    a.tiles = reinterpret_cast<Tile*>(p + w.tiles);
     a.line = reinterpret_cast<int64_t*>(p + w.line);
     a.first_tile = reinterpret_cast<int*>(p + w.first_tile);
     a.mask = reinterpret_cast<uint32_t*>(p + w.mask);
     a.depth = reinterpret_cast<int32_t*>(p + w.depth);
     a.part = reinterpret_cast<float*>(p + w.part);
-    cudaError_t e = launch_pdl(plan_kernel, dim3(parent ? B + 1 : 1), dim3(256), 0, st, a, kLeast);
+    cudaError_t e = cudaSuccess;
+    if (!few || parent || !few_plans(N, B)) e = launch_pdl(plan_kernel, dim3(parent ? B + 1 : 1), dim3(256), 0, st, a);
     if (e != cudaSuccess) return e;
-    if (plan == CANOPY_ATTEND_PLAN_TILES) return launch_tc(a, d, kLeast, st);
-    if (d == 128)
-        return R == 16 ? simt::launch<float, 128, 16>(a, kLeast, st) : simt::launch<float, 128, 64>(a, kLeast, st);
-    return R == 16 ? simt::launch<float, 64, 16>(a, kLeast, st) : simt::launch<float, 64, 64>(a, kLeast, st);
+    if (tiles) return launch_tc(a, d, st);
+    if (few) {
+        e = launch_few(a, d, st);
+        return e != cudaSuccess ? e : launch_join_bf16(a, d, st);
+    }
+    if (d == 128) {
+        e = R == 16 ? simt::launch<float, 128, 16>(a, st) : simt::launch<float, 128, 64>(a, st);
+        return e != cudaSuccess ? e : launch_join_rows<float, 128>(a, st);
+    }
+    e = R == 16 ? simt::launch<float, 64, 16>(a, st) : simt::launch<float, 64, 64>(a, st);
+    return e != cudaSuccess ? e : launch_join_rows<float, 64>(a, st);
 }
 
 }  // namespace canopy

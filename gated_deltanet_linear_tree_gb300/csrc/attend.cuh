@@ -7,8 +7,9 @@
 // kt keys, the units of the work.  A plan lists the row tiles of all sequences and the
 // running sum of their units over all key heads; CTA c of G takes units
 // [c U / G, (c + 1) U / G) of that line, so that every CTA has the same work
-// whatever the sequences' lengths.  A (row tile, key head) whose units fall to
-// several CTAs is merged by the one that finishes last, in the pieces' order.
+// whatever the sequences' lengths.  The pieces of a (row tile, key head) whose
+// units fall to several CTAs go to the workspace, and a second launch joins them in
+// order.
 #pragma once
 
 #include "common.cuh"
@@ -36,18 +37,15 @@ struct Args {
     int pages, log_page, max_pages;
     int window, sinks;
     float scale2;  // scale * log2(e): weights are powers of two
-    int rt, log_kt, ctas, max_tiles;
-    int slot_rows;  // rows of a slot
+    int rt, log_kt, ctas, least;  // tokens of a row tile, keys of a unit, CTAs at most, units of a CTA at least
+    int slot_rows;                // rows of a slot
     // workspace
     int32_t* err;
-    int4* seqs;       // [B]: first row, rows, ctx, first tile
-    Tile* tiles;      // [max_tiles]
-    int64_t* line;    // [max_tiles + 1]
+    int4* seqs;       // [B + 1]: first row, rows, ctx, first tile (of the last: the number of tiles)
+    int64_t* line;    // [number of tiles + 1]: units before the tile, of all key heads
     int* first_tile;  // [ctas]: the tile that CTA c begins in
-    int* total;       // number of tiles
     uint32_t* mask;   // trees: [N][kMaskWords], the nodes of a row's path that it sees
     int32_t* depth;   // trees: [N]
-    int32_t* done;    // [2 ctas]: pieces finished of the item that begins in CTA c (by halves of its rows)
     float* part;      // [2 ctas] slots
 };
 
@@ -123,12 +121,22 @@ __device__ inline Tile make_tile(const Args& a, int b, const int4& s, int t) {
     return r;
 }
 
-// The plan, by a whole block of NT threads: a.seqs, a.tiles, a.line, and the
-// number of tiles (returned).  Starts out of order or range are read as their
+// The sequence that tile i belongs to: the last whose first tile is not behind it.
+__device__ inline int sequence_at(const int4* seqs, int B, int i) {
+    int b = 0, e = B;
+    while (e - b > 1) {
+        const int m = (b + e) >> 1;
+        if (seqs[m].w <= i) b = m; else e = m;
+    }
+    return b;
+}
+
+// The plan, by a whole block of NT threads: seqs, line, and the number of tiles
+// (returned).  Starts out of order or range are read as their
 // running maximum, lengths and contexts as the nearest that fit; these set bits
 // in *bad.
 template <int NT>
-__device__ inline int make_plan(const Args& a, int* bad) {
+__device__ inline int make_plan(const Args& a, int4* seqs, int64_t* line_of, int* bad) {
     __shared__ int wi[NT / 32];
     __shared__ int64_t wl[NT / 32];
     const auto most = [](int x, int y) { return max(x, y); };
@@ -169,38 +177,33 @@ __device__ inline int make_plan(const Args& a, int* bad) {
         }
         const int nt = (n + a.rt - 1) / a.rt;
         const int upto = carry + block_scan<NT>(nt, isum, wi, total);
-        if (b < a.B) a.seqs[b] = make_int4(lo, n, ctx, upto - nt);
+        if (b < a.B) seqs[b] = make_int4(lo, n, ctx, upto - nt);
         carry += total;
     }
-    __syncthreads();
     const int ntiles = carry;
+    if (tid == 0) seqs[a.B] = make_int4(a.N, 0, 0, ntiles);
+    __syncthreads();
     int64_t line = 0, ltotal;
     for (int i0 = 0; i0 < ntiles; i0 += NT) {
         const int i = i0 + tid;
         int64_t units = 0;
         if (i < ntiles) {
-            int b = 0, e = a.B;  // the last sequence whose first tile is not behind i
-            while (e - b > 1) {
-                const int m = (b + e) >> 1;
-                if (a.seqs[m].w <= i) b = m; else e = m;
-            }
-            const int4 s = a.seqs[b];
-            const Tile t = make_tile(a, b, s, i - s.w);
-            a.tiles[i] = t;
-            units = int64_t(t.units) * a.HKV;
+            const int b = sequence_at(seqs, a.B, i);
+            const int4 s = seqs[b];
+            units = int64_t(make_tile(a, b, s, i - s.w).units) * a.HKV;
         }
         const int64_t upto = line + block_scan<NT>(units, sum, wl, ltotal);
-        if (i < ntiles) a.line[i] = upto - units;
+        if (i < ntiles) line_of[i] = upto - units;
         line += ltotal;
     }
-    if (tid == 0) a.line[ntiles] = line;
+    if (tid == 0) line_of[ntiles] = line;
     __syncthreads();
     return ntiles;
 }
 
 // How many CTAs share the work: no part is shorter than `least` units.
-__device__ inline int parts(const Args& a, int64_t units, int least) {
-    const int64_t most = units / least;
+__device__ inline int parts(const Args& a, int64_t units) {
+    const int64_t most = units / a.least;
     return int(most < 1 ? 1 : most < a.ctas ? most : a.ctas);
 }
 
@@ -218,25 +221,39 @@ __device__ inline int tile_at(const int64_t* line, int ntiles, int64_t u) {
 struct Piece {
     Tile tile;
     int h, u0, u1;
-    int slot;           // where an unfinished piece goes
-    int first, pieces;  // the CTA that the item begins in; CTAs that have a piece of it
+    bool whole;
+    int slot;  // where it goes if it is not the whole
 };
 
 // Walks a CTA's pieces.
 struct Walk {
+    const int4* seqs;
+    const int64_t* line;
     int64_t units, at, end;
-    int ctas, tile;
+    int ctas, tile, b;
+    // CTA c's part of the plan.
+    __device__ Walk(const Args& a, const int4* seqs, const int64_t* line, int c, const int* first_tile)
+        : seqs(seqs), line(line), units(0), at(0), end(0), ctas(1), tile(0), b(0) {
+        const int ntiles = seqs[a.B].w;
+        units = line[ntiles];
+        ctas = parts(a, units);
+        if (c >= ctas || units == 0) return;
+        at = cta_begin(units, ctas, c);
+        end = cta_begin(units, ctas, c + 1);
+        tile = first_tile ? first_tile[c] : tile_at(line, ntiles, at);
+        b = sequence_at(seqs, a.B, tile);
+    }
     __device__ bool next(const Args& a, Piece& p) {
         if (at >= end) return false;
-        while (a.line[tile + 1] <= at) ++tile;
-        p.tile = a.tiles[tile];
-        const int64_t rel = at - a.line[tile];
+        while (line[tile + 1] <= at) ++tile;
+        while (seqs[b + 1].w <= tile) ++b;
+        const int4 s = seqs[b];
+        p.tile = make_tile(a, b, s, tile - s.w);
+        const int64_t rel = at - line[tile];
         p.h = int(rel / p.tile.units);
         p.u0 = int(rel - int64_t(p.h) * p.tile.units);
         p.u1 = int(min(int64_t(p.tile.units), p.u0 + (end - at)));
-        const int64_t begin = at - p.u0;
-        p.first = p.u0 == 0 ? int(blockIdx.x) : cta_of(units, ctas, begin);
-        p.pieces = p.u1 == p.tile.units && p.u0 == 0 ? 1 : cta_of(units, ctas, begin + p.tile.units - 1) - p.first + 1;
+        p.whole = p.u0 == 0 && p.u1 == p.tile.units;
         p.slot = 2 * int(blockIdx.x) + (p.u0 == 0);
         at += p.u1 - p.u0;
         return true;
@@ -244,6 +261,82 @@ struct Walk {
 };
 // Slot of piece i of an item that begins in CTA `first`.
 __device__ inline int slot_of(int first, int i) { return 2 * (first + i) + (i == 0); }
+
+// ---------------------------------------------------------------------------
+// What the two kernels on the tensor cores share.
+
+constexpr float kGrow = 8.f;  // a row's maximum is kept until it grows by this, in powers of two
+
+__device__ inline float exp2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ inline uint32_t pack_bf16(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+
+// Bits [a, b) of a word.
+__device__ inline uint32_t range_bits(int a, int b) {
+    a = min(max(a, 0), 32);
+    b = min(max(b, a), 32);
+    return uint32_t((1ull << b) - (1ull << a));
+}
+// Which of the keys [base, base + 32) a row sees (att::sees for 32 keys).
+__device__ inline uint32_t seen_bits(const Args& a, const Tile& tile, int depth, const uint32_t* mask, int base) {
+    const int pos = tile.ctx + depth;
+    const int end = (mask ? min(pos, tile.ctx - 1) : pos) + 1;  // past the last one in the cache, or in all
+    const int64_t near = int64_t(pos) - a.window + 1 - base;
+    uint32_t bits = range_bits(int(near > 0 ? near : 0), end - base) | range_bits(0, min(a.sinks, end) - base);
+    const int p = base - tile.ctx;
+    if (mask && p > -32 && p < kMaxT) {
+        if (p < 0) {
+            bits |= mask[0] << -p;
+        } else {
+            const uint32_t lo = mask[p >> 5], hi = (p >> 5) + 1 < kMaskWords ? mask[(p >> 5) + 1] : 0u;
+            bits |= __funnelshift_r(lo, hi, p & 31);
+        }
+    }
+    return bits;
+}
+
+__device__ inline bool finite_pair(uint32_t x) {
+    return (x & 0x7F80u) != 0x7F80u && (x & 0x7F800000u) != 0x7F800000u;
+}
+
+// A wait of a whole warp, which goes on or gives up together.
+__device__ inline bool warp_wait(uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+// Waits for a barrier's phases in turn.
+struct Phase {
+    uint32_t bit = 0;
+    __device__ bool wait(uint64_t* bar) {
+        const bool ok = warp_wait(bar, bit);
+        bit ^= 1;
+        return ok;
+    }
+};
+// A place in the ring of stages.
+template <int STAGES>
+struct Ring {
+    int at = 0;
+    uint32_t phase = 0;
+    __device__ void step() {
+        if (++at == STAGES) {
+            at = 0;
+            phase ^= 1;
+        }
+    }
+    __device__ void back() {
+        if (at-- == 0) {
+            at = STAGES - 1;
+            phase ^= 1;
+        }
+    }
+};
 
 }  // namespace att
 }  // namespace canopy

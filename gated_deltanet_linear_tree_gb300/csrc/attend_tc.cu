@@ -32,7 +32,6 @@ namespace tcg {
 
 constexpr int KT = 128, NT = 384;
 constexpr uint32_t kCols = 512;
-constexpr float kGrow = 8.f;  // the maximum is kept until it grows by this, in powers of two
 
 template <int D>
 struct Shape {
@@ -40,8 +39,8 @@ struct Shape {
     static constexpr int STAGES = D == 128 ? 5 : 10;
     static constexpr int Q = 0, KV = 2 * TILE, BARS = KV + STAGES * TILE;
     // barriers: Q full, Q read, all products done; per stage full, empty, and V looked through; per half S full, P
-    // there, O full, piece written, its place in the order told
-    static constexpr int NBAR = 3 + 3 * STAGES + 10;
+    // there, O full
+    static constexpr int NBAR = 3 + 3 * STAGES + 6;
     static constexpr int POISON = BARS + 8 * NBAR;         // [STAGES][4] words: keys with a value that is not finite
     static constexpr int MISC = POISON + 16 * STAGES;      // tensor memory's address, flags
     static constexpr int TOTAL = MISC + 32;
@@ -64,92 +63,19 @@ __device__ inline uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-__device__ inline float exp2_approx(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ inline uint32_t pack_bf16(float a, float b) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-    return r;
-}
-
-// Bits [a, b) of a word.
-__device__ inline uint32_t range_bits(int a, int b) {
-    a = min(max(a, 0), 32);
-    b = min(max(b, a), 32);
-    return uint32_t((1ull << b) - (1ull << a));
-}
-// Which of the keys [base, base + 32) a row sees (att::sees for 32 keys).
-__device__ inline uint32_t seen_bits(const Args& a, const Tile& tile, int depth, const uint32_t* mask, int base) {
-    const int pos = tile.ctx + depth;
-    const int end = (mask ? min(pos, tile.ctx - 1) : pos) + 1;  // past the last one in the cache, or in all
-    const int64_t near = int64_t(pos) - a.window + 1 - base;
-    uint32_t bits = range_bits(int(near > 0 ? near : 0), end - base) | range_bits(0, min(a.sinks, end) - base);
-    const int p = base - tile.ctx;
-    if (mask && p > -32 && p < kMaxT) {
-        if (p < 0) {
-            bits |= mask[0] << -p;
-        } else {
-            const uint32_t lo = mask[p >> 5], hi = (p >> 5) + 1 < kMaskWords ? mask[(p >> 5) + 1] : 0u;
-            bits |= __funnelshift_r(lo, hi, p & 31);
-        }
-    }
-    return bits;
-}
-
-__device__ inline bool finite_pair(uint32_t x) {
-    return (x & 0x7F80u) != 0x7F80u && (x & 0x7F800000u) != 0x7F800000u;
-}
-
-// A wait of a whole warp, which goes on or gives up together.
-__device__ inline bool warp_wait(uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity));
-}
-// Waits for a barrier's phases in turn.
-struct Phase {
-    uint32_t bit = 0;
-    __device__ bool wait(uint64_t* bar) {
-        const bool ok = warp_wait(bar, bit);
-        bit ^= 1;
-        return ok;
-    }
-};
-// A place in the ring of stages.
-template <int STAGES>
-struct Ring {
-    int at = 0;
-    uint32_t phase = 0;
-    __device__ void step() {
-        if (++at == STAGES) {
-            at = 0;
-            phase ^= 1;
-        }
-    }
-    __device__ void back() {
-        if (at-- == 0) {
-            at = STAGES - 1;
-            phase ^= 1;
-        }
-    }
-};
-
 template <int D>
 __global__ void __launch_bounds__(NT, 1)
     attend_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
-                  const __grid_constant__ CUtensorMap mapV, const Args a, int least) {
+                  const __grid_constant__ CUtensorMap mapV, const Args a) {
     using Sh = Shape<D>;
     constexpr int HALVES = D / 64;
     extern __shared__ uint8_t raw[];
     uint8_t* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Sh::BARS);
     uint64_t *q_full = bars, *q_read = bars + 1, *full = bars + 2, *empty = full + Sh::STAGES,
-             *looked = empty + Sh::STAGES, *s_full = looked + Sh::STAGES, *p_there = s_full + 2, *o_full = p_there + 2,
-             *written = o_full + 2, *told = written + 2, *drained = told + 2;
+             *looked = empty + Sh::STAGES, *s_full = looked + Sh::STAGES, *p_there = s_full + 2, *o_full = p_there + 2, *drained = o_full + 2;
     uint32_t* poison = reinterpret_cast<uint32_t*>(sm + Sh::POISON);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Sh::MISC);
-    int* last = reinterpret_cast<int*>(sm + Sh::MISC + 8);  // [2]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (warp == 8) {
@@ -168,8 +94,6 @@ __global__ void __launch_bounds__(NT, 1)
             mbar_init(s_full + i, 1);
             mbar_init(p_there + i, 128);
             mbar_init(o_full + i, 1);
-            mbar_init(written + i, 128);
-            mbar_init(told + i, 1);
         }
         mbar_init(drained, 1);
         fence_mbar_init();
@@ -180,16 +104,7 @@ __global__ void __launch_bounds__(NT, 1)
     const uint32_t tmem = *tmem_slot;
     pdl_wait();
 
-    const int ntiles = *a.total;
-    const int64_t units = a.line[ntiles];
-    const int ctas = parts(a, units, least);
-    const bool work = int(blockIdx.x) < ctas && units > 0;
-    Walk walk{units, 0, 0, ctas, 0};
-    if (work) {
-        walk.at = cta_begin(units, ctas, blockIdx.x);
-        walk.end = cta_begin(units, ctas, blockIdx.x + 1);
-        walk.tile = a.first_tile[blockIdx.x];
-    }
+    Walk walk(a, a.seqs, a.line, blockIdx.x, a.first_tile);
     const int half_tok = a.rt / 2;  // tokens of a half
     bool ok = true;
     Piece p;
@@ -374,8 +289,7 @@ __global__ void __launch_bounds__(NT, 1)
         const int h = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16), S = lanes + 128 * h, O = lanes + 256 + D * h;
         Ring<Sh::STAGES> look;
-        Phase scores_ready, o_ready, place_told;
-        uint32_t write_phase = 0;
+        Phase scores_ready, o_ready;
         const int tok_in_half = r / a.g, head = r % a.g;
         while (ok && walk.next(a, p)) {
             const Tile& tile = p.tile;
@@ -470,8 +384,8 @@ __global__ void __launch_bounds__(NT, 1)
             ok = o_ready.wait(o_full + h);
             if (!ok) break;
             tc_fence_after();
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            if (p.pieces == 1) {
+            if (p.whole) {
+                const float inv = l == 0.f ? 0.f : 1.f / l;
                 __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + (size_t(row) * a.HQ + p.h * a.g + head) * D;
 #pragma unroll
                 for (int c = 0; c < D; c += 32) {
@@ -510,50 +424,6 @@ __global__ void __launch_bounds__(NT, 1)
                 slot[hr * D + r] = m;
                 slot[hr * D + hr + r] = l;
             }
-            __threadfence();
-            mbar_arrive(written + h);
-            if ((warp & 3) == 0) {
-                ok = warp_wait(written + h, write_phase);
-                write_phase ^= 1;
-                if (!ok) break;
-                if (lane == 0) {
-                    const int before = atomicAdd(a.done + 2 * p.first + h, 1);
-                    last[h] = before == p.pieces - 1;
-                    if (last[h]) a.done[2 * p.first + h] = 0;
-                    mbar_arrive(told + h);
-                }
-            }
-            ok = place_told.wait(told + h);
-            if (!ok) break;
-            if (last[h] == 0) continue;
-            __threadfence();
-            if (r < hr) {
-                float all_top = -INFINITY;
-                for (int i = 0; i < p.pieces; ++i)
-                    all_top = fmaxf(all_top, __ldcg(a.part + (size_t(slot_of(p.first, i)) * (a.slot_rows / hr) + h) * half + hr * D + r));
-                const float from = all_top == -INFINITY ? 0.f : all_top;
-                float sum = 0.f;
-                for (int i = 0; i < p.pieces; ++i) {
-                    const float* in = a.part + (size_t(slot_of(p.first, i)) * (a.slot_rows / hr) + h) * half + hr * D + r;
-                    sum += exp2_approx(__ldcg(in) - from) * __ldcg(in + hr);
-                }
-                const float f = sum == 0.f ? 0.f : 1.f / sum;
-                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + (size_t(row) * a.HQ + p.h * a.g + head) * D;
-                for (int c = 0; c < D / 4; c += 2) {
-                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-                    for (int i = 0; i < p.pieces; ++i) {
-                        const float* in = a.part + (size_t(slot_of(p.first, i)) * (a.slot_rows / hr) + h) * half;
-                        const float w = exp2_approx(__ldcg(in + hr * D + r) - from) * f;
-                        const float4 s = __ldcg(reinterpret_cast<const float4*>(in) + c * hr + r);
-                        const float4 t = __ldcg(reinterpret_cast<const float4*>(in) + (c + 1) * hr + r);
-                        x.x += w * s.x; x.y += w * s.y; x.z += w * s.z; x.w += w * s.w;
-                        y.x += w * t.x; y.y += w * t.y; y.z += w * t.z; y.w += w * t.w;
-                    }
-                    if (valid)
-                        *reinterpret_cast<uint4*>(out + 4 * c) = make_uint4(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w),
-                                                                            pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
-                }
-            }
         }
     }
     if (!ok && lane == 0) raise_err(a.err, CANOPY_DEVERR_TIMEOUT);
@@ -565,13 +435,59 @@ __global__ void __launch_bounds__(NT, 1)
     }
 }
 
+// Joins the pieces of an item that is cut: block (c, e) rows 8 e .. 8 e + 7 of the
+// one whose first cut is between CTA c and c + 1.  Thread: a row and four columns.
+template <int D>
+__global__ void __launch_bounds__(2 * D) join_kernel(const Args a) {
+    pdl_wait();
+    const int ntiles = a.seqs[a.B].w;
+    const int64_t units = a.line[ntiles];
+    const int ctas = parts(a, units), c = blockIdx.x;
+    if (c + 1 >= ctas || units == 0) return;
+    const int64_t cut = cta_begin(units, ctas, c + 1);
+    const int tile = tile_at(a.line, ntiles, cut);
+    const int per = int((a.line[tile + 1] - a.line[tile]) / a.HKV), h = int((cut - a.line[tile]) / per);
+    const int64_t begin = a.line[tile] + int64_t(h) * per;
+    if (begin == cut || cta_of(units, ctas, begin) != c) return;
+    const int pieces = cta_of(units, ctas, begin + per - 1) - c + 1;
+    const int b = sequence_at(a.seqs, a.B, tile);
+    const Tile t = make_tile(a, b, a.seqs[b], tile - a.seqs[b].w);
+    const int r = 8 * blockIdx.y + (threadIdx.x & 7), half = r >> 7, lane = r & 127, col = threadIdx.x >> 3;
+    const int tok = half * (a.rt / 2) + lane / a.g;
+    if (lane / a.g >= a.rt / 2 || tok >= t.ntok) return;
+    const int hr = min(a.slot_rows, 128);
+    const size_t size = size_t(hr) * (D + 2);
+    const float* part = a.part + half * size;
+    const size_t next = a.slot_rows / hr * size;
+    float top = -INFINITY;
+    for (int i = 0; i < pieces; ++i) top = fmaxf(top, part[slot_of(c, i) * next + hr * D + lane]);
+    const float from = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < pieces; ++i) {
+        const float* in = part + slot_of(c, i) * next;
+        const float w = exp2_approx(in[hr * D + lane] - from);
+        const float4 y = reinterpret_cast<const float4*>(in)[col * hr + lane];
+        sum += w * in[hr * D + hr + lane];
+        x.x += w * y.x;
+        x.y += w * y.y;
+        x.z += w * y.z;
+        x.w += w * y.w;
+    }
+    const float f = sum == 0.f ? 0.f : 1.f / sum;
+    __nv_bfloat16* out =
+        static_cast<__nv_bfloat16*>(a.o) + (size_t(t.row + tok) * a.HQ + h * a.g + lane % a.g) * D + 4 * col;
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(x.x * f, x.y * f), pack_bf16(x.z * f, x.w * f));
+}
+
 }  // namespace tcg
 
 // Rows of a tile are 2 (128 / g) tokens of g heads.
 int tc_tile_tokens(int g) { return 2 * (128 / g); }
 
 template <int D>
-static cudaError_t launch_tc_d(const Args& a, int least, cudaStream_t st) {
+static cudaError_t launch_tc_d(const Args& a, cudaStream_t st) {
     CUtensorMap mq, mk, mv;
     const uint64_t row = D * 2, page = uint64_t(1) << a.log_page;
     const uint32_t keys = uint32_t(page < tcg::KT ? page : tcg::KT);
@@ -582,13 +498,15 @@ static cudaError_t launch_tc_d(const Args& a, int least, cudaStream_t st) {
         return cudaErrorInvalidValue;
     const int smem = tcg::Shape<D>::TOTAL + 1024;
     static OncePerDevice once;
-    const cudaError_t e = once([=] { return allow_smem(tcg::attend_kernel<D>, smem); });
+    cudaError_t e = once([=] { return allow_smem(tcg::attend_kernel<D>, smem); });
     if (e != cudaSuccess) return e;
-    return launch_pdl(tcg::attend_kernel<D>, dim3(a.ctas), dim3(tcg::NT), smem, st, mq, mk, mv, a, least);
+    e = launch_pdl(tcg::attend_kernel<D>, dim3(a.ctas), dim3(tcg::NT), smem, st, mq, mk, mv, a);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(tcg::join_kernel<D>, dim3(a.ctas - 1, a.slot_rows / 8), dim3(2 * D), 0, st, a);
 }
 
-cudaError_t launch_tc(const Args& a, int d, int least, cudaStream_t st) {
-    return d == 128 ? launch_tc_d<128>(a, least, st) : launch_tc_d<64>(a, least, st);
+cudaError_t launch_tc(const Args& a, int d, cudaStream_t st) {
+    return d == 128 ? launch_tc_d<128>(a, st) : launch_tc_d<64>(a, st);
 }
 
 }  // namespace att

@@ -1,5 +1,5 @@
 // Argument marshalling of the calls that take a few microseconds (step,
-// prefill, accept), natively: the checks of a tensor, its pointers, the
+// prefill, accept, qk_prep, attend, cache_commit), natively: the checks of a tensor, its pointers, the
 // outputs and the stream cost 10 us and more in Python, as much as the
 // kernels themselves for a few streams.
 //
@@ -23,6 +23,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <exception>
 #include <initializer_list>
 
@@ -34,6 +35,10 @@ decltype(&canopy_step) step_fn = nullptr;
 decltype(&canopy_prefill) prefill_fn = nullptr;
 decltype(&canopy_prefill_workspace_bytes) prefill_bytes_fn = nullptr;
 decltype(&canopy_accept) accept_fn = nullptr;
+decltype(&canopy_qk_prep) qk_prep_fn = nullptr;
+decltype(&canopy_attend) attend_fn = nullptr;
+decltype(&canopy_attend_workspace_bytes) attend_bytes_fn = nullptr;
+decltype(&canopy_cache_commit) cache_commit_fn = nullptr;
 PyObject *bf16_obj = nullptr, *f32_obj = nullptr;  // torch.bfloat16, torch.float32
 
 // The tensor behind obj, if it is a contiguous CUDA tensor on device dev (any
@@ -268,6 +273,259 @@ PyObject* accept(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// The rows of an attention layer's call: their leading sizes and number.
+struct Rows {
+    c10::SmallVector<int64_t, 4> lead;
+    int64_t n = 0;
+    bool fits(const at::Tensor& t, int64_t heads, int64_t d) const {
+        if (t.dim() != int64_t(lead.size()) + 2 || t.size(-2) != heads || t.size(-1) != d) return false;
+        for (size_t i = 0; i < lead.size(); ++i)
+            if (t.size(i) != lead[i]) return false;
+        return true;
+    }
+};
+bool rows_of(const at::Tensor& q, Rows& r) {
+    if (q.dim() != 3 && q.dim() != 4) return false;
+    r.n = 1;
+    for (int64_t i = 0; i < q.dim() - 2; ++i) {
+        r.lead.push_back(q.size(i));
+        r.n *= q.size(i);
+    }
+    return true;
+}
+
+// A CUDA tensor of rows whose heads are dense but whose tokens may lie apart.
+const at::Tensor* spaced(PyObject* obj, int& dev, at::ScalarType type, const Rows& r, int64_t heads, int64_t d,
+                         int64_t& ld) {
+    if (!THPVariable_Check(obj)) return nullptr;
+    const at::Tensor& t = THPVariable_Unpack(obj);
+    if (!t.defined() || !t.is_cuda() || t.layout() != at::kStrided || t.get_device() != dev ||
+        t.scalar_type() != type || !r.fits(t, heads, d))
+        return nullptr;
+    const bool two = r.lead.size() == 2 && r.lead[0] > 1;
+    ld = r.lead.back() > 1 ? t.stride(-3) : two ? t.stride(0) : heads * d;
+    if ((d > 1 && t.stride(-1) != 1) || (heads > 1 && t.stride(-2) != d) || (two && t.stride(0) != ld * r.lead.back()))
+        return nullptr;
+    return &t;
+}
+
+// A paged cache and whose streams it is.
+struct Cache {
+    const at::Tensor *k, *v, *table, *context;
+    int64_t B, pages, page, most;
+};
+bool cache_of(PyObject* k, PyObject* v, PyObject* table, PyObject* context, int& dev, at::ScalarType type, int64_t HKV,
+              int64_t d, Cache& c) {
+    c.k = plain(k, dev);
+    c.table = plain(table, dev);
+    if (!c.k || !c.table || c.k->dim() != 4 || c.k->size(1) != HKV || c.k->size(3) != d ||
+        c.k->scalar_type() != type || c.table->dim() != 2 || c.table->scalar_type() != at::kInt)
+        return false;
+    c.B = c.table->size(0);
+    c.pages = c.k->size(0);
+    c.page = c.k->size(2);
+    c.most = c.table->size(1);
+    c.v = plain(v, dev, type, {c.pages, HKV, c.page, d});
+    c.context = plain(context, dev, at::kInt, {c.B});
+    return c.v && c.context && ints({c.B, c.pages, c.page, c.most});
+}
+bool of_streams(const Rows& r, int64_t B, bool packed) {
+    if (r.lead.size() == 2) return !packed && r.lead[0] == B;
+    return packed || r.lead[0] == B;
+}
+
+at::Tensor fresh_rows(const Rows& r, int64_t heads, int64_t d, at::ScalarType type, int dev) {
+    c10::SmallVector<int64_t, 4> shape = r.lead;
+    shape.push_back(heads);
+    shape.push_back(d);
+    return fresh(shape, type, dev);
+}
+// A rows' output given as obj, if it fits; None stays undefined for now.
+bool rows_output(PyObject* obj, int dev, at::ScalarType type, const Rows& r, int64_t heads, int64_t d,
+                 at::Tensor& out) {
+    if (obj == Py_None) return true;
+    const at::Tensor* t = plain(obj, dev);
+    if (!t || t->scalar_type() != type || !r.fits(*t, heads, d)) return false;
+    out = *t;
+    return true;
+}
+
+// qk_prep(q, k, v, norm, q_weight, k_weight, eps, freqs, positions, axis, pairs, q_out, k_out, k_cache, v_cache,
+//         page_table, context, starts, lengths, err)
+PyObject* qk_prep(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (n != 20 || !qk_prep_fn || !PyLong_Check(a[3]) || !PyFloat_Check(a[6]) || !PyLong_Check(a[10])) return none();
+    return guarded([&]() -> PyObject* {
+        if (!THPVariable_Check(a[0]) || !THPVariable_Check(a[1])) return none();
+        const at::Tensor &q0 = THPVariable_Unpack(a[0]), &k0 = THPVariable_Unpack(a[1]);
+        canopy_dtype type;
+        Rows r;
+        if (!q0.defined() || !q0.is_cuda() || !k0.defined() || !code_of(q0.scalar_type(), type) || !rows_of(q0, r) ||
+            k0.dim() != q0.dim())
+            return none();
+        int dev = q0.get_device();
+        const at::ScalarType st = q0.scalar_type();
+        const int64_t HQ = q0.size(-2), HKV = k0.size(-2), d = q0.size(-1);
+        int64_t ldq = 0, ldk = 0, ldv = 0;
+        const at::Tensor *q = spaced(a[0], dev, st, r, HQ, d, ldq), *k = spaced(a[1], dev, st, r, HKV, d, ldk), *v = nullptr;
+        bool ok = q && k && ints({r.n, HQ, HKV, d});
+        const bool cached = a[13] != Py_None, packed = a[17] != Py_None;
+        Cache c = {};
+        const at::Tensor *starts = nullptr, *lengths = nullptr;
+        if (cached) {
+            if (!ok || !cache_of(a[13], a[14], a[15], a[16], dev, st, HKV, d, c) || !of_streams(r, c.B, packed) ||
+                a[12] != Py_None || (a[18] != Py_None && r.lead.size() != 2))
+                return none();
+            v = spaced(a[2], dev, st, r, HKV, d, ldv);
+            starts = maybe(a[17], dev, at::kInt, {c.B + 1}, ok);
+            lengths = maybe(a[18], dev, at::kInt, {c.B}, ok);
+            ok = ok && v;
+        } else {
+            for (const int i : {2, 14, 15, 16, 17, 18}) ok = ok && a[i] == Py_None;
+        }
+        const at::Tensor *qw = maybe(a[4], dev, at::kFloat, {d}, ok), *kw = maybe(a[5], dev, at::kFloat, {d}, ok);
+        const at::Tensor *freqs = nullptr, *positions = nullptr;
+        int64_t half = 0, axes = 1;
+        if (a[7] != Py_None) {
+            freqs = plain(a[7], dev);
+            ok = ok && freqs && freqs->dim() == 1 && freqs->scalar_type() == at::kFloat;
+            if (ok) half = freqs->size(0);
+        }
+        if (ok && a[8] != Py_None) {
+            positions = plain(a[8], dev);
+            if (!positions || positions->scalar_type() != at::kInt) return none();
+            const int64_t more = positions->dim() - int64_t(r.lead.size());
+            if (more == 1) axes = positions->size(0);
+            else if (more != 0) return none();
+            for (size_t i = 0; i < r.lead.size(); ++i)
+                if (positions->size(i + more) != r.lead[i]) return none();
+        }
+        const at::Tensor* axis = maybe(a[9], dev, at::kInt, {half}, ok);
+        const at::Tensor* err = maybe(a[19], dev, at::kInt, {1}, ok);
+        at::Tensor q_out, k_out;
+        if (!ok || !ints({2 * half, axes}) || !rows_output(a[11], dev, st, r, HQ, d, q_out) ||
+            !rows_output(a[12], dev, st, r, HKV, d, k_out))
+            return none();
+        canopy_status s;
+        {
+            const OnDevice on(dev);
+            if (!q_out.defined()) q_out = fresh_rows(r, HQ, d, st, dev);
+            if (!cached && !k_out.defined()) k_out = fresh_rows(r, HKV, d, st, dev);
+            s = qk_prep_fn(q->data_ptr(), k->data_ptr(), ptr<void>(v), type, ldq, ldk, ldv,
+                           canopy_norm(PyLong_AsLong(a[3])), ptr<float>(qw), ptr<float>(kw),
+                           float(PyFloat_AS_DOUBLE(a[6])), ptr<float>(freqs), int(2 * half), ptr<int32_t>(positions),
+                           int(axes), ptr<int32_t>(axis), canopy_pairs(PyLong_AsLong(a[10])), int(r.n), int(c.B),
+                           int(HQ), int(HKV), int(d), q_out.data_ptr(), cached ? nullptr : k_out.data_ptr(),
+                           ptr<void>(c.k), ptr<void>(c.v), ptr<int32_t>(c.table), int(c.pages), int(c.page),
+                           int(c.most), ptr<int32_t>(c.context), ptr<int32_t>(starts), ptr<int32_t>(lengths),
+                           ptr<int32_t>(err), stream_of(dev));
+        }
+        if (s != CANOPY_OK) return PyLong_FromLong(s);
+        if (!cached) return pair_of(a[11], q_out, a[12], k_out);
+        PyObject* o = a[11] == Py_None ? THPVariable_Wrap(q_out) : Py_NewRef(a[11]);
+        if (!o) return nullptr;
+        PyObject* pair = PyTuple_Pack(2, o, Py_None);
+        Py_DECREF(o);
+        return pair;
+    });
+}
+
+// attend(q, k_cache, v_cache, page_table, context, ws, starts, parent, lengths, window, sinks, scale, out)
+PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (n != 13 || !attend_fn || !PyLong_Check(a[9]) || !PyLong_Check(a[10]) ||
+        (a[11] != Py_None && !PyFloat_Check(a[11])))
+        return none();
+    int over = 0;
+    const long window = PyLong_AsLongAndOverflow(a[9], &over), sinks = over ? -1 : PyLong_AsLongAndOverflow(a[10], &over);
+    if (over || window < 0 || sinks < 0) return none();
+    return guarded([&]() -> PyObject* {
+        int dev = -1;
+        const at::Tensor *q = plain(a[0], dev), *k = plain(a[1], dev), *ws = plain(a[5], dev);
+        canopy_dtype type;
+        Rows r;
+        if (!q || !k || !ws || k->dim() != 4 || ws->scalar_type() != at::kByte || !code_of(q->scalar_type(), type) ||
+            !rows_of(*q, r))
+            return none();
+        const at::ScalarType st = q->scalar_type();
+        const int64_t HQ = q->size(-2), HKV = k->size(1), d = q->size(-1);
+        const bool packed = a[6] != Py_None;
+        Cache c;
+        if (!cache_of(a[1], a[2], a[3], a[4], dev, st, HKV, d, c) || !of_streams(r, c.B, packed) ||
+            !ints({r.n, HQ, HKV, d, window, sinks}) || (r.lead.size() != 2 && (a[7] != Py_None || a[8] != Py_None)))
+            return none();
+        bool ok = true;
+        const at::Tensor* starts = maybe(a[6], dev, at::kInt, {c.B + 1}, ok);
+        const at::Tensor* parent = nullptr;
+        if (a[7] != Py_None) parent = maybe(a[7], dev, at::kInt, {r.lead[0], r.lead[1]}, ok);
+        const at::Tensor* lengths = maybe(a[8], dev, at::kInt, {c.B}, ok);
+        at::Tensor out;
+        if (!ok || !rows_output(a[12], dev, st, r, HQ, d, out) ||
+            size_t(ws->numel()) < attend_bytes_fn(int(r.n), int(c.B), int(HQ), int(HKV), int(d)))
+            return none();
+        const float scale = a[11] == Py_None ? float(1.0 / std::sqrt(double(d))) : float(PyFloat_AS_DOUBLE(a[11]));
+        canopy_status s;
+        {
+            const OnDevice on(dev);
+            if (!out.defined()) out = fresh_rows(r, HQ, d, st, dev);
+            s = attend_fn(q->data_ptr(), type, c.k->data_ptr(), c.v->data_ptr(), ptr<int32_t>(c.table), int(c.pages),
+                          int(c.page), int(c.most), ptr<int32_t>(c.context), ptr<int32_t>(starts),
+                          ptr<int32_t>(parent), ptr<int32_t>(lengths), int(r.n), int(c.B), int(HQ), int(HKV), int(d),
+                          int(window), int(sinks), scale, out.data_ptr(), ws->data_ptr(), stream_of(dev));
+        }
+        if (s != CANOPY_OK) return PyLong_FromLong(s);
+        return a[12] == Py_None ? THPVariable_Wrap(out) : Py_NewRef(a[12]);
+    });
+}
+
+// cache_commit(accepted, parent, k_cache, v_cache, page_table, context, lengths, err)
+PyObject* cache_commit(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (n != 8 || !cache_commit_fn) return none();
+    return guarded([&]() -> PyObject* {
+        int dev = -1;
+        const at::Tensor *k = plain(a[2], dev), *parent = plain(a[1], dev);
+        canopy_dtype type;
+        Cache c;
+        if (!k || !parent || k->dim() != 4 || parent->dim() != 2 || !code_of(k->scalar_type(), type) ||
+            !cache_of(a[2], a[3], a[4], a[5], dev, k->scalar_type(), k->size(1), k->size(3), c))
+            return none();
+        const int64_t T = parent->size(1), HKV = k->size(1), d = k->size(3);
+        bool ok = ints({T, HKV, d}) && plain(a[1], dev, at::kInt, {c.B, T});
+        const at::Tensor* accepted = plain(a[0], dev, at::kInt, {c.B});
+        const at::Tensor* lengths = maybe(a[6], dev, at::kInt, {c.B}, ok);
+        const at::Tensor* err = maybe(a[7], dev, at::kInt, {1}, ok);
+        if (!ok || !accepted) return none();
+        at::Tensor context;
+        canopy_status s;
+        {
+            const OnDevice on(dev);
+            context = fresh({c.B}, at::kInt, dev);
+            s = cache_commit_fn(ptr<int32_t>(accepted), ptr<int32_t>(parent), ptr<int32_t>(lengths), c.k->data_ptr(),
+                                c.v->data_ptr(), type, ptr<int32_t>(c.table), int(c.pages), int(c.page), int(c.most),
+                                ptr<int32_t>(c.context), int(T), int(c.B), int(HKV), int(d), ptr<int32_t>(&context),
+                                ptr<int32_t>(err), stream_of(dev));
+        }
+        if (s != CANOPY_OK) return PyLong_FromLong(s);
+        return THPVariable_Wrap(context);
+    });
+}
+
+// bind_attention(qk_prep, attend, attend_workspace_bytes, cache_commit)
+PyObject* bind_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (n != 4) {
+        PyErr_SetString(PyExc_TypeError, "bind_attention takes four addresses");
+        return nullptr;
+    }
+    void* f[4];
+    for (int i = 0; i < 4; ++i) {
+        f[i] = PyLong_AsVoidPtr(a[i]);
+        if (!f[i] && PyErr_Occurred()) return nullptr;
+    }
+    qk_prep_fn = reinterpret_cast<decltype(qk_prep_fn)>(f[0]);
+    attend_fn = reinterpret_cast<decltype(attend_fn)>(f[1]);
+    attend_bytes_fn = reinterpret_cast<decltype(attend_bytes_fn)>(f[2]);
+    cache_commit_fn = reinterpret_cast<decltype(cache_commit_fn)>(f[3]);
+    return none();
+}
+
 // bind(step, prefill, prefill_workspace_bytes, accept, torch.bfloat16, torch.float32)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (n != 6) {
@@ -297,6 +555,10 @@ PyMethodDef methods[] = {{"bind", fast(bind), METH_FASTCALL, nullptr},
                          {"step", fast(step), METH_FASTCALL, nullptr},
                          {"prefill", fast(prefill), METH_FASTCALL, nullptr},
                          {"accept", fast(accept), METH_FASTCALL, nullptr},
+                         {"bind_attention", fast(bind_attention), METH_FASTCALL, nullptr},
+                         {"qk_prep", fast(qk_prep), METH_FASTCALL, nullptr},
+                         {"attend", fast(attend), METH_FASTCALL, nullptr},
+                         {"cache_commit", fast(cache_commit), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods};

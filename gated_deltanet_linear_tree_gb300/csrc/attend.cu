@@ -17,8 +17,10 @@ __global__ void __launch_bounds__(256) plan_kernel(const Args a) {
         if (bad) raise_err(a.err, bad);
         const int64_t units = a.line[ntiles];
         const int ctas = parts(a, units);
-        for (int c = threadIdx.x; c < ctas; c += 256)
-            a.first_tile[c] = ntiles ? tile_at(a.line, ntiles, cta_begin(units, ctas, c)) : 0;
+        for (int c = threadIdx.x; c < ctas; c += 256) {
+            const int tile = ntiles ? tile_at(a.line, ntiles, cta_begin(units, ctas, c)) : 0;
+            a.first_tile[c] = make_int2(tile, sequence_at(a.seqs, a.B, tile));
+        }
         return;
     }
     __shared__ int sPtr[kMaxT], sLen[kMaxT];
@@ -357,7 +359,7 @@ Layout layout(int N, int B, int g, int d) {
     size_t o = 4096;  // the error word
     w.seqs = o;       o = ws_align(o + (size_t(B) + 1) * sizeof(int4));
     w.line = o;       o = ws_align(o + (size_t(N) + B + 1) * 8);
-    w.first_tile = o; o = ws_align(o + kFewCtas * 4);
+    w.first_tile = o; o = ws_align(o + (kFewCtas + 1) * 8);
     w.mask = o;       o = ws_align(o + size_t(N) * kMaskWords * 4);
     w.depth = o;      o = ws_align(o + size_t(N) * 4);
     const size_t most = size_t(2) * kSMs * slot_rows(N, g), few = size_t(2) * kFewCtas * 16;
@@ -419,7 +421,7 @@ cudaError_t launch_attend(const void* q, int bf16, const void* kc, const void* v
     a.err = reinterpret_cast<int32_t*>(p);
     a.seqs = reinterpret_cast<int4*>(p + w.seqs);
     a.line = reinterpret_cast<int64_t*>(p + w.line);
-    a.first_tile = reinterpret_cast<int*>(p + w.first_tile);
+    a.first_tile = reinterpret_cast<int2*>(p + w.first_tile);
     a.mask = reinterpret_cast<uint32_t*>(p + w.mask);
     a.depth = reinterpret_cast<int32_t*>(p + w.depth);
     a.part = reinterpret_cast<float*>(p + w.part);

@@ -43,7 +43,7 @@ struct Args {
     int32_t* err;
     int4* seqs;       // [B + 1]: first row, rows, ctx, first tile (of the last: the number of tiles)
     int64_t* line;    // [number of tiles + 1]: units before the tile, of all key heads
-    int* first_tile;  // [ctas]: the tile that CTA c begins in
+    int2* first_tile;  // [ctas]: the tile that CTA c begins in, and its sequence
     uint32_t* mask;   // trees: [N][kMaskWords], the nodes of a row's path that it sees
     int32_t* depth;   // trees: [N]
     float* part;      // [2 ctas] slots
@@ -232,7 +232,7 @@ struct Walk {
     int64_t units, at, end;
     int ctas, tile, b;
     // CTA c's part of the plan.
-    __device__ Walk(const Args& a, const int4* seqs, const int64_t* line, int c, const int* first_tile)
+    __device__ Walk(const Args& a, const int4* seqs, const int64_t* line, int c, const int2* first_tile)
         : seqs(seqs), line(line), units(0), at(0), end(0), ctas(1), tile(0), b(0) {
         const int ntiles = seqs[a.B].w;
         units = line[ntiles];
@@ -240,8 +240,13 @@ struct Walk {
         if (c >= ctas || units == 0) return;
         at = cta_begin(units, ctas, c);
         end = cta_begin(units, ctas, c + 1);
-        tile = first_tile ? first_tile[c] : tile_at(line, ntiles, at);
-        b = sequence_at(seqs, a.B, tile);
+        if (first_tile) {
+            tile = first_tile[c].x;
+            b = first_tile[c].y;
+        } else {
+            tile = tile_at(line, ntiles, at);
+            b = sequence_at(seqs, a.B, tile);
+        }
     }
     __device__ bool next(const Args& a, Piece& p) {
         if (at >= end) return false;

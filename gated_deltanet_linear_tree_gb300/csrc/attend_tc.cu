@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(NT, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_wait();
+    pdl_trigger();  // after the wait: the next launch may rely on everything before this one
 
     Walk walk(a, a.seqs, a.line, blockIdx.x, a.first_tile);
     const int half_tok = a.rt / 2;  // tokens of a half
@@ -435,50 +436,74 @@ __global__ void __launch_bounds__(NT, 1)
     }
 }
 
-// Joins the pieces of an item that is cut: block (c, e) rows 8 e .. 8 e + 7 of the
-// one whose first cut is between CTA c and c + 1.  Thread: a row and four columns.
+// Joins the pieces of an item that is cut: block (c, e) rows 32 e .. 32 e + 31 of the
+// one whose first cut is between CTA c and c + 1.  A thread has four columns of
+// four of the rows, eight threads side by side eight rows (128 bytes of a piece).
 template <int D>
 __global__ void __launch_bounds__(2 * D) join_kernel(const Args a) {
-    pdl_wait();
+    const int c = blockIdx.x;
+    // the plan is older than the launch that this one waits for
+    const int2 place = a.first_tile[c + 1];
     const int ntiles = a.seqs[a.B].w;
     const int64_t units = a.line[ntiles];
-    const int ctas = parts(a, units), c = blockIdx.x;
+    const int ctas = parts(a, units);
     if (c + 1 >= ctas || units == 0) return;
     const int64_t cut = cta_begin(units, ctas, c + 1);
-    const int tile = tile_at(a.line, ntiles, cut);
-    const int per = int((a.line[tile + 1] - a.line[tile]) / a.HKV), h = int((cut - a.line[tile]) / per);
-    const int64_t begin = a.line[tile] + int64_t(h) * per;
+    const int tile = place.x, b = place.y;
+    const int64_t at = a.line[tile];
+    const int per = int((a.line[tile + 1] - at) / a.HKV), h = int((cut - at) / per);
+    const int64_t begin = at + int64_t(h) * per;
     if (begin == cut || cta_of(units, ctas, begin) != c) return;
     const int pieces = cta_of(units, ctas, begin + per - 1) - c + 1;
-    const int b = sequence_at(a.seqs, a.B, tile);
-    const Tile t = make_tile(a, b, a.seqs[b], tile - a.seqs[b].w);
-    const int r = 8 * blockIdx.y + (threadIdx.x & 7), half = r >> 7, lane = r & 127, col = threadIdx.x >> 3;
-    const int tok = half * (a.rt / 2) + lane / a.g;
-    if (lane / a.g >= a.rt / 2 || tok >= t.ntok) return;
-    const int hr = min(a.slot_rows, 128);
-    const size_t size = size_t(hr) * (D + 2);
-    const float* part = a.part + half * size;
-    const size_t next = a.slot_rows / hr * size;
-    float top = -INFINITY;
-    for (int i = 0; i < pieces; ++i) top = fmaxf(top, part[slot_of(c, i) * next + hr * D + lane]);
-    const float from = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < pieces; ++i) {
-        const float* in = part + slot_of(c, i) * next;
-        const float w = exp2_approx(in[hr * D + lane] - from);
-        const float4 y = reinterpret_cast<const float4*>(in)[col * hr + lane];
-        sum += w * in[hr * D + hr + lane];
-        x.x += w * y.x;
-        x.y += w * y.y;
-        x.z += w * y.z;
-        x.w += w * y.w;
+    const int4 s = a.seqs[b];
+    const Tile t = make_tile(a, b, s, tile - s.w);
+    const int hr = min(a.slot_rows, 128), col = threadIdx.x >> 3;
+    const size_t size = size_t(hr) * (D + 2), next = a.slot_rows / hr * size;
+    pdl_wait();
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int r = 32 * blockIdx.y + 8 * e + (threadIdx.x & 7), half = r >> 7, lane = r & 127;
+        const int tok = half * (a.rt / 2) + lane / a.g;
+        if (r >= a.slot_rows || lane / a.g >= a.rt / 2 || tok >= t.ntok) continue;
+        const float* part = a.part + half * size;
+        float top = -INFINITY, sum = 0.f;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = 0; i0 < pieces; i0 += 4) {  // four pieces' reads at a time
+            float m[4], l[4];
+            float4 y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                m[i] = -INFINITY;
+                if (i0 + i >= pieces) continue;
+                const float* in = part + slot_of(c, i0 + i) * next;
+                m[i] = in[hr * D + lane];
+                l[i] = in[hr * D + hr + lane];
+                y[i] = reinterpret_cast<const float4*>(in)[col * hr + lane];
+            }
+            const float before = top;
+            top = fmaxf(fmaxf(top, fmaxf(m[0], m[1])), fmaxf(m[2], m[3]));
+            const float from = top == -INFINITY ? 0.f : top, keep = exp2_approx(before - from);
+            sum *= keep;
+            x.x *= keep;
+            x.y *= keep;
+            x.z *= keep;
+            x.w *= keep;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i0 + i >= pieces) continue;
+                const float w = exp2_approx(m[i] - from);
+                sum += w * l[i];
+                x.x += w * y[i].x;
+                x.y += w * y[i].y;
+                x.z += w * y[i].z;
+                x.w += w * y[i].w;
+            }
+        }
+        const float f = sum == 0.f ? 0.f : 1.f / sum;
+        __nv_bfloat16* out =
+            static_cast<__nv_bfloat16*>(a.o) + (size_t(t.row + tok) * a.HQ + h * a.g + lane % a.g) * D + 4 * col;
+        *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(x.x * f, x.y * f), pack_bf16(x.z * f, x.w * f));
     }
-    const float f = sum == 0.f ? 0.f : 1.f / sum;
-    __nv_bfloat16* out =
-        static_cast<__nv_bfloat16*>(a.o) + (size_t(t.row + tok) * a.HQ + h * a.g + lane % a.g) * D + 4 * col;
-    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(x.x * f, x.y * f), pack_bf16(x.z * f, x.w * f));
 }
 
 }  // namespace tcg
@@ -502,7 +527,7 @@ static cudaError_t launch_tc_d(const Args& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     e = launch_pdl(tcg::attend_kernel<D>, dim3(a.ctas), dim3(tcg::NT), smem, st, mq, mk, mv, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(tcg::join_kernel<D>, dim3(a.ctas - 1, a.slot_rows / 8), dim3(2 * D), 0, st, a);
+    return launch_pdl(tcg::join_kernel<D>, dim3(a.ctas - 1, (a.slot_rows + 31) / 32), dim3(2 * D), 0, st, a);
 }
 
 cudaError_t launch_tc(const Args& a, int d, cudaStream_t st) {

@@ -7,8 +7,10 @@
 //     (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin).
 // All in fp32, rounded once to the type.  The angle is kept in turns: freq_j /
 // 2 pi as a 64-bit binary fraction times the whole position wraps at whole turns
-// by itself, so that far positions lose nothing, and the top 32 bits go to
-// sincospi.
+// by itself, so that far positions lose nothing.  (The GPU has a 64th of the fp32
+// rate in fp64: two fp64 products a pair took 110 of 220 us for 16,383 tokens.)
+// Sine and cosine are their series about the nearest quarter turn, to the terms
+// that are below 2^-25 at an eighth of a turn.
 //
 // A lane holds four pairs of a head: for pairs (j, j + R/2) two chunks of four
 // elements R/2 apart, else eight elements in a row, so that a pair never leaves
@@ -30,7 +32,7 @@ struct Args {
     int norm, R, adjacent, axes;
     int N, T, B, HQ, HKV;
     int pages, log_page, max_pages;
-    int chunks;  // warps per token
+    int chunks, sets;  // warps per token; sets of heads each takes
 };
 
 // Four elements in fp32, and back.
@@ -90,15 +92,32 @@ __device__ inline int sequence_of(const Args& a, int n, int& i, int* bad) {
     return b;
 }
 
-// cos and sin of `position` times the frequency `f` (turns as a 64-bit fraction).
-__device__ inline void turn(int position, float freq, float& c, float& s) {
-    const double turns = double(freq) * 0.15915494309189535;  // 1 / 2 pi
-    const double part = turns - floor(turns);
-    const uint64_t fraction = uint64_t(part * 18446744073709551616.0);  // (2^64 for part rounding to 1 wraps to 0)
-    const int32_t top = int32_t((fraction * uint64_t(int64_t(position)) + 0x80000000ull) >> 32);
-    sincospif(float(top) * 4.656612873077393e-10f, &s, &c);  // 2^-31: top 2^-32 turns are top 2^-31 pi
+// freq / 2 pi as a 64-bit fraction of a turn: the significand, at the top of 64
+// bits, times 2^66 / 2 pi, its place given by the exponent.
+__device__ inline uint64_t turns_of(float freq) {
+    const uint32_t bits = __float_as_uint(freq);
+    const int exponent = int((bits >> 23) & 255) - 150;  // freq = significand * 2^exponent
+    const uint64_t significand = (bits & 0x7FFFFFu) | 0x800000u;
+    const uint64_t hi = __umul64hi(significand << 40, 0xA2F9836E4E44152Aull);  // significand * 2^42 / 2 pi
+    const int left = exponent + 22;
+    const uint64_t turns = left >= 64 || left <= -64 ? 0 : left >= 0 ? hi << left : hi >> -left;
+    return bits >> 31 ? 0 - turns : turns;
+}
+// cos and sin of `position` times a frequency.
+__device__ inline void turn(int position, uint64_t turns, float& c, float& s) {
+    const uint32_t top = uint32_t((turns * uint64_t(int64_t(position)) + 0x80000000ull) >> 32);
+    const uint32_t quarter = (top + 0x20000000u) >> 30;
+    const float x = float(int32_t(top - (quarter << 30))) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+    const float y = x * x;
+    const float si = x * fmaf(y, fmaf(y, fmaf(y, fmaf(y, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), 1.f);
+    const float co = fmaf(y, fmaf(y, fmaf(y, fmaf(y, 1.f / 40320, -1.f / 720), 1.f / 24), -0.5f), 1.f);
+    c = quarter & 1 ? si : co;
+    s = quarter & 1 ? co : si;
+    if ((quarter + 1) & 2) c = -c;
+    if (quarter & 2) s = -s;
 }
 
+// A warp: `sets` times 32 / LANES heads of a token, IT sets at a time.
 template <typename T, int D, int IT>
 __global__ void __launch_bounds__(128) prep_kernel(const Args a) {
     constexpr int LANES = D / 8, HEADS = 32 / LANES;  // lanes a head, heads a warp takes at a time
@@ -108,13 +127,30 @@ __global__ void __launch_bounds__(128) prep_kernel(const Args a) {
     const int n = int(w / a.chunks), chunk = int(w % a.chunks);
     if (n >= a.N) return;
     const int lane = threadIdx.x & 31, l = lane % LANES;
+    const bool turned = 8 * l < a.R, split = !a.adjacent && turned;
+    const int oa = split ? 4 * l : 8 * l, ob = split ? oa + a.R / 2 : oa + 4;
+    const int total = a.HQ + (a.kc ? 2 : 1) * a.HKV;
+    const int first = chunk * a.sets * HEADS + lane / LANES, end = min(total, (chunk + 1) * a.sets * HEADS);
+    const T *q = static_cast<const T*>(a.q) + n * a.ldq, *k = static_cast<const T*>(a.k) + n * a.ldk,
+            *v = static_cast<const T*>(a.v) + n * a.ldv;
+    float xa[IT][4], xb[IT][4];
+    auto load = [&](int h0) {
+#pragma unroll
+        for (int u = 0; u < IT; ++u) {
+            const int h = h0 + u * HEADS;
+            if (h >= end) continue;
+            const T* x = h < a.HQ ? q + h * D : h < a.HQ + a.HKV ? k + (h - a.HQ) * D : v + (h - a.HQ - a.HKV) * D;
+            get4(x + oa, xa[u]);
+            get4(x + ob, xb[u]);
+        }
+    };
+    load(first);  // ahead of the places' lookups
+
     int bad = 0, i = 0, b = -1;
+    bool here = true;
     if (a.context) {
         b = sequence_of(a, n, i, &bad);
-        if (b < 0) {
-            if (bad && lane == 0 && a.err) raise_err(a.err, bad);
-            return;
-        }
+        here = b >= 0;
     }
     int64_t slot = -1;  // the token's row in the pages, without the head
     int at = n;
@@ -134,62 +170,50 @@ __global__ void __launch_bounds__(128) prep_kernel(const Args a) {
             slot = ((int64_t(page) * a.HKV) << a.log_page) + (pos & ((1 << a.log_page) - 1));
     }
     if (bad && lane == 0 && a.err) raise_err(a.err, bad);
+    if (!here) return;
 
-    const bool split = !a.adjacent && l < a.R / 8;
-    const int oa = split ? 4 * l : 8 * l, ob = split ? oa + a.R / 2 : oa + 4;
     float c[4], s[4];
-    if (8 * l < a.R) {
+    if (turned) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int f = 4 * l + j;
             const int axis = a.axis ? min(max(a.axis[f], 0), a.axes - 1) : 0;
-            turn(a.positions ? a.positions[int64_t(axis) * a.N + n] : at, a.freqs[f], c[j], s[j]);
+            turn(a.positions ? a.positions[int64_t(axis) * a.N + n] : at, turns_of(a.freqs[f]), c[j], s[j]);
         }
     }
-    const int total = a.HQ + (a.kc ? 2 : 1) * a.HKV;
-    const int h0 = (chunk * IT) * HEADS + lane / LANES;
-    float xa[IT][4], xb[IT][4];
+    float wq[8], wk[8];  // the weights of this lane's columns
 #pragma unroll
-    for (int u = 0; u < IT; ++u) {
-        const int h = h0 + u * HEADS;
-        if (h >= total) continue;
-        const T* x;
-        if (h < a.HQ)
-            x = static_cast<const T*>(a.q) + n * a.ldq + h * D;
-        else if (h < a.HQ + a.HKV)
-            x = static_cast<const T*>(a.k) + n * a.ldk + (h - a.HQ) * D;
-        else
-            x = static_cast<const T*>(a.v) + n * a.ldv + (h - a.HQ - a.HKV) * D;
-        get4(x + oa, xa[u]);
-        get4(x + ob, xb[u]);
+    for (int j = 0; j < 8; ++j) {
+        const int col = j < 4 ? oa + j : ob + j - 4;
+        wq[j] = a.qw ? a.qw[col] : 1.f;
+        wk[j] = a.kw ? a.kw[col] : 1.f;
     }
+    const float share = a.norm == CANOPY_NORM_RMS ? 1.f / D : 1.f;
+    T* qo = static_cast<T*>(a.qo) + int64_t(n) * a.HQ * D;
+    T* ko = a.kc ? nullptr : static_cast<T*>(a.ko) + int64_t(n) * a.HKV * D;
+    for (int h0 = first; h0 - lane / LANES < end; h0 += IT * HEADS) {  // (a warp's lanes stay together)
+        if (h0 != first) load(h0);
 #pragma unroll
-    for (int u = 0; u < IT; ++u) {
-        const int h = h0 + u * HEADS;
-        const bool value = h >= a.HQ + a.HKV, key = h >= a.HQ && !value;
-        float ss = 0.f;
-        if (h < total)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) ss += xa[u][j] * xa[u][j] + xb[u][j] * xb[u][j];
-#pragma unroll
-        for (int m = LANES / 2; m; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-        if (h >= total) continue;
-        if (!value) {
+        for (int u = 0; u < IT; ++u) {
+            const int h = h0 + u * HEADS;
+            const bool there = h < end, query = h < a.HQ, value = h >= a.HQ + a.HKV;
+            float r = 1.f;
             if (a.norm != CANOPY_NORM_NONE) {
-                const float r = 1.f / sqrtf((a.norm == CANOPY_NORM_RMS ? ss * (1.f / D) : ss) + a.eps);
-                const float* wt = key ? a.kw : a.qw;
-                float wa[4] = {1.f, 1.f, 1.f, 1.f}, wb[4] = {1.f, 1.f, 1.f, 1.f};
-                if (wt) {
-                    get4(wt + oa, wa);
-                    get4(wt + ob, wb);
-                }
+                float ss = 0.f;
+                if (there)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) ss += xa[u][j] * xa[u][j] + xb[u][j] * xb[u][j];
+#pragma unroll
+                for (int m = LANES / 2; m; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+                r = rsqrtf(fmaf(ss, share, a.eps));
+            }
+            if (!there) continue;
+            if (!value) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    xa[u][j] *= r * wa[j];
-                    xb[u][j] *= r * wb[j];
+                    xa[u][j] *= r * (query ? wq[j] : wk[j]);
+                    xb[u][j] *= r * (query ? wq[4 + j] : wk[4 + j]);
                 }
-            }
-            if (8 * l < a.R) {
                 if (split) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -197,7 +221,7 @@ __global__ void __launch_bounds__(128) prep_kernel(const Args a) {
                         xa[u][j] = y * c[j] - z * s[j];
                         xb[u][j] = z * c[j] + y * s[j];
                     }
-                } else {
+                } else if (turned) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         float* p = j < 2 ? xa[u] + 2 * j : xb[u] + 2 * j - 4;
@@ -207,19 +231,19 @@ __global__ void __launch_bounds__(128) prep_kernel(const Args a) {
                     }
                 }
             }
+            T* out;
+            if (query) {
+                out = qo + h * D;
+            } else if (!a.kc) {
+                out = ko + (h - a.HQ) * D;
+            } else {
+                if (slot < 0) continue;
+                const int hk = value ? h - a.HQ - a.HKV : h - a.HQ;
+                out = static_cast<T*>(value ? a.vc : a.kc) + (slot + (int64_t(hk) << a.log_page)) * D;
+            }
+            put4(out + oa, xa[u]);
+            put4(out + ob, xb[u]);
         }
-        T* out;
-        if (h < a.HQ) {
-            out = static_cast<T*>(a.qo) + (int64_t(n) * a.HQ + h) * D;
-        } else if (!a.kc) {
-            out = static_cast<T*>(a.ko) + (int64_t(n) * a.HKV + h - a.HQ) * D;
-        } else {
-            if (slot < 0) continue;
-            const int hk = value ? h - a.HQ - a.HKV : h - a.HQ;
-            out = static_cast<T*>(value ? a.vc : a.kc) + (slot + (int64_t(hk) << a.log_page)) * D;
-        }
-        put4(out + oa, xa[u]);
-        put4(out + ob, xb[u]);
     }
 }
 
@@ -227,10 +251,16 @@ template <typename T, int D>
 cudaError_t launch(Args a, cudaStream_t st) {
     constexpr int HEADS = 256 / D;
     const int sets = (a.HQ + (a.kc ? 2 : 1) * a.HKV + HEADS - 1) / HEADS;
-    // few tokens: a warp to every set of heads; many: four sets a warp, the angles serving them all
+    // few tokens: a warp to every set of heads; many: as many sets a warp, in fours, as leave four warps to
+    // each place on the SMs, the angles serving them all
     const bool many = int64_t(a.N) * sets > 8 * 152 * 4;
-    const int it = many ? 4 : 1;
-    a.chunks = (sets + it - 1) / it;
+    a.sets = 1;
+    if (many) {
+        const int64_t fours = int64_t(a.N) * sets / (4 * 152 * 64);
+        a.sets = int(4 * (fours < 4 ? 1 : fours / 4));
+        if (a.sets > sets) a.sets = (sets + 3) / 4 * 4;
+    }
+    a.chunks = (sets + a.sets - 1) / a.sets;
     const dim3 grid(unsigned((int64_t(a.N) * a.chunks + 3) / 4));
     if (many) return launch_pdl(prep_kernel<T, D, 4>, grid, dim3(128), 0, st, a);
     return launch_pdl(prep_kernel<T, D, 1>, grid, dim3(128), 0, st, a);
@@ -246,7 +276,7 @@ cudaError_t launch_qk_prep(const void* q, const void* k, const void* v, int bf16
                            const int32_t* lengths, int32_t* err, cudaStream_t st) {
     qkp::Args a = {q, k, v, qo, ko, kc, vc, ldq, ldk, ldv, qw, kw, freqs, positions, axis, table, context, starts,
                    lengths, err, eps, norm, R, adjacent, axes, N, B ? N / B : N, B, HQ, HKV, pages, log_page,
-                   max_pages, 0};
+                   max_pages, 0, 0};
     using bf = __nv_bfloat16;
     if (bf16) return d == 128 ? qkp::launch<bf, 128>(a, st) : qkp::launch<bf, 64>(a, st);
     return d == 128 ? qkp::launch<float, 128>(a, st) : qkp::launch<float, 64>(a, st);

@@ -333,6 +333,7 @@ cudaError_t launch_join_bf16(const Args& a, int d, cudaStream_t st) {
 // ---------------------------------------------------------------------------
 
 int tc_tile_tokens(int g);
+int tc_tile_keys(int d);
 cudaError_t launch_tc(const Args& a, int d, cudaStream_t st);
 cudaError_t launch_few(const Args& a, int d, cudaStream_t st);
 bool few_plans(int N, int B);  // whether launch_few makes the plan itself
@@ -412,7 +413,7 @@ cudaError_t launch_attend(const void* q, int bf16, const void* kc, const void* v
     const bool tiles = plan == CANOPY_ATTEND_PLAN_TILES, few = plan == CANOPY_ATTEND_PLAN_FEW;
     const int R = a.g <= 16 && int64_t(N) * a.g <= int64_t(16) * B ? 16 : 64;  // rows of a tile, where not on 256
     a.rt = tiles ? tc_tile_tokens(a.g) : R / a.g;
-    a.log_kt = tiles ? 7 : 6;
+    a.kt = tiles ? tc_tile_keys(d) : 64;
     a.ctas = few ? kFewCtas : kSMs;
     a.least = kLeast;
     a.slot_rows = few ? 16 : slot_rows(N, a.g);

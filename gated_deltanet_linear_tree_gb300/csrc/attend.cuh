@@ -37,7 +37,7 @@ struct Args {
     int pages, log_page, max_pages;
     int window, sinks;
     float scale2;  // scale * log2(e): weights are powers of two
-    int rt, log_kt, ctas, least;  // tokens of a row tile, keys of a unit, CTAs at most, units of a CTA at least
+    int rt, kt, ctas, least;      // tokens of a row tile, keys of a unit, CTAs at most, units of a CTA at least
     int slot_rows;                // rows of a slot
     // workspace
     int32_t* err;
@@ -114,10 +114,9 @@ __device__ inline Tile make_tile(const Args& a, int b, const int4& s, int t) {
     const int64_t near = int64_t(r.ctx) + (a.parent ? 0 : r.t0) - a.window + 1;
     r.near = near > 0 ? int(near) : 0;
     r.sink_end = min(a.sinks, r.near);
-    const int kt = 1 << a.log_kt;
-    r.first = r.near >> a.log_kt;
-    r.sink_tiles = min((r.sink_end + kt - 1) >> a.log_kt, r.first);
-    r.units = r.sink_tiles + ((r.hi + kt - 1) >> a.log_kt) - r.first;
+    r.first = r.near / a.kt;
+    r.sink_tiles = min((r.sink_end + a.kt - 1) / a.kt, r.first);
+    r.units = r.sink_tiles + (r.hi + a.kt - 1) / a.kt - r.first;
     return r;
 }
 

@@ -2,24 +2,31 @@
 //
 // A CTA works on up to 256 rows of one (sequence, key head): two halves of 128
 // lanes, each of 128 / g tokens with the g query heads that share the key head,
-// against key tiles of 128.  Per half and key tile
-//     S = Q K^T            (128 x 128 x d, Q and K in shared memory)
-//     P = 2^(scale2 S - m) (four warps, a row a thread; bf16 over S's columns)
-//     O += P V             (128 x d x 128, P from tensor memory)
-// with S and O of both halves in the 512 columns of tensor memory.  While one
-// half's rows are in the softmax the other half's products run.  m is the
-// running maximum as of the last time that it grew by more than 2^8: until then
-// the weights are merely larger than 1, by less than 2^8, and neither sums nor
-// roundings know the difference; when it does grow, the row's thread scales O.
-// The weights are rounded to bf16 for the second product (their sum is of the
-// unrounded ones): a rounding of 2^-9 each, which averages out over the keys.
+// against tiles of KT keys.  Per half and key tile
+//     S = Q K^T            (128 x KT x d, Q and K in shared memory)
+//     P = 2^(scale2 S - m) (four warps, a row a thread; rounded to bf16)
+//     O += P V             (128 x d x KT, P from tensor memory)
+// with S, P and O of both halves in the 512 columns of tensor memory.  KT is what
+// leaves P a place of its own (80 for d = 128, 128 for d = 64): as soon as the
+// softmax has S in registers, the next tile's S is formed behind its back, and the
+// warps go from tile to tile without waiting for the products.  (Tiles of 128 with
+// P over S, each half's products during the other's softmax, took 3,300 cycles
+// per 128 keys in the best order found, of which the products are 2,048.)
+// A thread issues each half's products.
 //
-// Key tiles come by TMA, one box per page and 64 columns, into a ring of stages
-// that K and V tiles take in turns.  A page that no row sees is read at a
-// coordinate outside the cache, as zeros.  Where not every row sees every key of
-// a tile, two warps look through its V first: what no row sees, and what is not
-// finite, becomes zero (0 times it would reach every row's sum), and a row that
-// sees a key with such a value is NaN.
+// m is the running maximum as of the last time that it grew by more than 2^8:
+// until then the weights are merely larger than 1, by less than 2^8, and neither
+// sums nor roundings know the difference; when it does grow, the row's thread
+// scales O.  The weights are rounded to bf16 for the second product (their sum
+// is of the unrounded ones): a rounding of 2^-9 each, which averages out over the
+// keys.
+//
+// Key tiles come by TMA, one box per page (or 16 keys, where tiles and pages
+// cut each other) and 64 columns, into a ring of stages that K and V tiles take
+// in turns.  A page that no row sees is read at a coordinate outside the cache, as
+// zeros.  Where not every row sees every key of a tile, a warp looks through its
+// V first: what no row sees, and what is not finite, becomes zero (0 times it
+// would reach every row's sum), and a row that sees a key with such a value is NaN.
 #include "attend.cuh"
 
 namespace canopy {
@@ -30,20 +37,26 @@ bool make_bf16_box_map(CUtensorMap* m, const void* base, const uint64_t (&dim)[3
 namespace att {
 namespace tcg {
 
-constexpr int KT = 128, NT = 384;
+constexpr int NT = 384;
 constexpr uint32_t kCols = 512;
 
 template <int D>
 struct Shape {
-    static constexpr int TILE = 128 * D * 2;  // Q half, K or V tile: [d / 64][128 rows][128 bytes]
-    static constexpr int STAGES = D == 128 ? 5 : 10;
-    static constexpr int Q = 0, KV = 2 * TILE, BARS = KV + STAGES * TILE;
-    // barriers: Q full, Q read, all products done; per stage full, empty, and V looked through; per half S full, P
-    // there, O full
-    static constexpr int NBAR = 3 + 3 * STAGES + 6;
-    static constexpr int POISON = BARS + 8 * NBAR;         // [STAGES][4] words: keys with a value that is not finite
-    static constexpr int MISC = POISON + 16 * STAGES;      // tensor memory's address, flags
-    static constexpr int TOTAL = MISC + 32;
+    static constexpr int KT = D == 128 ? 80 : 128;  // keys of a tile
+    static constexpr int COLS = 256 - D;            // tensor memory of a half's S and P
+    static constexpr int PCOL = KT;                 // P's place in it
+    static_assert(KT + KT / 2 <= COLS, "S and P");
+    static constexpr int FIRST = (KT / 16 + 1) / 2;  // the 16-key steps of a tile's P that are handed over first
+    static constexpr int QTILE = 128 * D * 2;        // a half's Q: [d / 64][128 rows][128 bytes]
+    static constexpr int TILE = KT * D * 2;          // K or V: [d / 64][KT rows][128 bytes]
+    static constexpr int STAGES = (D == 128 ? 163840 : 131072) / TILE;
+    static constexpr int Q = 0, KV = 2 * QTILE, BARS = KV + STAGES * TILE;
+    // barriers: Q full, Q read; per stage full, empty, and V looked through; per half S full, S read, P there (in two
+    // parts), O done, and all done
+    static constexpr int NBAR = 2 + 3 * STAGES + 12;
+    static constexpr int POISON = BARS + 8 * NBAR;     // [STAGES][4] words: keys with a value that is not finite
+    static constexpr int MISC = POISON + 16 * STAGES;  // tensor memory's address
+    static constexpr int TOTAL = MISC + 16;
 };
 static_assert(Shape<128>::TOTAL + 1024 <= 232448 && Shape<64>::TOTAL + 1024 <= 232448, "shared memory");
 
@@ -63,17 +76,22 @@ __device__ inline uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+
+// Keys of a box at most: tiles and pages may cut each other anywhere but at multiples of 16 keys.
+__host__ __device__ constexpr int box_keys(int d) { return d == 128 ? 16 : 128; }
+
 template <int D>
 __global__ void __launch_bounds__(NT, 1)
     attend_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                   const __grid_constant__ CUtensorMap mapV, const Args a) {
     using Sh = Shape<D>;
-    constexpr int HALVES = D / 64;
+    constexpr int HALVES = D / 64, KT = Sh::KT, STAGES = Sh::STAGES;
     extern __shared__ uint8_t raw[];
     uint8_t* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Sh::BARS);
-    uint64_t *q_full = bars, *q_read = bars + 1, *full = bars + 2, *empty = full + Sh::STAGES,
-             *looked = empty + Sh::STAGES, *s_full = looked + Sh::STAGES, *p_there = s_full + 2, *o_full = p_there + 2, *drained = o_full + 2;
+    uint64_t *q_full = bars, *q_read = bars + 1, *full = bars + 2, *empty = full + STAGES, *looked = empty + STAGES,
+             *s_full = looked + STAGES, *s_read = s_full + 2, *p_there = s_read + 2, *o_done = p_there + 4,
+             *drained = o_done + 2;
     uint32_t* poison = reinterpret_cast<uint32_t*>(sm + Sh::POISON);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Sh::MISC);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -82,20 +100,22 @@ __global__ void __launch_bounds__(NT, 1)
         tmem_alloc(tmem_slot, kCols);
         tmem_relinquish();
     }
-    if (warp == 9 && lane == 0) {
+    if (warp == 10 && lane == 0) {
         mbar_init(q_full, 1);
-        mbar_init(q_read, 1);
-        for (int i = 0; i < Sh::STAGES; ++i) {
+        mbar_init(q_read, 2);
+        for (int i = 0; i < STAGES; ++i) {
             mbar_init(full + i, 1);
-            mbar_init(empty + i, 3);  // the products, and the two warps that look through V
-            mbar_init(looked + i, 64);
+            mbar_init(empty + i, 3);  // both halves' products, and the warp that looks through V
+            mbar_init(looked + i, 32);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + i, 1);
-            mbar_init(p_there + i, 128);
-            mbar_init(o_full + i, 1);
+            mbar_init(s_read + i, 128);
+            mbar_init(p_there + 2 * i, 128);
+            mbar_init(p_there + 2 * i + 1, 128);
+            mbar_init(o_done + i, 1);
+            mbar_init(drained + i, 1);
         }
-        mbar_init(drained, 1);
         fence_mbar_init();
     }
     tc_fence_before();
@@ -113,13 +133,13 @@ __global__ void __launch_bounds__(NT, 1)
     // 200 registers for the softmax's warps, 104 for the others: all of the 64,512 that the block was launched with
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-        if (warp == 9) {
-            // ---- loads -----------------------------------------------------------------
-            Ring<Sh::STAGES> ring;
+        if (warp == 10) {
+            // ---- loads ---------------------------------------------------------------------
+            Ring<STAGES> ring;
             uint32_t q_phase = 1;  // the first Q needs nothing read
             int q_loads = 0, loads = 0;
-            const int box = min(1 << a.log_page, KT), boxes = KT / box;  // keys of a box, boxes of a tile
-            const int i = lane / HALVES, part = lane % HALVES;           // this lane's boxes: i, i + 32 / HALVES, ...
+            const int box = min(1 << a.log_page, box_keys(D)), boxes = KT / box;  // keys of a box, boxes of a tile
+            const int i = lane / HALVES, part = lane % HALVES;                    // a lane's box
             int bad = 0;
             while (ok && walk.next(a, p)) {
                 const Tile& tile = p.tile;
@@ -132,22 +152,19 @@ __global__ void __launch_bounds__(NT, 1)
                     mbar_expect_tx(q_full, (two ? 2 : 1) * HALVES * half_tok * a.g * 128);
                     for (int h = 0; h < (two ? 2 : 1); ++h)
                         for (int c = 0; c < HALVES; ++c)
-                            tma_load_3d(sm + Sh::Q + h * Sh::TILE + c * 16384, &mapQ, q_full, 64 * c, p.h * a.g,
+                            tma_load_3d(sm + Sh::Q + h * Sh::QTILE + c * 16384, &mapQ, q_full, 64 * c, p.h * a.g,
                                         tile.row + h * half_tok);
                 }
                 for (int u = p.u0; ok && u < p.u1; ++u) {
                     const int key = key_tile(tile, u) * KT + i * box;
                     int z = a.pages * a.HKV;  // outside: zeros
-                    if (i < boxes) {
-                        bool reach = key < tile.sink_end || (key + box > tile.near && key < tile.hi);
-                        if (reach) {
-                            const int page = a.table[size_t(tile.b) * a.max_pages + (key >> a.log_page)];
-                            if (page < 0 || page >= a.pages) bad = CANOPY_DEVERR_PAGE;
-                            else z = page * a.HKV + p.h;
-                        }
+                    if (i < boxes && (key < tile.sink_end || (key + box > tile.near && key < tile.hi))) {
+                        const int page = a.table[size_t(tile.b) * a.max_pages + (key >> a.log_page)];
+                        if (page < 0 || page >= a.pages) bad = CANOPY_DEVERR_PAGE;
+                        else z = page * a.HKV + p.h;
                     }
                     const int slot = key & ((1 << a.log_page) - 1);
-    #pragma unroll
+#pragma unroll
                     for (int kv = 0; kv < 2; ++kv) {
                         ok = ok && warp_wait(empty + ring.at, ring.phase ^ 1);
                         if (!ok) break;
@@ -156,8 +173,8 @@ __global__ void __launch_bounds__(NT, 1)
                         if (lane == 0) mbar_expect_tx(full + ring.at, Sh::TILE);
                         __syncwarp();
                         if (i < boxes)
-                            tma_load_3d(dst + part * 16384 + i * box * 128, kv ? &mapV : &mapK, full + ring.at, 64 * part,
-                                        slot, z);
+                            tma_load_3d(dst + part * (KT * 128) + i * box * 128, kv ? &mapV : &mapK, full + ring.at,
+                                        64 * part, slot, z);
                         ring.step();
                     }
                 }
@@ -165,89 +182,90 @@ __global__ void __launch_bounds__(NT, 1)
             if (bad) raise_err(a.err, bad);
             // no copy is left in flight, should another warp have given up
             if (q_loads) warp_wait(q_full, (q_loads - 1) & 1);
-            for (int i = min(loads, Sh::STAGES); i > 0; --i) {
+            for (int i = min(loads, STAGES); i > 0; --i) {
                 ring.back();
                 warp_wait(full + ring.at, ring.phase);
             }
-        } else if (warp == 8) {
-            // ---- products ---------------------------------------------------------------
-            Ring<Sh::STAGES> ring, look;
-            Phase q_ready, p_ready[2];
-            const uint32_t qa = smem_u32(sm + Sh::Q), kv = smem_u32(sm + Sh::KV);
-            const bool lead = lane == 0;
-            // (descriptors hold addresses in units of 16 bytes: a step is an addition)
-            auto scores = [&](int h, int stage) {
-                const uint64_t q = sdesc_sw128(qa + h * Sh::TILE), k = sdesc_sw128(kv + stage * Sh::TILE);
-                if (lead)
-    #pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        const int step = (i >> 2) * 1024 + (i & 3) * 2;
-                        mma_bf16_ss(tmem + 128 * h, q + step, k + step, idesc_bf16(128, KT), i > 0);
-                    }
-            };
-            auto values = [&](int h, int stage, bool add) {
-                const uint64_t v = sdesc_sw128_mn(kv + stage * Sh::TILE, 16384);
-                if (lead)
-    #pragma unroll
-                    for (int i = 0; i < KT / 16; ++i)
-                        mma_bf16_ts(tmem + 256 + D * h, tmem + 128 * h + 8 * i, v + i * 128,
-                                    idesc_bf16(128, D) | kIdescBMnMajor, add || i > 0);
-            };
-            auto commit = [&](uint64_t* bar) {
-                if (lead) mma_commit(bar);
-                __syncwarp();
-            };
-            while (ok && walk.next(a, p)) {
-                const Tile& tile = p.tile;
-                const int nh = tile.ntok > half_tok ? 2 : 1;
-                ok = q_ready.wait(q_full) && warp_wait(full + ring.at, ring.phase);
-                if (!ok) break;
-                tc_fence_after();
-                for (int h = 0; h < nh; ++h) {
-                    scores(h, ring.at);
-                    commit(s_full + h);
-                }
-                commit(empty + ring.at);
-                if (p.u1 - p.u0 == 1) commit(q_read);
-                ring.step();
-                for (int u = p.u0; ok && u < p.u1; ++u) {
-                    const bool more = u + 1 < p.u1, all = all_see(a, tile, key_tile(tile, u) * KT, KT);
-                    const Ring<Sh::STAGES> v = ring;
+        } else if (warp < 10) {
+            // ---- products: of one half, by one thread ----------------------------------------
+            if (lane == 0) {
+                const int h = warp - 8;
+                Ring<STAGES> ring, look;
+                uint32_t q_phase = 0, s_phase = 1, p_phase = 0;
+                // (descriptors hold addresses in units of 16 bytes: a step is an addition)
+                const uint64_t q = sdesc_sw128(smem_u32(sm + Sh::Q) + h * Sh::QTILE);
+                const uint32_t kv = smem_u32(sm + Sh::KV), S = tmem + Sh::COLS * h, P = S + Sh::PCOL,
+                               O = tmem + 2 * Sh::COLS + D * h;
+                // S of the key tile in the ring's next stage, once the one before is in registers
+                auto scores = [&](bool last) {
+                    if (!mbar_wait(full + ring.at, ring.phase) || !mbar_wait(s_read + h, s_phase)) return false;
+                    s_phase ^= 1;
+                    tc_fence_after();
+                    const uint64_t k = sdesc_sw128(kv + ring.at * Sh::TILE);
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i)
+                        mma_bf16_ss(S, q + (i >> 2) * 1024 + (i & 3) * 2, k + (i >> 2) * (KT * 8) + (i & 3) * 2,
+                                    idesc_bf16(128, KT), i > 0);
+                    mma_commit(s_full + h);
+                    mma_commit(empty + ring.at);
+                    if (last) mma_commit(q_read);
                     ring.step();
-                    ok = warp_wait(full + v.at, v.phase);
-                    if (ok && !all) {
-                        ok = warp_wait(looked + look.at, look.phase);
-                        look.step();
-                    }
-                    for (int h = 0; ok && h < nh; ++h) {
-                        ok = p_ready[h].wait(p_there + h);
-                        if (!ok) break;
-                        tc_fence_after();
-                        values(h, v.at, u > p.u0);
-                        if (h == nh - 1) commit(empty + v.at);
-                        if (!more) {
-                            commit(o_full + h);
-                            continue;
+                    return true;
+                };
+                while (ok && walk.next(a, p)) {
+                    const Tile& tile = p.tile;
+                    const bool mine = h == 0 || tile.ntok > half_tok;
+                    ok = mbar_wait(q_full, q_phase);
+                    q_phase ^= 1;
+                    if (!ok) break;
+                    if (!mine) {  // the stages pass by
+                        mbar_arrive(q_read);
+                        for (int u = p.u0; ok && u < p.u1; ++u) {
+                            for (int i = 0; ok && i < 2; ++i) {
+                                ok = mbar_wait(full + ring.at, ring.phase);
+                                mbar_arrive(empty + ring.at);
+                                ring.step();
+                            }
+                            if (!all_see(a, tile, key_tile(tile, u) * KT, KT)) look.step();
                         }
-                        if (h == 0) ok = warp_wait(full + ring.at, ring.phase);
-                        if (!ok) break;
-                        tc_fence_after();
-                        scores(h, ring.at);
-                        commit(s_full + h);
-                        if (h == nh - 1) {
-                            commit(empty + ring.at);
-                            if (u + 2 == p.u1) commit(q_read);
-                        }
+                        continue;
                     }
-                    if (more) ring.step();
+                    ok = scores(p.u0 + 1 == p.u1);
+                    for (int u = p.u0; ok && u < p.u1; ++u) {
+                        const bool all = all_see(a, tile, key_tile(tile, u) * KT, KT);
+                        const Ring<STAGES> v = ring;
+                        ring.step();
+                        if (u + 1 < p.u1) ok = scores(u + 2 == p.u1);
+                        ok = ok && mbar_wait(full + v.at, v.phase);
+                        if (ok && !all) {
+                            ok = mbar_wait(looked + look.at, look.phase);
+                            look.step();
+                        }
+                        const uint64_t vd = sdesc_sw128_mn(kv + v.at * Sh::TILE, KT * 128);
+#pragma unroll
+                        for (int part = 0; part < 2; ++part) {
+                            ok = ok && mbar_wait(p_there + 2 * h + part, p_phase);
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int i = part * Sh::FIRST; i < (part ? KT / 16 : Sh::FIRST); ++i)
+                                mma_bf16_ts(O, P + 8 * i, vd + i * 128, idesc_bf16(128, D) | kIdescBMnMajor,
+                                            u > p.u0 || i > 0);
+                        }
+                        if (!ok) break;
+                        p_phase ^= 1;
+                        mma_commit(o_done + h);
+                        mma_commit(empty + v.at);
+                    }
                 }
+                mma_commit(drained + h);
+                mbar_wait(drained + h, 0);
             }
-            commit(drained);
-            warp_wait(drained, 0);
-        } else if (warp >= 10) {
-            // ---- looks through V where not every row sees every key ---------------------
-            // Every stage is waited for and let go, so that these warps neither fall behind the ring nor get ahead of it.
-            Ring<Sh::STAGES> ring, look;
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+        } else {
+            // ---- looks through V where not every row sees every key ---------------------------
+            // Every stage is waited for and let go, so that this warp neither falls behind the ring nor gets ahead of it.
+            Ring<STAGES> ring, look;
             while (ok && walk.next(a, p)) {
                 const Tile& tile = p.tile;
                 for (int u = p.u0; ok && u < p.u1; ++u)
@@ -256,23 +274,19 @@ __global__ void __launch_bounds__(NT, 1)
                         if (!ok) break;
                         const int key = key_tile(tile, u) * KT;
                         if (kv && !all_see(a, tile, key, KT)) {
-                            const int row0 = 64 * (warp - 10);  // this warp's keys
                             uint32_t* words = poison + 4 * look.at;
-                            if (lane < 2) words[2 * (warp - 10) + lane] = 0;
+                            if (lane < 4) words[lane] = 0;
                             __syncwarp();
-    #pragma unroll
-                            for (int c = 0; c < HALVES; ++c) {
-                                uint4* v = reinterpret_cast<uint4*>(sm + Sh::KV + ring.at * Sh::TILE + c * 16384) + 8 * row0;
-    #pragma unroll 8
-                                for (int e = lane; e < 64 * 8; e += 32) {
-                                    const int row = row0 + (e >> 3);
-                                    const uint4 x = v[e];
-                                    const bool there = in_reach(tile, key + row);
-                                    if (there && finite_pair(x.x) && finite_pair(x.y) && finite_pair(x.z) && finite_pair(x.w))
-                                        continue;
-                                    v[e] = make_uint4(0, 0, 0, 0);
-                                    if (there) atomicOr(words + (row >> 5), 1u << (row & 31));
-                                }
+                            uint4* v = reinterpret_cast<uint4*>(sm + Sh::KV + ring.at * Sh::TILE);
+#pragma unroll 8
+                            for (int e = lane; e < Sh::TILE / 16; e += 32) {
+                                const int row = (e >> 3) % KT;
+                                const uint4 x = v[e];
+                                const bool there = in_reach(tile, key + row);
+                                if (there && finite_pair(x.x) && finite_pair(x.y) && finite_pair(x.z) && finite_pair(x.w))
+                                    continue;
+                                v[e] = make_uint4(0, 0, 0, 0);
+                                if (there) atomicOr(words + (row >> 5), 1u << (row & 31));
                             }
                             fence_proxy_async_smem();
                             mbar_arrive(looked + look.at);
@@ -288,9 +302,10 @@ __global__ void __launch_bounds__(NT, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         // ---- softmax ------------------------------------------------------------------
         const int h = warp >> 2, r = threadIdx.x & 127;
-        const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16), S = lanes + 128 * h, O = lanes + 256 + D * h;
-        Ring<Sh::STAGES> look;
-        Phase scores_ready, o_ready;
+        const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16), S = lanes + Sh::COLS * h, P = S + Sh::PCOL,
+                       O = lanes + 2 * Sh::COLS + D * h;
+        Ring<STAGES> look;
+        Phase scores_ready, added;
         const int tok_in_half = r / a.g, head = r % a.g;
         while (ok && walk.next(a, p)) {
             const Tile& tile = p.tile;
@@ -305,37 +320,46 @@ __global__ void __launch_bounds__(NT, 1)
             for (int u = p.u0; u < p.u1; ++u) {
                 const int key = key_tile(tile, u) * KT;
                 const bool all = all_see(a, tile, key, KT);
-                const Ring<Sh::STAGES> v = look;
+                const Ring<STAGES> v = look;
                 if (!all) look.step();
                 if (!mine) continue;
                 ok = scores_ready.wait(s_full + h);
                 if (!ok) break;
                 tc_fence_after();
-                uint32_t s[128];
+                uint32_t s[KT];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(S + 32 * c, s + 32 * c);
+                for (int c = 0; c + 32 <= KT; c += 32) tmem_ld32(S + c, s + c);
+                if (KT % 32) tmem_ld16(S + KT / 32 * 32, *reinterpret_cast<uint32_t(*)[16]>(s + KT / 32 * 32));
                 tmem_wait_ld();
+                tc_fence_before();
+                mbar_arrive(s_read + h);
                 if (!all) {
-                    uint32_t seen[4];
+                    constexpr int W = (KT + 31) / 32;
+                    uint32_t seen[W];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) seen[c] = seen_bits(a, tile, depth, mask, key + 32 * c);
+                    for (int c = 0; c < W; ++c) seen[c] = seen_bits(a, tile, depth, mask, key + 32 * c);
 #pragma unroll
-                    for (int j = 0; j < 128; ++j)
+                    for (int j = 0; j < KT; ++j)
                         if (!((seen[j >> 5] >> (j & 31)) & 1u)) s[j] = 0xFF800000u;
                     ok = warp_wait(looked + v.at, v.phase);
                     if (!ok) break;
-                    const uint32_t* words = poison + 4 * v.at;
-                    if ((words[0] & seen[0]) | (words[1] & seen[1]) | (words[2] & seen[2]) | (words[3] & seen[3]))
-                        l = NAN;
+#pragma unroll
+                    for (int c = 0; c < W; ++c)
+                        if (poison[4 * v.at + c] & seen[c]) l = NAN;
                 }
                 float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int j = 0; j < 128; j += 8)
+                for (int j = 0; j < KT; j += 8)
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
                         top[c] = fmaxf(top[c], fmaxf(__uint_as_float(s[j + 2 * c]), __uint_as_float(s[j + 2 * c + 1])));
                 const float t = a.scale2 * fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                 const bool grow = t > m + kGrow;  // (the first finite one too)
+                if (u > p.u0) {  // the product before has read P and added to O
+                    ok = added.wait(o_done + h);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
                 if (__any_sync(0xffffffffu, grow)) {
                     const float keep = grow ? exp2_approx(m - t) : 1.f;
                     if (grow) {
@@ -358,31 +382,34 @@ __global__ void __launch_bounds__(NT, 1)
                 const uint64_t sc = pack2(a.scale2, a.scale2), mb = pack2(-base, -base);
                 uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
-                for (int c = 0; c < 128; c += 32) {
-                    uint32_t w[16];
+                for (int c = 0; c < KT / 16; ++c) {
+                    uint32_t w[8];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
+                    for (int j = 0; j < 8; ++j) {
                         float x, y;
-                        unpack2(fma2(pack2(__uint_as_float(s[c + 2 * j]), __uint_as_float(s[c + 2 * j + 1])), sc, mb), x,
-                                y);
+                        unpack2(fma2(pack2(__uint_as_float(s[16 * c + 2 * j]), __uint_as_float(s[16 * c + 2 * j + 1])),
+                                     sc, mb),
+                                x, y);
                         x = exp2_approx(x);
                         y = exp2_approx(y);
                         if (j & 1) sum1 = add2(sum1, pack2(x, y));
                         else sum0 = add2(sum0, pack2(x, y));
                         w[j] = pack_bf16(x, y);
                     }
-                    tmem_st16(S + c / 2, w);
+                    tmem_st8(P + 8 * c, w);
+                    if (c == Sh::FIRST - 1 || c == KT / 16 - 1) {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        mbar_arrive(p_there + 2 * h + (c != Sh::FIRST - 1));
+                    }
                 }
                 float x, y;
                 unpack2(add2(sum0, sum1), x, y);
                 l += x + y;
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(p_there + h);
             }
             if (!ok) break;
             if (!mine) continue;
-            ok = o_ready.wait(o_full + h);
+            ok = added.wait(o_done + h);
             if (!ok) break;
             tc_fence_after();
             if (p.whole) {
@@ -510,12 +537,13 @@ __global__ void __launch_bounds__(2 * D) join_kernel(const Args a) {
 
 // Rows of a tile are 2 (128 / g) tokens of g heads.
 int tc_tile_tokens(int g) { return 2 * (128 / g); }
+int tc_tile_keys(int d) { return d == 128 ? tcg::Shape<128>::KT : tcg::Shape<64>::KT; }
 
 template <int D>
 static cudaError_t launch_tc_d(const Args& a, cudaStream_t st) {
     CUtensorMap mq, mk, mv;
     const uint64_t row = D * 2, page = uint64_t(1) << a.log_page;
-    const uint32_t keys = uint32_t(page < tcg::KT ? page : tcg::KT);
+    const uint32_t keys = uint32_t(page < tcg::box_keys(D) ? page : tcg::box_keys(D));
     if (!make_bf16_box_map(&mq, a.q, {D, uint64_t(a.HQ), uint64_t(a.N)}, {row, a.HQ * row},
                            {64, uint32_t(a.g), uint32_t(a.rt / 2)}) ||
         !make_bf16_box_map(&mk, a.kc, {D, page, uint64_t(a.pages) * a.HKV}, {row, page * row}, {64, keys, 1}) ||

@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(NT) attend_kernel(const Args a) {
             mask[r] = a.parent ? a.mask + size_t(tile.row + i) * kMaskWords : nullptr;
         }
         for (int u = p.u0; u < p.u1; ++u) {
-            const int key0 = key_tile(tile, u) * KT;
+            const int kt = key_tile(tile, u), key0 = kt * KT;
             __syncthreads();
             for (int e = tid; e < KT * (D / 4); e += NT) {
                 const int j = e / (D / 4), c = 4 * (e % (D / 4));
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(NT) attend_kernel(const Args a) {
                         s[r][j] += x.x * k4[j].x + x.y * k4[j].y + x.z * k4[j].z + x.w * k4[j].w;
                 }
             }
-            const bool all = all_see(a, tile, key0, KT);
+            const bool all = all_see(tile, kt);
 #pragma unroll
             for (int r = 0; r < RR; ++r) {
                 float top = -INFINITY;

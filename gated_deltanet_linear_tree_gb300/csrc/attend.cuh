@@ -27,6 +27,7 @@ struct Tile {
     int sink_end, near, hi;  // keys [0, sink_end) and [near, hi) are seen by some row
     int sink_tiles, first;   // key tiles [0, sink_tiles) and from `first` on
     int units;               // how many key tiles
+    int sink_full, full_from, full_to;  // key tiles [0, sink_full) and [full_from, full_to) are seen whole by all rows
 };
 
 struct Args {
@@ -58,11 +59,9 @@ __device__ inline bool sees(const Args& a, const Tile& tile, int depth, const ui
     const int pos = tile.ctx + depth;
     return key <= pos && (pos - key < a.window || key < a.sinks);
 }
-// Whether every row of the tile sees keys [key, key + kt).
-__device__ inline bool all_see(const Args& a, const Tile& tile, int key, int kt) {
-    const int last = key + kt - 1;
-    if (last >= tile.ctx + (a.parent ? 0 : tile.t0 + 1)) return false;
-    return last < a.sinks || tile.ctx + (a.parent ? tile.n : tile.t0 + tile.ntok) - 1 - key < a.window;
+// Whether every row of the tile sees all of a key tile.
+__device__ inline bool all_see(const Tile& tile, int key_tile) {
+    return key_tile < tile.sink_full || (key_tile >= tile.full_from && key_tile < tile.full_to);
 }
 // Whether some row of the tile may see the key (the others' pages may be gone).
 __device__ inline bool in_reach(const Tile& tile, int key) {
@@ -117,6 +116,12 @@ __device__ inline Tile make_tile(const Args& a, int b, const int4& s, int t) {
     r.first = r.near / a.kt;
     r.sink_tiles = min((r.sink_end + a.kt - 1) / a.kt, r.first);
     r.units = r.sink_tiles + (r.hi + a.kt - 1) / a.kt - r.first;
+    // all rows see the keys before the first row's new ones, as far back as the last row's window
+    const int lim = r.ctx + (a.parent ? 0 : r.t0 + 1);
+    const int64_t low = int64_t(r.ctx) + (a.parent ? r.n : r.t0 + r.ntok) - a.window;
+    r.sink_full = min(a.sinks, lim) / a.kt;
+    r.full_from = low > 0 ? int((low + a.kt - 1) / a.kt) : 0;
+    r.full_to = lim / a.kt;
     return r;
 }
 

@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(NT, 2)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
             for (int u = p.u0; u < p.u1; ++u) {
-                const int key = key_tile(tile, u) * KT + 32 * warp;  // this warp's 32 keys
+                const int kt = key_tile(tile, u), key = kt * KT + 32 * warp;  // this warp's 32 keys
                 ok = warp_wait(sm.full + ring.at, ring.phase);
                 if (!ok) break;
                 const uint32_t K = smem_u32(sm.kv[ring.at][0]), V = smem_u32(sm.kv[ring.at][1]);
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(NT, 2)
                         mma16816(s[2 * n], q[k], b[0], b[1]);
                         mma16816(s[2 * n + 1], q[k], b[2], b[3]);
                     }
-                const bool all = all_see(a, tile, key - 32 * warp, KT);
+                const bool all = all_see(tile, kt);
                 uint32_t keep = 0xFFFFFFFFu, check = 0;  // keys that some row sees; those that some but not all see
                 uint32_t seen[2] = {keep, keep};
                 if (!all) {

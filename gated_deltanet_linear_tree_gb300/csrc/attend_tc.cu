@@ -60,23 +60,11 @@ struct Shape {
 };
 static_assert(Shape<128>::TOTAL + 1024 <= 232448 && Shape<64>::TOTAL + 1024 <= 232448, "shared memory");
 
-__device__ inline uint64_t pack2(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+__device__ inline float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
-__device__ inline void unpack2(uint64_t x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
-__device__ inline uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ inline uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 // Keys of a box at most: tiles and pages may cut each other anywhere but at multiples of 16 keys.
 __host__ __device__ constexpr int box_keys(int d) { return d == 128 ? 16 : 128; }
 
@@ -226,13 +214,13 @@ __global__ void __launch_bounds__(NT, 1)
                                 mbar_arrive(empty + ring.at);
                                 ring.step();
                             }
-                            if (!all_see(a, tile, key_tile(tile, u) * KT, KT)) look.step();
+                            if (!all_see(tile, key_tile(tile, u))) look.step();
                         }
                         continue;
                     }
                     ok = scores(p.u0 + 1 == p.u1);
                     for (int u = p.u0; ok && u < p.u1; ++u) {
-                        const bool all = all_see(a, tile, key_tile(tile, u) * KT, KT);
+                        const bool all = all_see(tile, key_tile(tile, u));
                         const Ring<STAGES> v = ring;
                         ring.step();
                         if (u + 1 < p.u1) ok = scores(u + 2 == p.u1);
@@ -272,21 +260,32 @@ __global__ void __launch_bounds__(NT, 1)
                     for (int kv = 0; kv < 2; ++kv) {
                         ok = warp_wait(full + ring.at, ring.phase);
                         if (!ok) break;
-                        const int key = key_tile(tile, u) * KT;
-                        if (kv && !all_see(a, tile, key, KT)) {
-                            uint32_t* words = poison + 4 * look.at;
-                            if (lane < 4) words[lane] = 0;
-                            __syncwarp();
+                        const int kt = key_tile(tile, u), key = kt * KT;
+                        if (kv && !all_see(tile, kt)) {
                             uint4* v = reinterpret_cast<uint4*>(sm + Sh::KV + ring.at * Sh::TILE);
-#pragma unroll 8
-                            for (int e = lane; e < Sh::TILE / 16; e += 32) {
-                                const int row = (e >> 3) % KT;
-                                const uint4 x = v[e];
-                                const bool there = in_reach(tile, key + row);
-                                if (there && finite_pair(x.x) && finite_pair(x.y) && finite_pair(x.z) && finite_pair(x.w))
-                                    continue;
-                                v[e] = make_uint4(0, 0, 0, 0);
-                                if (there) atomicOr(words + (row >> 5), 1u << (row & 31));
+                            for (int w = 0; w < (KT + 31) / 32; ++w) {  // 32 keys; four a time, eight lanes each
+                                uint32_t bad = 0;
+#pragma unroll
+                                for (int c = 0; c < HALVES; ++c) {
+                                    uint4 x[8];  // read together
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e) {
+                                        const int row = 32 * w + 4 * e + (lane >> 3);
+                                        if (row < KT) x[e] = v[(c * KT + row) * 8 + (lane & 7)];
+                                    }
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e) {
+                                        const int row = 32 * w + 4 * e + (lane >> 3);
+                                        const bool there = in_reach(tile, key + row);
+                                        if (row >= KT || (there && finite_pair(x[e].x) && finite_pair(x[e].y) &&
+                                                          finite_pair(x[e].z) && finite_pair(x[e].w)))
+                                            continue;
+                                        v[(c * KT + row) * 8 + (lane & 7)] = make_uint4(0, 0, 0, 0);
+                                        if (there) bad |= 1u << (row & 31);
+                                    }
+                                }
+                                bad = __reduce_or_sync(0xffffffffu, bad);
+                                if (lane == 0) poison[4 * look.at + w] = bad;
                             }
                             fence_proxy_async_smem();
                             mbar_arrive(looked + look.at);
@@ -318,8 +317,8 @@ __global__ void __launch_bounds__(NT, 1)
             float m = -INFINITY, base = 0.f;  // the maximum that the weights are relative to, scaled
             float l = 0.f;
             for (int u = p.u0; u < p.u1; ++u) {
-                const int key = key_tile(tile, u) * KT;
-                const bool all = all_see(a, tile, key, KT);
+                const int kt = key_tile(tile, u), key = kt * KT;
+                const bool all = all_see(tile, kt);
                 const Ring<STAGES> v = look;
                 if (!all) look.step();
                 if (!mine) continue;
@@ -352,7 +351,7 @@ __global__ void __launch_bounds__(NT, 1)
                 for (int j = 0; j < KT; j += 8)
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        top[c] = fmaxf(top[c], fmaxf(__uint_as_float(s[j + 2 * c]), __uint_as_float(s[j + 2 * c + 1])));
+                        top[c] = max3(top[c], __uint_as_float(s[j + 2 * c]), __uint_as_float(s[j + 2 * c + 1]));
                 const float t = a.scale2 * fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                 const bool grow = t > m + kGrow;  // (the first finite one too)
                 if (u > p.u0) {  // the product before has read P and added to O

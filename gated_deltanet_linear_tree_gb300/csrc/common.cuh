@@ -102,6 +102,29 @@ __device__ inline float4 load4(const __nv_bfloat16* p) {
 __device__ inline void store_out(float* p, float x) { *p = x; }
 __device__ inline void store_out(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
+// Two fp32 values in a register pair, and operations on both.
+__device__ inline uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ inline void unpack2(uint64_t x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ inline uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ inline uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ inline uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // Gate checks: alpha must be finite and > 0 where its logarithm is taken, beta
 // finite.
 __device__ inline bool gate_ok(float a, float b) {

@@ -35,25 +35,36 @@ struct Args {
     int chunks, sets;  // warps per token; sets of heads each takes
 };
 
-// Four elements in fp32, and back.
-__device__ inline void get4(const float* p, float (&x)[4]) {
-    const float4 t = *reinterpret_cast<const float4*>(p);
-    x[0] = t.x; x[1] = t.y; x[2] = t.z; x[3] = t.w;
+// Four elements in fp32 (two pairs), and back.
+struct Four {
+    uint64_t lo, hi;
+};
+__device__ inline Four get4(const float* p) {
+    const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(p);
+    return {t.x, t.y};
 }
-__device__ inline void get4(const __nv_bfloat16* p, float (&x)[4]) {
+__device__ inline Four get4(const __nv_bfloat16* p) {
     const uint2 t = *reinterpret_cast<const uint2*>(p);
-    x[0] = __uint_as_float(t.x << 16); x[1] = __uint_as_float(t.x & 0xFFFF0000u);
-    x[2] = __uint_as_float(t.y << 16); x[3] = __uint_as_float(t.y & 0xFFFF0000u);
+    return {pack2(__uint_as_float(t.x << 16), __uint_as_float(t.x & 0xFFFF0000u)),
+            pack2(__uint_as_float(t.y << 16), __uint_as_float(t.y & 0xFFFF0000u))};
 }
-__device__ inline void put4(float* p, const float (&x)[4]) {
-    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+__device__ inline void put4(float* p, const Four& x) { *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(x.lo, x.hi); }
+__device__ inline void put4(__nv_bfloat16* p, const Four& x) {
+    float a, b, c, d;
+    unpack2(x.lo, a, b);
+    unpack2(x.hi, c, d);
+    const __nv_bfloat162 y = __floats2bfloat162_rn(a, b), z = __floats2bfloat162_rn(c, d);
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&y), *reinterpret_cast<const uint32_t*>(&z));
 }
-__device__ inline void put4(__nv_bfloat16* p, const float (&x)[4]) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-    uint2 t;
-    t.x = *reinterpret_cast<const uint32_t*>(&a);
-    t.y = *reinterpret_cast<const uint32_t*>(&b);
-    *reinterpret_cast<uint2*>(p) = t;
+__device__ inline Four operator*(const Four& a, const Four& b) { return {mul2(a.lo, b.lo), mul2(a.hi, b.hi)}; }
+__device__ inline Four fma4(const Four& a, const Four& b, const Four& c) {
+    return {fma2(a.lo, b.lo, c.lo), fma2(a.hi, b.hi, c.hi)};
+}
+__device__ inline float sum4(const Four& x) {
+    float a, b;
+    unpack2(add2(x.lo, x.hi), a, b);
+    return a + b;
 }
 
 // The sequence that token n belongs to (-1: none) and its index there; for a
@@ -117,132 +128,145 @@ __device__ inline void turn(int position, uint64_t turns, float& c, float& s) {
     if (quarter & 2) s = -s;
 }
 
-// A warp: `sets` times 32 / LANES heads of a token, IT sets at a time.
+// A warp: `sets` of a token's sets of 32 / LANES heads (queries, keys and values have
+// sets of their own, so that a warp does one thing at a time), IT sets at a time.
 template <typename T, int D, int IT>
-__global__ void __launch_bounds__(128) prep_kernel(const Args a) {
-    constexpr int LANES = D / 8, HEADS = 32 / LANES;  // lanes a head, heads a warp takes at a time
+__global__ void __launch_bounds__(128, IT == 1 ? 8 : 7) prep_kernel(const Args a) {
+    constexpr int LANES = D / 8, HEADS = 32 / LANES;  // lanes a head, heads of a set
     pdl_wait();
     pdl_trigger();
-    const int64_t w = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const int n = int(w / a.chunks), chunk = int(w % a.chunks);
-    if (n >= a.N) return;
-    const int lane = threadIdx.x & 31, l = lane % LANES;
+    const int lane = threadIdx.x & 31, l = lane % LANES, sub = lane / LANES;
     const bool turned = 8 * l < a.R, split = !a.adjacent && turned;
     const int oa = split ? 4 * l : 8 * l, ob = split ? oa + a.R / 2 : oa + 4;
-    const int total = a.HQ + (a.kc ? 2 : 1) * a.HKV;
-    const int first = chunk * a.sets * HEADS + lane / LANES, end = min(total, (chunk + 1) * a.sets * HEADS);
-    const T *q = static_cast<const T*>(a.q) + n * a.ldq, *k = static_cast<const T*>(a.k) + n * a.ldk,
-            *v = static_cast<const T*>(a.v) + n * a.ldv;
-    float xa[IT][4], xb[IT][4];
-    auto load = [&](int h0) {
-#pragma unroll
-        for (int u = 0; u < IT; ++u) {
-            const int h = h0 + u * HEADS;
-            if (h >= end) continue;
-            const T* x = h < a.HQ ? q + h * D : h < a.HQ + a.HKV ? k + (h - a.HQ) * D : v + (h - a.HQ - a.HKV) * D;
-            get4(x + oa, xa[u]);
-            get4(x + ob, xb[u]);
-        }
-    };
-    load(first);  // ahead of the places' lookups
-
-    int bad = 0, i = 0, b = -1;
-    bool here = true;
-    if (a.context) {
-        b = sequence_of(a, n, i, &bad);
-        here = b >= 0;
-    }
-    int64_t slot = -1;  // the token's row in the pages, without the head
-    int at = n;
-    if (b >= 0) {
-        int ctx = a.context[b];
-        if (ctx < 0) {
-            bad |= CANOPY_DEVERR_LENGTH;
-            ctx = 0;
-        }
-        const int64_t pos = int64_t(ctx) + i;
-        at = int(pos < 0x7FFFFFFF ? pos : 0x7FFFFFFF);
-        const int64_t entry = pos >> a.log_page;
-        const int page = entry < a.max_pages ? a.table[int64_t(b) * a.max_pages + entry] : -1;
-        if (page < 0 || page >= a.pages)
-            bad |= CANOPY_DEVERR_PAGE;
-        else
-            slot = ((int64_t(page) * a.HKV) << a.log_page) + (pos & ((1 << a.log_page) - 1));
-    }
-    if (bad && lane == 0 && a.err) raise_err(a.err, bad);
-    if (!here) return;
-
-    float c[4], s[4];
+    const int qsets = (a.HQ + HEADS - 1) / HEADS, ksets = (a.HKV + HEADS - 1) / HEADS;
+    uint64_t turns[4] = {};
+    int axis[4] = {};
     if (turned) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int f = 4 * l + j;
-            const int axis = a.axis ? min(max(a.axis[f], 0), a.axes - 1) : 0;
-            turn(a.positions ? a.positions[int64_t(axis) * a.N + n] : at, turns_of(a.freqs[f]), c[j], s[j]);
+            turns[j] = turns_of(a.freqs[4 * l + j]);
+            axis[j] = a.axis ? min(max(a.axis[4 * l + j], 0), a.axes - 1) : 0;
         }
     }
-    float wq[8], wk[8];  // the weights of this lane's columns
+    for (uint32_t w = blockIdx.x * 4 + (threadIdx.x >> 5); w < uint32_t(a.N) * a.chunks; w += 4 * gridDim.x) {
+        const int n = int(w / a.chunks), chunk = int(w % a.chunks);
+        const int first = chunk * a.sets, end = min(qsets + (a.kc ? 2 : 1) * ksets, first + a.sets);
+        const T *q = static_cast<const T*>(a.q) + n * a.ldq, *k = static_cast<const T*>(a.k) + n * a.ldk,
+                *v = static_cast<const T*>(a.v) + n * a.ldv;
+        Four xa[IT], xb[IT];
+        auto load = [&](int s0) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int col = j < 4 ? oa + j : ob + j - 4;
-        wq[j] = a.qw ? a.qw[col] : 1.f;
-        wk[j] = a.kw ? a.kw[col] : 1.f;
-    }
-    const float share = a.norm == CANOPY_NORM_RMS ? 1.f / D : 1.f;
-    T* qo = static_cast<T*>(a.qo) + int64_t(n) * a.HQ * D;
-    T* ko = a.kc ? nullptr : static_cast<T*>(a.ko) + int64_t(n) * a.HKV * D;
-    for (int h0 = first; h0 - lane / LANES < end; h0 += IT * HEADS) {  // (a warp's lanes stay together)
-        if (h0 != first) load(h0);
+            for (int u = 0; u < IT; ++u) {
+                const int s = s0 + u;
+                if (s >= end) continue;
+                const bool query = s < qsets;
+                const int h = (query ? s : s < qsets + ksets ? s - qsets : s - qsets - ksets) * HEADS + sub;
+                const T* x = (query ? q : s < qsets + ksets ? k : v) + h * D;
+                if (h >= (query ? a.HQ : a.HKV)) continue;
+                xa[u] = get4(x + oa);
+                xb[u] = get4(x + ob);
+            }
+        };
+        load(first);  // ahead of the places' lookups
+
+        int bad = 0, i = 0, b = -1;
+        bool here = true;
+        if (a.context) {
+            b = sequence_of(a, n, i, &bad);
+            here = b >= 0;
+        }
+        int64_t slot = -1;  // the token's row in the pages, without the head
+        int at = n;
+        if (b >= 0) {
+            int ctx = a.context[b];
+            if (ctx < 0) {
+                bad |= CANOPY_DEVERR_LENGTH;
+                ctx = 0;
+            }
+            const int64_t pos = int64_t(ctx) + i;
+            at = int(pos < 0x7FFFFFFF ? pos : 0x7FFFFFFF);
+            const int64_t entry = pos >> a.log_page;
+            const int page = entry < a.max_pages ? a.table[int64_t(b) * a.max_pages + entry] : -1;
+            if (page < 0 || page >= a.pages)
+                bad |= CANOPY_DEVERR_PAGE;
+            else
+                slot = ((int64_t(page) * a.HKV) << a.log_page) + (pos & ((1 << a.log_page) - 1));
+        }
+        if (bad && lane == 0 && a.err) raise_err(a.err, bad);
+        if (!here) continue;
+
+        Four co = {0, 0}, si = {0, 0}, minus = {0, 0};  // cosines, sines and their negatives of this lane's pairs
+        if (turned && first < qsets + ksets) {
+            float c[4], s[4];
 #pragma unroll
-        for (int u = 0; u < IT; ++u) {
-            const int h = h0 + u * HEADS;
-            const bool there = h < end, query = h < a.HQ, value = h >= a.HQ + a.HKV;
-            float r = 1.f;
+            for (int j = 0; j < 4; ++j)
+                turn(a.positions ? a.positions[int64_t(axis[j]) * a.N + n] : at, turns[j], c[j], s[j]);
+            co = {pack2(c[0], c[1]), pack2(c[2], c[3])};
+            si = {pack2(s[0], s[1]), pack2(s[2], s[3])};
+            minus = {pack2(-s[0], -s[1]), pack2(-s[2], -s[3])};
+        }
+        const float share = a.norm == CANOPY_NORM_RMS ? 1.f / D : 1.f;
+        T* qo = static_cast<T*>(a.qo) + int64_t(n) * a.HQ * D;
+        T* ko = a.kc ? nullptr : static_cast<T*>(a.ko) + int64_t(n) * a.HKV * D;
+        // norm and rotation; `weight` this head's, or null
+        auto finish = [&](Four& x, Four& y, bool there, const float* weight) {
             if (a.norm != CANOPY_NORM_NONE) {
-                float ss = 0.f;
-                if (there)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) ss += xa[u][j] * xa[u][j] + xb[u][j] * xb[u][j];
+                float ss = there ? sum4(fma4(x, x, y * y)) : 0.f;
 #pragma unroll
                 for (int m = LANES / 2; m; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-                r = rsqrtf(fmaf(ss, share, a.eps));
-            }
-            if (!there) continue;
-            if (!value) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    xa[u][j] *= r * (query ? wq[j] : wk[j]);
-                    xb[u][j] *= r * (query ? wq[4 + j] : wk[4 + j]);
-                }
-                if (split) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float y = xa[u][j], z = xb[u][j];
-                        xa[u][j] = y * c[j] - z * s[j];
-                        xb[u][j] = z * c[j] + y * s[j];
-                    }
-                } else if (turned) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float* p = j < 2 ? xa[u] + 2 * j : xb[u] + 2 * j - 4;
-                        const float y = p[0], z = p[1];
-                        p[0] = y * c[j] - z * s[j];
-                        p[1] = z * c[j] + y * s[j];
-                    }
+                const float r = rsqrtf(fmaf(ss, share, a.eps));
+                const Four rr = {pack2(r, r), pack2(r, r)};
+                if (weight) {
+                    x = x * (rr * get4(weight + oa));
+                    y = y * (rr * get4(weight + ob));
+                } else {
+                    x = x * rr;
+                    y = y * rr;
                 }
             }
-            T* out;
-            if (query) {
-                out = qo + h * D;
-            } else if (!a.kc) {
-                out = ko + (h - a.HQ) * D;
-            } else {
-                if (slot < 0) continue;
-                const int hk = value ? h - a.HQ - a.HKV : h - a.HQ;
-                out = static_cast<T*>(value ? a.vc : a.kc) + (slot + (int64_t(hk) << a.log_page)) * D;
+            if (split) {
+                const Four t = x;
+                x = fma4(y, minus, x * co);
+                y = fma4(t, si, y * co);
+            } else if (turned) {  // neighbours: (x0, x1), (x2, x3), (y0, y1), (y2, y3)
+                float p0, p1, p2, p3, p4, p5, p6, p7;
+                unpack2(x.lo, p0, p1);
+                unpack2(x.hi, p2, p3);
+                unpack2(y.lo, p4, p5);
+                unpack2(y.hi, p6, p7);
+                const Four e = {pack2(p0, p2), pack2(p4, p6)}, o = {pack2(p1, p3), pack2(p5, p7)};
+                const Four te = fma4(o, minus, e * co), to = fma4(e, si, o * co);
+                unpack2(te.lo, p0, p2);
+                unpack2(te.hi, p4, p6);
+                unpack2(to.lo, p1, p3);
+                unpack2(to.hi, p5, p7);
+                x = {pack2(p0, p1), pack2(p2, p3)};
+                y = {pack2(p4, p5), pack2(p6, p7)};
             }
-            put4(out + oa, xa[u]);
-            put4(out + ob, xb[u]);
+        };
+        for (int s0 = first; s0 < end; s0 += IT) {
+            if (s0 != first) load(s0);
+#pragma unroll
+            for (int u = 0; u < IT; ++u) {
+                const int s = s0 + u;
+                if (s >= end) continue;
+                if (s < qsets) {
+                    const int h = s * HEADS + sub;
+                    finish(xa[u], xb[u], h < a.HQ, a.qw);
+                    if (h >= a.HQ) continue;
+                    put4(qo + h * D + oa, xa[u]);
+                    put4(qo + h * D + ob, xb[u]);
+                    continue;
+                }
+                const bool value = s >= qsets + ksets;
+                const int h = (value ? s - qsets - ksets : s - qsets) * HEADS + sub;
+                if (!value) finish(xa[u], xb[u], h < a.HKV, a.kw);
+                if (h >= a.HKV || (a.kc && slot < 0)) continue;
+                T* out = !a.kc ? ko + h * D
+                               : static_cast<T*>(value ? a.vc : a.kc) + (slot + (int64_t(h) << a.log_page)) * D;
+                put4(out + oa, xa[u]);
+                put4(out + ob, xb[u]);
+            }
         }
     }
 }
@@ -250,20 +274,22 @@ __global__ void __launch_bounds__(128) prep_kernel(const Args a) {
 template <typename T, int D>
 cudaError_t launch(Args a, cudaStream_t st) {
     constexpr int HEADS = 256 / D;
-    const int sets = (a.HQ + (a.kc ? 2 : 1) * a.HKV + HEADS - 1) / HEADS;
-    // few tokens: a warp to every set of heads; many: as many sets a warp, in fours, as leave four warps to
-    // each place on the SMs, the angles serving them all
+    const int sets = (a.HQ + HEADS - 1) / HEADS + (a.kc ? 2 : 1) * ((a.HKV + HEADS - 1) / HEADS);
+    // few tokens: a warp to every set of heads; many: up to all sets of a token to a warp, which goes from token
+    // to token (what it does once for all tokens and once for a token's sets is as much as ten sets take)
+    constexpr int MOST = 152 * 7;  // resident blocks
     const bool many = int64_t(a.N) * sets > 8 * 152 * 4;
-    a.sets = 1;
+    int chunks = sets;
     if (many) {
-        const int64_t fours = int64_t(a.N) * sets / (4 * 152 * 64);
-        a.sets = int(4 * (fours < 4 ? 1 : fours / 4));
-        if (a.sets > sets) a.sets = (sets + 3) / 4 * 4;
+        chunks = int((2 * 4 * MOST + a.N - 1) / a.N);
+        if (chunks > (sets + 3) / 4) chunks = (sets + 3) / 4;
     }
+    a.sets = (sets + chunks - 1) / chunks;
     a.chunks = (sets + a.sets - 1) / a.sets;
-    const dim3 grid(unsigned((int64_t(a.N) * a.chunks + 3) / 4));
-    if (many) return launch_pdl(prep_kernel<T, D, 4>, grid, dim3(128), 0, st, a);
-    return launch_pdl(prep_kernel<T, D, 1>, grid, dim3(128), 0, st, a);
+    const int64_t blocks = (int64_t(a.N) * a.chunks + 3) / 4;
+    if (many)
+        return launch_pdl(prep_kernel<T, D, 4>, dim3(unsigned(blocks < MOST ? blocks : MOST)), dim3(128), 0, st, a);
+    return launch_pdl(prep_kernel<T, D, 1>, dim3(unsigned(blocks)), dim3(128), 0, st, a);
 }
 
 }  // namespace qkp

@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(NT, 2)
         fence_mbar_init();
     }
     pdl_wait();
+    pdl_trigger();  // after the wait: the next launch may rely on everything before this one
     const int4* seqs = a.seqs;
     const int64_t* line = a.line;
     if (plans) {

@@ -128,168 +128,217 @@ __device__ inline void turn(int position, uint64_t turns, float& c, float& s) {
     if (quarter & 2) s = -s;
 }
 
-// A warp: `sets` of a token's sets of 32 / LANES heads (queries, keys and values have
-// sets of their own, so that a warp does one thing at a time), IT sets at a time.
-template <typename T, int D, int IT>
-__global__ void __launch_bounds__(128, IT == 1 ? 8 : 7) prep_kernel(const Args a) {
-    constexpr int LANES = D / 8, HEADS = 32 / LANES;  // lanes a head, heads of a set
-    pdl_wait();
-    pdl_trigger();
-    const int lane = threadIdx.x & 31, l = lane % LANES, sub = lane / LANES;
-    const bool turned = 8 * l < a.R, split = !a.adjacent && turned;
-    const int oa = split ? 4 * l : 8 * l, ob = split ? oa + a.R / 2 : oa + 4;
-    const int qsets = (a.HQ + HEADS - 1) / HEADS, ksets = (a.HKV + HEADS - 1) / HEADS;
-    uint64_t turns[4] = {};
-    int axis[4] = {};
-    if (turned) {
+// A lane's columns of a head, and what it does to them.
+template <int D>
+struct Lane {
+    static constexpr int LANES = D / 8, HEADS = 32 / LANES;  // lanes a head, heads of a set
+    int sub, l, oa, ob;                                      // which head of a set, which lane of it; two columns
+    bool turned, split;
+    uint64_t turns[4];
+    int axis[4];
+    Four co, si, minus;  // cosines, sines and their negatives of the lane's pairs
+
+    __device__ explicit Lane(const Args& a) {
+        const int lane = threadIdx.x & 31;
+        l = lane % LANES;
+        sub = lane / LANES;
+        turned = 8 * l < a.R;
+        split = !a.adjacent && turned;
+        oa = split ? 4 * l : 8 * l;
+        ob = split ? oa + a.R / 2 : oa + 4;
+        if (turned)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            turns[j] = turns_of(a.freqs[4 * l + j]);
-            axis[j] = a.axis ? min(max(a.axis[4 * l + j], 0), a.axes - 1) : 0;
+            for (int j = 0; j < 4; ++j) {
+                turns[j] = turns_of(a.freqs[4 * l + j]);
+                axis[j] = a.axis ? min(max(a.axis[4 * l + j], 0), a.axes - 1) : 0;
+            }
+    }
+    // The angles of token n at place `at` of its stream.
+    __device__ void token(const Args& a, int n, int at) {
+        if (!turned) return;
+        float c[4], s[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            turn(a.positions ? a.positions[int64_t(axis[j]) * a.N + n] : at, turns[j], c[j], s[j]);
+        co = {pack2(c[0], c[1]), pack2(c[2], c[3])};
+        si = {pack2(s[0], s[1]), pack2(s[2], s[3])};
+        minus = {pack2(-s[0], -s[1]), pack2(-s[2], -s[3])};
+    }
+    // Norm and rotation of a head's columns; wx, wy the weights.  (A lane without a head takes part in the sum of none.)
+    __device__ void finish(const Args& a, Four& x, Four& y, const Four& wx, const Four& wy) const {
+        if (a.norm != CANOPY_NORM_NONE) {
+            float ss = sum4(fma4(x, x, y * y));
+#pragma unroll
+            for (int m = LANES / 2; m; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+            const float r = rsqrtf(fmaf(ss, a.norm == CANOPY_NORM_RMS ? 1.f / D : 1.f, a.eps));
+            const Four rr = {pack2(r, r), pack2(r, r)};
+            x = x * (rr * wx);
+            y = y * (rr * wy);
+        }
+        if (split) {
+            const Four t = x;
+            x = fma4(y, minus, x * co);
+            y = fma4(t, si, y * co);
+        } else if (turned) {  // neighbours: (x0, x1), (x2, x3), (y0, y1), (y2, y3)
+            float p0, p1, p2, p3, p4, p5, p6, p7;
+            unpack2(x.lo, p0, p1);
+            unpack2(x.hi, p2, p3);
+            unpack2(y.lo, p4, p5);
+            unpack2(y.hi, p6, p7);
+            const Four e = {pack2(p0, p2), pack2(p4, p6)}, o = {pack2(p1, p3), pack2(p5, p7)};
+            const Four te = fma4(o, minus, e * co), to = fma4(e, si, o * co);
+            unpack2(te.lo, p0, p2);
+            unpack2(te.hi, p4, p6);
+            unpack2(to.lo, p1, p3);
+            unpack2(to.hi, p5, p7);
+            x = {pack2(p0, p1), pack2(p2, p3)};
+            y = {pack2(p4, p5), pack2(p6, p7)};
         }
     }
+    __device__ void weights(const float* w, Four& wx, Four& wy) const {
+        const uint64_t one = pack2(1.f, 1.f);
+        wx = w ? get4(w + oa) : Four{one, one};
+        wy = w ? get4(w + ob) : Four{one, one};
+    }
+};
+
+// Where token n goes: whether it is there at all, its place in its stream (n without a cache), and its row in the
+// pages without the head (-1: none).  For a whole warp.
+__device__ inline bool place_of(const Args& a, int n, int& at, int64_t& slot) {
+    at = n;
+    slot = -1;
+    if (!a.context) return true;
+    int bad = 0, i = 0;
+    const int b = sequence_of(a, n, i, &bad);
+    if (b >= 0) {
+        int ctx = a.context[b];
+        if (ctx < 0) {
+            bad |= CANOPY_DEVERR_LENGTH;
+            ctx = 0;
+        }
+        const int64_t pos = int64_t(ctx) + i;
+        at = int(pos < 0x7FFFFFFF ? pos : 0x7FFFFFFF);
+        const int64_t entry = pos >> a.log_page;
+        const int page = entry < a.max_pages ? a.table[int64_t(b) * a.max_pages + entry] : -1;
+        if (page < 0 || page >= a.pages)
+            bad |= CANOPY_DEVERR_PAGE;
+        else
+            slot = ((int64_t(page) * a.HKV) << a.log_page) + (pos & ((1 << a.log_page) - 1));
+    }
+    if (bad && (threadIdx.x & 31) == 0 && a.err) raise_err(a.err, bad);
+    return b >= 0;
+}
+
+// Few tokens: a warp to every set of heads (queries, keys and values have sets of their own), whose columns are on
+// their way while the token's place is looked up.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) prep_few_kernel(const Args a) {
+    pdl_wait();
+    pdl_trigger();
+    using L = Lane<D>;
+    const uint32_t w = blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (w >= uint32_t(a.N) * a.sets) return;
+    const int n = int(w / a.sets), s = int(w % a.sets);
+    const int qsets = (a.HQ + L::HEADS - 1) / L::HEADS, ksets = (a.HKV + L::HEADS - 1) / L::HEADS;
+    const bool query = s < qsets, value = s >= qsets + ksets;
+    L lane(a);
+    const int h = (query ? s : value ? s - qsets - ksets : s - qsets) * L::HEADS + lane.sub;
+    const bool there = h < (query ? a.HQ : a.HKV);
+    const T* in = query ? static_cast<const T*>(a.q) + n * a.ldq
+                        : value ? static_cast<const T*>(a.v) + n * a.ldv : static_cast<const T*>(a.k) + n * a.ldk;
+    Four x = {0, 0}, y = {0, 0}, wx, wy;
+    if (there) {
+        x = get4(in + h * D + lane.oa);
+        y = get4(in + h * D + lane.ob);
+    }
+    lane.weights(query ? a.qw : a.kw, wx, wy);
+    int at;
+    int64_t slot;
+    if (!place_of(a, n, at, slot)) return;
+    if (!value) {
+        lane.token(a, n, at);
+        lane.finish(a, x, y, wx, wy);
+    }
+    if (!there || (!query && a.kc && slot < 0)) return;
+    T* out = query ? static_cast<T*>(a.qo) + (int64_t(n) * a.HQ + h) * D
+                   : !a.kc ? static_cast<T*>(a.ko) + (int64_t(n) * a.HKV + h) * D
+                           : static_cast<T*>(value ? a.vc : a.kc) + (slot + (int64_t(h) << a.log_page)) * D;
+    put4(out + lane.oa, x);
+    put4(out + lane.ob, y);
+}
+
+// Many tokens: a warp goes from token to token, four sets of heads at a time at constant distances (the addresses
+// of one set at a time took half of all instructions).  `chunks` warps share a token, each kind's sets between them.
+template <typename T, int D>
+__global__ void __launch_bounds__(128, 5) prep_many_kernel(const Args a) {
+    pdl_wait();
+    pdl_trigger();
+    using L = Lane<D>;
+    constexpr int IT = 4, STEP = L::HEADS * D;
+    L lane(a);
+    // `heads` rows from in to out, those out_step apart per set
+    auto run = [&](const T* in, T* out, int64_t out_step, int heads, int chunk, const float* weight, bool plain) {
+        const int sets = (heads + L::HEADS - 1) / L::HEADS, each = (sets + a.chunks - 1) / a.chunks;
+        int s = chunk * each;
+        const int end = min(sets, s + each);
+        in += s * STEP + lane.sub * D;
+        out += s * out_step;
+        Four wx, wy;
+        lane.weights(weight, wx, wy);
+        for (; s < end; s += IT, in += IT * STEP, out += IT * out_step) {
+            const int left = (heads - s * L::HEADS - lane.sub + L::HEADS - 1) / L::HEADS;  // sets in which this lane has a head
+            const int many = min(IT, end - s);
+            Four x[IT], y[IT];
+#pragma unroll
+            for (int u = 0; u < IT; ++u) {
+                x[u] = y[u] = {0, 0};
+                if (u < many && u < left) {
+                    x[u] = get4(in + u * STEP + lane.oa);
+                    y[u] = get4(in + u * STEP + lane.ob);
+                }
+            }
+            T* to = out;
+#pragma unroll
+            for (int u = 0; u < IT; ++u, to += out_step) {
+                if (u >= many) break;
+                if (!plain) lane.finish(a, x[u], y[u], wx, wy);
+                if (u < left) {
+                    put4(to + lane.oa, x[u]);
+                    put4(to + lane.ob, y[u]);
+                }
+            }
+        }
+    };
     for (uint32_t w = blockIdx.x * 4 + (threadIdx.x >> 5); w < uint32_t(a.N) * a.chunks; w += 4 * gridDim.x) {
         const int n = int(w / a.chunks), chunk = int(w % a.chunks);
-        const int first = chunk * a.sets, end = min(qsets + (a.kc ? 2 : 1) * ksets, first + a.sets);
-        const T *q = static_cast<const T*>(a.q) + n * a.ldq, *k = static_cast<const T*>(a.k) + n * a.ldk,
-                *v = static_cast<const T*>(a.v) + n * a.ldv;
-        Four xa[IT], xb[IT];
-        auto load = [&](int s0) {
-#pragma unroll
-            for (int u = 0; u < IT; ++u) {
-                const int s = s0 + u;
-                if (s >= end) continue;
-                const bool query = s < qsets;
-                const int h = (query ? s : s < qsets + ksets ? s - qsets : s - qsets - ksets) * HEADS + sub;
-                const T* x = (query ? q : s < qsets + ksets ? k : v) + h * D;
-                if (h >= (query ? a.HQ : a.HKV)) continue;
-                xa[u] = get4(x + oa);
-                xb[u] = get4(x + ob);
-            }
-        };
-        load(first);  // ahead of the places' lookups
-
-        int bad = 0, i = 0, b = -1;
-        bool here = true;
-        if (a.context) {
-            b = sequence_of(a, n, i, &bad);
-            here = b >= 0;
-        }
-        int64_t slot = -1;  // the token's row in the pages, without the head
-        int at = n;
-        if (b >= 0) {
-            int ctx = a.context[b];
-            if (ctx < 0) {
-                bad |= CANOPY_DEVERR_LENGTH;
-                ctx = 0;
-            }
-            const int64_t pos = int64_t(ctx) + i;
-            at = int(pos < 0x7FFFFFFF ? pos : 0x7FFFFFFF);
-            const int64_t entry = pos >> a.log_page;
-            const int page = entry < a.max_pages ? a.table[int64_t(b) * a.max_pages + entry] : -1;
-            if (page < 0 || page >= a.pages)
-                bad |= CANOPY_DEVERR_PAGE;
-            else
-                slot = ((int64_t(page) * a.HKV) << a.log_page) + (pos & ((1 << a.log_page) - 1));
-        }
-        if (bad && lane == 0 && a.err) raise_err(a.err, bad);
-        if (!here) continue;
-
-        Four co = {0, 0}, si = {0, 0}, minus = {0, 0};  // cosines, sines and their negatives of this lane's pairs
-        if (turned && first < qsets + ksets) {
-            float c[4], s[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                turn(a.positions ? a.positions[int64_t(axis[j]) * a.N + n] : at, turns[j], c[j], s[j]);
-            co = {pack2(c[0], c[1]), pack2(c[2], c[3])};
-            si = {pack2(s[0], s[1]), pack2(s[2], s[3])};
-            minus = {pack2(-s[0], -s[1]), pack2(-s[2], -s[3])};
-        }
-        const float share = a.norm == CANOPY_NORM_RMS ? 1.f / D : 1.f;
-        T* qo = static_cast<T*>(a.qo) + int64_t(n) * a.HQ * D;
-        T* ko = a.kc ? nullptr : static_cast<T*>(a.ko) + int64_t(n) * a.HKV * D;
-        // norm and rotation; `weight` this head's, or null
-        auto finish = [&](Four& x, Four& y, bool there, const float* weight) {
-            if (a.norm != CANOPY_NORM_NONE) {
-                float ss = there ? sum4(fma4(x, x, y * y)) : 0.f;
-#pragma unroll
-                for (int m = LANES / 2; m; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-                const float r = rsqrtf(fmaf(ss, share, a.eps));
-                const Four rr = {pack2(r, r), pack2(r, r)};
-                if (weight) {
-                    x = x * (rr * get4(weight + oa));
-                    y = y * (rr * get4(weight + ob));
-                } else {
-                    x = x * rr;
-                    y = y * rr;
-                }
-            }
-            if (split) {
-                const Four t = x;
-                x = fma4(y, minus, x * co);
-                y = fma4(t, si, y * co);
-            } else if (turned) {  // neighbours: (x0, x1), (x2, x3), (y0, y1), (y2, y3)
-                float p0, p1, p2, p3, p4, p5, p6, p7;
-                unpack2(x.lo, p0, p1);
-                unpack2(x.hi, p2, p3);
-                unpack2(y.lo, p4, p5);
-                unpack2(y.hi, p6, p7);
-                const Four e = {pack2(p0, p2), pack2(p4, p6)}, o = {pack2(p1, p3), pack2(p5, p7)};
-                const Four te = fma4(o, minus, e * co), to = fma4(e, si, o * co);
-                unpack2(te.lo, p0, p2);
-                unpack2(te.hi, p4, p6);
-                unpack2(to.lo, p1, p3);
-                unpack2(to.hi, p5, p7);
-                x = {pack2(p0, p1), pack2(p2, p3)};
-                y = {pack2(p4, p5), pack2(p6, p7)};
-            }
-        };
-        for (int s0 = first; s0 < end; s0 += IT) {
-            if (s0 != first) load(s0);
-#pragma unroll
-            for (int u = 0; u < IT; ++u) {
-                const int s = s0 + u;
-                if (s >= end) continue;
-                if (s < qsets) {
-                    const int h = s * HEADS + sub;
-                    finish(xa[u], xb[u], h < a.HQ, a.qw);
-                    if (h >= a.HQ) continue;
-                    put4(qo + h * D + oa, xa[u]);
-                    put4(qo + h * D + ob, xb[u]);
-                    continue;
-                }
-                const bool value = s >= qsets + ksets;
-                const int h = (value ? s - qsets - ksets : s - qsets) * HEADS + sub;
-                if (!value) finish(xa[u], xb[u], h < a.HKV, a.kw);
-                if (h >= a.HKV || (a.kc && slot < 0)) continue;
-                T* out = !a.kc ? ko + h * D
-                               : static_cast<T*>(value ? a.vc : a.kc) + (slot + (int64_t(h) << a.log_page)) * D;
-                put4(out + oa, xa[u]);
-                put4(out + ob, xb[u]);
-            }
+        int at;
+        int64_t slot;
+        if (!place_of(a, n, at, slot)) continue;
+        lane.token(a, n, at);
+        run(static_cast<const T*>(a.q) + n * a.ldq, static_cast<T*>(a.qo) + (int64_t(n) * a.HQ + lane.sub) * D, STEP,
+            a.HQ, chunk, a.qw, false);
+        if (!a.kc) {
+            run(static_cast<const T*>(a.k) + n * a.ldk, static_cast<T*>(a.ko) + (int64_t(n) * a.HKV + lane.sub) * D,
+                STEP, a.HKV, chunk, a.kw, false);
+        } else if (slot >= 0) {
+            const int64_t row = (slot + (int64_t(lane.sub) << a.log_page)) * D, step = int64_t(STEP) << a.log_page;
+            run(static_cast<const T*>(a.k) + n * a.ldk, static_cast<T*>(a.kc) + row, step, a.HKV, chunk, a.kw, false);
+            run(static_cast<const T*>(a.v) + n * a.ldv, static_cast<T*>(a.vc) + row, step, a.HKV, chunk, nullptr, true);
         }
     }
 }
 
 template <typename T, int D>
 cudaError_t launch(Args a, cudaStream_t st) {
-    constexpr int HEADS = 256 / D;
-    const int sets = (a.HQ + HEADS - 1) / HEADS + (a.kc ? 2 : 1) * ((a.HKV + HEADS - 1) / HEADS);
-    // few tokens: a warp to every set of heads; many: up to all sets of a token to a warp, which goes from token
-    // to token (what it does once for all tokens and once for a token's sets is as much as ten sets take)
-    constexpr int MOST = 152 * 7;  // resident blocks
-    const bool many = int64_t(a.N) * sets > 8 * 152 * 4;
-    int chunks = sets;
-    if (many) {
-        chunks = int((2 * 4 * MOST + a.N - 1) / a.N);
-        if (chunks > (sets + 3) / 4) chunks = (sets + 3) / 4;
-    }
-    a.sets = (sets + chunks - 1) / chunks;
-    a.chunks = (sets + a.sets - 1) / a.sets;
+    constexpr int HEADS = 256 / D, MOST = 152 * 5;  // resident blocks
+    a.sets = (a.HQ + HEADS - 1) / HEADS + (a.kc ? 2 : 1) * ((a.HKV + HEADS - 1) / HEADS);
+    const int64_t warps = int64_t(a.N) * a.sets;
+    if (warps <= 8 * 152 * 4)
+        return launch_pdl(prep_few_kernel<T, D>, dim3(unsigned((warps + 3) / 4)), dim3(128), 0, st, a);
+    // as many warps to a token as leave none of the resident ones idle
+    a.chunks = (4 * MOST + a.N - 1) / a.N;
     const int64_t blocks = (int64_t(a.N) * a.chunks + 3) / 4;
-    if (many)
-        return launch_pdl(prep_kernel<T, D, 4>, dim3(unsigned(blocks < MOST ? blocks : MOST)), dim3(128), 0, st, a);
-    return launch_pdl(prep_kernel<T, D, 1>, dim3(unsigned(blocks)), dim3(128), 0, st, a);
+    return launch_pdl(prep_many_kernel<T, D>, dim3(unsigned(blocks < MOST ? blocks : MOST)), dim3(128), 0, st, a);
 }
 
 }  // namespace qkp

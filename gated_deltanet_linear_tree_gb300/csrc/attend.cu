@@ -5,6 +5,8 @@
 // scale log2(e) q_i.k_j over the keys that i sees, m_i the running maximum.
 #include "attend.cuh"
 
+#include <type_traits>
+
 namespace canopy {
 namespace att {
 
@@ -58,9 +60,10 @@ __global__ void __launch_bounds__(256) plan_kernel(const Args a) {
 }
 
 // ---------------------------------------------------------------------------
-// CUDA cores.  256 threads on R rows x 64 keys: thread (ty, tx) forms the
+// fp32 on CUDA cores.  256 threads on R rows x 64 keys: thread (ty, tx) forms the
 // scores of R / 16 rows with keys tx + 16 j, and D / 16 columns of those rows'
-// outputs; a row's statistics stay with its 16 threads.
+// outputs; a row's statistics stay with its 16 threads.  Rows and keys come by
+// asynchronous copies, the next unit's while one is worked on.
 namespace simt {
 
 constexpr int KT = 64, NT = 256;
@@ -68,44 +71,61 @@ constexpr int KT = 64, NT = 256;
 template <int D, int R>
 struct Smem {
     static constexpr int LD = D + 4, LP = KT + 4;  // float4 reads of neighbouring rows on other banks
-    float q[R * LD], k[KT * LD], v[KT * LD], p[R * LP];
+    float q[R * LD], kv[2][2][KT * LD], p[R * LP];
 };
 
-template <typename InT>
-__device__ inline float4 load_row4(const void* cache, const Args& a, const Tile& tile, int h, int D, int key, int c,
-                                   int& bad) {
-    if (!in_reach(tile, key)) return make_float4(0.f, 0.f, 0.f, 0.f);
-    const int page = a.table[size_t(tile.b) * a.max_pages + (key >> a.log_page)];
-    if (page < 0 || page >= a.pages) {
-        bad = CANOPY_DEVERR_PAGE;
-        return make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    const size_t row = ((size_t(page) * a.HKV + h) << a.log_page) + (key & ((1 << a.log_page) - 1));
-    return load4(static_cast<const InT*>(cache) + row * D + c);
+// 16 bytes to shared memory, or zeros (src is not read then).
+__device__ inline void copy16(float* dst, const float* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0)
+                 : "memory");
+}
+__device__ inline void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ inline void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <typename InT, int D, int R>
+template <int D, int R>
 __global__ void __launch_bounds__(NT) attend_kernel(const Args a) {
     constexpr int RR = R / 16, C4 = D / 64, LD = Smem<D, R>::LD, LP = Smem<D, R>::LP;
     extern __shared__ __align__(16) uint8_t raw[];
     Smem<D, R>& sm = *reinterpret_cast<Smem<D, R>*>(raw);
     pdl_wait();
+    pdl_trigger();  // after the wait: the next launch may rely on everything before this one
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    const float *q = static_cast<const float*>(a.q), *kc = static_cast<const float*>(a.kc),
+                *vc = static_cast<const float*>(a.vc);
     Walk walk(a, a.seqs, a.line, blockIdx.x, a.first_tile);
     int bad = 0;
     Piece p;
     while (walk.next(a, p)) {
         const Tile& tile = p.tile;
         const int rows = tile.ntok * a.g;
+        auto stage = [&](int u) {
+            float *k = sm.kv[(u - p.u0) & 1][0], *v = sm.kv[(u - p.u0) & 1][1];
+            for (int e = tid; e < KT * (D / 4); e += NT) {
+                const int j = e / (D / 4), c = 4 * (e % (D / 4)), key = key_tile(tile, u) * KT + j;
+                size_t from = 0;
+                bool there = in_reach(tile, key);
+                if (there) {
+                    const int page = a.table[size_t(tile.b) * a.max_pages + (key >> a.log_page)];
+                    there = page >= 0 && page < a.pages;
+                    if (there)
+                        from = (((size_t(page) * a.HKV + p.h) << a.log_page) + (key & ((1 << a.log_page) - 1))) * D + c;
+                    else
+                        bad = CANOPY_DEVERR_PAGE;
+                }
+                copy16(k + j * LD + c, kc + from, there);
+                copy16(v + j * LD + c, vc + from, there);
+            }
+        };
         __syncthreads();
         for (int e = tid; e < R * (D / 4); e += NT) {
-            const int r = e / (D / 4), c = 4 * (e % (D / 4));
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < rows)
-                x = load4(static_cast<const InT*>(a.q) +
-                          (size_t(tile.row + r / a.g) * a.HQ + p.h * a.g + r % a.g) * D + c);
-            *reinterpret_cast<float4*>(sm.q + r * LD + c) = x;
+            const int r = e / (D / 4), c = 4 * (e % (D / 4)), i = min(r, rows - 1);
+            copy16(sm.q + r * LD + c, q + (size_t(tile.row + i / a.g) * a.HQ + p.h * a.g + i % a.g) * D + c, r < rows);
         }
+        stage(p.u0);
+        copies_end();
         float m[RR], l[RR];
         float4 o[RR][C4];
         int depth[RR];
@@ -121,20 +141,19 @@ __global__ void __launch_bounds__(NT) attend_kernel(const Args a) {
             mask[r] = a.parent ? a.mask + size_t(tile.row + i) * kMaskWords : nullptr;
         }
         for (int u = p.u0; u < p.u1; ++u) {
-            const int kt = key_tile(tile, u), key0 = kt * KT;
+            if (u + 1 < p.u1) stage(u + 1);
+            copies_end();
+            copies_wait<1>();
             __syncthreads();
-            for (int e = tid; e < KT * (D / 4); e += NT) {
-                const int j = e / (D / 4), c = 4 * (e % (D / 4));
-                *reinterpret_cast<float4*>(sm.k + j * LD + c) = load_row4<InT>(a.kc, a, tile, p.h, D, key0 + j, c, bad);
-                *reinterpret_cast<float4*>(sm.v + j * LD + c) = load_row4<InT>(a.vc, a, tile, p.h, D, key0 + j, c, bad);
-            }
-            __syncthreads();
+            const float *k = sm.kv[(u - p.u0) & 1][0], *v = sm.kv[(u - p.u0) & 1][1];
+            const int kt = key_tile(tile, u);
+            const bool all = all_see(tile, kt);
             float s[RR][4] = {};
 #pragma unroll 4
             for (int c = 0; c < D; c += 4) {
                 float4 k4[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) k4[j] = *reinterpret_cast<const float4*>(sm.k + (tx + 16 * j) * LD + c);
+                for (int j = 0; j < 4; ++j) k4[j] = *reinterpret_cast<const float4*>(k + (tx + 16 * j) * LD + c);
 #pragma unroll
                 for (int r = 0; r < RR; ++r) {
                     const float4 x = *reinterpret_cast<const float4*>(sm.q + (ty * RR + r) * LD + c);
@@ -143,14 +162,18 @@ __global__ void __launch_bounds__(NT) attend_kernel(const Args a) {
                         s[r][j] += x.x * k4[j].x + x.y * k4[j].y + x.z * k4[j].z + x.w * k4[j].w;
                 }
             }
-            const bool all = all_see(tile, kt);
 #pragma unroll
             for (int r = 0; r < RR; ++r) {
                 float top = -INFINITY;
+                uint32_t seen[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+                if (!all) {
+                    seen[0] = seen_bits(a, tile, depth[r], mask[r], kt * KT);
+                    seen[1] = seen_bits(a, tile, depth[r], mask[r], kt * KT + 32);
+                }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     s[r][j] *= a.scale2;
-                    if (!all && !sees(a, tile, depth[r], mask[r], key0 + tx + 16 * j)) s[r][j] = -INFINITY;
+                    if (!((seen[j >> 1] >> (tx + 16 * (j & 1))) & 1u)) s[r][j] = -INFINITY;
                     top = fmaxf(top, s[r][j]);
                 }
 #pragma unroll
@@ -174,40 +197,54 @@ __global__ void __launch_bounds__(NT) attend_kernel(const Args a) {
                 }
             }
             __syncwarp();  // a row's weights are written and read by one half warp
-            for (int j = 0; j < KT; ++j) {
-                float4 v4[C4];
+            auto sums = [&](auto masked_type) {
+                constexpr bool masked = decltype(masked_type)::value;
+                // (what a row does not see does not reach it, whatever it holds)
+                auto add = [](float& x, float w, float y) { x = masked && w == 0.f ? x : fmaf(w, y, x); };
+#pragma unroll 2
+                for (int j = 0; j < KT; j += 4) {
+                    float4 v4[4][C4];
 #pragma unroll
-                for (int c = 0; c < C4; ++c)
-                    v4[c] = *reinterpret_cast<const float4*>(sm.v + j * LD + 4 * tx + 64 * c);
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int r = 0; r < RR; ++r) {
-                    const float w = sm.p[(ty * RR + r) * LP + j];
-                    if (!all && w == 0.f) continue;  // what a row does not see does not reach it, whatever it holds
+                        for (int c = 0; c < C4; ++c)
+                            v4[i][c] = *reinterpret_cast<const float4*>(v + (j + i) * LD + 4 * tx + 64 * c);
 #pragma unroll
-                    for (int c = 0; c < C4; ++c) {
-                        o[r][c].x += w * v4[c].x;
-                        o[r][c].y += w * v4[c].y;
-                        o[r][c].z += w * v4[c].z;
-                        o[r][c].w += w * v4[c].w;
+                    for (int r = 0; r < RR; ++r) {
+                        const float4 w4 = *reinterpret_cast<const float4*>(sm.p + (ty * RR + r) * LP + j);
+                        const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int c = 0; c < C4; ++c) {
+                                add(o[r][c].x, w[i], v4[i][c].x);
+                                add(o[r][c].y, w[i], v4[i][c].y);
+                                add(o[r][c].z, w[i], v4[i][c].z);
+                                add(o[r][c].w, w[i], v4[i][c].w);
+                            }
                     }
                 }
-            }
+            };
+            if (all) sums(std::false_type());
+            else sums(std::true_type());
+            __syncthreads();
         }
 #pragma unroll
         for (int r = 0; r < RR; ++r)
 #pragma unroll
             for (int x = 8; x; x >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], x);
         if (!p.whole) {  // a slot: [rows][D], then the rows' m and l
-            float* out = a.part + size_t(p.slot) * a.slot_rows * (D + 2);
+            float* out = a.part + size_t(p.slot) * R * (D + 2);
 #pragma unroll
             for (int r = 0; r < RR; ++r) {
                 const int row = ty * RR + r;
+                if (row >= rows) continue;
 #pragma unroll
                 for (int c = 0; c < C4; ++c)
                     *reinterpret_cast<float4*>(out + row * D + 4 * tx + 64 * c) = o[r][c];
                 if (tx == 0) {
-                    out[a.slot_rows * D + row] = m[r];
-                    out[a.slot_rows * D + a.slot_rows + row] = l[r];
+                    out[R * D + row] = m[r];
+                    out[R * D + R + row] = l[r];
                 }
             }
             continue;
@@ -217,23 +254,20 @@ __global__ void __launch_bounds__(NT) attend_kernel(const Args a) {
             const int row = ty * RR + r;
             if (row >= rows) continue;
             const float f = l[r] == 0.f ? 0.f : 1.f / l[r];
-            InT* out = static_cast<InT*>(a.o) + (size_t(tile.row + row / a.g) * a.HQ + p.h * a.g + row % a.g) * D;
+            float* out = static_cast<float*>(a.o) + (size_t(tile.row + row / a.g) * a.HQ + p.h * a.g + row % a.g) * D;
 #pragma unroll
-            for (int c = 0; c < C4; ++c) {
-                store_out(out + 4 * tx + 64 * c, o[r][c].x * f);
-                store_out(out + 4 * tx + 64 * c + 1, o[r][c].y * f);
-                store_out(out + 4 * tx + 64 * c + 2, o[r][c].z * f);
-                store_out(out + 4 * tx + 64 * c + 3, o[r][c].w * f);
-            }
+            for (int c = 0; c < C4; ++c)
+                *reinterpret_cast<float4*>(out + 4 * tx + 64 * c) =
+                    make_float4(o[r][c].x * f, o[r][c].y * f, o[r][c].z * f, o[r][c].w * f);
         }
     }
     if (bad) raise_err(a.err, bad);
 }
 
-template <typename InT, int D, int R>
+template <int D, int R>
 cudaError_t launch(const Args& a, cudaStream_t st) {
     static OncePerDevice once;
-    const auto kernel = attend_kernel<InT, D, R>;
+    const auto kernel = attend_kernel<D, R>;
     cudaError_t e = once([&] { return allow_smem(kernel, int(sizeof(Smem<D, R>))); });
     if (e != cudaSuccess) return e;
     return launch_pdl(kernel, dim3(a.ctas), dim3(NT), sizeof(Smem<D, R>), st, a);
@@ -363,8 +397,9 @@ Layout layout(int N, int B, int g, int d) {
     w.first_tile = o; o = ws_align(o + (kFewCtas + 1) * 8);
     w.mask = o;       o = ws_align(o + size_t(N) * kMaskWords * 4);
     w.depth = o;      o = ws_align(o + size_t(N) * 4);
-    const size_t most = size_t(2) * kSMs * slot_rows(N, g), few = size_t(2) * kFewCtas * 16;
-    w.part = o;       o = ws_align(o + (most > few ? most : few) * (d + 2) * 4);
+    const int rows = slot_rows(N, g);
+    const size_t tiles = size_t(2) * kSMs * rows, fewer = size_t(2) * kFewCtas * (rows < 64 ? 16 : 64);
+    w.part = o;       o = ws_align(o + (tiles > fewer ? tiles : fewer) * (d + 2) * 4);
     w.end = o;
     return w;
 }
@@ -414,9 +449,9 @@ cudaError_t launch_attend(const void* q, int bf16, const void* kc, const void* v
     const int R = a.g <= 16 && int64_t(N) * a.g <= int64_t(16) * B ? 16 : 64;  // rows of a tile, where not on 256
     a.rt = tiles ? tc_tile_tokens(a.g) : R / a.g;
     a.kt = tiles ? tc_tile_keys(d) : 64;
-    a.ctas = few ? kFewCtas : kSMs;
-    a.least = kLeast;
-    a.slot_rows = few ? 16 : slot_rows(N, a.g);
+    a.ctas = tiles ? kSMs : kFewCtas;
+    a.least = bf16 ? kLeast : 1;  // (a unit takes the CUDA cores 3 us)
+    a.slot_rows = few ? 16 : tiles ? slot_rows(N, a.g) : R;
     const Layout w = layout(N, B, a.g, d);
     char* p = static_cast<char*>(workspace);
     a.err = reinterpret_cast<int32_t*>(p);
@@ -435,10 +470,10 @@ cudaError_t launch_attend(const void* q, int bf16, const void* kc, const void* v
         return e != cudaSuccess ? e : launch_join_bf16(a, d, st);
     }
     if (d == 128) {
-        e = R == 16 ? simt::launch<float, 128, 16>(a, st) : simt::launch<float, 128, 64>(a, st);
+        e = R == 16 ? simt::launch<128, 16>(a, st) : simt::launch<128, 64>(a, st);
         return e != cudaSuccess ? e : launch_join_rows<float, 128>(a, st);
     }
-    e = R == 16 ? simt::launch<float, 64, 16>(a, st) : simt::launch<float, 64, 64>(a, st);
+    e = R == 16 ? simt::launch<64, 16>(a, st) : simt::launch<64, 64>(a, st);
     return e != cudaSuccess ? e : launch_join_rows<float, 64>(a, st);
 }
 

@@ -274,6 +274,10 @@ __device__ inline int slot_of(int first, int i) { return 2 * (first + i) + (i ==
 // ---------------------------------------------------------------------------
 // What the two kernels on the tensor cores share.
 
+__device__ inline void prefetch_map(const CUtensorMap* m) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+
 constexpr float kGrow = 8.f;  // a row's maximum is kept until it grows by this, in powers of two
 
 __device__ inline float exp2_approx(float x) {

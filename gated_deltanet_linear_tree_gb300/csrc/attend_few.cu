@@ -74,6 +74,10 @@ __global__ void __launch_bounds__(NT, 2)
     extern __shared__ uint8_t raw[];
     Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw + ((1024 - (smem_u32(raw) & 1023)) & 1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 64) {
+        prefetch_map(&mapK);
+        prefetch_map(&mapV);
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(sm.full + i, 1);

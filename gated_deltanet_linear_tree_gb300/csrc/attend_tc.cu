@@ -88,6 +88,11 @@ __global__ void __launch_bounds__(NT, 1)
         tmem_alloc(tmem_slot, kCols);
         tmem_relinquish();
     }
+    if (warp == 9 && lane == 0) {
+        prefetch_map(&mapQ);
+        prefetch_map(&mapK);
+        prefetch_map(&mapV);
+    }
     if (warp == 10 && lane == 0) {
         mbar_init(q_full, 1);
         mbar_init(q_read, 2);

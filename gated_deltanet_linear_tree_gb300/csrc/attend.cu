@@ -309,20 +309,33 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) join_rows_kernel(const A
         }
     }
     float m = -INFINITY, l = 0.f, o[C] = {};
-    if (cut) {
+    if (cut) {  // (the same for a whole warp)
         const size_t size = size_t(a.slot_rows) * (D + 2);
         const float* stat = a.part + a.slot_rows * D + r;
-        for (int i = w; i < pieces; i += W) m = fmaxf(m, stat[slot_of(first, i) * size]);
-        const float from = m == -INFINITY ? 0.f : m;
-#pragma unroll 8
-        for (int i = w; i < pieces; i += W) {
-            const size_t slot = slot_of(first, i) * size;
-            const float f = exp2f(stat[slot] - from);
-            l += f * stat[slot + a.slot_rows];
-            const float* in = a.part + slot + r * D + C * lane;
+        for (int base = w; base < pieces; base += 32 * W) {  // a lane reads a piece's statistics
+            const int mine = base + W * lane, count = min(32, (pieces - base + W - 1) / W);
+            const bool there = mine < pieces;
+            const size_t slot = slot_of(first, there ? mine : base) * size;
+            const float mi = there ? stat[slot] : -INFINITY, li = there ? stat[slot + a.slot_rows] : 0.f;
+            float top = mi;
 #pragma unroll
-            for (int c = 0; c < C; ++c) o[c] += f * in[c];
+            for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            top = fmaxf(top, m);
+            const float from = top == -INFINITY ? 0.f : top, keep = exp2f(m - from), f = exp2f(mi - from);
+            m = top;
+            l = l * keep + f * li;
+#pragma unroll
+            for (int c = 0; c < C; ++c) o[c] *= keep;
+#pragma unroll 8
+            for (int i = 0; i < count; ++i) {
+                const float* in = a.part + slot_of(first, base + W * i) * size + r * D + C * lane;
+                const float fi = __shfl_sync(0xffffffffu, f, i);
+#pragma unroll
+                for (int c = 0; c < C; ++c) o[c] += fi * in[c];
+            }
         }
+#pragma unroll
+        for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
     }
     if (W > 1) {
 #pragma unroll
@@ -354,8 +367,9 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) join_rows_kernel(const A
 
 template <typename OutT, int D>
 cudaError_t launch_join_rows(const Args& a, cudaStream_t st) {
-    // (row tile, key head) items at least; each is cut into about ctas / items pieces
-    const int64_t rows = int64_t(a.N) * a.HQ, items = int64_t(a.B) * a.HKV, each = a.ctas / items;
+    // (row tile, key head) items, about; each is cut into about ctas / items pieces
+    const int64_t rows = int64_t(a.N) * a.HQ, tiles = (a.N + a.rt - 1) / a.rt;
+    const int64_t each = a.ctas / ((tiles > a.B ? tiles : a.B) * a.HKV);
     if (each >= 32) return launch_pdl(join_rows_kernel<OutT, D, 16>, dim3(unsigned(rows)), dim3(512), 0, st, a);
     if (each >= 4) return launch_pdl(join_rows_kernel<OutT, D, 4>, dim3(unsigned(rows)), dim3(128), 0, st, a);
     return launch_pdl(join_rows_kernel<OutT, D, 1>, dim3(unsigned((rows + 3) / 4)), dim3(128), 0, st, a);

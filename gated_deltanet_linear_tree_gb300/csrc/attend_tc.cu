@@ -24,8 +24,8 @@
 // Key tiles come by TMA, one box per page (or 16 keys, where tiles and pages
 // cut each other) and 64 columns, into a ring of stages that K and V tiles take
 // in turns.  A page that no row sees is read at a coordinate outside the cache, as
-// zeros.  Where not every row sees every key of a tile, a warp looks through its
-// V first: what no row sees, and what is not finite, becomes zero (0 times it
+// zeros.  Where not every row sees every key of a tile, the softmax's
+// warps look through its V first: what no row sees, and what is not finite, becomes zero (0 times it
 // would reach every row's sum), and a row that sees a key with such a value is NaN.
 #include "attend.cuh"
 
@@ -54,8 +54,9 @@ struct Shape {
     // barriers: Q full, Q read; per stage full, empty, and V looked through; per half S full, S read, P there (in two
     // parts), O done, and all done
     static constexpr int NBAR = 2 + 3 * STAGES + 12;
-    static constexpr int POISON = BARS + 8 * NBAR;     // [STAGES][4] words: keys with a value that is not finite
-    static constexpr int MISC = POISON + 16 * STAGES;  // tensor memory's address
+    static_assert(STAGES % 2 == 0, "K tiles in even stages, V tiles in odd ones");
+    static constexpr int POISON = (BARS + 8 * NBAR + 15) / 16 * 16;  // [STAGES][8]: keys with a value that is not finite, by the warp
+    static constexpr int MISC = POISON + 32 * STAGES;                // tensor memory's address
     static constexpr int TOTAL = MISC + 16;
 };
 static_assert(Shape<128>::TOTAL + 1024 <= 232448 && Shape<64>::TOTAL + 1024 <= 232448, "shared memory");
@@ -98,8 +99,8 @@ __global__ void __launch_bounds__(NT, 1)
         mbar_init(q_read, 2);
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(full + i, 1);
-            mbar_init(empty + i, 3);  // both halves' products, and the warp that looks through V
-            mbar_init(looked + i, 32);
+            mbar_init(empty + i, 2);  // both halves' products
+            mbar_init(looked + i, 256);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + i, 1);
@@ -126,9 +127,12 @@ __global__ void __launch_bounds__(NT, 1)
     // 200 registers for the softmax's warps, 104 for the others: all of the 64,512 that the block was launched with
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-        if (warp == 10) {
-            // ---- loads ---------------------------------------------------------------------
+        if (warp >= 10) {
+            // ---- loads: Q and K tiles by one warp, V tiles by the other -----------------------
+            // (the issue of a box takes 85 cycles and more, one lane after the other)
+            const bool keys = warp == 10;
             Ring<STAGES> ring;
+            if (!keys) ring.step();  // K tiles are the even stages, V tiles the odd ones
             uint32_t q_phase = 1;  // the first Q needs nothing read
             int q_loads = 0, loads = 0;
             const int box = min(1 << a.log_page, box_keys(D)), boxes = KT / box;  // keys of a box, boxes of a tile
@@ -137,16 +141,18 @@ __global__ void __launch_bounds__(NT, 1)
             while (ok && walk.next(a, p)) {
                 const Tile& tile = p.tile;
                 const bool two = tile.ntok > half_tok;
-                ok = warp_wait(q_read, q_phase);
-                q_phase ^= 1;
-                if (!ok) break;
-                ++q_loads;
-                if (lane == 0) {
-                    mbar_expect_tx(q_full, (two ? 2 : 1) * HALVES * half_tok * a.g * 128);
-                    for (int h = 0; h < (two ? 2 : 1); ++h)
-                        for (int c = 0; c < HALVES; ++c)
-                            tma_load_3d(sm + Sh::Q + h * Sh::QTILE + c * 16384, &mapQ, q_full, 64 * c, p.h * a.g,
-                                        tile.row + h * half_tok);
+                if (keys) {
+                    ok = warp_wait(q_read, q_phase);
+                    q_phase ^= 1;
+                    if (!ok) break;
+                    ++q_loads;
+                    if (lane == 0) {
+                        mbar_expect_tx(q_full, (two ? 2 : 1) * HALVES * half_tok * a.g * 128);
+                        for (int h = 0; h < (two ? 2 : 1); ++h)
+                            for (int c = 0; c < HALVES; ++c)
+                                tma_load_3d(sm + Sh::Q + h * Sh::QTILE + c * 16384, &mapQ, q_full, 64 * c, p.h * a.g,
+                                            tile.row + h * half_tok);
+                    }
                 }
                 for (int u = p.u0; ok && u < p.u1; ++u) {
                     const int key = key_tile(tile, u) * KT + i * box;
@@ -156,30 +162,27 @@ __global__ void __launch_bounds__(NT, 1)
                         if (page < 0 || page >= a.pages) bad = CANOPY_DEVERR_PAGE;
                         else z = page * a.HKV + p.h;
                     }
-                    const int slot = key & ((1 << a.log_page) - 1);
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv) {
-                        ok = ok && warp_wait(empty + ring.at, ring.phase ^ 1);
-                        if (!ok) break;
-                        ++loads;
-                        uint8_t* dst = sm + Sh::KV + ring.at * Sh::TILE;
-                        if (lane == 0) mbar_expect_tx(full + ring.at, Sh::TILE);
-                        __syncwarp();
-                        if (i < boxes)
-                            tma_load_3d(dst + part * (KT * 128) + i * box * 128, kv ? &mapV : &mapK, full + ring.at,
-                                        64 * part, slot, z);
-                        ring.step();
-                    }
+                    ok = warp_wait(empty + ring.at, ring.phase ^ 1);
+                    if (!ok) break;
+                    ++loads;
+                    if (lane == 0) mbar_expect_tx(full + ring.at, Sh::TILE);
+                    __syncwarp();
+                    if (i < boxes)
+                        tma_load_3d(sm + Sh::KV + ring.at * Sh::TILE + part * (KT * 128) + i * box * 128,
+                                    keys ? &mapK : &mapV, full + ring.at, 64 * part, key & ((1 << a.log_page) - 1), z);
+                    ring.step();
+                    ring.step();
                 }
             }
             if (bad) raise_err(a.err, bad);
             // no copy is left in flight, should another warp have given up
             if (q_loads) warp_wait(q_full, (q_loads - 1) & 1);
-            for (int i = min(loads, STAGES); i > 0; --i) {
+            for (int i = min(loads, STAGES / 2); i > 0; --i) {
+                ring.back();
                 ring.back();
                 warp_wait(full + ring.at, ring.phase);
             }
-        } else if (warp < 10) {
+        } else {
             // ---- products: of one half, by one thread ----------------------------------------
             if (lane == 0) {
                 const int h = warp - 8;
@@ -255,52 +258,6 @@ __global__ void __launch_bounds__(NT, 1)
                 mbar_wait(drained + h, 0);
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
-        } else {
-            // ---- looks through V where not every row sees every key ---------------------------
-            // Every stage is waited for and let go, so that this warp neither falls behind the ring nor gets ahead of it.
-            Ring<STAGES> ring, look;
-            while (ok && walk.next(a, p)) {
-                const Tile& tile = p.tile;
-                for (int u = p.u0; ok && u < p.u1; ++u)
-                    for (int kv = 0; kv < 2; ++kv) {
-                        ok = warp_wait(full + ring.at, ring.phase);
-                        if (!ok) break;
-                        const int kt = key_tile(tile, u), key = kt * KT;
-                        if (kv && !all_see(tile, kt)) {
-                            uint4* v = reinterpret_cast<uint4*>(sm + Sh::KV + ring.at * Sh::TILE);
-                            for (int w = 0; w < (KT + 31) / 32; ++w) {  // 32 keys; four a time, eight lanes each
-                                uint32_t bad = 0;
-#pragma unroll
-                                for (int c = 0; c < HALVES; ++c) {
-                                    uint4 x[8];  // read together
-#pragma unroll
-                                    for (int e = 0; e < 8; ++e) {
-                                        const int row = 32 * w + 4 * e + (lane >> 3);
-                                        if (row < KT) x[e] = v[(c * KT + row) * 8 + (lane & 7)];
-                                    }
-#pragma unroll
-                                    for (int e = 0; e < 8; ++e) {
-                                        const int row = 32 * w + 4 * e + (lane >> 3);
-                                        const bool there = in_reach(tile, key + row);
-                                        if (row >= KT || (there && finite_pair(x[e].x) && finite_pair(x[e].y) &&
-                                                          finite_pair(x[e].z) && finite_pair(x[e].w)))
-                                            continue;
-                                        v[(c * KT + row) * 8 + (lane & 7)] = make_uint4(0, 0, 0, 0);
-                                        if (there) bad |= 1u << (row & 31);
-                                    }
-                                }
-                                bad = __reduce_or_sync(0xffffffffu, bad);
-                                if (lane == 0) poison[4 * look.at + w] = bad;
-                            }
-                            fence_proxy_async_smem();
-                            mbar_arrive(looked + look.at);
-                            look.step();
-                        }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(empty + ring.at);
-                        ring.step();
-                    }
-            }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
@@ -308,12 +265,13 @@ __global__ void __launch_bounds__(NT, 1)
         const int h = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16), S = lanes + Sh::COLS * h, P = S + Sh::PCOL,
                        O = lanes + 2 * Sh::COLS + D * h;
-        Ring<STAGES> look;
+        Ring<STAGES> look, ring;
+        ring.step();  // the stage of the unit's V
         Phase scores_ready, added;
         const int tok_in_half = r / a.g, head = r % a.g;
         while (ok && walk.next(a, p)) {
             const Tile& tile = p.tile;
-            const bool mine = h == 0 || tile.ntok > half_tok;  // this half has rows
+            const bool two = tile.ntok > half_tok, mine = h == 0 || two;  // this half has rows
             const int tok = h * half_tok + tok_in_half;
             const bool valid = tok_in_half < half_tok && tok < tile.ntok;
             const int row = tile.row + min(tok, tile.ntok - 1);
@@ -324,8 +282,10 @@ __global__ void __launch_bounds__(NT, 1)
             for (int u = p.u0; u < p.u1; ++u) {
                 const int kt = key_tile(tile, u), key = kt * KT;
                 const bool all = all_see(tile, kt);
-                const Ring<STAGES> v = look;
+                const Ring<STAGES> v = look, stage = ring;
                 if (!all) look.step();
+                ring.step();
+                ring.step();
                 if (!mine) continue;
                 ok = scores_ready.wait(s_full + h);
                 if (!ok) break;
@@ -345,11 +305,36 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
                     for (int j = 0; j < KT; ++j)
                         if (!((seen[j >> 5] >> (j & 31)) & 1u)) s[j] = 0xFF800000u;
+                    // this warp's eighth of V (of one half's four warps two)
+                    ok = warp_wait(full + stage.at, stage.phase);
+                    if (!ok) break;
+                    constexpr int ROWS = KT / 8, CHUNKS = ROWS * HALVES * 8 / 32;  // keys, 16 bytes a lane
+                    uint32_t* found = poison + 8 * v.at;
+                    for (int w = warp; w < 8; w += two ? 8 : 4) {
+                        uint4* tile_v = reinterpret_cast<uint4*>(sm + Sh::KV + stage.at * Sh::TILE);
+                        uint32_t bad = 0;
+#pragma unroll
+                        for (int e = 0; e < CHUNKS; ++e) {
+                            const int id = 32 * e + lane, j = (id >> 3) % ROWS;
+                            uint4* at = tile_v + ((id >> 3) / ROWS * KT + ROWS * w + j) * 8 + (id & 7);
+                            const uint4 x = *at;
+                            const bool there = in_reach(tile, key + ROWS * w + j);
+                            if (there && finite_pair(x.x) && finite_pair(x.y) && finite_pair(x.z) && finite_pair(x.w))
+                                continue;
+                            *at = make_uint4(0, 0, 0, 0);
+                            if (there) bad |= 1u << j;
+                        }
+                        bad = __reduce_or_sync(0xffffffffu, bad);
+                        if (lane == 0) found[w] = bad;
+                        fence_proxy_async_smem();
+                        mbar_arrive(looked + v.at);
+                    }
                     ok = warp_wait(looked + v.at, v.phase);
                     if (!ok) break;
-#pragma unroll
-                    for (int c = 0; c < W; ++c)
-                        if (poison[4 * v.at + c] & seen[c]) l = NAN;
+                    const uint4 f0 = *reinterpret_cast<uint4*>(found), f1 = *reinterpret_cast<uint4*>(found + 4);
+                    if (f0.x | f0.y | f0.z | f0.w | f1.x | f1.y | f1.z | f1.w)
+                        for (int j = 0; j < KT; ++j)
+                            if (((seen[j >> 5] >> (j & 31)) & 1u) && ((found[j / ROWS] >> (j % ROWS)) & 1u)) l = NAN;
                 }
                 float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -491,49 +476,59 @@ __global__ void __launch_bounds__(2 * D) join_kernel(const Args a) {
     const int hr = min(a.slot_rows, 128), col = threadIdx.x >> 3;
     const size_t size = size_t(hr) * (D + 2), next = a.slot_rows / hr * size;
     pdl_wait();
+    // four rows a thread, whose reads of two pieces are all on their way at a time
+    const float* part[4];
+    float top[4], sum[4];
+    float4 x[4];
+    int lanes[4], out_row[4];
+    bool there[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const int r = 32 * blockIdx.y + 8 * e + (threadIdx.x & 7), half = r >> 7, lane = r & 127;
         const int tok = half * (a.rt / 2) + lane / a.g;
-        if (r >= a.slot_rows || lane / a.g >= a.rt / 2 || tok >= t.ntok) continue;
-        const float* part = a.part + half * size;
-        float top = -INFINITY, sum = 0.f;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i0 = 0; i0 < pieces; i0 += 4) {  // four pieces' reads at a time
-            float m[4], l[4];
-            float4 y[4];
+        there[e] = r < a.slot_rows && lane / a.g < a.rt / 2 && tok < t.ntok;
+        out_row[e] = (t.row + tok) * a.HQ + h * a.g + lane % a.g;
+        part[e] = a.part + half * size;
+        lanes[e] = lane;
+        top[e] = -INFINITY;
+        sum[e] = 0.f;
+        x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int i0 = 0; i0 < pieces; i0 += 2) {
+        float m[4][2], l[4][2];
+        float4 y[4][2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                m[i] = -INFINITY;
-                if (i0 + i >= pieces) continue;
-                const float* in = part + slot_of(c, i0 + i) * next;
-                m[i] = in[hr * D + lane];
-                l[i] = in[hr * D + hr + lane];
-                y[i] = reinterpret_cast<const float4*>(in)[col * hr + lane];
-            }
-            const float before = top;
-            top = fmaxf(fmaxf(top, fmaxf(m[0], m[1])), fmaxf(m[2], m[3]));
-            const float from = top == -INFINITY ? 0.f : top, keep = exp2_approx(before - from);
-            sum *= keep;
-            x.x *= keep;
-            x.y *= keep;
-            x.z *= keep;
-            x.w *= keep;
+        for (int e = 0; e < 4; ++e)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (i0 + i >= pieces) continue;
-                const float w = exp2_approx(m[i] - from);
-                sum += w * l[i];
-                x.x += w * y[i].x;
-                x.y += w * y[i].y;
-                x.z += w * y[i].z;
-                x.w += w * y[i].w;
+            for (int i = 0; i < 2; ++i) {
+                m[e][i] = -INFINITY;
+                l[e][i] = 0.f;
+                y[e][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (!there[e] || i0 + i >= pieces) continue;
+                const float* in = part[e] + slot_of(c, i0 + i) * next;
+                m[e][i] = in[hr * D + lanes[e]];
+                l[e][i] = in[hr * D + hr + lanes[e]];
+                y[e][i] = reinterpret_cast<const float4*>(in)[col * hr + lanes[e]];
             }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float before = top[e];
+            top[e] = fmaxf(top[e], fmaxf(m[e][0], m[e][1]));
+            const float from = top[e] == -INFINITY ? 0.f : top[e], keep = exp2_approx(before - from);
+            const float f0 = exp2_approx(m[e][0] - from), f1 = exp2_approx(m[e][1] - from);
+            sum[e] = sum[e] * keep + f0 * l[e][0] + f1 * l[e][1];
+            x[e].x = x[e].x * keep + f0 * y[e][0].x + f1 * y[e][1].x;
+            x[e].y = x[e].y * keep + f0 * y[e][0].y + f1 * y[e][1].y;
+            x[e].z = x[e].z * keep + f0 * y[e][0].z + f1 * y[e][1].z;
+            x[e].w = x[e].w * keep + f0 * y[e][0].w + f1 * y[e][1].w;
         }
-        const float f = sum == 0.f ? 0.f : 1.f / sum;
-        __nv_bfloat16* out =
-            static_cast<__nv_bfloat16*>(a.o) + (size_t(t.row + tok) * a.HQ + h * a.g + lane % a.g) * D + 4 * col;
-        *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(x.x * f, x.y * f), pack_bf16(x.z * f, x.w * f));
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (!there[e]) continue;
+        const float f = sum[e] == 0.f ? 0.f : 1.f / sum[e];
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + size_t(out_row[e]) * D + 4 * col) =
+            make_uint2(pack_bf16(x[e].x * f, x[e].y * f), pack_bf16(x[e].z * f, x[e].w * f));
     }
 }
 

@@ -13,6 +13,7 @@ namespace att {
 // Block 0 plans; block 1 + b, with trees, lists the paths of stream b.
 __global__ void __launch_bounds__(256) plan_kernel(const Args a) {
     pdl_wait();
+    pdl_trigger();  // after the wait: the next launch may rely on everything before this one
     if (blockIdx.x == 0) {
         int bad = 0;
         const int ntiles = make_plan<256>(a, a.seqs, a.line, &bad);
@@ -285,6 +286,7 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) join_rows_kernel(const A
     constexpr int ROWS = W > 4 ? 1 : 4 / W, C = D / 32;
     __shared__ float part_o[ROWS * W][D], part_m[ROWS * W], part_l[ROWS * W];
     pdl_wait();
+    pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp % W;
     const int64_t id = int64_t(blockIdx.x) * ROWS + warp / W;
     const int row = int(id / a.HQ), hq = int(id % a.HQ), h = hq / a.g;

@@ -165,7 +165,7 @@ __device__ inline int make_plan(const Args& a, int4* seqs, int64_t* line_of, int
         int ctx = 0;
         if (b < a.B) {
             n = min(n, stream_len(a.lengths, b, a.T, bad));
-            ctx = a.context[b];
+            ctx = n > 0 ? a.context[b] : 0;
             if (ctx < 0) {
                 ctx = 0;
                 *bad |= CANOPY_DEVERR_LENGTH;

@@ -8,11 +8,12 @@
 //     O += P V             (128 x d x KT, P from tensor memory)
 // with S, P and O of both halves in the 512 columns of tensor memory.  KT is what
 // leaves P a place of its own (80 for d = 128, 128 for d = 64): as soon as the
-// softmax has S in registers, the next tile's S is formed behind its back, and the
-// warps go from tile to tile without waiting for the products.  (Tiles of 128 with
-// P over S, each half's products during the other's softmax, took 3,300 cycles
-// per 128 keys in the best order found, of which the products are 2,048.)
-// A thread issues each half's products.
+// softmax has S in registers the next tile's S is formed, and one thread a half
+// issues both products.  Tiles of 128 with P over S were as fast only with the
+// halves half a tile apart (a chunk of 4,096 tokens behind 28,672, 32/8 heads: 1,594
+// us; 1,585 this way, 1.30 PFLOP/s, and a window of 1,024 292 and 194 us); tiles of
+// 64 with two P took 1,976 us.  The softmax's warps hold it: 2,300 cycles a tile of
+// 80 keys, where the products take 1,280 (tensor pipe 0.55 of active cycles).
 //
 // m is the running maximum as of the last time that it grew by more than 2^8:
 // until then the weights are merely larger than 1, by less than 2^8, and neither
@@ -24,9 +25,10 @@
 // Key tiles come by TMA, one box per page (or 16 keys, where tiles and pages
 // cut each other) and 64 columns, into a ring of stages that K and V tiles take
 // in turns.  A page that no row sees is read at a coordinate outside the cache, as
-// zeros.  Where not every row sees every key of a tile, the softmax's
-// warps look through its V first: what no row sees, and what is not finite, becomes zero (0 times it
-// would reach every row's sum), and a row that sees a key with such a value is NaN.
+// zeros.  Where not every row sees every key of a tile, the softmax's warps look
+// through its V first: what no row sees, and what is not finite, becomes zero (0
+// times it would reach every row's sum), and a row that sees a key with such a
+// value is NaN.  (A warp of its own for that took 246 us for the window case.)
 #include "attend.cuh"
 
 namespace canopy {
@@ -55,8 +57,9 @@ struct Shape {
     // parts), O done, and all done
     static constexpr int NBAR = 2 + 3 * STAGES + 12;
     static_assert(STAGES % 2 == 0, "K tiles in even stages, V tiles in odd ones");
-    static constexpr int POISON = (BARS + 8 * NBAR + 15) / 16 * 16;  // [STAGES][8]: keys with a value that is not finite, by the warp
-    static constexpr int MISC = POISON + 32 * STAGES;                // tensor memory's address
+    // [STAGES][8]: keys with a value that is not finite, by the warp that found them
+    static constexpr int POISON = (BARS + 8 * NBAR + 15) / 16 * 16;
+    static constexpr int MISC = POISON + 32 * STAGES;  // tensor memory's address
     static constexpr int TOTAL = MISC + 16;
 };
 static_assert(Shape<128>::TOTAL + 1024 <= 232448 && Shape<64>::TOTAL + 1024 <= 232448, "shared memory");
@@ -458,24 +461,31 @@ __global__ void __launch_bounds__(NT, 1)
 template <int D>
 __global__ void __launch_bounds__(2 * D) join_kernel(const Args a) {
     const int c = blockIdx.x;
-    // the plan is older than the launch that this one waits for
+    // The plan is older than the launch that this one waits for.  Every block waits, one without a cut too: the
+    // launch behind this one relies on the one before it through this one's end.
     const int2 place = a.first_tile[c + 1];
     const int ntiles = a.seqs[a.B].w;
     const int64_t units = a.line[ntiles];
     const int ctas = parts(a, units);
-    if (c + 1 >= ctas || units == 0) return;
-    const int64_t cut = cta_begin(units, ctas, c + 1);
-    const int tile = place.x, b = place.y;
-    const int64_t at = a.line[tile];
-    const int per = int((a.line[tile + 1] - at) / a.HKV), h = int((cut - at) / per);
-    const int64_t begin = at + int64_t(h) * per;
-    if (begin == cut || cta_of(units, ctas, begin) != c) return;
-    const int pieces = cta_of(units, ctas, begin + per - 1) - c + 1;
-    const int4 s = a.seqs[b];
-    const Tile t = make_tile(a, b, s, tile - s.w);
+    bool cut = c + 1 < ctas && units > 0;
+    int h = 0, pieces = 0;
+    Tile t = {};
+    if (cut) {
+        const int tile = place.x, b = place.y;
+        const int64_t at = a.line[tile], split = cta_begin(units, ctas, c + 1);
+        const int per = int((a.line[tile + 1] - at) / a.HKV);
+        h = int((split - at) / per);
+        const int64_t begin = at + int64_t(h) * per;
+        cut = begin != split && cta_of(units, ctas, begin) == c;
+        pieces = cta_of(units, ctas, begin + per - 1) - c + 1;
+        const int4 s = a.seqs[b];
+        t = make_tile(a, b, s, tile - s.w);
+    }
     const int hr = min(a.slot_rows, 128), col = threadIdx.x >> 3;
     const size_t size = size_t(hr) * (D + 2), next = a.slot_rows / hr * size;
     pdl_wait();
+    pdl_trigger();
+    if (!cut) return;
     // four rows a thread, whose reads of two pieces are all on their way at a time
     const float* part[4];
     float top[4], sum[4];

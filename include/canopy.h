@@ -415,9 +415,10 @@ canopy_attend_plan_t canopy_attend_plan(int N, int B, int HQ, int HKV, canopy_dt
  * and starts NULL, as canopy_tree_verify takes it) the places j < c and those of its
  * root path, itself among them.  With window > 0 of these only the tokens whose
  * position is less than window before t_i, and those at positions < sinks.
- *   scale > 0; q, o [N][HQ][d] in dtype; the places that no row of a sequence sees (behind its
+ *   scale > 0; q, o [N][HQ][d] in dtype (o not q); the places that no row of a sequence sees (behind its
  *   last row, out of the window) need no page and may hold anything; what a place
- *   holds reaches no row that does not see it.
+ *   holds reaches no row that does not see it (where rows see different places, a
+ *   bf16 row that sees a value that is not finite may be NaN throughout).
  * bf16: products on the tensor cores with fp32 sums and statistics, the weights
  * rounded to bf16 for the second product; fp32: fp32 throughout.
  * Data errors (parent, starts, lengths, context, pages) set bits in the workspace's

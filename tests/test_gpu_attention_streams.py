@@ -121,6 +121,29 @@ def test_native_and_python_marshalling_agree(lib, monkeypatch):
     assert equal(layer(lib, inputs(8), ws), native)
 
 
+@pytest.mark.parametrize("rows,ctx", [(1, 2000), (130, 900), (700, 3000)])
+def test_the_next_call_waits(lib, rows, ctx):
+    """A call that overwrites what the one before it reads (its queries, its keys) comes after it, pieces cut or not."""
+    rng = np.random.RandomState(rows)
+    k, v, table = cache(rng, [ctx + rows], 1, D, 64, True)
+    q0 = tensor(rounded(rng.standard_normal((rows, 2, D)), True), True)
+    k0, v0 = tensor(k, True), tensor(v, True)
+    td, cd = tensor(table), tensor(np.array([ctx], np.int32))
+    starts = tensor(np.array([0, rows], np.int32))
+    ws = lib.attend_workspace(rows, 1, 2, 1, D)
+    ref = lib.attend(q0, k0, v0, td, cd, ws, starts=starts)
+    new = torch.ones(rows, 1, D, device="cuda", dtype=torch.bfloat16)
+    for _ in range(20):
+        q, kd, vd = q0.clone(), k0.clone(), v0.clone()
+        torch.cuda.synchronize()
+        o = lib.attend(q, kd, vd, td, cd, ws, starts=starts)
+        lib.qk_prep(q, new, new, norm="l2", q_out=q, k_cache=kd, v_cache=vd, page_table=td, context=cd, starts=starts)
+        p = lib.attend(q, kd, vd, td, cd, ws, starts=starts)
+        torch.cuda.synchronize()
+        assert torch.equal(o, ref)
+        assert torch.equal(p, lib.attend(q, kd, vd, td, cd, ws, starts=starts))
+
+
 def test_no_rows_at_all(lib):
     """Sequences whose rows are all missing: nothing is written."""
     x, ws = inputs(9), workspace(lib)

@@ -20,9 +20,22 @@ __global__ void __launch_bounds__(256) plan_kernel(const Args a) {
         if (bad) raise_err(a.err, bad);
         const int64_t units = a.line[ntiles];
         const int ctas = parts(a, units);
-        for (int c = threadIdx.x; c < ctas; c += 256) {
-            const int tile = ntiles ? tile_at(a.line, ntiles, cta_begin(units, ctas, c)) : 0;
-            a.first_tile[c] = make_int2(tile, sequence_at(a.seqs, a.B, tile));
+        for (int c = threadIdx.x; c < a.ctas; c += 256) {
+            int4 join = make_int4(0, 0, 0, 0);
+            if (c < ctas && ntiles) {
+                const int64_t at = cta_begin(units, ctas, c);
+                const int tile = tile_at(a.line, ntiles, at), b = sequence_at(a.seqs, a.B, tile);
+                a.first_tile[c] = make_int2(tile, b);
+                // whether the item that CTA c begins in was begun by the CTA before, and by no earlier one
+                const int64_t line = a.line[tile];
+                const int per = int((a.line[tile + 1] - line) / a.HKV), h = int((at - line) / per);
+                const int64_t begin = line + int64_t(h) * per;
+                if (begin != at && cta_of(units, ctas, begin) == c - 1) {
+                    const Tile t = make_tile(a, b, a.seqs[b], tile - a.seqs[b].w);
+                    join = make_int4(t.row, t.ntok, h, cta_of(units, ctas, begin + per - 1) - c + 2);
+                }
+            }
+            if (c) a.joins[c - 1] = join;
         }
         return;
     }
@@ -401,7 +414,7 @@ int slot_rows(int N, int g) {
 }
 
 struct Layout {
-    size_t seqs, line, first_tile, mask, depth, part, end;
+    size_t seqs, line, first_tile, joins, mask, depth, part, end;
 };
 
 // For the smallest row tile that a call of these sizes may take.
@@ -411,6 +424,7 @@ Layout layout(int N, int B, int g, int d) {
     w.seqs = o;       o = ws_align(o + (size_t(B) + 1) * sizeof(int4));
     w.line = o;       o = ws_align(o + (size_t(N) + B + 1) * 8);
     w.first_tile = o; o = ws_align(o + (kFewCtas + 1) * 8);
+    w.joins = o;      o = ws_align(o + kFewCtas * sizeof(int4));
     w.mask = o;       o = ws_align(o + size_t(N) * kMaskWords * 4);
     w.depth = o;      o = ws_align(o + size_t(N) * 4);
     const int rows = slot_rows(N, g);
@@ -474,6 +488,7 @@ cudaError_t launch_attend(const void* q, int bf16, const void* kc, const void* v
     a.seqs = reinterpret_cast<int4*>(p + w.seqs);
     a.line = reinterpret_cast<int64_t*>(p + w.line);
     a.first_tile = reinterpret_cast<int2*>(p + w.first_tile);
+    a.joins = reinterpret_cast<int4*>(p + w.joins);
     a.mask = reinterpret_cast<uint32_t*>(p + w.mask);
     a.depth = reinterpret_cast<int32_t*>(p + w.depth);
     a.part = reinterpret_cast<float*>(p + w.part);

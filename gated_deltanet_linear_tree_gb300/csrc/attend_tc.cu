@@ -11,9 +11,9 @@
 // softmax has S in registers the next tile's S is formed, and one thread a half
 // issues both products.  Tiles of 128 with P over S were as fast only with the
 // halves half a tile apart (a chunk of 4,096 tokens behind 28,672, 32/8 heads: 1,594
-// us; 1,585 this way, 1.30 PFLOP/s, and a window of 1,024 292 and 194 us); tiles of
+// us; 1,580 this way, 1.31 PFLOP/s, and a window of 1,024 292 and 190 us); tiles of
 // 64 with two P took 1,976 us.  The softmax's warps hold it: 2,300 cycles a tile of
-// 80 keys, where the products take 1,280 (tensor pipe 0.55 of active cycles).
+// 80 keys, where the products take 1,280 (tensor pipe 0.61 of active cycles).
 //
 // m is the running maximum as of the last time that it grew by more than 2^8:
 // until then the weights are merely larger than 1, by less than 2^8, and neither
@@ -460,32 +460,16 @@ __global__ void __launch_bounds__(NT, 1)
 // four of the rows, eight threads side by side eight rows (128 bytes of a piece).
 template <int D>
 __global__ void __launch_bounds__(2 * D) join_kernel(const Args a) {
-    const int c = blockIdx.x;
     // The plan is older than the launch that this one waits for.  Every block waits, one without a cut too: the
     // launch behind this one relies on the one before it through this one's end.
-    const int2 place = a.first_tile[c + 1];
-    const int ntiles = a.seqs[a.B].w;
-    const int64_t units = a.line[ntiles];
-    const int ctas = parts(a, units);
-    bool cut = c + 1 < ctas && units > 0;
-    int h = 0, pieces = 0;
-    Tile t = {};
-    if (cut) {
-        const int tile = place.x, b = place.y;
-        const int64_t at = a.line[tile], split = cta_begin(units, ctas, c + 1);
-        const int per = int((a.line[tile + 1] - at) / a.HKV);
-        h = int((split - at) / per);
-        const int64_t begin = at + int64_t(h) * per;
-        cut = begin != split && cta_of(units, ctas, begin) == c;
-        pieces = cta_of(units, ctas, begin + per - 1) - c + 1;
-        const int4 s = a.seqs[b];
-        t = make_tile(a, b, s, tile - s.w);
-    }
+    const int c = blockIdx.x;
+    const int4 join = a.joins[c];
+    const int row = join.x, ntok = join.y, h = join.z, pieces = join.w;
     const int hr = min(a.slot_rows, 128), col = threadIdx.x >> 3;
     const size_t size = size_t(hr) * (D + 2), next = a.slot_rows / hr * size;
     pdl_wait();
     pdl_trigger();
-    if (!cut) return;
+    if (pieces == 0) return;
     // four rows a thread, whose reads of two pieces are all on their way at a time
     const float* part[4];
     float top[4], sum[4];
@@ -496,8 +480,8 @@ __global__ void __launch_bounds__(2 * D) join_kernel(const Args a) {
     for (int e = 0; e < 4; ++e) {
         const int r = 32 * blockIdx.y + 8 * e + (threadIdx.x & 7), half = r >> 7, lane = r & 127;
         const int tok = half * (a.rt / 2) + lane / a.g;
-        there[e] = r < a.slot_rows && lane / a.g < a.rt / 2 && tok < t.ntok;
-        out_row[e] = (t.row + tok) * a.HQ + h * a.g + lane % a.g;
+        there[e] = r < a.slot_rows && lane / a.g < a.rt / 2 && tok < ntok;
+        out_row[e] = (row + tok) * a.HQ + h * a.g + lane % a.g;
         part[e] = a.part + half * size;
         lanes[e] = lane;
         top[e] = -INFINITY;

@@ -606,7 +606,8 @@ def qk_prep(q, k, v=None, norm: str = "rms", q_weight=None, k_weight=None, eps: 
             raise CanopyError("freqs must have shape (R / 2,)")
         R = 2 * freqs.shape[0]
     if positions is not None:
-        if not isinstance(positions, torch.Tensor) or tuple(positions.shape) not in (lead, (*positions.shape[:1], *lead)):
+        if not isinstance(positions, torch.Tensor) or \
+                tuple(positions.shape) not in (lead, (*positions.shape[:1], *lead)):
             raise CanopyError(f"positions must have shape {lead} or (axes, *{lead})")
         if positions.dim() > len(lead):
             axes = positions.shape[0]

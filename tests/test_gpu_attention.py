@@ -150,6 +150,40 @@ def test_trees(lib, HQ, HKV, d, T, tree, bf16):
 
 
 @pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("T,lens", [(3, [3, 1, 0]), (70, [70, 0, 41])])
+def test_rows_of_streams_without_a_tree(lib, T, lens, bf16):
+    check_attend(lib, attend_case(T, lens, [0, 100, 129], 8, 4, 128, 32, bf16, T=T))
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_far_pages(lib, bf16):
+    """Pages beyond 2^31 elements and 2^32 bytes of the caches: prepared, attended and moved as near ones are."""
+    HQ, HKV, d, page, pages, T = 8, 8, 128, 64, 40000, 12
+    dt = torch.bfloat16 if bf16 else torch.float32
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(0)
+    small = [torch.randn(9, HKV, page, d, device="cuda", generator=gen).to(dt) for _ in range(2)]
+    big = [torch.empty(pages, HKV, page, d, device="cuda", dtype=dt) for _ in range(2)]
+    for x, y in zip(small, big):
+        y[-9:] = x
+    near = torch.tensor([[0, 5, 2, 7], [1, 3, 8, 4]], dtype=torch.int32, device="cuda")
+    context = torch.tensor([150, 70], dtype=torch.int32, device="cuda")
+    parent = torch.tensor([[-1] + [(i - 1) // 2 for i in range(1, T)]] * 2, dtype=torch.int32, device="cuda")
+    accepted = torch.tensor([T - 1, 6], dtype=torch.int32, device="cuda")
+    x = [torch.randn(2, T, H, d, device="cuda", generator=gen).to(dt) for H in (HQ, HKV, HKV)]
+    one = torch.randn(2, HQ, d, device="cuda", generator=gen).to(dt)
+    ws = lib.attend_workspace(2 * T, 2, HQ, HKV, d)
+    out = []
+    for (k, v), table in ((small, near), (big, near + pages - 9)):
+        q, _ = lib.qk_prep(*x, norm="l2", k_cache=k, v_cache=v, page_table=table, context=context)
+        o = lib.attend(q, k, v, table, context, ws, parent=parent)
+        c = lib.cache_commit(accepted, parent, k, v, table, context)
+        out.append([q, o, c, lib.attend(one, k, v, table, c, ws), k[-9:], v[-9:]])
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+    assert lib.read_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("bf16", [True, False])
 @pytest.mark.parametrize("HQ,HKV,d", HEADS)
 @pytest.mark.parametrize("lens,ctxs", [([1], [0]), ([300], [0]), ([5, 0, 130, 64, 1], [0, 9, 128, 250, 513]),
                                        ([17, 257], [600, 31])])

@@ -382,6 +382,7 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) join_rows_kernel(const A
 
 template <typename OutT, int D>
 cudaError_t launch_join_rows(const Args& a, cudaStream_t st) {
+    if (a.ctas == 1) return cudaSuccess;  // nothing is cut
     // (row tile, key head) items, about; each is cut into about ctas / items pieces
     const int64_t rows = int64_t(a.N) * a.HQ, tiles = (a.N + a.rt - 1) / a.rt;
     const int64_t each = a.ctas / ((tiles > a.B ? tiles : a.B) * a.HKV);
@@ -479,8 +480,11 @@ cudaError_t launch_attend(const void* q, int bf16, const void* kc, const void* v
     const int R = a.g <= 16 && int64_t(N) * a.g <= int64_t(16) * B ? 16 : 64;  // rows of a tile, where not on 256
     a.rt = tiles ? tc_tile_tokens(a.g) : R / a.g;
     a.kt = tiles ? tc_tile_keys(d) : 64;
-    a.ctas = tiles ? kSMs : kFewCtas;
     a.least = bf16 ? kLeast : 1;  // (a unit takes the CUDA cores 3 us)
+    // no more CTAs than the units that the page table has room for, were every tile's cache full
+    const int64_t most_tiles = N / a.rt + B < N ? N / a.rt + B : N, room = int64_t(max_pages) << log_page;
+    const int64_t units = most_tiles * HKV * (room / a.kt + 1) / a.least, ctas = tiles ? kSMs : kFewCtas;
+    a.ctas = int(units < ctas ? (units < 1 ? 1 : units) : ctas);
     a.slot_rows = few ? 16 : tiles ? slot_rows(N, a.g) : R;
     const Layout w = layout(N, B, a.g, d);
     char* p = static_cast<char*>(workspace);

@@ -136,6 +136,20 @@ __device__ inline int sequence_at(const int4* seqs, int B, int i) {
     return b;
 }
 
+// Rows and context of a sequence brought into what its page table has room for.
+__device__ inline void fit(const Args& a, int& n, int& ctx, int* bad) {
+    if (ctx < 0) {
+        ctx = 0;
+        *bad |= CANOPY_DEVERR_LENGTH;
+    }
+    const int room = a.max_pages << a.log_page;
+    if (n > room || ctx > room - n) {
+        *bad |= CANOPY_DEVERR_PAGE;
+        n = min(n, room);
+        ctx = min(ctx, room - n);
+    }
+}
+
 // The plan, by a whole block of NT threads: seqs, line, and the number of tiles
 // (returned).  Starts out of order or range are read as their
 // running maximum, lengths and contexts as the nearest that fit; these set bits
@@ -148,6 +162,32 @@ __device__ inline int make_plan(const Args& a, int4* seqs, int64_t* line_of, int
     const auto sum = [](int64_t x, int64_t y) { return x + y; };
     const auto isum = [](int x, int y) { return x + y; };
     const int tid = threadIdx.x;
+    if (!a.starts && a.B <= 32 && a.T <= a.rt) {  // a tile a stream at most: one warp, no meetings on the way
+        if (tid < 32) {
+            const bool stream = tid < a.B;
+            int n = stream ? min(a.T, stream_len(a.lengths, tid, a.T, bad)) : 0;
+            int ctx = n > 0 ? a.context[tid] : 0;
+            fit(a, n, ctx, bad);
+            const uint32_t filled = __ballot_sync(0xffffffffu, n > 0);
+            const int tile = __popc(filled & ((1u << tid) - 1)), ntiles = __popc(filled);
+            const int4 s = make_int4(tid * a.T, n, ctx, tile);
+            const int64_t units = n > 0 ? int64_t(make_tile(a, tid, s, 0).units) * a.HKV : 0;
+            int64_t upto = units;
+#pragma unroll
+            for (int x = 1; x < 32; x *= 2) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, upto, x);
+                if (tid >= x) upto += y;
+            }
+            if (stream) seqs[tid] = s;
+            if (n > 0) line_of[tile] = upto - units;
+            if (tid == 31) {
+                seqs[a.B] = make_int4(a.N, 0, 0, ntiles);
+                line_of[ntiles] = upto;
+            }
+        }
+        __syncthreads();
+        return seqs[a.B].w;
+    }
     int carry_lo = 0, carry_hi = 0, carry = 0, total;
     if (a.starts) carry_lo = carry_hi = start_in_range(a.starts, 0, a.N);
     for (int b0 = 0; b0 < a.B; b0 += NT) {
@@ -167,16 +207,7 @@ __device__ inline int make_plan(const Args& a, int4* seqs, int64_t* line_of, int
         if (b < a.B) {
             n = min(n, stream_len(a.lengths, b, a.T, bad));
             ctx = n > 0 ? a.context[b] : 0;
-            if (ctx < 0) {
-                ctx = 0;
-                *bad |= CANOPY_DEVERR_LENGTH;
-            }
-            const int room = a.max_pages << a.log_page;
-            if (n > room || ctx > room - n) {
-                *bad |= CANOPY_DEVERR_PAGE;
-                n = min(n, room);
-                ctx = min(ctx, room - n);
-            }
+            fit(a, n, ctx, bad);
         } else {
             n = 0;
         }

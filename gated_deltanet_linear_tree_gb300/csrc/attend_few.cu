@@ -13,7 +13,7 @@
 // 64 streams behind 4,000 to 16,000 tokens, 32/8 heads: 390 us, 6.8 TB/s, the
 // measured copy bandwidth (128-row products in attend_tc.cu: 492).  One behind
 // 262,143 tokens, 16/2 heads: 44 us, 0.9 of it, and 10 for the launch that joins the
-// pieces.  One behind 700: two launches' latencies, 11.5 us.
+// pieces.  One behind 700: two launches' latencies, 10.8 us.
 //
 // The running maximum is kept until it grows by 2^8 (attend_tc.cu), and the two
 // warps keep one each until the piece ends, when the second's sums join the

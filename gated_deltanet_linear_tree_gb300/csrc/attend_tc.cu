@@ -548,6 +548,7 @@ static cudaError_t launch_tc_d(const Args& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     e = launch_pdl(tcg::attend_kernel<D>, dim3(a.ctas), dim3(tcg::NT), smem, st, mq, mk, mv, a);
     if (e != cudaSuccess) return e;
+    if (a.ctas == 1) return cudaSuccess;  // nothing is cut
     return launch_pdl(tcg::join_kernel<D>, dim3(a.ctas - 1, (a.slot_rows + 31) / 32), dim3(2 * D), 0, st, a);
 }
 

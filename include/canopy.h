@@ -403,7 +403,7 @@ typedef enum {
     CANOPY_ATTEND_PLAN_NONE = -1, /* the call would be refused                                   */
     CANOPY_ATTEND_PLAN_FP32 = 0,  /* fp32: CUDA cores                                           */
     CANOPY_ATTEND_PLAN_FEW = 1,   /* bf16, few rows a sequence: bound by the cache's reads        */
-    CANOPY_ATTEND_PLAN_TILES = 2  /* bf16, many rows: tensor-core tiles of 256 rows x 128 keys  */
+    CANOPY_ATTEND_PLAN_TILES = 2  /* bf16, many rows: tensor-core tiles of up to 256 rows         */
 } canopy_attend_plan_t;
 canopy_attend_plan_t canopy_attend_plan(int N, int B, int HQ, int HKV, canopy_dtype dtype, int d);
 

@@ -68,8 +68,8 @@ SIGNATURES = {
     "canopy_prefill_plan": (_I, [_I, _I, _I, _I, _I, _I, _I, ctypes.c_uint]),
     "canopy_step": (_I, [_P, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _I, _P, _P]),
     "canopy_accept": (_I, [_P, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P]),
-    "canopy_qk_prep": (_I, [_P, _P, _P, _I, _L, _L, _L, _I, _P, _P, _F, _P, _I, _P, _I, _P, _I, _I, _I, _I, _I, _I,
-                            _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P]),
+    "canopy_qk_prep": (_I, [_P, _P, _P, _I, _L, _L, _L, _I, _P, _P, _F, _P, _I, _P, _I, _L, _L, _P, _I, _I, _I, _I,
+                            _I, _I, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P]),
     "canopy_attend_workspace_bytes": (_S, [_I, _I, _I, _I, _I]),
     "canopy_attend_plan": (_I, [_I, _I, _I, _I, _I, _I]),
     "canopy_attend": (_I, [_P, _I, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P,
@@ -561,8 +561,8 @@ def qk_prep(q, k, v=None, norm: str = "rms", q_weight=None, k_weight=None, eps: 
     """Queries and keys of a layer in one pass: (q_out, k_out).  Every head's
     row normed ("rms", "l2" for unit rows, or "none"; weights fp32 [d] or
     None), the first 2 len(freqs) columns rotated by position (freqs fp32;
-    positions int32 of the rows' shape, or [axes, ...] with axis int32
-    [len(freqs)] each pair's axis, or None for the place in the cache; pairs
+    positions int32 of the rows' shape, or [axes, ...] (expanded or transposed
+    ones too) with axis int32 [len(freqs)] each pair's axis, or None for the place in the cache; pairs
     "half" (j, j + R/2) or "adjacent" (2j, 2j + 1)), rounded once.
     q [N, HQ, d], k, v [N, HKV, d]: packed sequences at starts int32 [B+1], or
     one token of each stream; or [B, T, heads, d], of which lengths int32 [B] (or
@@ -588,7 +588,7 @@ def qk_prep(q, k, v=None, norm: str = "rms", q_weight=None, k_weight=None, eps: 
     ldq = _need_rows(q, "q", dev, dt, (*lead, HQ, d))
     ldk = _need_rows(k, "k", dev, dt, (*lead, HKV, d))
     R = ldv = B = pages = page_size = max_pages = 0
-    axes = 1
+    axes, axis_step, row_step = 1, 0, 1
     if k_cache is not None:
         B, pages, page_size, max_pages = _cache(k_cache, v_cache, page_table, context, dt, HKV, d, dev)
         _streams(lead, B, starts)
@@ -609,9 +609,16 @@ def qk_prep(q, k, v=None, norm: str = "rms", q_weight=None, k_weight=None, eps: 
         if not isinstance(positions, torch.Tensor) or \
                 tuple(positions.shape) not in (lead, (*positions.shape[:1], *lead)):
             raise CanopyError(f"positions must have shape {lead} or (axes, *{lead})")
+        if not positions.is_cuda or positions.dtype != i32:
+            raise CanopyError("positions must be an int32 CUDA tensor")
+        if positions.get_device() != dev:
+            raise CanopyError("positions must be on the same device as the other tensors")
         if positions.dim() > len(lead):
-            axes = positions.shape[0]
-        _need_all(dev, (positions, "positions", i32, positions.shape))
+            axes, axis_step = positions.shape[0], positions.stride(0)
+        two = len(lead) == 2 and lead[0] > 1
+        row_step = positions.stride(-1) if lead[-1] > 1 else positions.stride(-2) if two else 1
+        if two and positions.stride(-2) != row_step * lead[-1]:
+            raise CanopyError("positions must have their tokens at one distance")
     _need_given(dev, (axis, "axis", i32, (R // 2,)))
     lib = load()
     with torch.cuda.device(dev):
@@ -620,8 +627,9 @@ def qk_prep(q, k, v=None, norm: str = "rms", q_weight=None, k_weight=None, eps: 
         if k_out is None and k_cache is None:
             k_out = torch.empty((*lead, HKV, d), dtype=dt, device=q.device)
         st = lib.canopy_qk_prep(q.data_ptr(), k.data_ptr(), _opt(v), code, ldq, ldk, ldv, NORM[norm], _opt(q_weight),
-                                _opt(k_weight), eps, _opt(freqs), R, _opt(positions), axes, _opt(axis), PAIRS[pairs],
-                                N, B, HQ, HKV, d, q_out.data_ptr(), _opt(k_out), _opt(k_cache), _opt(v_cache),
+                                _opt(k_weight), eps, _opt(freqs), R, _opt(positions), axes, axis_step, row_step,
+                                _opt(axis), PAIRS[pairs], N, B, HQ, HKV, d, q_out.data_ptr(), _opt(k_out),
+                                _opt(k_cache), _opt(v_cache),
                                 _opt(page_table), pages, page_size, max_pages, _opt(context), _opt(starts),
                                 _opt(lengths), _opt(err), _raw_stream(dev))
     _check(st, "canopy_qk_prep")

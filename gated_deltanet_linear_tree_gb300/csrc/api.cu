@@ -61,10 +61,11 @@ cudaError_t launch_accept(const void* p, const void* q, int bf16, const int32_t*
                           int32_t* accepted, int32_t* out, int32_t* count, int32_t* err, cudaStream_t st);
 cudaError_t launch_qk_prep(const void* q, const void* k, const void* v, int bf16, int64_t ldq, int64_t ldk,
                            int64_t ldv, int norm, const float* qw, const float* kw, float eps, const float* freqs,
-                           int R, const int32_t* positions, int axes, const int32_t* axis, int adjacent, int N, int B,
-                           int HQ, int HKV, int d, void* qo, void* ko, void* kc, void* vc, const int32_t* table,
-                           int pages, int log_page, int max_pages, const int32_t* context, const int32_t* starts,
-                           const int32_t* lengths, int32_t* err, cudaStream_t st);
+                           int R, const int32_t* positions, int axes, int64_t axis_step, int64_t row_step,
+                           const int32_t* axis, int adjacent, int N, int B, int HQ, int HKV, int d, void* qo, void* ko,
+                           void* kc, void* vc, const int32_t* table, int pages, int log_page, int max_pages,
+                           const int32_t* context, const int32_t* starts, const int32_t* lengths, int32_t* err,
+                           cudaStream_t st);
 size_t attend_ws_bytes(int N, int B, int HQ, int HKV, int d);
 canopy_attend_plan_t attend_plan(int N, int B, int HQ, int HKV, int bf16, int d);
 cudaError_t launch_attend(const void* q, int bf16, const void* kc, const void* vc, const int32_t* table, int pages,
@@ -401,7 +402,8 @@ canopy_status canopy_accept(const void* p, const void* q, canopy_dtype dtype, co
 canopy_status canopy_qk_prep(const void* q, const void* k, const void* v, canopy_dtype dtype, int64_t ldq,
                              int64_t ldk, int64_t ldv, canopy_norm norm, const float* q_weight,
                              const float* k_weight, float eps, const float* freqs, int R, const int32_t* positions,
-                             int axes, const int32_t* axis, canopy_pairs pairs, int N, int B, int HQ, int HKV, int d,
+                             int axes, int64_t axis_step, int64_t row_step, const int32_t* axis, canopy_pairs pairs,
+                             int N, int B, int HQ, int HKV, int d,
                              void* q_out, void* k_out, void* k_cache, void* v_cache, const int32_t* page_table,
                              int pages, int page_size, int max_pages, const int32_t* context, const int32_t* starts,
                              const int32_t* lengths, int32_t* err, void* stream) {
@@ -421,7 +423,8 @@ canopy_status canopy_qk_prep(const void* q, const void* k, const void* v, canopy
         (pairs != CANOPY_PAIRS_HALF && pairs != CANOPY_PAIRS_ADJACENT) || !(eps >= 0.f) || !std::isfinite(eps) ||
         (norm == CANOPY_NORM_NONE && (q_weight || k_weight)))
         return CANOPY_ERR_ARG;
-    if (R < 0 || R > d || (R > 0) != (freqs != nullptr) || (positions && axes < 1) || (axis && !positions) ||
+    if (R < 0 || R > d || (R > 0) != (freqs != nullptr) || (axis && !positions) ||
+        (positions && (axes < 1 || axis_step < 0 || row_step < 0)) ||
         (R && !positions && !cached) || (positions && !R))
         return CANOPY_ERR_ARG;
     const canopy_status as = layer_sizes(N, cached ? B : 1, HQ, HKV, d);
@@ -438,9 +441,10 @@ canopy_status canopy_qk_prep(const void* q, const void* k, const void* v, canopy
         if (starts ? lengths != nullptr : N % B != 0) return CANOPY_ERR_ARG;
     }
     return cuda_status(launch_qk_prep(q, k, v, dtype == CANOPY_BF16, ldq, ldk, ldv, norm, q_weight, k_weight, eps,
-                                      freqs, R, positions, axes, axis, pairs == CANOPY_PAIRS_ADJACENT, N, B, HQ, HKV,
-                                      d, q_out, k_out, k_cache, v_cache, page_table, pages, log_page, max_pages,
-                                      context, starts, lengths, err, static_cast<cudaStream_t>(stream)));
+                                      freqs, R, positions, axes, axis_step, row_step, axis,
+                                      pairs == CANOPY_PAIRS_ADJACENT, N, B, HQ, HKV, d, q_out, k_out, k_cache, v_cache,
+                                      page_table, pages, log_page, max_pages, context, starts, lengths, err,
+                                      static_cast<cudaStream_t>(stream)));
 }
 
 size_t canopy_attend_workspace_bytes(int N, int B, int HQ, int HKV, int d) {

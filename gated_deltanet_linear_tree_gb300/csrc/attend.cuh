@@ -45,7 +45,8 @@ struct Args {
     int4* seqs;       // [B + 1]: first row, rows, ctx, first tile (of the last: the number of tiles)
     int64_t* line;    // [number of tiles + 1]: units before the tile, of all key heads
     int2* first_tile;  // [ctas]: the tile that CTA c begins in, and its sequence
-    int4* joins;      // [ctas - 1]: of the item first cut behind CTA c its first row, tokens, key head, pieces (0: none)
+    int4* joins;      // [ctas - 1]: of the item first cut behind CTA c its first row, tokens, key head, and
+                      // pieces (0: none is)
     uint32_t* mask;   // trees: [N][kMaskWords], the nodes of a row's path that it sees
     int32_t* depth;   // trees: [N]
     float* part;      // [2 ctas] slots

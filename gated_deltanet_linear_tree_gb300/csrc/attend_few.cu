@@ -258,8 +258,9 @@ __global__ void __launch_bounds__(NT, 2)
                     uint32_t bad = 0;
                     for (int e = lane; e < 32 * D / 2; e += 32) {
                         const int j = e / (D / 2), c = e % (D / 2);
-                        const uint32_t x = reinterpret_cast<const uint32_t*>(sm.kv[ring.at][1])[
-                            (c / 32) * (KT * 32) + (32 * warp + j) * 32 + (c & 31)];  // (the chunks' order does not matter)
+                        // (the order of a row's chunks does not matter)
+                        const uint32_t x = reinterpret_cast<const uint32_t*>(
+                            sm.kv[ring.at][1])[(c / 32) * (KT * 32) + (32 * warp + j) * 32 + (c & 31)];
                         if (bad_pair(x)) bad |= 1u << j;
                     }
                     bad = __reduce_or_sync(0xffffffffu, bad) & check;

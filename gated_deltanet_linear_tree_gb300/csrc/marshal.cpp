@@ -366,7 +366,8 @@ PyObject* qk_prep(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::ScalarType st = q0.scalar_type();
         const int64_t HQ = q0.size(-2), HKV = k0.size(-2), d = q0.size(-1);
         int64_t ldq = 0, ldk = 0, ldv = 0;
-        const at::Tensor *q = spaced(a[0], dev, st, r, HQ, d, ldq), *k = spaced(a[1], dev, st, r, HKV, d, ldk), *v = nullptr;
+        const at::Tensor *q = spaced(a[0], dev, st, r, HQ, d, ldq), *k = spaced(a[1], dev, st, r, HKV, d, ldk);
+        const at::Tensor* v = nullptr;
         bool ok = q && k && ints({r.n, HQ, HKV, d});
         const bool cached = a[13] != Py_None, packed = a[17] != Py_None;
         Cache c = {};
@@ -384,20 +385,29 @@ PyObject* qk_prep(PyObject*, PyObject* const* a, Py_ssize_t n) {
         }
         const at::Tensor *qw = maybe(a[4], dev, at::kFloat, {d}, ok), *kw = maybe(a[5], dev, at::kFloat, {d}, ok);
         const at::Tensor *freqs = nullptr, *positions = nullptr;
-        int64_t half = 0, axes = 1;
+        int64_t half = 0, axes = 1, axis_step = 0, row_step = 1;
         if (a[7] != Py_None) {
             freqs = plain(a[7], dev);
             ok = ok && freqs && freqs->dim() == 1 && freqs->scalar_type() == at::kFloat;
             if (ok) half = freqs->size(0);
         }
         if (ok && a[8] != Py_None) {
-            positions = plain(a[8], dev);
-            if (!positions || positions->scalar_type() != at::kInt) return none();
+            if (!THPVariable_Check(a[8])) return none();
+            positions = &THPVariable_Unpack(a[8]);
+            if (!positions->defined() || !positions->is_cuda() || positions->layout() != at::kStrided ||
+                positions->get_device() != dev || positions->scalar_type() != at::kInt)
+                return none();
             const int64_t more = positions->dim() - int64_t(r.lead.size());
-            if (more == 1) axes = positions->size(0);
-            else if (more != 0) return none();
+            if (more != 0 && more != 1) return none();
             for (size_t i = 0; i < r.lead.size(); ++i)
                 if (positions->size(i + more) != r.lead[i]) return none();
+            if (more == 1) {
+                axes = positions->size(0);
+                axis_step = positions->stride(0);
+            }
+            const bool two = r.lead.size() == 2 && r.lead[0] > 1;
+            row_step = r.lead.back() > 1 ? positions->stride(-1) : two ? positions->stride(-2) : 1;
+            if (two && positions->stride(-2) != row_step * r.lead.back()) return none();
         }
         const at::Tensor* axis = maybe(a[9], dev, at::kInt, {half}, ok);
         const at::Tensor* err = maybe(a[19], dev, at::kInt, {1}, ok);
@@ -413,8 +423,9 @@ PyObject* qk_prep(PyObject*, PyObject* const* a, Py_ssize_t n) {
             s = qk_prep_fn(q->data_ptr(), k->data_ptr(), ptr<void>(v), type, ldq, ldk, ldv,
                            canopy_norm(PyLong_AsLong(a[3])), ptr<float>(qw), ptr<float>(kw),
                            float(PyFloat_AS_DOUBLE(a[6])), ptr<float>(freqs), int(2 * half), ptr<int32_t>(positions),
-                           int(axes), ptr<int32_t>(axis), canopy_pairs(PyLong_AsLong(a[10])), int(r.n), int(c.B),
-                           int(HQ), int(HKV), int(d), q_out.data_ptr(), cached ? nullptr : k_out.data_ptr(),
+                           int(axes), axis_step, row_step, ptr<int32_t>(axis), canopy_pairs(PyLong_AsLong(a[10])),
+                           int(r.n), int(c.B), int(HQ), int(HKV), int(d), q_out.data_ptr(),
+                           cached ? nullptr : k_out.data_ptr(),
                            ptr<void>(c.k), ptr<void>(c.v), ptr<int32_t>(c.table), int(c.pages), int(c.page),
                            int(c.most), ptr<int32_t>(c.context), ptr<int32_t>(starts), ptr<int32_t>(lengths),
                            ptr<int32_t>(err), stream_of(dev));
@@ -435,7 +446,8 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
         (a[11] != Py_None && !PyFloat_Check(a[11])))
         return none();
     int over = 0;
-    const long window = PyLong_AsLongAndOverflow(a[9], &over), sinks = over ? -1 : PyLong_AsLongAndOverflow(a[10], &over);
+    const long window = PyLong_AsLongAndOverflow(a[9], &over);
+    const long sinks = over ? -1 : PyLong_AsLongAndOverflow(a[10], &over);
     if (over || window < 0 || sinks < 0) return none();
     return guarded([&]() -> PyObject* {
         int dev = -1;

@@ -29,7 +29,8 @@ namespace qkp {
 struct Args {
     const void *q, *k, *v;
     void *qo, *ko, *kc, *vc;
-    int64_t ldq, ldk, ldv;  // elements from a token to the next
+    int64_t ldq, ldk, ldv;        // elements from a token to the next
+    int64_t axis_step, row_step;  // of the positions: from an axis, from a token to the next
     const float *qw, *kw, *freqs;
     const int32_t *positions, *axis, *table, *context, *starts, *lengths;
     int32_t* err;
@@ -53,7 +54,9 @@ __device__ inline Four get4(const __nv_bfloat16* p) {
     return {pack2(__uint_as_float(t.x << 16), __uint_as_float(t.x & 0xFFFF0000u)),
             pack2(__uint_as_float(t.y << 16), __uint_as_float(t.y & 0xFFFF0000u))};
 }
-__device__ inline void put4(float* p, const Four& x) { *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(x.lo, x.hi); }
+__device__ inline void put4(float* p, const Four& x) {
+    *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(x.lo, x.hi);
+}
 __device__ inline void put4(__nv_bfloat16* p, const Four& x) {
     float a, b, c, d;
     unpack2(x.lo, a, b);
@@ -164,12 +167,13 @@ struct Lane {
         float c[4], s[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            turn(a.positions ? a.positions[int64_t(axis[j]) * a.N + n] : at, turns[j], c[j], s[j]);
+            turn(a.positions ? a.positions[axis[j] * a.axis_step + n * a.row_step] : at, turns[j], c[j], s[j]);
         co = {pack2(c[0], c[1]), pack2(c[2], c[3])};
         si = {pack2(s[0], s[1]), pack2(s[2], s[3])};
         minus = {pack2(-s[0], -s[1]), pack2(-s[2], -s[3])};
     }
-    // Norm and rotation of a head's columns; wx, wy the weights.  (A lane without a head takes part in the sum of none.)
+    // Norm and rotation of a head's columns; wx, wy the weights.  (A lane without a head takes part in the sum of
+    // none.)
     __device__ void finish(const Args& a, Four& x, Four& y, const Four& wx, const Four& wy) const {
         if (a.norm != CANOPY_NORM_NONE) {
             float ss = sum4(fma4(x, x, y * y));
@@ -291,7 +295,8 @@ __global__ void __launch_bounds__(128, 5) prep_many_kernel(const Args a) {
         Four wx, wy;
         lane.weights(weight, wx, wy);
         for (; s < end; s += IT, in += IT * STEP, out += IT * out_step) {
-            const int left = (heads - s * L::HEADS - lane.sub + L::HEADS - 1) / L::HEADS;  // sets in which this lane has a head
+            // sets in which this lane has a head, and sets of this batch
+            const int left = (heads - s * L::HEADS - lane.sub + L::HEADS - 1) / L::HEADS;
             const int many = min(IT, end - s);
             Four x[IT], y[IT];
 #pragma unroll
@@ -350,13 +355,14 @@ cudaError_t launch(Args a, cudaStream_t st) {
 
 cudaError_t launch_qk_prep(const void* q, const void* k, const void* v, int bf16, int64_t ldq, int64_t ldk,
                            int64_t ldv, int norm, const float* qw, const float* kw, float eps, const float* freqs,
-                           int R, const int32_t* positions, int axes, const int32_t* axis, int adjacent, int N, int B,
-                           int HQ, int HKV, int d, void* qo, void* ko, void* kc, void* vc, const int32_t* table,
-                           int pages, int log_page, int max_pages, const int32_t* context, const int32_t* starts,
-                           const int32_t* lengths, int32_t* err, cudaStream_t st) {
-    qkp::Args a = {q, k, v, qo, ko, kc, vc, ldq, ldk, ldv, qw, kw, freqs, positions, axis, table, context, starts,
-                   lengths, err, eps, norm, R, adjacent, axes, N, B ? N / B : N, B, HQ, HKV, pages, log_page,
-                   max_pages, 0, 0};
+                           int R, const int32_t* positions, int axes, int64_t axis_step, int64_t row_step,
+                           const int32_t* axis, int adjacent, int N, int B, int HQ, int HKV, int d, void* qo, void* ko,
+                           void* kc, void* vc, const int32_t* table, int pages, int log_page, int max_pages,
+                           const int32_t* context, const int32_t* starts, const int32_t* lengths, int32_t* err,
+                           cudaStream_t st) {
+    qkp::Args a = {q, k, v, qo, ko, kc, vc, ldq, ldk, ldv, axis_step, row_step, qw, kw, freqs, positions, axis, table,
+                   context, starts, lengths, err, eps, norm, R, adjacent, axes, N, B ? N / B : N, B, HQ, HKV, pages,
+                   log_page, max_pages, 0, 0};
     using bf = __nv_bfloat16;
     if (bf16) return d == 128 ? qkp::launch<bf, 128>(a, st) : qkp::launch<bf, 64>(a, st);
     return d == 128 ? qkp::launch<float, 128>(a, st) : qkp::launch<float, 64>(a, st);

@@ -372,8 +372,10 @@ typedef enum { CANOPY_PAIRS_HALF = 0, CANOPY_PAIRS_ADJACENT = 1 } canopy_pairs;
  *   NULL (NULL with CANOPY_NORM_NONE).
  *   freqs device fp32 [R/2] (NULL for R = 0): pair j of the first R columns
  *   (R a multiple of 8, at most d) turns by position * freqs[j]; pairs are columns
- *   (j, j + R/2), or (2j, 2j + 1) with CANOPY_PAIRS_ADJACENT.  positions device int32
- *   [axes][N], or NULL for the token's place in the cache; axis device int32
+ *   (j, j + R/2), or (2j, 2j + 1) with CANOPY_PAIRS_ADJACENT.  positions device int32,
+ *   token n's on axis a at positions[a * axis_step + n * row_step] (N and 1 for
+ *   [axes][N]; 0 for axes that are alike), or NULL for the token's place in the
+ *   cache; axis device int32
  *   [R/2], the axis whose position pair j turns by (a value outside
  *   [0, axes) is read as the nearest), or NULL for axis 0.
  *   q_out [N][HQ][d] (may be q, where that is dense).  With caches, keys and
@@ -387,7 +389,8 @@ typedef enum { CANOPY_PAIRS_HALF = 0, CANOPY_PAIRS_ADJACENT = 1 } canopy_pairs;
 canopy_status canopy_qk_prep(const void* q, const void* k, const void* v, canopy_dtype dtype, int64_t ldq,
                              int64_t ldk, int64_t ldv, canopy_norm norm, const float* q_weight,
                              const float* k_weight, float eps, const float* freqs, int R, const int32_t* positions,
-                             int axes, const int32_t* axis, canopy_pairs pairs, int N, int B, int HQ, int HKV, int d,
+                             int axes, int64_t axis_step, int64_t row_step, const int32_t* axis,
+                             canopy_pairs pairs, int N, int B, int HQ, int HKV, int d,
                              void* q_out, void* k_out, void* k_cache, void* v_cache, const int32_t* page_table,
                              int pages, int page_size, int max_pages, const int32_t* context, const int32_t* starts,
                              const int32_t* lengths, int32_t* err, void* stream);

@@ -74,9 +74,11 @@ def test_qk_prep_refused(canopy):
     lib = canopy.load()
 
     def call(q=P[0], k=P[1], v=P[2], dt=1, ldq=512, ldk=256, ldv=256, norm=1, qw=P[3], kw=P[4], eps=1e-6, freqs=P[5],
-             R=64, positions=None, axes=1, axis=None, pairs=0, N=8, B=2, HQ=4, HKV=2, d=128, qo=P[6], ko=None,
+             R=64, positions=None, axes=1, steps=(8, 1), axis=None, pairs=0, N=8, B=2, HQ=4, HKV=2, d=128, qo=P[6],
+             ko=None,
              kc=P[7], vc=P[8], table=P[9], pages=9, ps=64, most=4, ctx=P[10], starts=P[11], lengths=None, err=None):
-        return lib.canopy_qk_prep(q, k, v, dt, ldq, ldk, ldv, norm, qw, kw, eps, freqs, R, positions, axes, axis,
+        return lib.canopy_qk_prep(q, k, v, dt, ldq, ldk, ldv, norm, qw, kw, eps, freqs, R, positions, axes, *steps,
+                                  axis,
                                   pairs, N, B, HQ, HKV, d, qo, ko, kc, vc, table, pages, ps, most, ctx, starts,
                                   lengths, err, None)
 
@@ -84,12 +86,14 @@ def test_qk_prep_refused(canopy):
     for kw in (dict(q=None), dict(k=ODD16), dict(v=None), dict(qo=None), dict(vc=None), dict(table=None),
                dict(ctx=None), dict(ko=P[12]), dict(dt=2), dict(norm=3), dict(norm=0), dict(pairs=2), dict(eps=-1.0),
                dict(eps=float("nan")), dict(R=-8), dict(R=136), dict(R=0), dict(freqs=None), dict(axis=P[13]),
-               dict(positions=P[13], axes=0), dict(ldq=504), dict(ldk=260), dict(ldv=255), dict(qw=ODD16),
+               dict(positions=P[13], axes=0), dict(positions=P[13], steps=(-1, 1)),
+               dict(positions=P[13], steps=(8, -1)), dict(ldq=504), dict(ldk=260), dict(ldv=255), dict(qw=ODD16),
                dict(lengths=P[13]), dict(starts=None, N=9), dict(N=0), dict(HKV=3), dict(err=ODD4),
                dict(R=0, freqs=None, positions=P[13]), dict(bare, ko=None), dict(bare, v=P[2]), dict(bare, starts=P[3]),
                dict(bare, positions=None), dict(bare, B=1)):
         assert call(**kw) == 1, kw
-    for kw in (dict(R=60), dict(d=32, ldq=512, R=8), dict(ps=8), dict(ps=48), dict(B=70000), dict(HQ=130, ldq=130 * 128)):
+    for kw in (dict(R=60), dict(d=32, ldq=512, R=8), dict(ps=8), dict(ps=48), dict(B=70000),
+               dict(HQ=130, ldq=130 * 128)):
         assert call(**kw) == 3, kw
 
 
@@ -177,14 +181,16 @@ def test_combinations_that_are_refused(canopy, no_calls):
     starts = on(0, 3, dtype=torch.int32)
     packed = on(0, 9, 4, 64)
     for kw in (dict(starts=starts), dict(q=packed, out=None), dict(q=packed, out=None, starts=starts),
-               dict(q=packed, out=None, parent=None, starts=starts), dict(q=packed, out=None, parent=None, lengths=None),
+               dict(q=packed, out=None, parent=None, starts=starts),
+               dict(q=packed, out=None, parent=None, lengths=None),
                dict(q=a["q"].half()), dict(k_cache=a["k_cache"].bfloat16()), dict(ws=on(0, 4, dtype=torch.uint8)),
                dict(window=2 ** 31)):
         with pytest.raises(canopy.CanopyError):
             canopy.attend(**{**a, **kw})
     p = {n: on(0, *s, dtype=dtype_of(n)) for n, s in PREP.items()}
     for kw in (dict(k_out=p["k"]), dict(v=None), dict(k_cache=None), dict(starts=starts),
-               dict(positions=on(0, 2, 2, dtype=torch.int32)), dict(q=p["q"].transpose(1, 2).contiguous().transpose(1, 2))):
+               dict(positions=on(0, 2, 2, dtype=torch.int32)),
+               dict(q=p["q"].transpose(1, 2).contiguous().transpose(1, 2))):
         with pytest.raises(canopy.CanopyError):
             canopy.qk_prep(**{**p, **kw})
 

@@ -54,6 +54,32 @@ def test_prep_without_a_cache(lib, N, HQ, HKV, d, norm, rot, axes, pairs, bf16):
         assert (off <= prep_bound(x[src], ref, x[w], bf16, d)).all()
 
 
+@pytest.mark.parametrize("how", ["expanded", "transposed", "spaced"])
+def test_prep_positions_of_any_layout(lib, how, monkeypatch):
+    """Axes that are alike by expansion, axes last in memory, tokens apart: the results of dense positions."""
+    x = prep_inputs(4, 60, 4, 2, 64, False, 32, 3, "none")
+    q, k = tensor(x["q"]).view(5, 12, 4, 64), tensor(x["k"]).view(5, 12, 2, 64)
+    dense = tensor(x["positions"]).view(3, 5, 12)
+    if how == "expanded":
+        laid = dense[1].expand(3, 5, 12)
+        dense = laid.contiguous()
+    elif how == "transposed":
+        laid = dense.permute(1, 2, 0).contiguous().permute(2, 0, 1)
+    else:
+        laid = torch.zeros(3, 5, 12, 2, dtype=torch.int32, device="cuda")[..., 0]
+        laid.copy_(dense)
+    assert not laid.is_contiguous()
+    args = dict(norm="none", freqs=tensor(x["freqs"]), axis=tensor(x["axis"]))
+    ref = lib.qk_prep(q, k, positions=dense, **args)
+    got = lib.qk_prep(q, k, positions=laid, **args)
+    monkeypatch.setattr(lib, "_marshal", type("Stub", (), {"qk_prep": staticmethod(lambda *a: None)}))
+    py = lib.qk_prep(q, k, positions=laid, **args)
+    for a, b, c in zip(ref, got, py):
+        assert torch.equal(a, b) and torch.equal(a, c)
+    with pytest.raises(lib.CanopyError, match="distance"):
+        lib.qk_prep(q, k, positions=torch.zeros(3, 5, 24, dtype=torch.int32, device="cuda")[..., :12], **args)
+
+
 def test_prep_far_positions(lib):
     """Angles of positions near 2^31 and of negative ones keep their precision."""
     x = prep_inputs(3, 64, 2, 2, 128, False, 128, 1, "none")

@@ -220,19 +220,19 @@ __device__ inline bool place_of(const Args& a, int n, int& at, int64_t& slot) {
     int bad = 0, i = 0;
     const int b = sequence_of(a, n, i, &bad);
     if (b >= 0) {
-        int ctx = a.context[b];
-        if (ctx < 0) {
-            bad |= CANOPY_DEVERR_LENGTH;
-            ctx = 0;
-        }
-        const int64_t pos = int64_t(ctx) + i;
+        const int ctx = a.context[b];
+        const int64_t pos = int64_t(ctx < 0 ? 0 : ctx) + i;
         at = int(pos < 0x7FFFFFFF ? pos : 0x7FFFFFFF);
-        const int64_t entry = pos >> a.log_page;
-        const int page = entry < a.max_pages ? a.table[int64_t(b) * a.max_pages + entry] : -1;
-        if (page < 0 || page >= a.pages)
-            bad |= CANOPY_DEVERR_PAGE;
-        else
-            slot = ((int64_t(page) * a.HKV) << a.log_page) + (pos & ((1 << a.log_page) - 1));
+        if (ctx < 0) {  // (its first places hold tokens: only the queries go on, from place 0)
+            bad |= CANOPY_DEVERR_LENGTH;
+        } else {
+            const int64_t entry = pos >> a.log_page;
+            const int page = entry < a.max_pages ? a.table[int64_t(b) * a.max_pages + entry] : -1;
+            if (page < 0 || page >= a.pages)
+                bad |= CANOPY_DEVERR_PAGE;
+            else
+                slot = ((int64_t(page) * a.HKV) << a.log_page) + (pos & ((1 << a.log_page) - 1));
+        }
     }
     if (bad && (threadIdx.x & 31) == 0 && a.err) raise_err(a.err, bad);
     return b >= 0;

@@ -113,7 +113,7 @@ typedef enum {
 #define CANOPY_DEVERR_GATE     0x2  /* g <= 0 (prefill, step: < 0), g or beta not finite */
 #define CANOPY_DEVERR_ACCEPTED 0x4  /* commit: accepted node not in [-1, T)             */
 #define CANOPY_DEVERR_TIMEOUT  0x8  /* an internal bounded wait gave up                 */
-#define CANOPY_DEVERR_LENGTH   0x10 /* lengths[b] not in [0, T], or starts out of order  */
+#define CANOPY_DEVERR_LENGTH   0x10 /* lengths[b] not in [0, T], starts out of order, a context below zero */
 #define CANOPY_DEVERR_TOKEN    0x20 /* accept: a drafted token not in [0, V)            */
 #define CANOPY_DEVERR_PAGE     0x40 /* a place beyond the page table, or a page not in [0, pages) */
 
@@ -384,8 +384,9 @@ typedef enum { CANOPY_PAIRS_HALF = 0, CANOPY_PAIRS_ADJACENT = 1 } canopy_pairs;
  *   v, v_cache, page_table, context, starts and lengths are NULL, B 0.
  * Norm and rotation in fp32 (angles of any int32 position to 1e-7), rounded once.
  * err: an optional device int32 (OR-ed): a place without a page sets
- * CANOPY_DEVERR_PAGE and is not written.  Any other value of q_out, k_out and the
- * caches stays as it was. */
+ * CANOPY_DEVERR_PAGE and is not written, nor are the places of a stream whose context
+ * is below zero (CANOPY_DEVERR_LENGTH; its queries are made as from place 0).  Any
+ * other value of q_out, k_out and the caches stays as it was. */
 canopy_status canopy_qk_prep(const void* q, const void* k, const void* v, canopy_dtype dtype, int64_t ldq,
                              int64_t ldk, int64_t ldv, canopy_norm norm, const float* q_weight,
                              const float* k_weight, float eps, const float* freqs, int R, const int32_t* positions,

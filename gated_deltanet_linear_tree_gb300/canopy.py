@@ -181,13 +181,19 @@ def workspace_bytes(B: int, T: int, HV: int, d: int) -> int:
     return int(load().canopy_workspace_bytes(B, T, HV, d, d))
 
 
+def _new_workspace(n: int, cleared: int, device) -> torch.Tensor:
+    """n bytes on `device`, the first of them cleared on its own current stream (the calls' one)."""
+    with torch.cuda.device(device):
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        _check(load().canopy_workspace_init(_ptr(ws), cleared, _stream()), "canopy_workspace_init")
+    return ws
+
+
 def workspace(B: int, T: int, HV: int, d: int, device="cuda") -> torch.Tensor:
     n = workspace_bytes(B, T, HV, d)
     if n == 0:
         raise CanopyError("unsupported sizes for the workspace")
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
-    _check(load().canopy_workspace_init(_ptr(ws), n, _stream()), "canopy_workspace_init")
-    return ws
+    return _new_workspace(n, n, device)
 
 
 def workspace_views(ws, B: int, T: int, HV: int, d: int) -> dict:
@@ -388,9 +394,7 @@ def prefill_workspace(N: int, B: int, HV: int, d: int, device="cuda") -> torch.T
     n = int(load().canopy_prefill_workspace_bytes(N, B, HV, d, d))
     if n == 0:
         raise CanopyError("unsupported sizes for the prefill workspace")
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
-    _check(load().canopy_workspace_init(_ptr(ws), 256, _stream()), "canopy_workspace_init")
-    return ws
+    return _new_workspace(n, 256, device)
 
 
 def prefill(q, k, v, g, beta, S0, starts, ws, o_dtype=torch.float32, out=None, S_out=None, scale: float = 1.0,
@@ -642,9 +646,7 @@ def attend_workspace(N: int, B: int, HQ: int, HKV: int, d: int, device="cuda") -
     n = int(load().canopy_attend_workspace_bytes(N, B, HQ, HKV, d))
     if n == 0:
         raise CanopyError("unsupported sizes for the attend workspace")
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
-    _check(load().canopy_workspace_init(_ptr(ws), 4096, _stream()), "canopy_workspace_init")
-    return ws
+    return _new_workspace(n, 4096, device)
 
 
 def attend_plan(N: int, B: int, HQ: int, HKV: int, bf16: bool, d: int) -> str:

@@ -782,7 +782,9 @@ def conv_commit(accepted, x, parent, conv_state, out=None, err=None):
 
 
 def read_device_error(ws) -> int:
-    """Synchronise the current stream, return and clear the device error word."""
+    """Synchronise the current stream of the workspace's device, return and
+    clear the device error word."""
     err = ctypes.c_int32(0)
-    _check(load().canopy_read_device_error(_ptr(ws), ctypes.byref(err), _stream()), "canopy_read_device_error")
+    with torch.cuda.device(ws.device):
+        _check(load().canopy_read_device_error(_ptr(ws), ctypes.byref(err), _stream()), "canopy_read_device_error")
     return int(err.value)

@@ -69,3 +69,14 @@ def test_on_the_current_device_by_default(world, name):
     with torch.cuda.device(3):
         getattr(canopy, name)(*MAKE[name])
     assert log == [("allocate", 3), ("clear", 3, ("stream of", 3))]
+
+
+def test_error_word_read_on_the_workspaces_device(world, monkeypatch):
+    """...behind the calls of that device's stream, which set its bits."""
+    canopy, log = world
+    ws = torch.zeros(8, dtype=torch.uint8).as_subclass(type("OnGpu", (torch.Tensor,), {"get_device": lambda t: 1,
+                                                                                        "device": torch.device("cuda", 1)}))
+    lib = type("Lib", (), {"canopy_read_device_error": staticmethod(lambda p, e, stream: log.append(stream) or 0)})
+    monkeypatch.setattr(canopy, "load", lambda: lib)
+    assert canopy.read_device_error(ws) == 0
+    assert log == [("stream of", 1)]

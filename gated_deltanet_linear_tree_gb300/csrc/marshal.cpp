@@ -91,6 +91,15 @@ bool ints(std::initializer_list<int64_t> sizes) {
     return true;
 }
 
+// A Python int that fits a C int (asked while this thread still holds the interpreter's lock).
+bool int_of(PyObject* obj, int& x) {
+    if (!PyLong_Check(obj)) return false;
+    int over = 0;
+    const long y = PyLong_AsLongAndOverflow(obj, &over);
+    x = int(y);
+    return !over && x == y;
+}
+
 // The output given as obj, if it fits; None stays undefined for now.
 bool output(PyObject* obj, int dev, at::ScalarType type, std::initializer_list<int64_t> shape, at::Tensor& out) {
     if (obj == Py_None) return true;
@@ -353,7 +362,8 @@ bool rows_output(PyObject* obj, int dev, at::ScalarType type, const Rows& r, int
 // qk_prep(q, k, v, norm, q_weight, k_weight, eps, freqs, positions, axis, pairs, q_out, k_out, k_cache, v_cache,
 //         page_table, context, starts, lengths, err)
 PyObject* qk_prep(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (n != 20 || !qk_prep_fn || !PyLong_Check(a[3]) || !PyFloat_Check(a[6]) || !PyLong_Check(a[10])) return none();
+    int norm = 0, pairs = 0;
+    if (n != 20 || !qk_prep_fn || !int_of(a[3], norm) || !PyFloat_Check(a[6]) || !int_of(a[10], pairs)) return none();
     return guarded([&]() -> PyObject* {
         if (!THPVariable_Check(a[0]) || !THPVariable_Check(a[1])) return none();
         const at::Tensor &q0 = THPVariable_Unpack(a[0]), &k0 = THPVariable_Unpack(a[1]);
@@ -421,9 +431,9 @@ PyObject* qk_prep(PyObject*, PyObject* const* a, Py_ssize_t n) {
             if (!q_out.defined()) q_out = fresh_rows(r, HQ, d, st, dev);
             if (!cached && !k_out.defined()) k_out = fresh_rows(r, HKV, d, st, dev);
             s = qk_prep_fn(q->data_ptr(), k->data_ptr(), ptr<void>(v), type, ldq, ldk, ldv,
-                           canopy_norm(PyLong_AsLong(a[3])), ptr<float>(qw), ptr<float>(kw),
+                           canopy_norm(norm), ptr<float>(qw), ptr<float>(kw),
                            float(PyFloat_AS_DOUBLE(a[6])), ptr<float>(freqs), int(2 * half), ptr<int32_t>(positions),
-                           int(axes), axis_step, row_step, ptr<int32_t>(axis), canopy_pairs(PyLong_AsLong(a[10])),
+                           int(axes), axis_step, row_step, ptr<int32_t>(axis), canopy_pairs(pairs),
                            int(r.n), int(c.B), int(HQ), int(HKV), int(d), q_out.data_ptr(),
                            cached ? nullptr : k_out.data_ptr(),
                            ptr<void>(c.k), ptr<void>(c.v), ptr<int32_t>(c.table), int(c.pages), int(c.page),
@@ -442,13 +452,10 @@ PyObject* qk_prep(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // attend(q, k_cache, v_cache, page_table, context, ws, starts, parent, lengths, window, sinks, scale, out)
 PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (n != 13 || !attend_fn || !PyLong_Check(a[9]) || !PyLong_Check(a[10]) ||
+    int window = 0, sinks = 0;
+    if (n != 13 || !attend_fn || !int_of(a[9], window) || !int_of(a[10], sinks) || window < 0 || sinks < 0 ||
         (a[11] != Py_None && !PyFloat_Check(a[11])))
         return none();
-    int over = 0;
-    const long window = PyLong_AsLongAndOverflow(a[9], &over);
-    const long sinks = over ? -1 : PyLong_AsLongAndOverflow(a[10], &over);
-    if (over || window < 0 || sinks < 0) return none();
     return guarded([&]() -> PyObject* {
         int dev = -1;
         const at::Tensor *q = plain(a[0], dev), *k = plain(a[1], dev), *ws = plain(a[5], dev);
@@ -462,7 +469,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const bool packed = a[6] != Py_None;
         Cache c;
         if (!cache_of(a[1], a[2], a[3], a[4], dev, st, HKV, d, c) || !of_streams(r, c.B, packed) ||
-            !ints({r.n, HQ, HKV, d, window, sinks}) || (r.lead.size() != 2 && (a[7] != Py_None || a[8] != Py_None)))
+            !ints({r.n, HQ, HKV, d}) || (r.lead.size() != 2 && (a[7] != Py_None || a[8] != Py_None)))
             return none();
         bool ok = true;
         const at::Tensor* starts = maybe(a[6], dev, at::kInt, {c.B + 1}, ok);
@@ -481,7 +488,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
             s = attend_fn(q->data_ptr(), type, c.k->data_ptr(), c.v->data_ptr(), ptr<int32_t>(c.table), int(c.pages),
                           int(c.page), int(c.most), ptr<int32_t>(c.context), ptr<int32_t>(starts),
                           ptr<int32_t>(parent), ptr<int32_t>(lengths), int(r.n), int(c.B), int(HQ), int(HKV), int(d),
-                          int(window), int(sinks), scale, out.data_ptr(), ws->data_ptr(), stream_of(dev));
+                          window, sinks, scale, out.data_ptr(), ws->data_ptr(), stream_of(dev));
         }
         if (s != CANOPY_OK) return PyLong_FromLong(s);
         return a[12] == Py_None ? THPVariable_Wrap(out) : Py_NewRef(a[12]);

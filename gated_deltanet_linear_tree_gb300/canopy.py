@@ -666,8 +666,8 @@ def attend(q, k_cache, v_cache, page_table, context, ws, starts=None, parent=Non
     before it and the new ones up to itself, or on its root path; with window > 0
     only those less than window positions before it and the first `sinks`.
     k_cache, v_cache [pages, HKV, page_size, d], page_table int32
-    [B, max_pages].  scale: d ** -0.5 unless given.  ws: attend_workspace for at
-    least these sizes."""
+    [B, max_pages].  scale: d ** -0.5 unless given.  out lies apart from q and the
+    caches.  ws: attend_workspace for at least these sizes."""
     if _marshal is None:
         load()
     r = _marshal.attend(q, k_cache, v_cache, page_table, context, ws, starts, parent, lengths, window, sinks, scale,

@@ -183,6 +183,12 @@ canopy_prefill_plan_t prefill_plan(int N, int B, int HV, canopy_dtype in_dtype, 
 bool dtype_ok(canopy_dtype t) { return t == CANOPY_F32 || t == CANOPY_BF16; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// Whether two pieces of memory share none (an absent one shares none).
+bool apart(const void* a, size_t an, const void* b, size_t bn) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return !a || !b || x + an <= y || y + bn <= x;
+}
+
 // Sizes of an attention layer's call: rows, sequences, heads.
 canopy_status layer_sizes(int N, int B, int HQ, int HKV, int d) {
     if (N <= 0 || B <= 0 || !heads_ok(HKV, HQ)) return CANOPY_ERR_ARG;
@@ -440,6 +446,21 @@ canopy_status canopy_qk_prep(const void* q, const void* k, const void* v, canopy
         if (cs != CANOPY_OK) return cs;
         if (starts ? lengths != nullptr : N % B != 0) return CANOPY_ERR_ARG;
     }
+    // outputs lie apart from the inputs and each other, but for q and k made in place
+    const size_t es = dtype == CANOPY_BF16 ? 2 : 4;
+    const auto span = [&](int64_t ld, int H) { return (size_t(N - 1) * ld + size_t(H) * d) * es; };
+    const size_t rq = span(ldq, HQ), rk = span(ldk, HKV), rv = span(ldv, HKV);
+    const size_t nq = size_t(N) * HQ * d * es, nk = size_t(N) * HKV * d * es;
+    if (!(q_out == q && rq == nq) && !apart(q_out, nq, q, rq)) return CANOPY_ERR_ARG;
+    if (!(k_out == k && rk == nk) && !apart(k_out, nk, k, rk)) return CANOPY_ERR_ARG;
+    if (!apart(q_out, nq, k, rk) || !apart(q_out, nq, v, rv) || !apart(k_out, nk, q, rq) ||
+        !apart(q_out, nq, k_out, nk))
+        return CANOPY_ERR_ARG;
+    const size_t cache = cached ? size_t(pages) * HKV * page_size * d * es : 0;
+    if (!apart(k_cache, cache, v_cache, cache)) return CANOPY_ERR_ARG;
+    for (const void* c : {static_cast<const void*>(k_cache), static_cast<const void*>(v_cache)})
+        if (!apart(c, cache, q, rq) || !apart(c, cache, k, rk) || !apart(c, cache, v, rv) || !apart(c, cache, q_out, nq))
+            return CANOPY_ERR_ARG;
     return cuda_status(launch_qk_prep(q, k, v, dtype == CANOPY_BF16, ldq, ldk, ldv, norm, q_weight, k_weight, eps,
                                       freqs, R, positions, axes, axis_step, row_step, axis,
                                       pairs == CANOPY_PAIRS_ADJACENT, N, B, HQ, HKV, d, q_out, k_out, k_cache, v_cache,
@@ -474,6 +495,10 @@ canopy_status canopy_attend(const void* q, canopy_dtype dtype, const void* k_cac
     if (cs != CANOPY_OK) return cs;
     if (starts ? parent || lengths : N % B != 0) return CANOPY_ERR_ARG;
     if (parent && N / B > kMaxT) return CANOPY_ERR_UNSUPPORTED;
+    const size_t es = dtype == CANOPY_BF16 ? 2 : 4, rows = size_t(N) * HQ * d * es;
+    const size_t cache = size_t(pages) * HKV * page_size * d * es;
+    if (!apart(o, rows, q, rows) || !apart(o, rows, k_cache, cache) || !apart(o, rows, v_cache, cache))
+        return CANOPY_ERR_ARG;
     return cuda_status(launch_attend(q, dtype == CANOPY_BF16, k_cache, v_cache, page_table, pages, log_page,
                                      max_pages, context, starts, parent, lengths, N, B, HQ, HKV, d, window, sinks,
                                      scale, o, workspace, static_cast<cudaStream_t>(stream)));
@@ -485,7 +510,7 @@ canopy_status canopy_cache_commit(const int32_t* accepted, const int32_t* parent
                                   int HKV, int d, int32_t* context_new, int32_t* err, void* stream) {
     if (!accepted || !aligned4(accepted) || !parent || !aligned4(parent) || !aligned4(lengths) ||
         !aligned16(k_cache) || !aligned16(v_cache) || !page_table || !aligned4(page_table) || !context ||
-        !aligned4(context) || !context_new || !aligned4(context_new) || context_new == context || !aligned4(err))
+        !aligned4(context) || !context_new || !aligned4(context_new) || !aligned4(err))
         return CANOPY_ERR_ARG;
     if (!dtype_ok(dtype) || T <= 0) return CANOPY_ERR_ARG;
     const canopy_status as = layer_sizes(1, B, HKV, HKV, d);
@@ -494,6 +519,11 @@ canopy_status canopy_cache_commit(const int32_t* accepted, const int32_t* parent
     const canopy_status cs = cache_sizes(pages, page_size, max_pages, HKV, log_page);
     if (cs != CANOPY_OK) return cs;
     if (T > kMaxT) return CANOPY_ERR_UNSUPPORTED;
+    const size_t cache = size_t(pages) * HKV * page_size * d * (dtype == CANOPY_BF16 ? 2 : 4), n = size_t(B) * 4;
+    if (!apart(k_cache, cache, v_cache, cache) || !apart(context_new, n, context, n) ||
+        !apart(context_new, n, accepted, n) || !apart(context_new, n, lengths, n) ||
+        !apart(context_new, n, parent, n * T))
+        return CANOPY_ERR_ARG;
     return cuda_status(launch_cache_commit(accepted, parent, lengths, k_cache, v_cache, dtype == CANOPY_BF16,
                                            page_table, pages, log_page, max_pages, context, T, B, HKV, d,
                                            context_new, err, static_cast<cudaStream_t>(stream)));

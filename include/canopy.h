@@ -378,7 +378,8 @@ typedef enum { CANOPY_PAIRS_HALF = 0, CANOPY_PAIRS_ADJACENT = 1 } canopy_pairs;
  *   cache; axis device int32
  *   [R/2], the axis whose position pair j turns by (a value outside
  *   [0, axes) is read as the nearest), or NULL for axis 0.
- *   q_out [N][HQ][d] (may be q, where that is dense).  With caches, keys and
+ *   q_out [N][HQ][d] (may be q, where that is dense; outputs and caches lie apart
+ *   from the inputs and each other otherwise, or the call is refused).  With caches, keys and
  *   values go into them, k_out is NULL and v, page_table and context are given.
  *   Without (k_cache NULL), k_out [N][HKV][d] (may be k) receives the keys, and
  *   v, v_cache, page_table, context, starts and lengths are NULL, B 0.
@@ -419,7 +420,8 @@ canopy_attend_plan_t canopy_attend_plan(int N, int B, int HQ, int HKV, canopy_dt
  * and starts NULL, as canopy_tree_verify takes it) the places j < c and those of its
  * root path, itself among them.  With window > 0 of these only the tokens whose
  * position is less than window before t_i, and those at positions < sinks.
- *   scale > 0; q, o [N][HQ][d] in dtype (o not q); the places that no row of a sequence sees (behind its
+ *   scale > 0; q, o [N][HQ][d] in dtype (o apart from q and the caches, or the call
+ *   is refused); the places that no row of a sequence sees (behind its
  *   last row, out of the window) need no page and may hold anything; what a place
  *   holds reaches no row that does not see it (where rows see different places, a
  *   bf16 row that sees a value that is not finite may be NaN throughout).
@@ -436,7 +438,7 @@ canopy_status canopy_attend(const void* q, canopy_dtype dtype, const void* k_cac
 /* The cache after accepting node accepted[b] of every stream's tree (as
  * canopy_commit takes it): the accepted node's root path, whose keys and values
  * lie at places context[b] + node, moves to context[b] + 0, 1, 2, ... in depth
- * order, in place, and context_new[b] (device int32 [B], not context itself) =
+ * order, in place, and context_new[b] (device int32 [B], apart from the inputs) =
  * context[b] + the path's length.  accepted -1 keeps nothing of the tree; an
  * accepted node out of range sets CANOPY_DEVERR_ACCEPTED in *err and does the same.
  * parent device int32 [B][T], T <= 256; lengths as canopy_tree_verify takes it. */

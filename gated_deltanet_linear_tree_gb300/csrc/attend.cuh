@@ -324,6 +324,10 @@ __device__ inline uint32_t pack_bf16(float a, float b) {
     return r;
 }
 
+// The first and the second of a pair of bf16 values.
+__device__ inline float first_of(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ inline float second_of(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
+
 // Bits [a, b) of a word.
 __device__ inline uint32_t range_bits(int a, int b) {
     a = min(max(a, 0), 32);
@@ -348,8 +352,42 @@ __device__ inline uint32_t seen_bits(const Args& a, const Tile& tile, int depth,
     return bits;
 }
 
+// Of a pair of bf16 values: whether both are finite, and the pair with those that are not as zeros.
 __device__ inline bool finite_pair(uint32_t x) {
     return (x & 0x7F80u) != 0x7F80u && (x & 0x7F800000u) != 0x7F800000u;
+}
+__device__ inline uint32_t finite_part(uint32_t x) {
+    return x & (((x & 0x7F80u) != 0x7F80u ? 0x0000FFFFu : 0u) | ((x & 0x7F800000u) != 0x7F800000u ? 0xFFFF0000u : 0u));
+}
+
+// What the products leave out for a row that sees it: the values that are not
+// finite, in the tiles of [u0, u1) whose keys the tile's rows see in part.  They go
+// to the row's sums behind the last product, add(c, x) for the column pairs c =
+// first, first + step, ... < d (x: two bf16 values, the finite ones zero), read from
+// the pages again: a row that sees such a value is rare.
+template <typename Add>
+__device__ inline void add_not_finite(const Args& a, const Piece& p, int depth, const uint32_t* mask, int d, int first,
+                                      int step, Add add) {
+    const uint32_t* vc = static_cast<const uint32_t*>(a.vc);
+#pragma unroll 1
+    for (int u = p.u0; u < p.u1; ++u) {
+        const int kt = key_tile(p.tile, u);
+        if (all_see(p.tile, kt)) continue;
+        const int end = min((kt + 1) * a.kt, p.tile.hi);
+#pragma unroll 1
+        for (int key = kt * a.kt; key < end; ++key) {
+            if (!(seen_bits(a, p.tile, depth, mask, key) & 1u)) continue;
+            const int page = a.table[size_t(p.tile.b) * a.max_pages + (key >> a.log_page)];
+            if (page < 0 || page >= a.pages) continue;
+            const uint32_t* row =
+                vc + (((size_t(page) * a.HKV + p.h) << a.log_page) + (key & ((1 << a.log_page) - 1))) * (d / 2);
+#pragma unroll 1
+            for (int c = first; c < d / 2; c += step) {
+                const uint32_t x = row[c];
+                if (!finite_pair(x)) add(c, x ^ finite_part(x));
+            }
+        }
+    }
 }
 
 // A wait of a whole warp, which goes on or gives up together.

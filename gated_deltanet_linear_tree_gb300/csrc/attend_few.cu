@@ -38,6 +38,7 @@ struct Smem {
     uint8_t kv[STAGES][2][TILE];
     float other[16][D + 4];  // the second warp's sums (rows on other banks)
     float other_m[16], other_l[16];
+    uint32_t other_left;  // rows of which its products left out a value that they see
     int4 seqs[kPlanSeqs + 1];
     int64_t line[kPlanTiles + 1];
     uint64_t full[STAGES], empty[STAGES], given, taken;
@@ -66,9 +67,6 @@ __device__ inline void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t 
 // Keeps of a pair of values (two keys of one column) those with a bit.
 __device__ inline uint32_t keep_pair(uint32_t x, uint32_t bits) {
     return x & ((bits & 1 ? 0x0000FFFFu : 0u) | (bits & 2 ? 0xFFFF0000u : 0u));
-}
-__device__ inline uint32_t bad_pair(uint32_t x) {
-    return uint32_t((x & 0x7F80u) == 0x7F80u) | (uint32_t((x & 0x7F800000u) == 0x7F800000u) << 1);
 }
 
 template <int D>
@@ -172,6 +170,7 @@ __global__ void __launch_bounds__(NT, 2)
                 }
             }
             float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[D / 8][4];
+            uint32_t left_out = 0;  // which of the 16 rows see a value that their products leave out
 #pragma unroll
             for (int n = 0; n < D / 8; ++n)
 #pragma unroll
@@ -254,19 +253,23 @@ __global__ void __launch_bounds__(NT, 2)
                         l[x] += y + z;
                         w[n >> 1][2 * (n & 1) + x] = pack_bf16(y, z);
                     }
-                if (check) {  // values that are not finite, of keys that not every row sees
+                if (check) {  // values that are not finite, where not every row sees every key
                     uint32_t bad = 0;
                     for (int e = lane; e < 32 * D / 2; e += 32) {
                         const int j = e / (D / 2), c = e % (D / 2);
                         // (the order of a row's chunks does not matter)
-                        const uint32_t x = reinterpret_cast<const uint32_t*>(
+                        uint32_t& x = reinterpret_cast<uint32_t*>(
                             sm.kv[ring.at][1])[(c / 32) * (KT * 32) + (32 * warp + j) * 32 + (c & 31)];
-                        if (bad_pair(x)) bad |= 1u << j;
+                        if (!finite_pair(x)) {
+                            bad |= 1u << j;
+                            x = finite_part(x);
+                        }
                     }
-                    bad = __reduce_or_sync(0xffffffffu, bad) & check;
-                    keep &= ~bad;
-                    if (bad & seen[0]) l[0] = NAN;
-                    if (bad & seen[1]) l[1] = NAN;
+                    bad = __reduce_or_sync(0xffffffffu, bad) & keep;
+                    if (bad & seen[0]) left_out |= 1u << r0;
+                    if (bad & seen[1]) left_out |= 1u << (r0 + 8);
+                    fence_proxy_async_smem();  // (before the stage's next load)
+                    __syncwarp();
                 }
 #pragma unroll
                 for (int n = 0; n < D / 16; ++n)
@@ -312,6 +315,8 @@ __global__ void __launch_bounds__(NT, 2)
                         sm.other_l[r0 + 8 * x] = l[x];
                     }
                 }
+                left_out = __reduce_or_sync(0xffffffffu, left_out);
+                if (lane == 0) sm.other_left = left_out;
                 mbar_arrive(&sm.given);
                 continue;
             }
@@ -350,6 +355,27 @@ __global__ void __launch_bounds__(NT, 2)
                     }
                 }
             }
+            left_out |= sm.other_left;
+            if (left_out)
+#pragma unroll 1
+                for (int x = 0; x < 2; ++x) {
+                    const int r = r0 + 8 * x;
+                    if (!((left_out >> r) & 1u)) continue;
+                    uint32_t* out = reinterpret_cast<uint32_t*>(
+                        static_cast<__nv_bfloat16*>(a.o) +
+                        (size_t(tile.row + r / a.g) * a.HQ + p.h * a.g + r % a.g) * D);
+                    float* sum = a.part + size_t(p.slot) * 16 * (D + 2) + r * D;
+                    add_not_finite(a, p, x ? depth[1] : depth[0], x ? mask[1] : mask[0], D, c0 / 2, 4,
+                                   [&](int c, uint32_t v) {
+                                       if (p.whole) {
+                                           out[c] = pack_bf16(first_of(out[c]) + first_of(v),
+                                                              second_of(out[c]) + second_of(v));
+                                       } else {
+                                           sum[2 * c] += first_of(v);
+                                           sum[2 * c + 1] += second_of(v);
+                                       }
+                                   });
+                }
             mbar_arrive(&sm.taken);
         }
     }

@@ -27,8 +27,9 @@
 // in turns.  A page that no row sees is read at a coordinate outside the cache, as
 // zeros.  Where not every row sees every key of a tile, the softmax's warps look
 // through its V first: what no row sees, and what is not finite, becomes zero (0
-// times it would reach every row's sum), and a row that sees a key with such a
-// value is NaN.  (A warp of its own for that took 246 us for the window case.)
+// times it would reach every row's sum), and a row that sees such a value has it
+// added to its sum behind the last product.  (A warp of its own for the look took
+// 246 us for the window case.)
 #include "attend.cuh"
 
 namespace canopy {
@@ -282,6 +283,7 @@ __global__ void __launch_bounds__(NT, 1)
             const uint32_t* mask = a.parent ? a.mask + size_t(row) * kMaskWords : nullptr;
             float m = -INFINITY, base = 0.f;  // the maximum that the weights are relative to, scaled
             float l = 0.f;
+            bool left_out = false;  // the row sees a value that its products leave out
             for (int u = p.u0; u < p.u1; ++u) {
                 const int kt = key_tile(tile, u), key = kt * KT;
                 const bool all = all_see(tile, kt);
@@ -324,7 +326,8 @@ __global__ void __launch_bounds__(NT, 1)
                             const bool there = in_reach(tile, key + ROWS * w + j);
                             if (there && finite_pair(x.x) && finite_pair(x.y) && finite_pair(x.z) && finite_pair(x.w))
                                 continue;
-                            *at = make_uint4(0, 0, 0, 0);
+                            *at = there ? make_uint4(finite_part(x.x), finite_part(x.y), finite_part(x.z), finite_part(x.w))
+                                        : make_uint4(0, 0, 0, 0);
                             if (there) bad |= 1u << j;
                         }
                         bad = __reduce_or_sync(0xffffffffu, bad);
@@ -337,7 +340,7 @@ __global__ void __launch_bounds__(NT, 1)
                     const uint4 f0 = *reinterpret_cast<uint4*>(found), f1 = *reinterpret_cast<uint4*>(found + 4);
                     if (f0.x | f0.y | f0.z | f0.w | f1.x | f1.y | f1.z | f1.w)
                         for (int j = 0; j < KT; ++j)
-                            if (((seen[j >> 5] >> (j & 31)) & 1u) && ((found[j / ROWS] >> (j % ROWS)) & 1u)) l = NAN;
+                            if (((seen[j >> 5] >> (j & 31)) & 1u) && ((found[j / ROWS] >> (j % ROWS)) & 1u)) left_out = true;
                 }
                 float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -423,6 +426,12 @@ __global__ void __launch_bounds__(NT, 1)
                             *reinterpret_cast<uint4*>(out + c + 8 * j) = w;
                         }
                 }
+                if (valid && left_out)
+                    add_not_finite(a, p, depth, mask, D, 0, 1, [&](int c, uint32_t x) {
+                        uint32_t& y = reinterpret_cast<uint32_t*>(out)[c];
+                        y = pack_bf16(first_of(y) + first_of(x), second_of(y) + second_of(x));
+                    });
+                __syncwarp();
                 continue;
             }
             // a slot: per half [D / 4][rows] float4, then the rows' m and l
@@ -444,6 +453,13 @@ __global__ void __launch_bounds__(NT, 1)
                 slot[hr * D + r] = m;
                 slot[hr * D + hr + r] = l;
             }
+            if (valid && left_out)
+                add_not_finite(a, p, depth, mask, D, 0, 1, [&](int c, uint32_t x) {
+                    float* at = slot + (c / 2 * hr + r) * 4 + 2 * (c % 2);
+                    at[0] += first_of(x);
+                    at[1] += second_of(x);
+                });
+            __syncwarp();
         }
     }
     if (!ok && lane == 0) raise_err(a.err, CANOPY_DEVERR_TIMEOUT);

@@ -423,8 +423,8 @@ canopy_attend_plan_t canopy_attend_plan(int N, int B, int HQ, int HKV, canopy_dt
  *   scale > 0; q, o [N][HQ][d] in dtype (o apart from q and the caches, or the call
  *   is refused); the places that no row of a sequence sees (behind its
  *   last row, out of the window) need no page and may hold anything; what a place
- *   holds reaches no row that does not see it (where rows see different places, a
- *   bf16 row that sees a value that is not finite may be NaN throughout).
+ *   holds reaches no row that does not see it, and a value that is not finite
+ *   reaches no column but its own (as an infinity or NaN).
  * bf16: products on the tensor cores with fp32 sums and statistics, the weights
  * rounded to bf16 for the second product; fp32: fp32 throughout.
  * Data errors (parent, starts, lengths, context, pages) set bits in the workspace's

@@ -15,6 +15,10 @@
 #include "common.cuh"
 
 namespace canopy {
+
+bool make_bf16_box_map(CUtensorMap* m, const void* base, const uint64_t (&dim)[3], const uint64_t (&stride)[2],
+                       const uint32_t (&size)[3]);  // verify_tc.cu
+
 namespace att {
 
 constexpr int kMaskWords = kMaxT / 32;
@@ -53,14 +57,6 @@ struct Args {
 };
 
 // ---------------------------------------------------------------------------
-// Which keys a row sees.  t: the row's index in its sequence, depth its depth (t
-// without a tree), mask its path (null without a tree).
-__device__ inline bool sees(const Args& a, const Tile& tile, int depth, const uint32_t* mask, int key) {
-    const int p = key - tile.ctx;
-    if (mask && p >= 0) return p < tile.n && ((mask[p >> 5] >> (p & 31)) & 1u);
-    const int pos = tile.ctx + depth;
-    return key <= pos && (pos - key < a.window || key < a.sinks);
-}
 // Whether every row of the tile sees all of a key tile.
 __device__ inline bool all_see(const Tile& tile, int key_tile) {
     return key_tile < tile.sink_full || (key_tile >= tile.full_from && key_tile < tile.full_to);
@@ -334,7 +330,11 @@ __device__ inline uint32_t range_bits(int a, int b) {
     b = min(max(b, a), 32);
     return uint32_t((1ull << b) - (1ull << a));
 }
-// Which of the keys [base, base + 32) a row sees (att::sees for 32 keys).
+// Which of the keys [base, base + 32) a row sees, by its depth (its index in the
+// sequence without a tree) and its path (mask, null without a tree).  With key j's
+// place j - ctx among the new ones p and the row's position t = ctx + depth: in a tree
+// the new ones on its path (those out of the window are not in its mask); else
+// j <= t, and t - j < window or j < sinks.
 __device__ inline uint32_t seen_bits(const Args& a, const Tile& tile, int depth, const uint32_t* mask, int base) {
     const int pos = tile.ctx + depth;
     const int end = (mask ? min(pos, tile.ctx - 1) : pos) + 1;  // past the last one in the cache, or in all

@@ -21,10 +21,6 @@
 #include "attend.cuh"
 
 namespace canopy {
-
-bool make_bf16_box_map(CUtensorMap* m, const void* base, const uint64_t (&dim)[3], const uint64_t (&stride)[2],
-                       const uint32_t (&size)[3]);
-
 namespace att {
 namespace few {
 

@@ -19,7 +19,7 @@
 // until then the weights are merely larger than 1, by less than 2^8, and neither
 // sums nor roundings know the difference; when it does grow, the row's thread
 // scales O.  The weights are rounded to bf16 for the second product (their sum
-// is of the unrounded ones): a rounding of 2^-9 each, which averages out over the
+// is of the unrounded ones): off by up to 2^-8 each, which averages out over the
 // keys.
 //
 // Key tiles come by TMA, one box per page (or 16 keys, where tiles and pages
@@ -33,10 +33,6 @@
 #include "attend.cuh"
 
 namespace canopy {
-
-bool make_bf16_box_map(CUtensorMap* m, const void* base, const uint64_t (&dim)[3], const uint64_t (&stride)[2],
-                       const uint32_t (&size)[3]);
-
 namespace att {
 namespace tcg {
 

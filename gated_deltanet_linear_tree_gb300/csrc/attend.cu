@@ -383,7 +383,10 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) join_rows_kernel(const A
 template <typename OutT, int D>
 cudaError_t launch_join_rows(const Args& a, cudaStream_t st) {
     if (a.ctas == 1) return cudaSuccess;  // nothing is cut
-    // (row tile, key head) items, about; each is cut into about ctas / items pieces
+    // (row tile, key head) items, about; each is cut into about ctas / items pieces.  Measured, the whole call with 16,
+    // 4 and 1 warps a row, us: 152 pieces (one token behind 262,143, 16/2 heads) 53.6, 58.3 and 88.4; 38 (behind 32,000,
+    // 16/8) 31.6, 32.7, 41.9; 19 (two, 32/8) 49.9, 49.9, 53.7; 9 (four behind 16,000) 50.3, 49.8, 52.0; 4 (eight) 88.9,
+    // 89.6, 90.5; 2 (sixteen behind 8,000) 91.7, 89.0, 88.5.
     const int64_t rows = int64_t(a.N) * a.HQ, tiles = (a.N + a.rt - 1) / a.rt;
     const int64_t each = a.ctas / ((tiles > a.B ? tiles : a.B) * a.HKV);
     if (each >= 32) return launch_pdl(join_rows_kernel<OutT, D, 16>, dim3(unsigned(rows)), dim3(512), 0, st, a);
@@ -441,7 +444,14 @@ Layout layout(int N, int B, int g, int d) {
 
 size_t attend_ws_bytes(int N, int B, int HQ, int HKV, int d) { return att::layout(N, B, HQ / HKV, d).end; }
 // Rows of a sequence and key head on average: up to 16 are one row tile of the
-// kernel for few rows.
+// kernel for few rows, which reads the cache once for each.  Measured, few / tiles,
+// us, 4 to 16 rows and from 20 on: 64 streams behind 4,000, 32/8 heads, 170-177 /
+// 191-195 and 330-643 / 195-199; 16 streams, 16/4 heads, 32-41 / 38-43 and 60-91 / 43;
+// 64 streams of 16/16 heads, 16 rows, 184 / 208.  A lone stream behind 4,000 is
+// taken to the tiles early: 17.9 / 21.2 at 16 rows, 20.0 / 25.3 at 32, 22.4 / 25.4 at 64.
+// The host knows the average only: 127 single tokens and a chunk of 385 rows (16/4
+// heads, behind 4,000) take 220 us with few rows, one row more 236 with tiles, and 214
+// in a call each.
 canopy_attend_plan_t attend_plan(int N, int B, int HQ, int HKV, int bf16, int d) {
     if (!bf16) return CANOPY_ATTEND_PLAN_FP32;
     const int g = HQ / HKV;

@@ -10,8 +10,8 @@
 // and one that loads: three stages of K and V tiles by TMA, one box per page and
 // 64 columns.  Two CTAs an SM, 192 KB of reads in flight.
 //
-// 64 streams behind 4,000 to 16,000 tokens, 32/8 heads: 390 us, 6.8 TB/s, the
-// measured copy bandwidth (128-row products in attend_tc.cu: 492).  One behind
+// 64 streams behind 4,000 to 16,000 tokens, 32/8 heads: 394 to 399 us, 6.7 TB/s, 0.98
+// of the measured copy bandwidth (128-row products in attend_tc.cu: 492).  One behind
 // 262,143 tokens, 16/2 heads: 44 us, 0.9 of it, and 10 for the launch that joins the
 // pieces.  One behind 700: two launches' latencies, 10.8 us.
 //
@@ -25,7 +25,10 @@ namespace att {
 namespace few {
 
 constexpr int KT = 64, NT = 96;
-constexpr int kPlanSeqs = 128, kPlanTiles = 256;  // up to these sizes every CTA makes the plan for itself
+// Up to these sizes every CTA makes the plan for itself: what shared memory has room for.  Measured against a launch
+// that plans, us: one stream behind 100 tokens 7.9 / 9.7, 32 10.0 / 12.8, 128 21.6 / 24.9; behind 2,000 9.5 / 11.7,
+// 34 / 38 and 96 / 99 (16/4 heads).
+constexpr int kPlanSeqs = 128, kPlanTiles = 256;
 
 template <int D>
 struct Smem {

@@ -19,8 +19,9 @@
 //
 // 16,383 tokens, 32/8 heads, three axes, into pages of 16: 82 us, 4.9 TB/s (0.73 of
 // the measured copy bandwidth; the reads in flight bound it, at 20 warps an SM and
-// 64 bytes a lane: more warps spill, fewer have less in flight).  1,024 unit rows of
-// 16/16 heads 6.7 us; one token 2.7 us in a graph, 5.6 by its call.
+// 64 bytes a lane: more warps spill, fewer have less in flight); in fp32 137 us, 0.87.
+// 1,024 unit rows of 16/16 heads 5.5 us in a graph, 6.8 to 8.3 by calls; one token 2.8
+// us in a graph, 5.4 to 6.8 by its call.
 #include "common.cuh"
 
 namespace canopy {
@@ -112,7 +113,9 @@ __device__ inline int sequence_of(const Args& a, int n, int& i, int* bad) {
 }
 
 // freq / 2 pi as a 64-bit fraction of a turn: the significand, at the top of 64
-// bits, times 2^66 / 2 pi, its place given by the exponent.
+// bits, times 2^66 / 2 pi, its place given by the exponent.  The product keeps 64
+// bits: off by up to 2^-64 of a turn below freq = 2, doubling with every power of
+// two above; times a position of 2^31 that is an angle of 2.3e-8 at freq = 64.
 __device__ inline uint64_t turns_of(float freq) {
     const uint32_t bits = __float_as_uint(freq);
     const int exponent = int((bits >> 23) & 255) - 150;  // freq = significand * 2^exponent
@@ -343,6 +346,10 @@ cudaError_t launch(Args a, cudaStream_t st) {
     constexpr int HEADS = 256 / D, MOST = 152 * 5;  // resident blocks
     a.sets = (a.HQ + HEADS - 1) / HEADS + (a.kc ? 2 : 1) * ((a.HKV + HEADS - 1) / HEADS);
     const int64_t warps = int64_t(a.N) * a.sets;
+    // Up to eight warps a scheduler (four an SM), a warp a set.  Measured, few / many, us in a graph: 16/4 heads
+    // into the cache 4.9 / 7.7 at 4,864 warps, 7.0 / 8.9 at 8,000, 9.5 / 9.2 at 12,000, 28 / 18 at 40,000; unit rows of
+    // 16/16 heads 2.2 / 3.2, 3.1 / 5.2, 4.4 / 5.4 and 12.9 / 10.0; fp32, 16/4 heads of 64, 4.7 / 7.6, 6.7 / 7.8, 9.5 /
+    // 11.3 and 27 / 20.  (The sides cross at 12,000 to 20,000 warps: the border is on the low side.)
     if (warps <= 8 * 152 * 4)
         return launch_pdl(prep_few_kernel<T, D>, dim3(unsigned((warps + 3) / 4)), dim3(128), 0, st, a);
     // as many warps to a token as leave none of the resident ones idle

@@ -383,7 +383,8 @@ typedef enum { CANOPY_PAIRS_HALF = 0, CANOPY_PAIRS_ADJACENT = 1 } canopy_pairs;
  *   values go into them, k_out is NULL and v, page_table and context are given.
  *   Without (k_cache NULL), k_out [N][HKV][d] (may be k) receives the keys, and
  *   v, v_cache, page_table, context, starts and lengths are NULL, B 0.
- * Norm and rotation in fp32 (angles of any int32 position to 1e-7), rounded once.
+ * Norm and rotation in fp32 (angles of any int32 position to 1e-7, for frequencies
+ * up to 64), rounded once.
  * err: an optional device int32 (OR-ed): a place without a page sets
  * CANOPY_DEVERR_PAGE and is not written, nor are the places of a stream whose context
  * is below zero (CANOPY_DEVERR_LENGTH; its queries are made as from place 0).  Any

@@ -362,31 +362,47 @@ __device__ inline uint32_t finite_part(uint32_t x) {
 
 // What the products leave out for a row that sees it: the values that are not
 // finite, in the tiles of [u0, u1) whose keys the tile's rows see in part.  They go
-// to the row's sums behind the last product, add(c, x) for the column pairs c =
-// first, first + step, ... < d (x: two bf16 values, the finite ones zero), read from
-// the pages again: a row that sees such a value is rare.
-template <typename Add>
+// to the row's sums behind the last product, add(c, x, y) for column pair c, read
+// from the pages again: a row that sees such a value is rare.  A thread has Words
+// first, first + step, ... of a row, of W pairs each.
+template <typename Words, typename Add>
 __device__ inline void add_not_finite(const Args& a, const Piece& p, int depth, const uint32_t* mask, int d, int first,
                                       int step, Add add) {
-    const uint32_t* vc = static_cast<const uint32_t*>(a.vc);
+    constexpr int W = sizeof(Words) / 4;
+    const int words = d / (2 * W);
 #pragma unroll 1
-    for (int u = p.u0; u < p.u1; ++u) {
-        const int kt = key_tile(p.tile, u);
-        if (all_see(p.tile, kt)) continue;
-        const int end = min((kt + 1) * a.kt, p.tile.hi);
+    for (int c = first; c < words; c += step) {
+        float sum[2 * W] = {};
+        bool more = true;  // some column may still change
 #pragma unroll 1
-        for (int key = kt * a.kt; key < end; ++key) {
-            if (!(seen_bits(a, p.tile, depth, mask, key) & 1u)) continue;
-            const int page = a.table[size_t(p.tile.b) * a.max_pages + (key >> a.log_page)];
-            if (page < 0 || page >= a.pages) continue;
-            const uint32_t* row =
-                vc + (((size_t(page) * a.HKV + p.h) << a.log_page) + (key & ((1 << a.log_page) - 1))) * (d / 2);
+        for (int u = p.u0; more && u < p.u1; ++u) {
+            const int kt = key_tile(p.tile, u), end = (kt + 1) * a.kt;
+            if (all_see(p.tile, kt)) continue;
 #pragma unroll 1
-            for (int c = first; c < d / 2; c += step) {
-                const uint32_t x = row[c];
-                if (!finite_pair(x)) add(c, x ^ finite_part(x));
+            for (int base = kt * a.kt; more && base < end; base += 32) {
+                uint32_t seen = seen_bits(a, p.tile, depth, mask, base) & range_bits(0, end - base);
+#pragma unroll 1
+                for (; seen; seen &= seen - 1) {
+                    const int key = base + __ffs(seen) - 1;
+                    const int page = a.table[size_t(p.tile.b) * a.max_pages + (key >> a.log_page)];
+                    if (page < 0 || page >= a.pages) continue;
+                    const size_t row = (((size_t(page) * a.HKV + p.h) << a.log_page) + (key & ((1 << a.log_page) - 1)));
+                    const Words x = static_cast<const Words*>(a.vc)[row * words + c];
+#pragma unroll
+                    for (int i = 0; i < W; ++i) {
+                        const uint32_t y = reinterpret_cast<const uint32_t*>(&x)[i], bad = y ^ finite_part(y);
+                        sum[2 * i] += first_of(bad);
+                        sum[2 * i + 1] += second_of(bad);
+                    }
+                }
+                more = false;
+#pragma unroll
+                for (int i = 0; i < 2 * W; ++i) more |= sum[i] == sum[i];
             }
         }
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            if (sum[2 * i] != 0.f || sum[2 * i + 1] != 0.f) add(W * c + i, sum[2 * i], sum[2 * i + 1]);
     }
 }
 

@@ -424,9 +424,9 @@ __global__ void __launch_bounds__(NT, 1)
                         }
                 }
                 if (valid && left_out)
-                    add_not_finite(a, p, depth, mask, D, 0, 1, [&](int c, uint32_t x) {
-                        uint32_t& y = reinterpret_cast<uint32_t*>(out)[c];
-                        y = pack_bf16(first_of(y) + first_of(x), second_of(y) + second_of(x));
+                    add_not_finite<uint4>(a, p, depth, mask, D, 0, 1, [&](int c, float x, float y) {
+                        uint32_t& pair = reinterpret_cast<uint32_t*>(out)[c];
+                        pair = pack_bf16(first_of(pair) + x, second_of(pair) + y);
                     });
                 __syncwarp();
                 continue;
@@ -451,10 +451,10 @@ __global__ void __launch_bounds__(NT, 1)
                 slot[hr * D + hr + r] = l;
             }
             if (valid && left_out)
-                add_not_finite(a, p, depth, mask, D, 0, 1, [&](int c, uint32_t x) {
+                add_not_finite<uint4>(a, p, depth, mask, D, 0, 1, [&](int c, float x, float y) {
                     float* at = slot + (c / 2 * hr + r) * 4 + 2 * (c % 2);
-                    at[0] += first_of(x);
-                    at[1] += second_of(x);
+                    at[0] += x;
+                    at[1] += y;
                 });
             __syncwarp();
         }

@@ -3,6 +3,7 @@ columns, finite sums in all others, wherever tiles and pieces end."""
 
 import numpy as np
 import pytest
+import torch
 
 from attention_cases import TREES, attend_bound, attend_case, attend_reference, run_attend
 
@@ -52,3 +53,21 @@ def test_values_that_are_not_finite_stay_in_their_columns(lib, kind, window, sin
     # the other columns' sums are those of the values without the bad ones, which have no part in them
     off = np.abs(o - plain)[~hit]
     assert (off <= attend_bound(c, plain, weight, int((c["ctxs"] + c["lens"]).max()))[~hit]).all()
+
+
+@pytest.mark.parametrize("kind", ["window", "trees", "tokens"])
+def test_caches_of_nothing_but_nan(lib, kind):
+    """Every row sees such values in every tile: NaN throughout, and no wait gives up."""
+    d, HKV, page = 128, 2, 64
+    B, n, ctx = (2, 1500, 3000) if kind == "window" else (6, 64 if kind == "trees" else 1, 1000)
+    pages = -(-(n + ctx) // page)
+    k = torch.randn(B * pages, HKV, page, d, device="cuda").bfloat16()
+    v = torch.full_like(k, float("nan"))
+    table = torch.arange(B * pages, dtype=torch.int32, device="cuda").view(B, pages)
+    context = torch.full((B,), ctx, dtype=torch.int32, device="cuda")
+    q = torch.randn(B, n, 4 * HKV, d, device="cuda").bfloat16()
+    ws = lib.attend_workspace(B * n, B, 4 * HKV, HKV, d)
+    args = dict(parent=torch.arange(-1, n - 1, dtype=torch.int32, device="cuda").expand(B, n).contiguous()) \
+        if kind == "trees" else dict(window=700, sinks=70)
+    assert lib.attend(q, k, v, table, context, ws, **args).isnan().all()
+    assert lib.read_device_error(ws) == 0

@@ -11,10 +11,10 @@
 // softmax has S in registers the next tile's S is formed, and one thread a half
 // issues both products.  Tiles of 128 with P over S were as fast only with the
 // halves half a tile apart (a chunk of 4,096 tokens behind 28,672, 32/8 heads: 1,594
-// us; 1,485 to 1,587 this way, 1.3 PFLOP/s, and a window of 1,024 292 and 187 us);
+// us; 1,460 to 1,587 this way, 1.3 PFLOP/s, and a window of 1,024 292 and 187 us);
 // tiles of 64 with two P took 1,976 us.  The softmax's warps hold it: 2,300 cycles a tile of
 // 80 keys, where the products take 1,280 (tensor pipe 0.6 of active cycles).  They
-// spill 64 bytes of stores and 108 of loads (d = 64: 164 and 252) at 168 registers.
+// spill 64 bytes of stores and 108 of loads (d = 64: 132 and 224) at 168 registers.
 //
 // m is the running maximum as of the last time that it grew by more than 2^8:
 // until then the weights are merely larger than 1, by less than 2^8, and neither

@@ -331,10 +331,10 @@ __device__ inline uint32_t range_bits(int a, int b) {
     return uint32_t((1ull << b) - (1ull << a));
 }
 // Which of the keys [base, base + 32) a row sees, by its depth (its index in the
-// sequence without a tree) and its path (mask, null without a tree).  With key j's
-// place j - ctx among the new ones p and the row's position t = ctx + depth: in a tree
-// the new ones on its path (those out of the window are not in its mask); else
-// j <= t, and t - j < window or j < sinks.
+// sequence without a tree) and its path (mask, null without a tree).  The row is at
+// position t = ctx + depth.  Key j is a new one of a tree if j >= ctx there: it is seen
+// if node j - ctx is in the mask (those out of the window are not).  Any other is seen
+// if j <= t, and t - j < window or j < sinks.
 __device__ inline uint32_t seen_bits(const Args& a, const Tile& tile, int depth, const uint32_t* mask, int base) {
     const int pos = tile.ctx + depth;
     const int end = (mask ? min(pos, tile.ctx - 1) : pos) + 1;  // past the last one in the cache, or in all

@@ -364,15 +364,15 @@ __global__ void __launch_bounds__(NT, 2)
                         static_cast<__nv_bfloat16*>(a.o) +
                         (size_t(tile.row + r / a.g) * a.HQ + p.h * a.g + r % a.g) * D);
                     float* sum = a.part + size_t(p.slot) * 16 * (D + 2) + r * D;
-                    add_not_finite<uint32_t>(a, p, x ? depth[1] : depth[0], x ? mask[1] : mask[0], D, c0 / 2, 4,
-                                   [&](int c, float y, float z) {
-                                       if (p.whole) {
-                                           out[c] = pack_bf16(first_of(out[c]) + y, second_of(out[c]) + z);
-                                       } else {
-                                           sum[2 * c] += y;
-                                           sum[2 * c + 1] += z;
-                                       }
-                                   });
+                    const auto add = [&](int c, float y, float z) {
+                        if (p.whole) {
+                            out[c] = pack_bf16(first_of(out[c]) + y, second_of(out[c]) + z);
+                        } else {
+                            sum[2 * c] += y;
+                            sum[2 * c + 1] += z;
+                        }
+                    };
+                    add_not_finite<uint32_t>(a, p, x ? depth[1] : depth[0], x ? mask[1] : mask[0], D, c0 / 2, 4, add);
                 }
             mbar_arrive(&sm.taken);
         }

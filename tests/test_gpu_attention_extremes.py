@@ -144,3 +144,33 @@ def test_first_calls_captured(lib, T, bf16):
     r = subprocess.run([sys.executable, "-c", FIRST.format(bf16=bf16, T=T)], cwd=ROOT, capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("lead", [(3, 5), (3, 1), (1, 5), (1, 1), (400, 3), (7,), (1,), (2500,)])
+@pytest.mark.parametrize("native", [True, False])
+def test_slices_of_a_projection(lib, lead, native, bf16, monkeypatch):
+    """Queries, keys and values side by side in one buffer, with a gap behind them: the results of dense ones."""
+    lib.load()
+    if not native:
+        monkeypatch.setattr(lib, "_marshal", type("Stub", (), {"qk_prep": staticmethod(lambda *a: None)}))
+    HQ, HKV, d, page = 6, 2, 64, 16
+    dt = torch.bfloat16 if bf16 else torch.float32
+    torch.manual_seed(len(lead) + lead[0])
+    wide = torch.randn(*lead, HQ + 2 * HKV + 1, d, device="cuda").to(dt)
+    q, k, v, _ = wide.split([HQ, HKV, HKV, 1], -2)
+    B, T = lead if len(lead) == 2 else (lead[0], 1)
+    pages = -(-(T + 20) // page)
+    caches = torch.randn(2, B * pages, HKV, page, d, device="cuda").to(dt)
+    table = torch.randperm(B * pages, device="cuda").int().view(B, pages)
+    context = torch.randint(0, 20, (B,), dtype=torch.int32, device="cuda")
+    freqs = torch.rand(16, device="cuda")
+    out = []
+    for rows in ((q, k, v), [x.contiguous() for x in (q, k, v)]):
+        mine = caches.clone()
+        args = dict(lengths=torch.full((B,), max(1, T - 1), dtype=torch.int32, device="cuda")) if len(lead) == 2 else {}
+        p, _ = lib.qk_prep(*rows, freqs=freqs, k_cache=mine[0], v_cache=mine[1], page_table=table, context=context,
+                           q_out=torch.full((*lead, HQ, d), 7.0, device="cuda", dtype=dt), **args)
+        out.append([p, mine, *lib.qk_prep(*rows[:2], norm="l2")])
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+    assert not torch.equal(out[0][1], caches)
